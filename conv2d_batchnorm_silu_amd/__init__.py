@@ -2,7 +2,9 @@
 
 The compute path is a C-ABI shared library (``libtgconv.so``, built from
 ``csrc/``) of hand-written HIP kernels; ``binding`` wraps it with ctypes and
-uses PyTorch only for device memory and streams. ``inputs`` holds the seeded
+uses PyTorch only for device memory and streams; ``sequence`` does the same
+for the sequence operators (layer norm, causal convolution, selective scan).
+``inputs`` holds the seeded
 synthetic data recipes shared by tests and the benchmark.
 
 Importing this package does not load the shared library; the first use of a
@@ -14,10 +16,18 @@ _BINDING_NAMES = {
     "ConvBnSilu", "bn_fold", "library", "Kernel", "Dtype", "TgError", "status_string",
     "kernel_name", "library_path", "build_library", "exported_symbols", "Table", "dispatch_choose",
 }
+_SEQUENCE_NAMES = {
+    "layer_norm", "layer_norm_train", "layer_norm_backward", "causal_conv",
+    "causal_conv_backward", "causal_conv_step", "selective_scan", "selective_scan_train",
+    "selective_scan_backward", "selective_scan_step", "ScanGradients",
+}
 
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
         return getattr(binding, name)
+    if name in _SEQUENCE_NAMES:
+        from . import sequence
+        return getattr(sequence, name)
     raise AttributeError(name)

@@ -17,6 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 LIB_PATH = os.path.join(_HERE, "libtgconv.so")
 HEADER = os.path.join(_ROOT, "include", "tg_conv_bn_silu.h")
+HEADERS = (HEADER, os.path.join(_ROOT, "include", "tg_sequence.h"))
 
 _lock = threading.Lock()
 _lib = None
@@ -26,6 +27,7 @@ class Dtype(enum.IntEnum):
     F16 = 0
     F32 = 1
     F8_E4M3 = 2  # output only
+    BF16 = 3  # sequence operators only
 
 
 class Kernel(enum.IntEnum):
@@ -132,8 +134,8 @@ def library():
 
 
 def exported_symbols() -> list:
-    """Function names the public header declares."""
-    text = open(HEADER).read()
+    """Function names the public headers declare."""
+    text = "".join(open(h).read() for h in HEADERS)
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(tg_[a-z0-9_]+)\s*\(", text)))
 

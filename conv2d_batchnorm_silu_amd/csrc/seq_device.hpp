@@ -1,0 +1,126 @@
+// seq_device.hpp -- what the sequence operators' kernels share: element types,
+// where the sequences of a batch lie, and wave reductions.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "tg_device.hpp"
+#include "tg_sequence.h"
+
+namespace tg {
+
+typedef __bf16 bf16;
+
+template <typename T, int V>
+struct VecOf {
+    typedef T type __attribute__((ext_vector_type(V)));
+};
+template <typename T>
+struct VecOf<T, 1> {
+    typedef T type;
+};
+
+// V consecutive elements at p (aligned to V elements) as fp32, and back with
+// one rounding to nearest even.
+template <typename T, int V>
+__device__ __forceinline__ void load_f32(const T* p, float (&v)[V]) {
+    if constexpr (V == 1) {
+        v[0] = (float)*p;
+    } else {
+        const typename VecOf<T, V>::type r = *(const typename VecOf<T, V>::type*)p;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = (float)r[i];
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_f32(T* p, const float (&v)[V]) {
+    if constexpr (V == 1) {
+        *p = (T)v[0];
+    } else {
+        typename VecOf<T, V>::type r;
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = (T)v[i];
+        *(typename VecOf<T, V>::type*)p = r;
+    }
+}
+
+// Sum over the 64 lanes, in every lane, in a fixed order.
+__device__ __forceinline__ float wave_sum(float v) {
+    v = row_sum16(v);
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    return v;
+}
+
+// Where the sequences of a batch lie. L: rows of each sequence of a dense
+// batch. The packed offsets are cut to 0 .. rows and to a non-negative
+// length, so a wrong one cannot lead outside the tensors.
+struct SeqMap {
+    const int32_t* offsets;
+    int seqs, rows, L;
+    __device__ __forceinline__ int start(int s) const {
+        if (!offsets) return s * L;
+        const int v = offsets[s];
+        return v < 0 ? 0 : (v > rows ? rows : v);
+    }
+    __device__ __forceinline__ int end(int s) const {
+        if (!offsets) return (s + 1) * L;
+        const int b = start(s), v = offsets[s + 1];
+        return v < b ? b : (v > rows ? rows : v);
+    }
+    // Pieces of P rows, counted through the batch: sequence s owns the slots
+    // from start(s)/P + s on, one for each P rows of it (the last may be
+    // short). floor(a/P) + floor(b/P) <= floor((a+b)/P) keeps the sequences'
+    // slots apart, so rows/P + seqs slots serve any lengths, which the host
+    // does not know.
+    __device__ __forceinline__ int slot0(int s, int P) const { return start(s) / P + s; }
+    // The sequence that owns `slot`: the last one whose slot0 is not past it.
+    __device__ __forceinline__ int owner(int slot, int P) const {
+        if (!offsets) {
+            // start(s)/P + s grows by at least one with s, so s <= slot.
+            const int64_t step = (int64_t)L + P;  // (s*L)/P + s = floor(s*(L+P)/P)
+            int64_t s = (((int64_t)slot + 1) * P - 1) / step;
+            return (int)(s < seqs - 1 ? s : seqs - 1);
+        }
+        int lo = 0, hi = seqs - 1;
+        while (lo < hi) {
+            const int m = (lo + hi + 1) >> 1;
+            if (slot0(m, P) <= slot) lo = m;
+            else hi = m - 1;
+        }
+        return lo;
+    }
+};
+
+// Rows of a tensor in element strides; row l (packed: row start+l) of
+// sequence s.
+template <typename P>
+struct Rows {
+    P* p;
+    int64_t seq, row;
+};
+template <typename T, typename P>
+__device__ __forceinline__ T* row_of(const Rows<P>& r, const SeqMap& m, int s, int start, int l) {
+    return (T*)r.p + (m.offsets ? ((int64_t)start + l) * r.row
+                                : (int64_t)s * r.seq + (int64_t)l * r.row);
+}
+
+inline SeqMap map_of(const tg_seqs& s) {
+    return {s.offsets, (int)s.seqs, (int)s.rows, (int)(s.rows / s.seqs)};
+}
+template <typename P>
+Rows<P> rows_of(const tg_rows& r) {
+    return {(P*)r.p, r.seq_stride, r.row_stride};
+}
+
+// log(1 + e^v) to a few units in the last place at both ends: small step
+// sizes come from far negative v, where 1 + e^v would drop e^v's bits.
+__device__ __forceinline__ float softplus_f32(float v) {
+    return fmaxf(v, 0.0f) + log1pf(__builtin_amdgcn_exp2f(-fabsf(v) * kLog2e));
+}
+__device__ __forceinline__ float sigmoid_f32(float v) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
+}
+
+}  // namespace tg

@@ -58,7 +58,12 @@ typedef enum {
  * E4M3 (1 sign, 4 exponent, 3 mantissa bits, bias 7, largest finite 448),
  * one byte per element, rounded to nearest even; results beyond +-448 are
  * outside the format and not specified. */
-typedef enum { TG_F16 = 0, TG_F32 = 1, TG_F8_E4M3 = 2 } tg_dtype;
+typedef enum {
+    TG_F16 = 0,
+    TG_F32 = 1,
+    TG_F8_E4M3 = 2,
+    TG_BF16 = 3 /* the sequence operators only (tg_sequence.h) */
+} tg_dtype;
 
 /* Kernel selection ("Fusing an Epilogue", section "Three kernels for one
  * operation": one scalar, one spatially tiled, one GEMM-shaped kernel, picked

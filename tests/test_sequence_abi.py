@@ -1,0 +1,193 @@
+"""The sequence operators' C entry points on the host: every argument error is
+found before a launch (no call here reaches the GPU), sizes are what the header
+says, and the Python layer refuses tensors that are not on a device."""
+import ctypes
+
+import pytest
+import torch
+
+import conv2d_batchnorm_silu_amd as tg
+from conv2d_batchnorm_silu_amd import sequence as S
+
+OK, INVAL, UNSUP, ALIGN, WS, HIPERR = range(6)
+F16, F32, F8, BF16 = 0, 1, 2, 3
+P = 0x1000  # an aligned address that nothing reads
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return S._lib()
+
+
+def _norm(lib, x=P, xs=8, res=0, rs=0, gamma=P, beta=P, eps=1e-5, rows=4, C=8, dt=F16, y=P, sum=0,
+          mean=0, rstd=0):
+    return lib.tg_layer_norm(x, xs, res, rs, gamma, beta, eps, rows, C, dt, y, sum, mean, rstd, 0)
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(rows=-1), INVAL), (dict(C=0), INVAL), (dict(eps=-1.0), INVAL), (dict(eps=float("nan")), INVAL),
+    (dict(gamma=0), INVAL), (dict(x=0), INVAL), (dict(y=0), INVAL), (dict(res=P), INVAL),
+    (dict(sum=P), INVAL), (dict(mean=P), INVAL), (dict(xs=7), INVAL), (dict(xs=-8), INVAL),
+    (dict(res=P, sum=P, rs=3), INVAL), (dict(dt=F8), UNSUP), (dict(dt=9), UNSUP),
+    (dict(rows=1 << 31), UNSUP), (dict(C=1 << 21, xs=1 << 21), UNSUP), (dict(x=P + 1), ALIGN),
+    (dict(gamma=P + 2), ALIGN), (dict(dt=F32, y=P + 2), ALIGN), (dict(rows=0, x=0, y=0), OK)])
+def test_norm_arguments(lib, bad, want):
+    assert _norm(lib, **bad) == want
+
+
+def test_norm_backward_arguments(lib):
+    n = ctypes.c_size_t()
+    assert lib.tg_layer_norm_backward_workspace(4, 8, F16, None) == INVAL
+    assert lib.tg_layer_norm_backward_workspace(4, 8, F8, ctypes.byref(n)) == UNSUP
+    assert lib.tg_layer_norm_backward_workspace(-1, 8, F16, ctypes.byref(n)) == INVAL
+    assert lib.tg_layer_norm_backward_workspace(4, 8, F16, ctypes.byref(n)) == OK and n.value > 0
+
+    def call(dy=P, dys=8, s=P, ss=8, gamma=P, mean=P, rstd=P, dsum=0, dss=0, rows=4, C=8, dt=F16, dx=P,
+             dg=P, db=P, ws=P, size=n.value):
+        return lib.tg_layer_norm_backward(dy, dys, s, ss, gamma, mean, rstd, dsum, dss, rows, C, dt, dx,
+                                          dg, db, ws, size, 0)
+    for bad in (dict(dy=0), dict(s=0), dict(mean=0), dict(rstd=0), dict(dx=0), dict(dg=0), dict(gamma=0),
+                dict(dys=4), dict(ss=-8), dict(dsum=P, dss=5), dict(C=0)):
+        assert call(**bad) == INVAL, bad
+    assert call(ws=0) == WS and call(size=n.value - 1) == WS
+    assert call(ws=P + 4) == ALIGN and call(dx=P + 1) == ALIGN and call(dt=7) == UNSUP
+
+
+def _rows(p=P, seq=0, row=8):
+    return S._Rows(p, seq, row)
+
+
+def _conv(**kw):
+    a = S._ConvArgs(S._Seqs(kw.pop("seqs", 1), kw.pop("rows", 4), kw.pop("offsets", 0)), 8, 4, F16, 0)
+    a.x, a.y, a.w = _rows(seq=32), _rows(seq=32), P
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(seqs=0), INVAL), (dict(rows=-1), INVAL), (dict(seqs=3), INVAL), (dict(D=0), INVAL),
+    (dict(K=0), INVAL), (dict(K=1), UNSUP), (dict(K=9), UNSUP), (dict(w=0), INVAL), (dict(dtype=F8), UNSUP),
+    (dict(act=1), UNSUP), (dict(x=_rows(0)), INVAL), (dict(y=_rows(0)), INVAL),
+    (dict(y=_rows(seq=32, row=7)), INVAL), (dict(y=_rows(row=0)), INVAL), (dict(x=_rows(row=-8)), INVAL),
+    (dict(rows=1 << 30, offsets=P), UNSUP), (dict(offsets=P + 2), ALIGN), (dict(x=_rows(P + 1, 32)), ALIGN),
+    (dict(initial=P + 1), ALIGN), (dict(bias=P + 2), ALIGN)])
+def test_conv_arguments(lib, bad, want):
+    assert lib.tg_causal_conv(ctypes.byref(_conv(**bad)), 0) == want
+
+
+def test_conv_backward_arguments(lib):
+    n = ctypes.c_size_t()
+    a = _conv()
+    assert lib.tg_causal_conv_backward_workspace(ctypes.byref(a), None) == INVAL
+    assert lib.tg_causal_conv_backward_workspace(ctypes.byref(a), ctypes.byref(n)) == OK and n.value > 0
+
+    def call(a=a, dy=_rows(seq=32), dx=_rows(seq=32), dw=P, ws=P, size=n.value, dinit=0):
+        return lib.tg_causal_conv_backward(ctypes.byref(a), dy, dx, dw, P, 0, dinit, ws, size, 0)
+    assert call(dw=0) == INVAL and call(dy=_rows(0)) == INVAL and call(dx=_rows(0)) == INVAL
+    assert call(dx=_rows(seq=32, row=4)) == INVAL and call(ws=0) == WS and call(size=n.value - 1) == WS
+    assert call(dinit=P + 1) == ALIGN and call(ws=P + 8) == ALIGN
+    assert lib.tg_causal_conv(None, 0) == INVAL
+
+
+def test_conv_step_arguments(lib):
+    def call(x=P, xs=8, st=P, num=4, slots=0, w=P, n=4, D=8, K=4, dt=F16, act=0, y=P):
+        return lib.tg_causal_conv_step(x, xs, st, num, slots, w, 0, n, D, K, dt, act, y, 0)
+    assert call(n=5) == INVAL and call(x=0) == INVAL and call(y=0) == INVAL and call(st=0) == INVAL
+    assert call(w=0) == INVAL and call(xs=4) == INVAL and call(n=-1) == INVAL and call(num=-1) == INVAL
+    assert call(K=9) == UNSUP and call(dt=F8) == UNSUP and call(act=2) == UNSUP
+    assert call(slots=P + 1) == ALIGN and call(x=P + 1) == ALIGN and call(n=0, x=0, y=0) == OK
+
+
+def _scan(**kw):
+    a = S._ScanArgs(S._Seqs(kw.pop("seqs", 1), kw.pop("rows", 4), kw.pop("offsets", 0)), 8, 16, 1, F16, 1)
+    a.x = a.dt = a.y = a.z = _rows(seq=32)
+    a.B = a.C = _rows(seq=64, row=16)
+    a.A = P
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+BAD_SCAN = [(dict(seqs=0), INVAL), (dict(seqs=3), INVAL), (dict(D=0), INVAL), (dict(N=0), INVAL), (dict(G=0), INVAL),
+            (dict(G=3), INVAL), (dict(N=129), UNSUP), (dict(dtype=F8), UNSUP), (dict(A=0), INVAL),
+            (dict(x=_rows(0)), INVAL), (dict(dt=_rows(0)), INVAL), (dict(B=_rows(0)), INVAL),
+            (dict(C=_rows(0)), INVAL), (dict(A=P + 2), ALIGN), (dict(B=_rows(P + 1, 64, 16)), ALIGN),
+            (dict(initial=P + 2), ALIGN)]
+
+
+@pytest.mark.parametrize("bad,want", BAD_SCAN + [(dict(y=_rows(0)), INVAL), (dict(y=_rows(seq=32, row=4)), INVAL)])
+def test_scan_arguments(lib, bad, want):
+    assert lib.tg_selective_scan(ctypes.byref(_scan(**bad)), P, 1 << 40, 0, 0, 0) == want
+
+
+def _sizes(lib, a):
+    v = [ctypes.c_size_t() for _ in range(3)]
+    assert lib.tg_selective_scan_sizes(ctypes.byref(a), *(ctypes.byref(t) for t in v)) == OK
+    return [t.value for t in v]
+
+
+def test_scan_workspaces(lib):
+    a = _scan()
+    work, saved, back = _sizes(lib, a)
+    assert saved >= 8 * 16 * 4 and back > 0
+    assert lib.tg_selective_scan(ctypes.byref(a), P, work, P, saved - 1, 0) == WS
+    if work:
+        assert lib.tg_selective_scan(ctypes.byref(a), 0, 0, 0, 0, 0) == WS
+    # A packed batch has room for every split of its rows into sequences.
+    assert _sizes(lib, _scan(seqs=9, rows=1000, offsets=P))[1] >= _sizes(lib, _scan(rows=1000))[1]
+
+
+@pytest.mark.parametrize("bad,want", BAD_SCAN)
+def test_scan_backward_arguments(lib, bad, want):
+    g = S._ScanGrads(_rows(seq=32), 0, _rows(seq=32), _rows(seq=32), _rows(seq=64, row=16),
+                     _rows(seq=64, row=16), _rows(seq=32), P)
+    assert lib.tg_selective_scan_backward(ctypes.byref(_scan(**bad)), ctypes.byref(g), P, 1 << 40, P, 1 << 40, 0) == want
+
+
+def test_scan_backward_gradients(lib):
+    _, saved, back = _sizes(lib, _scan())
+    full = dict(dy=_rows(seq=32), dx=_rows(seq=32), ddt=_rows(seq=32), dB=_rows(seq=64, row=16),
+                dC=_rows(seq=64, row=16), dz=_rows(seq=32), dA=P)
+
+    def call(sv=P, svn=saved, ws=P, wsn=back, **kw):
+        g = S._ScanGrads()
+        for k, v in dict(full, **kw).items():
+            setattr(g, k, v)
+        return lib.tg_selective_scan_backward(ctypes.byref(_scan()), ctypes.byref(g), sv, svn, ws, wsn, 0)
+    for name in ("dy", "dx", "ddt", "dB", "dC", "dz"):
+        assert call(**{name: _rows(0)}) == INVAL, name
+    assert call(dA=0) == INVAL and call(dB=_rows(seq=64, row=15)) == INVAL
+    assert call(sv=0) == WS and call(svn=saved - 1) == WS and call(ws=0) == WS and call(wsn=back - 1) == WS
+    assert call(dinitial=P + 2) == ALIGN and call(dx=_rows(P + 1, 32)) == ALIGN
+
+
+def test_scan_step_arguments(lib):
+    def call(state=P, num=4, slots=0, **kw):
+        return lib.tg_selective_scan_step(ctypes.byref(_scan(**dict(dict(seqs=4, rows=4), **kw))), state, num, slots, 0)
+    assert call(state=0) == INVAL and call(num=3) == INVAL and call(rows=8) == INVAL and call(offsets=P) == INVAL
+    assert call(num=-1) == INVAL and call(state=P + 2) == ALIGN and call(slots=P + 1) == ALIGN
+    assert call(N=200) == UNSUP and call(y=_rows(0)) == INVAL and call(A=0) == INVAL
+    assert call(seqs=0, rows=0) == OK
+
+
+def test_python_refuses_host_tensors():
+    x, w = torch.zeros(2, 3, 8, dtype=torch.float16), torch.zeros(4, 8)
+    b = torch.zeros(2, 3, 1, 4, dtype=torch.float16)
+    with pytest.raises(ValueError, match="device tensor"):
+        tg.layer_norm(x, w[0])
+    with pytest.raises(ValueError, match="device tensor"):
+        tg.layer_norm_backward(x, x, w[0], w[0], w[0])
+    for f in (lambda: tg.causal_conv(x, w), lambda: tg.causal_conv_backward(x, x, w),
+              lambda: tg.causal_conv_step(x[0], x, w), lambda: tg.selective_scan(x, x, w, b, b),
+              lambda: tg.selective_scan_train(x, x, w, b, b),
+              lambda: tg.selective_scan_backward(x, x, x, w, b, b, w),
+              lambda: tg.selective_scan_step(x[0], x[0], w, b[0], b[0], w)):
+        with pytest.raises(ValueError, match="device tensor"):
+            f()
+
+
+def test_symbols_are_declared():
+    names = tg.exported_symbols()
+    for n in ("tg_layer_norm", "tg_causal_conv_step", "tg_selective_scan_backward"):
+        assert n in names
