@@ -114,10 +114,22 @@ Rows<P> rows_of(const tg_rows& r) {
     return {(P*)r.p, r.seq_stride, r.row_stride};
 }
 
-// log(1 + e^v) to a few units in the last place at both ends: small step
-// sizes come from far negative v, where 1 + e^v would drop e^v's bits.
+// log(1 + e^v) = max(v, 0) + log(1 + u), u = e^-|v|, to a few units in the last
+// place at both ends: small step sizes come from far negative v, where 1 + u would
+// drop u's bits. log(1 + u) = 2 atanh(s) with s = u / (2 + u) <= 1/3, by the series
+// s * (1 + s^2/3 + s^4/5 + ...): the first term left out is below 2^-29 of the sum.
 __device__ __forceinline__ float softplus_f32(float v) {
-    return fmaxf(v, 0.0f) + log1pf(__builtin_amdgcn_exp2f(-fabsf(v) * kLog2e));
+    const float u = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e);
+    const float s = u * __builtin_amdgcn_rcpf(2.0f + u), q = s * s;
+    float r = 1.0f / 15.0f;
+    r = __builtin_fmaf(r, q, 1.0f / 13.0f);
+    r = __builtin_fmaf(r, q, 1.0f / 11.0f);
+    r = __builtin_fmaf(r, q, 1.0f / 9.0f);
+    r = __builtin_fmaf(r, q, 1.0f / 7.0f);
+    r = __builtin_fmaf(r, q, 1.0f / 5.0f);
+    r = __builtin_fmaf(r, q, 1.0f / 3.0f);
+    r = __builtin_fmaf(r, q, 1.0f);
+    return __builtin_fmaf(s + s, r, fmaxf(v, 0.0f));
 }
 __device__ __forceinline__ float sigmoid_f32(float v) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));

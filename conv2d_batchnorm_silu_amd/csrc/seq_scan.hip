@@ -15,11 +15,22 @@
 // share out the TT x 16 (token, channel) items, so that softplus is computed
 // once for each, and put d, d*x and the tokens' B and C into LDS in fp32; then
 // every lane runs its states through the TT tokens; the sums over n are
-// joined over the 4 lanes.
+// joined over the 4 lanes, which leaves each lane the results of its own items.
+//
+// The recurrence is linear, so tokens can be split up: a segment's last state is
+//   P * (state before it) + (last state from zero),  P[n] = 2^(A[n] log2 e * sum d).
+// The W waves of a workgroup take TT tokens each side by side: every wave
+// runs its segment from zero, they exchange P and the last states through LDS, and
+// each adds what the state before it gives. With few sequences and channels the
+// workgroups split the tokens in the same way (parts of PL tokens): a first
+// kernel computes the parts' P and last states.
 //
 // Tokens past the end count as d = x = B = C = 0: a = 1, and the state stays.
+#include <type_traits>
+
 #include "seq_device.hpp"
 #include "seq_internal.hpp"
+#include "tg_internal.hpp"
 
 namespace tg {
 namespace {
@@ -27,138 +38,503 @@ namespace {
 constexpr int kCh = 16;  // channels of a wave
 constexpr float kLn2 = 0.69314718055994531f;
 
+// Tokens that a wave takes at a time: the decays of TT tokens and NS states
+// stay in registers.
+constexpr int chunk_for(int ns) { return ns <= 4 ? 16 : 64 / ns < 4 ? 4 : 64 / ns; }
+// Waves of a workgroup side by side: what they exchange (2*NS values for
+// each lane, in two buffers) stays within 64 KB of LDS.
+constexpr int waves_for(int ns) { return ns <= 8 ? 8 : 64 / ns; }
+
 struct ScanArgs {
     SeqMap seqs;
     int D, N, G, Dg, bpg;  // Dg: channels of a group, in bpg blocks of 16
-    int softplus;
+    int softplus, PL;      // PL: tokens of a part; 0: sequences are not split
     Rows<const void> x, dt, B, C, z;
     Rows<void> y;
     const float *A, *D_skip, *dt_bias, *initial;
     float *final, *saved;
+    float* parts;  // [slots of PL tokens][2][D][4*NS]: P and last state
 };
 
+// Value k of a pair over two lanes: the lane whose bit is clear keeps a, the
+// other b, each summed over both lanes. o is what the other lane wants.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                         0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kRor4 = 0x124, kRor8 = 0x128, kRor12 = 0x12C;
+
 __device__ __forceinline__ float quad_sum(float v) {
-    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, false));
-    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x4E, 0xF, 0xF, false));
+    v += dpp<kXor1>(v);
+    v += dpp<kXor2>(v);
     return v;
+}
+// The sums of v[0..3] over the 4 lanes of a quad, v[q] in lane q.
+__device__ __forceinline__ float quad_sums(float v0, float v1, float v2, float v3, int q) {
+    const bool b0 = q & 1, b1 = q & 2;
+    const float a = (b0 ? v1 : v0) + dpp<kXor1>(b0 ? v0 : v1);
+    const float b = (b0 ? v3 : v2) + dpp<kXor1>(b0 ? v2 : v3);
+    return (b1 ? b : a) + dpp<kXor2>(b1 ? a : b);
+}
+// The sums over the 16 channels (lane bits 2 to 5) in levels, each of which
+// joins two lanes and halves the values a lane holds: of a pair, the lane whose
+// bit is clear keeps the first and the other the second.
+template <int BIT>
+__device__ __forceinline__ float join(float v0, float v1, int lane) {
+    if constexpr (BIT == 5 || BIT == 4) {
+        const unsigned u0 = __builtin_bit_cast(unsigned, v0), u1 = __builtin_bit_cast(unsigned, v1);
+        const auto w = BIT == 5 ? __builtin_amdgcn_permlane32_swap(u0, u1, false, false)
+                                : __builtin_amdgcn_permlane16_swap(u0, u1, false, false);
+        // (A bit cast of a vector's element itself would take element 0.)
+        const unsigned r0 = w[0], r1 = w[1];
+        return __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
+    } else {
+        const bool up = lane & (1 << BIT);
+        const float o = up ? v0 : v1;
+        if constexpr (BIT == 3) return (up ? v1 : v0) + dpp<kRor8>(o);
+        // Lane i ^ 4 is 4 up or down within the row. Both moves by all lanes: in a
+        // branch they would read lanes that are switched off.
+        const float down = dpp<kRor4>(o), above = dpp<kRor12>(o);
+        return (up ? v1 : v0) + (up ? down : above);
+    }
+}
+// Of n values v[0..n) (n a power of two), the level of BIT; n/2 remain.
+template <int BIT, int N>
+__device__ __forceinline__ void join_all(float* v, int lane) {
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) v[k] = join<BIT>(v[2 * k], v[2 * k + 1], lane);
+}
+// How many of the levels (bits 5, 4, 3, 2) a token's own NS values take.
+constexpr int levels_of(int ns) { return ns >= 4 ? 2 : ns == 2 ? 1 : 0; }
+// The levels of one token's values ...
+template <int NS>
+__device__ __forceinline__ void join_token(float (&v)[NS], int lane) {
+    if constexpr (NS >= 2) join_all<5, NS>(v, lane);
+    if constexpr (NS >= 4) join_all<4, NS / 2>(v, lane);
+}
+// ... and the rest over the tokens of a group, which leave a lane value
+// b5 + 2*b4 + 4*b3 + 8*b2 of each 16 in token order.
+template <int NS>
+__device__ __forceinline__ float join_group(float* v, int lane) {
+    if constexpr (NS == 1) join_all<5, 16>(v, lane);
+    if constexpr (NS <= 2) join_all<4, 8>(v, lane);
+    join_all<3, 4>(v, lane);
+    return join<2>(v[0], v[1], lane);
 }
 
 // What a wave keeps in LDS of TT tokens.
 template <int NS, int TT>
-struct Tile {
-    float2 d[TT][kCh];     // d, d*x
+struct alignas(16) Tile {
+    float2 d[TT][kCh];  // d, d*x
     float B[TT][4 * NS];
     float C[TT][4 * NS];
-    float dy[TT][kCh];     // backward only
 };
-
-// The wave's place: its sequence, block of channels and states. Neighbouring
-// blocks share the cache lines of x, dt, z and y (16 channels are a quarter of
-// one), so they run on one XCD.
-struct Place {
-    int s, start, len, block, g, cl, q, ch;
-    bool in;
-    __device__ __forceinline__ Place(const SeqMap& m, int G, int Dg, int bpg) {
-        const int tile = xcd_contiguous_tile(blockIdx.x, gridDim.x);
-        s = tile / (G * bpg);
-        block = tile - s * (G * bpg);
-        start = m.start(s);
-        len = m.end(s) - start;
-        g = block / bpg;
-        const int c0 = (block - g * bpg) * kCh;
-        cl = (threadIdx.x & 63) >> 2;
-        q = threadIdx.x & 3;
-        in = c0 + cl < Dg;
-        ch = g * Dg + c0 + (in ? cl : 0);
-    }
+// The backward pass: dL/dv too, and the items' x, dt + bias, z and dy, which
+// would take 16 registers until the end of the chunk.
+template <int NS, int TT>
+struct alignas(16) BackTile {
+    Tile<NS, TT> f;
+    float dv[TT][kCh];
+    float4 item[TT / 4][64];
 };
-
-template <typename T, int NS, int TT>
-__device__ __forceinline__ void stage_bc(const ScanArgs& a, const Place& p, int l0,
-                                         Tile<NS, TT>& tile) {
-    const int lane = threadIdx.x & 63;
+// NS consecutive floats of LDS or memory (NS floats aligned).
+template <int NS>
+__device__ __forceinline__ void get(const float* p, float (&v)[NS]) {
+    constexpr int V = NS < 4 ? NS : 4;
 #pragma unroll
-    for (int k = 0; k < TT * NS * 4; k += 64) {
-        const int i = k + lane, t = i / (4 * NS), n = i % (4 * NS), l = l0 + t;
-        if (TT * NS * 4 % 64 == 0 || t < TT) {
-            float b = 0.0f, c = 0.0f;
-            if (n < a.N && l < p.len) {
-                b = (float)row_of<const T>(a.B, a.seqs, p.s, p.start, l)[p.g * a.N + n];
-                c = (float)row_of<const T>(a.C, a.seqs, p.s, p.start, l)[p.g * a.N + n];
-            }
-            tile.B[t][n] = b;
-            tile.C[t][n] = c;
-        }
+    for (int j = 0; j < NS; j += V) load_f32<float, V>(p + j, *(float (*)[V])(v + j));
+}
+template <int NS>
+__device__ __forceinline__ void put(float* p, const float (&v)[NS]) {
+    constexpr int V = NS < 4 ? NS : 4;
+#pragma unroll
+    for (int j = 0; j < NS; j += V) store_f32<float, V>(p + j, *(const float (*)[V])(v + j));
+}
+
+// Computes v here: the compiler would move a sum to its use further down and
+// keep all of its operands for that long.
+__device__ __forceinline__ void pin(float& v) { asm volatile("" : "+v"(v)); }
+
+// One token of a tile as a lane reads it.
+template <int NS>
+struct Token {
+    float2 d;
+    float B[NS], C[NS];
+};
+// Run body(t, token) over the TT tokens, up or down, each token's LDS reads
+// issued one token ahead. Without the scheduling fence the compiler hoists the
+// reads of all TT tokens to the front, and without the opaque lane indices it
+// keeps what one pass over the tile read for the next; both spill.
+template <int NS, int TT, bool WITH_B, bool WITH_C, bool UP, typename Body>
+__device__ __forceinline__ void for_tokens(const Tile<NS, TT>& tile, int cl, int q, Body body) {
+    asm volatile("" : "+v"(cl), "+v"(q));
+    const auto read = [&](int t) {
+        Token<NS> k;
+        k.d = tile.d[t][cl];
+        if constexpr (WITH_B) get<NS>(&tile.B[t][q * NS], k.B);
+        if constexpr (WITH_C) get<NS>(&tile.C[t][q * NS], k.C);
+        return k;
+    };
+    Token<NS> cur = read(UP ? 0 : TT - 1);
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+        const int t = UP ? i : TT - 1 - i;
+        Token<NS> next;
+        if (i + 1 < TT) next = read(UP ? t + 1 : t - 1);
+        body(t, cur);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + 1 < TT) cur = next;
     }
 }
 
+// Order LDS accesses of one wave among its lanes: the hardware keeps a wave's
+// LDS accesses in order, so only the compiler has to.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// A workgroup's place: its sequence, part of it (tokens lo to hi) and block of
+// channels; a lane's channel and states. Neighbouring blocks share the cache lines of
+// x, dt, z and y (16 channels are a quarter of one), so they run on one XCD.
+struct Place {
+    int s, start, len, lo, hi, block, g, cl, q, ch, w;
+    int64_t part0;  // the slot of the sequence's first part
+    bool in;
+    __device__ __forceinline__ explicit Place(const ScanArgs& a) {
+        const SeqMap& m = a.seqs;
+        const int tile = xcd_contiguous_tile(blockIdx.x, gridDim.x), nb = a.G * a.bpg;
+        const int slot = tile / nb;
+        block = tile - slot * nb;
+        s = a.PL ? m.owner(slot, a.PL) : slot;
+        start = m.start(s);
+        len = m.end(s) - start;
+        lo = 0, hi = len, part0 = 0;
+        if (a.PL) {
+            part0 = m.slot0(s, a.PL);
+            const int64_t l = (int64_t)(slot - part0) * a.PL;
+            // A slot past the sequence's parts belongs to nobody; an empty
+            // sequence has one part, which passes its state on.
+            lo = l < len || l == 0 ? (int)l : -1;
+            hi = imin(len, lo + a.PL);
+        }
+        g = block / a.bpg;
+        const int c0 = (block - g * a.bpg) * kCh;
+        w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        cl = (threadIdx.x & 63) >> 2;
+        q = threadIdx.x & 3;
+        in = c0 + cl < a.Dg;
+        ch = g * a.Dg + c0 + (in ? cl : 0);
+    }
+    __device__ __forceinline__ int part(int PL) const { return PL ? lo / PL : 0; }
+};
+
+// A tensor's rows of one sequence: uniform, and a row stride of 32 bits (the
+// host checks it), so that addresses are scalar plus a 32-bit lane offset.
+template <typename T>
+struct Col {
+    T* base;
+    int row;
+    template <typename P>
+    __device__ __forceinline__ Col(const Rows<P>& r, const SeqMap& m, const Place& p, int at = 0)
+        : base(row_of<T>(r, m, p.s, p.start, 0) + at), row((int)r.row) {}
+    __device__ __forceinline__ T* at(int l) const { return base + (int64_t)l * row; }
+};
+// Element `off` of a uniform address; the offset's bytes fit 32 bits.
+template <typename T>
+__device__ __forceinline__ T& elem(T* base, uint32_t off) {
+    typedef typename std::conditional<std::is_const<T>::value, const char, char>::type Byte;
+    return *(T*)((Byte*)base + off * (uint32_t)sizeof(T));
+}
+
+// The items of a lane in one tensor, as loaded: token q + 4*i of the chunk at
+// l, the lane's channel. Tokens past hi are not read.
+template <typename T, int TT>
+struct Items {
+    T v[TT / 4];
+    __device__ __forceinline__ void load(const Col<const T>& r, const Place& p, int l) {
+        const uint32_t off = (uint32_t)p.q * (uint32_t)r.row + (uint32_t)p.ch;
+        const T* const base = r.at(l);
+        const int64_t step = 4 * (int64_t)r.row;
+        if (l + TT <= p.hi) {
+#pragma unroll
+            for (int i = 0; i < TT / 4; ++i) v[i] = elem(base + i * step, off);
+        } else {
+#pragma unroll
+            for (int i = 0; i < TT / 4; ++i) {
+                v[i] = (T)0.0f;
+                if (l + p.q + 4 * i < p.hi) v[i] = elem(base + i * step, off);
+            }
+        }
+    }
+};
+template <typename T>
+__device__ __forceinline__ void store_item(const Col<T>& r, const Place& p, int l, int i, float v) {
+    elem(r.at(l) + i * (4 * (int64_t)r.row), (uint32_t)p.q * (uint32_t)r.row + (uint32_t)p.ch) = (T)v;
+}
+
+// A wave's share of TT tokens' B or C: element lane + 64*k of [TT][4*NS].
 template <typename T, int NS, int TT>
-__global__ __launch_bounds__(64) void scan_fwd(const ScanArgs a) {
-    constexpr int kItems = TT / 4;
-    __shared__ Tile<NS, TT> tile;
-    const Place p(a.seqs, a.G, a.Dg, a.bpg);
-    float A2[NS], h[NS];
+struct Shared {
+    static constexpr int kN = 4 * NS, kPer = TT * kN / 64;
+    T v[kPer];
+    __device__ __forceinline__ void load(const Col<const T>& r, const Place& p, int N, int l) {
+        const int lane = threadIdx.x & 63;
+        const T* const base = r.at(l);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            // Rows k*64/kN (the same for all lanes) and lane/kN (for short rows).
+            const int t0 = k * 64 / kN, t = kN < 64 ? lane / kN : 0;
+            const int n = kN < 64 ? lane % kN : (k * 64 % kN) + lane;
+            v[k] = (T)0.0f;
+            if (n < N && l + t0 + t < p.hi)
+                v[k] = elem(base + t0 * (int64_t)r.row, (uint32_t)t * (uint32_t)r.row + (uint32_t)n);
+        }
+    }
+    __device__ __forceinline__ void put(float (&to)[TT][kN]) const {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) (&to[0][0])[k * 64 + (threadIdx.x & 63)] = (float)v[k];
+    }
+};
+
+// A wave's states (or their adjoints) after its segment from zero, and the decay over it:
+// LDS [W][2][64][NS] floats.
+template <int NS>
+__device__ __forceinline__ float* exchange_at(float* ex, int w, int which) {
+    return ex + ((w * 2 + which) * 64 + (threadIdx.x & 63)) * NS;
+}
+
+// log2(a) = d * A2 of the lane's states, zero past N and for lanes without a
+// channel.
+template <int NS>
+__device__ __forceinline__ void load_A2(const ScanArgs& a, const Place& p, float (&A2)[NS]) {
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
         const int n = p.q * NS + j;
-        const bool in = p.in && n < a.N;
-        A2[j] = in ? a.A[(int64_t)p.ch * a.N + n] * kLog2e : 0.0f;
-        h[j] = in && a.initial ? a.initial[((int64_t)p.s * a.D + p.ch) * a.N + n] : 0.0f;
+        A2[j] = p.in && n < a.N ? a.A[(int64_t)p.ch * a.N + n] * kLog2e : 0.0f;
+    }
+}
+template <int NS>
+__device__ __forceinline__ void load_state(const float* st, const ScanArgs& a, const Place& p,
+                                           float (&h)[NS]) {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        const int n = p.q * NS + j;
+        h[j] = st && p.in && n < a.N ? st[((int64_t)p.s * a.D + p.ch) * a.N + n] : 0.0f;
+    }
+}
+template <int NS>
+__device__ __forceinline__ void store_state(float* st, const ScanArgs& a, const Place& p,
+                                            const float (&h)[NS]) {
+    if (!st || !p.in) return;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        const int n = p.q * NS + j;
+        if (n < a.N) st[((int64_t)p.s * a.D + p.ch) * a.N + n] = h[j];
+    }
+}
+template <int NS>
+__device__ __forceinline__ float* part_at(const ScanArgs& a, const Place& p, int part, int which) {
+    return a.parts + (((p.part0 + part) * 2 + which) * a.D + p.ch) * (4 * NS) + p.q * NS;
+}
+
+__device__ __forceinline__ float step_size(const ScanArgs& a, float raw) {
+    return a.softplus ? softplus_f32(raw) : raw;
+}
+
+template <typename T, int NS, int TT, bool SPLIT>
+__global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_fwd(const ScanArgs a) {
+    constexpr int kItems = TT / 4;
+    extern __shared__ float4 lds[];
+    const int W = SPLIT ? blockDim.x >> 6 : 1;
+    const Place p(a);
+    if (p.lo < 0) return;
+    Tile<NS, TT>& tile = ((Tile<NS, TT>*)lds)[p.w];
+    float* const exchange = (float*)((Tile<NS, TT>*)lds + W);
+    float A2[NS], h[NS];
+    load_A2<NS>(a, p, A2);
+    load_state<NS>(a.initial, a, p, h);
+    for (int k = 0; k < p.part(a.PL); ++k) {
+        float P[NS], e[NS];
+        get<NS>(part_at<NS>(a, p, k, 0), P);
+        get<NS>(part_at<NS>(a, p, k, 1), e);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(P[j], h[j], e[j]);
     }
     const float skip = a.D_skip ? a.D_skip[p.ch] : 0.0f;
     const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
-    int64_t slot = a.seqs.slot0(p.s, TT);
-    for (int l0 = 0; l0 < p.len; l0 += TT, ++slot) {
+    int64_t slot = a.seqs.slot0(p.s, TT) + p.lo / TT + p.w;
+    const Col<const T> cx(a.x, a.seqs, p), cdt(a.dt, a.seqs, p), cz(a.z, a.seqs, p),
+        cB(a.B, a.seqs, p, p.g * a.N), cC(a.C, a.seqs, p, p.g * a.N);
+    const Col<T> cy(a.y, a.seqs, p);
+    Items<T, TT> rx, rdt, rz;
+    Shared<T, NS, TT> rB, rC;
+    const auto fetch = [&](int l) {
+        rx.load(cx, p, l);
+        rdt.load(cdt, p, l);
+        if (a.z.p) rz.load(cz, p, l);
+        rB.load(cB, p, a.N, l);
+        rC.load(cC, p, a.N, l);
+    };
+    int flip = 0;
+    if (p.lo < p.hi) fetch(p.lo + p.w * TT);
+    for (int l0 = p.lo; l0 < p.hi; l0 += W * TT, slot += W) {
+        const int l = l0 + p.w * TT;
         float x[kItems], z[kItems], v[kItems];
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const int t = p.q + 4 * i, l = l0 + t;
-            float d = 0.0f;
-            x[i] = z[i] = v[i] = 0.0f;
-            if (l < p.len) {
-                x[i] = (float)row_of<const T>(a.x, a.seqs, p.s, p.start, l)[p.ch];
-                d = (float)row_of<const T>(a.dt, a.seqs, p.s, p.start, l)[p.ch] + bias;
-                if (a.z.p) z[i] = (float)row_of<const T>(a.z, a.seqs, p.s, p.start, l)[p.ch];
-                if (a.softplus) d = softplus_f32(d);
-            }
+            const int t = p.q + 4 * i;
+            x[i] = (float)rx.v[i];
+            z[i] = a.z.p ? (float)rz.v[i] : 0.0f;
+            const float d = l + t < p.hi ? step_size(a, (float)rdt.v[i] + bias) : 0.0f;
             tile.d[t][p.cl] = make_float2(d, d * x[i]);
         }
-        stage_bc<T, NS, TT>(a, p, l0, tile);
-        __syncthreads();
-        if (a.saved && p.in)
+        rB.put(tile.B);
+        rC.put(tile.C);
+        wave_sync();
+        // The next tokens arrive while these are computed.
+        if (l0 + W * TT < p.hi) fetch(l + W * TT);
+        if constexpr (SPLIT) {
+            float dec[TT][NS], e[NS], y[TT], sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < NS; ++j)
-                a.saved[(slot * a.D + p.ch) * (4 * NS) + p.q * NS + j] = h[j];
+            for (int j = 0; j < NS; ++j) e[j] = 0.0f;
+            for_tokens<NS, TT, true, true, true>(tile, p.cl, p.q, [&](int t, const Token<NS>& k) {
+                sum += k.d.x;
+                y[t] = 0.0f;
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const float2 d = tile.d[t][p.cl];
-            float y = 0.0f;
+                for (int j = 0; j < NS; ++j) {
+                    dec[t][j] = __builtin_amdgcn_exp2f(k.d.x * A2[j]);
+                    e[j] = __builtin_fmaf(dec[t][j], e[j], k.d.y * k.B[j]);
+                    y[t] = __builtin_fmaf(e[j], k.C[j], y[t]);
+                }
+                pin(y[t]);
+            });
+            float P[NS];
 #pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                const float e = __builtin_amdgcn_exp2f(d.x * A2[j]);
-                h[j] = __builtin_fmaf(e, h[j], d.y * tile.B[t][p.q * NS + j]);
-                y = __builtin_fmaf(h[j], tile.C[t][p.q * NS + j], y);
+            for (int j = 0; j < NS; ++j) P[j] = __builtin_amdgcn_exp2f(sum * A2[j]);
+            float* const ex = exchange + flip * (W * 128 * NS);
+            flip ^= 1;
+            put<NS>(exchange_at<NS>(ex, p.w, 0), P);
+            put<NS>(exchange_at<NS>(ex, p.w, 1), e);
+            __syncthreads();
+            // The other buffer is written next, past this barrier of the next
+            // round: nobody still reads it then.
+            float r[NS];
+            for (int k = 0; k < W; ++k) {
+                if (k == p.w)
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) r[j] = h[j];
+                get<NS>(exchange_at<NS>(ex, k, 0), P);
+                get<NS>(exchange_at<NS>(ex, k, 1), e);
+#pragma unroll
+                for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(P[j], h[j], e[j]);
             }
-            y = quad_sum(y);
-            if ((t & 3) == p.q) v[t >> 2] = y;
+            if (a.saved && p.in && l < p.hi)
+                put<NS>(a.saved + (slot * a.D + p.ch) * (4 * NS) + p.q * NS, r);
+            // What the state before the segment adds: it decays, token by token.
+            for_tokens<NS, TT, false, true, true>(tile, p.cl, p.q, [&](int t, const Token<NS>& k) {
+#pragma unroll
+                for (int j = 0; j < NS; ++j) {
+                    r[j] *= dec[t][j];
+                    y[t] = __builtin_fmaf(r[j], k.C[j], y[t]);
+                }
+                pin(y[t]);
+            });
+#pragma unroll
+            for (int i = 0; i < kItems; ++i)
+                v[i] = quad_sums(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3], p.q);
+        } else {
+            if (a.saved && p.in) put<NS>(a.saved + (slot * a.D + p.ch) * (4 * NS) + p.q * NS, h);
+            float y[4];
+            for_tokens<NS, TT, true, true, true>(tile, p.cl, p.q, [&](int t, const Token<NS>& k) {
+                float s = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NS; ++j) {
+                    const float e = __builtin_amdgcn_exp2f(k.d.x * A2[j]);
+                    h[j] = __builtin_fmaf(e, h[j], k.d.y * k.B[j]);
+                    s = __builtin_fmaf(h[j], k.C[j], s);
+                }
+                y[t & 3] = s;
+                pin(y[t & 3]);
+                if ((t & 3) == 3) {
+                    v[t >> 2] = quad_sums(y[0], y[1], y[2], y[3], p.q);
+                    pin(v[t >> 2]);
+                }
+            });
         }
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int l = l0 + p.q + 4 * i;
-            if (l < p.len && p.in) {
+        for (int i = 0; i < kItems; ++i)
+            if (l + p.q + 4 * i < p.hi && p.in) {
                 float o = __builtin_fmaf(skip, x[i], v[i]);
                 if (a.z.p) o *= silu_f32(z[i]);
-                row_of<T>(a.y, a.seqs, p.s, p.start, l)[p.ch] = (T)o;
+                store_item(cy, p, l, i, o);
             }
-        }
-        __syncthreads();
+        wave_sync();
     }
-    if (a.final && p.in)
+    if (p.w == 0 && p.hi == p.len) store_state<NS>(a.final, a, p, h);
+}
+
+// The parts' decays and last states from zero, for all parts but a sequence's
+// last. The waves take a part's tokens in W runs side by side.
+template <typename T, int NS, int TT>
+__global__ __launch_bounds__(64 * waves_for(NS)) void scan_parts(const ScanArgs a) {
+    extern __shared__ float4 lds[];
+    const int W = blockDim.x >> 6;
+    const Place p(a);
+    if (p.lo < 0 || p.hi == p.len) return;
+    Tile<NS, TT>& tile = ((Tile<NS, TT>*)lds)[p.w];
+    float* const ex = (float*)((Tile<NS, TT>*)lds + W);
+    float A2[NS], h[NS], sum = 0.0f;
+    load_A2<NS>(a, p, A2);
 #pragma unroll
-        for (int j = 0; j < NS; ++j) {
-            const int n = p.q * NS + j;
-            if (n < a.N) a.final[((int64_t)p.s * a.D + p.ch) * a.N + n] = h[j];
+    for (int j = 0; j < NS; ++j) h[j] = 0.0f;
+    const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
+    const int run = a.PL / W;  // PL is a multiple of W * TT
+    const Col<const T> cx(a.x, a.seqs, p), cdt(a.dt, a.seqs, p), cB(a.B, a.seqs, p, p.g * a.N);
+    Items<T, TT> rx, rdt;
+    Shared<T, NS, TT> rB;
+    const auto fetch = [&](int l) {
+        rx.load(cx, p, l);
+        rdt.load(cdt, p, l);
+        rB.load(cB, p, a.N, l);
+    };
+    const int first = p.lo + p.w * run;
+    fetch(first);
+    for (int l = first; l < first + run; l += TT) {
+#pragma unroll
+        for (int i = 0; i < TT / 4; ++i) {
+            const float d = step_size(a, (float)rdt.v[i] + bias);
+            tile.d[p.q + 4 * i][p.cl] = make_float2(d, d * (float)rx.v[i]);
         }
+        rB.put(tile.B);
+        wave_sync();
+        if (l + TT < first + run) fetch(l + TT);
+        for_tokens<NS, TT, true, false, true>(tile, p.cl, p.q, [&](int, const Token<NS>& k) {
+            sum += k.d.x;
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+                h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(k.d.x * A2[j]), h[j], k.d.y * k.B[j]);
+        });
+        wave_sync();
+    }
+    float P[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) P[j] = __builtin_amdgcn_exp2f(sum * A2[j]);
+    put<NS>(exchange_at<NS>(ex, p.w, 0), P);
+    put<NS>(exchange_at<NS>(ex, p.w, 1), h);
+    __syncthreads();
+    if (p.w != 0) return;
+    for (int k = 1; k < W; ++k) {
+        float Q[NS], e[NS];
+        get<NS>(exchange_at<NS>(ex, k, 0), Q);
+        get<NS>(exchange_at<NS>(ex, k, 1), e);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(Q[j], h[j], e[j]), P[j] *= Q[j];
+    }
+    if (!p.in) return;
+    put<NS>(part_at<NS>(a, p, p.part(a.PL), 0), P);
+    put<NS>(part_at<NS>(a, p, p.part(a.PL), 1), h);
 }
 
 struct ScanGrads {
@@ -166,146 +542,319 @@ struct ScanGrads {
     const float *dfinal, *saved;
     Rows<void> dx, ddt, dz;
     float* dinitial;
-    float* part_bc;   // [blocks of channels][rows][2][4*NS]: dB, dC of a block
-    float* part_a;    // [seqs][D][N]
-    float* part_d;    // [seqs][2][D]: dD, ddt_bias
+    float* part_bc;  // [blocks of channels][rows][2][4*NS]: dB, dC of a block
+    float* part_a;   // [slots][D][N]
+    float* part_d;   // [slots][2][D]: dD, ddt_bias
 };
 
-// The chunks of a sequence from the last to the first. In each, the states
+// The chunks of a sequence (or part) from the last to the first. In each, the states
 // are computed again from the one the forward pass saved at its start and held
 // in registers with the decays, and then the adjoint runs backwards:
 //   g[t] = dv[t]*C[t] + a[t+1]*g[t+1]                 (dL/dh[t])
 //   dd[t]  = sum_n g*(A*a[t]*h[t-1] + B*x),  dx[t] = d * sum_n g*B + D*dv
 //   dA += g*a[t]*h[t-1]*d,   dB = sum_c g*d*x,   dC = sum_c dv*h
-template <typename T, int NS, int TT>
-__global__ __launch_bounds__(64) void scan_bwd(const ScanArgs a, const ScanGrads b) {
-    constexpr int kItems = TT / 4;
-    __shared__ Tile<NS, TT> tile;
-    const Place p(a.seqs, a.G, a.Dg, a.bpg);
-    float A2[NS], dA[NS], carry[NS];
+// Split over waves and workgroups like the forward pass: what a segment passes
+// to the tokens before it, a[first]*g[first], is linear in what reaches it.
+template <typename T, int NS, int TT, bool SPLIT>
+__global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(const ScanArgs a,
+                                                                            const ScanGrads b) {
+    // dB and dC: values of a token after its own levels, and tokens of a group.
+    constexpr int kItems = TT / 4, kHeld = NS >> levels_of(NS), GT = NS < 16 ? 16 / NS : 1;
+    extern __shared__ float4 lds[];
+    const int W = SPLIT ? blockDim.x >> 6 : 1;
+    const Place p(a);
+    if (p.lo < 0) return;
+    BackTile<NS, TT>& both = ((BackTile<NS, TT>*)lds)[p.w];
+    Tile<NS, TT>& tile = both.f;
+    float* const exchange = (float*)((BackTile<NS, TT>*)lds + W);
+    const int lane = threadIdx.x & 63;
+    float A2[NS], carry[NS], dA[NS], lost[NS];
+    load_A2<NS>(a, p, A2);
+    load_state<NS>(b.dfinal, a, p, carry);
+    if (a.PL)
+        for (int k = (p.len - 1) / a.PL; k > p.part(a.PL); --k) {
+            float P[NS], e[NS];
+            get<NS>(part_at<NS>(a, p, k, 0), P);
+            get<NS>(part_at<NS>(a, p, k, 1), e);
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-        const int n = p.q * NS + j;
-        const bool in = p.in && n < a.N;
-        A2[j] = in ? a.A[(int64_t)p.ch * a.N + n] * kLog2e : 0.0f;
-        carry[j] = in && b.dfinal ? b.dfinal[((int64_t)p.s * a.D + p.ch) * a.N + n] : 0.0f;
-        dA[j] = 0.0f;
-    }
+            for (int j = 0; j < NS; ++j) carry[j] = __builtin_fmaf(P[j], carry[j], e[j]);
+        }
+#pragma unroll
+    for (int j = 0; j < NS; ++j) dA[j] = lost[j] = 0.0f;
     const float skip = a.D_skip ? a.D_skip[p.ch] : 0.0f;
     const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
     float dD = 0.0f, dbias = 0.0f;
     const int64_t slot0 = a.seqs.slot0(p.s, TT);
-    const int row0 = p.start;  // of the flat rows, dense or packed
-    for (int l0 = (p.len - 1) / TT * TT; l0 >= 0 && p.len > 0; l0 -= TT) {
-        float x[kItems], raw[kItems], dl[kItems], z[kItems], dout[kItems];
-        float v[kItems], e1[kItems], e2[kItems];
+    const Col<const T> cx(a.x, a.seqs, p), cdt(a.dt, a.seqs, p), cz(a.z, a.seqs, p),
+        cdy(b.dy, a.seqs, p), cB(a.B, a.seqs, p, p.g * a.N), cC(a.C, a.seqs, p, p.g * a.N);
+    const Col<T> cdx(b.dx, a.seqs, p), cddt(b.ddt, a.seqs, p), cdz(b.dz, a.seqs, p);
+    Items<T, TT> rx, rdt, rz, rdy;
+    Shared<T, NS, TT> rB, rC;
+    const auto fetch = [&](int l) {
+        rx.load(cx, p, l);
+        rdt.load(cdt, p, l);
+        if (a.z.p) rz.load(cz, p, l);
+        rdy.load(cdy, p, l);
+        rB.load(cB, p, a.N, l);
+        rC.load(cC, p, a.N, l);
+    };
+    int flip = 0;
+    const int chunks = (p.hi - p.lo + W * TT - 1) / (W * TT);
+    if (chunks > 0) fetch(p.lo + ((chunks - 1) * W + p.w) * TT);
+    for (int chunk = chunks - 1; chunk >= 0; --chunk) {
+        const int l = p.lo + (chunk * W + p.w) * TT;
+        float h0[NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) h0[j] = 0.0f;
+        if (p.in && l < p.hi)
+            get<NS>(b.saved + ((slot0 + l / TT) * a.D + p.ch) * (4 * NS) + p.q * NS, h0);
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const int t = p.q + 4 * i, l = l0 + t;
-            x[i] = raw[i] = z[i] = dout[i] = dl[i] = 0.0f;
-            v[i] = e1[i] = e2[i] = 0.0f;
-            if (l < p.len && p.in) {
-                x[i] = (float)row_of<const T>(a.x, a.seqs, p.s, p.start, l)[p.ch];
-                raw[i] = (float)row_of<const T>(a.dt, a.seqs, p.s, p.start, l)[p.ch] + bias;
-                if (a.z.p) z[i] = (float)row_of<const T>(a.z, a.seqs, p.s, p.start, l)[p.ch];
-                dout[i] = (float)row_of<const T>(b.dy, a.seqs, p.s, p.start, l)[p.ch];
-                dl[i] = a.softplus ? softplus_f32(raw[i]) : raw[i];
-            }
-            tile.d[t][p.cl] = make_float2(dl[i], dl[i] * x[i]);
-            tile.dy[t][p.cl] = a.z.p ? dout[i] * silu_f32(z[i]) : dout[i];
+            const int t = p.q + 4 * i;
+            const float x = (float)rx.v[i], raw = (float)rdt.v[i] + bias;
+            const float d = l + t < p.hi ? step_size(a, raw) : 0.0f;
+            const float z = a.z.p ? (float)rz.v[i] : 0.0f;
+            const float dout = p.in ? (float)rdy.v[i] : 0.0f;
+            tile.d[t][p.cl] = make_float2(d, p.in ? d * x : 0.0f);
+            both.dv[t][p.cl] = a.z.p ? dout * silu_f32(z) : dout;
+            both.item[i][lane] = make_float4(x, raw, z, dout);
         }
-        stage_bc<T, NS, TT>(a, p, l0, tile);
-        __syncthreads();
-        float h0[NS], dec[TT][NS], h[TT][NS];
-        const int64_t slot = slot0 + l0 / TT;
+        rB.put(tile.B);
+        rC.put(tile.C);
+        wave_sync();
+        float dec[TT][NS], h[TT][NS], v[kItems], e1[kItems], e2[kItems], sum = 0.0f;
+        {
+            float y[4];
+            for_tokens<NS, TT, true, true, true>(tile, p.cl, p.q, [&](int t, const Token<NS>& k) {
+                float s = 0.0f;
+                sum += k.d.x;
 #pragma unroll
-        for (int j = 0; j < NS; ++j)
-            h0[j] = p.in ? b.saved[(slot * a.D + p.ch) * (4 * NS) + p.q * NS + j] : 0.0f;
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const float2 d = tile.d[t][p.cl];
-            float y = 0.0f;
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                dec[t][j] = __builtin_amdgcn_exp2f(d.x * A2[j]);
-                h[t][j] = __builtin_fmaf(dec[t][j], t ? h[t - 1][j] : h0[j],
-                                         d.y * tile.B[t][p.q * NS + j]);
-                y = __builtin_fmaf(h[t][j], tile.C[t][p.q * NS + j], y);
-            }
-            y = quad_sum(y);
-            if ((t & 3) == p.q) v[t >> 2] = y;
+                for (int j = 0; j < NS; ++j) {
+                    dec[t][j] = __builtin_amdgcn_exp2f(k.d.x * A2[j]);
+                    h[t][j] = __builtin_fmaf(dec[t][j], t ? h[t - 1][j] : h0[j], k.d.y * k.B[j]);
+                    s = __builtin_fmaf(h[t][j], k.C[j], s);
+                }
+                y[t & 3] = s;
+                pin(y[t & 3]);
+                if ((t & 3) == 3) {
+                    v[t >> 2] = quad_sums(y[0], y[1], y[2], y[3], p.q);
+                    pin(v[t >> 2]);
+                }
+            });
         }
+        float c[NS];  // a[t+1]*g[t+1] of the next token
+        if constexpr (SPLIT) {
+            float P[NS], e[NS];
 #pragma unroll
-        for (int t = TT - 1; t >= 0; --t) {
-            const float2 d = tile.d[t][p.cl];
-            const float dy = tile.dy[t][p.cl];
+            for (int j = 0; j < NS; ++j) e[j] = 0.0f;
+            for_tokens<NS, TT, false, true, false>(tile, p.cl, p.q, [&](int t, const Token<NS>& k) {
+                const float dv = both.dv[t][p.cl];
+#pragma unroll
+                for (int j = 0; j < NS; ++j) e[j] = __builtin_fmaf(dv, k.C[j], e[j]) * dec[t][j];
+            });
+#pragma unroll
+            for (int j = 0; j < NS; ++j) P[j] = __builtin_amdgcn_exp2f(sum * A2[j]);
+            float* const ex = exchange + flip * (W * 128 * NS);
+            flip ^= 1;
+            put<NS>(exchange_at<NS>(ex, p.w, 0), P);
+            put<NS>(exchange_at<NS>(ex, p.w, 1), e);
+            __syncthreads();
+            for (int m = W - 1; m >= 0; --m) {
+                if (m == p.w)
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) c[j] = carry[j];
+                get<NS>(exchange_at<NS>(ex, m, 0), P);
+                get<NS>(exchange_at<NS>(ex, m, 1), e);
+#pragma unroll
+                for (int j = 0; j < NS; ++j) carry[j] = __builtin_fmaf(P[j], carry[j], e[j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NS; ++j) c[j] = carry[j];
+        }
+        float dAc[NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) dAc[j] = 0.0f;
+        float gB[kHeld * GT], gC[kHeld * GT];
+        for_tokens<NS, TT, true, true, false>(tile, p.cl, p.q, [&](int t, const Token<NS>& k) {
+            const float dv = both.dv[t][p.cl];
             float f1 = 0.0f, f2 = 0.0f, dB[NS], dC[NS];
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
-                const float g = __builtin_fmaf(dy, tile.C[t][p.q * NS + j], carry[j]);
-                carry[j] = g * dec[t][j];
-                const float gu = carry[j] * (t ? h[t - 1][j] : h0[j]);
+                const float g = __builtin_fmaf(dv, k.C[j], c[j]);
+                c[j] = g * dec[t][j];
+                const float gu = c[j] * (t ? h[t - 1][j] : h0[j]);
                 f1 = __builtin_fmaf(gu, A2[j], f1);
-                f2 = __builtin_fmaf(g, tile.B[t][p.q * NS + j], f2);
-                dA[j] = __builtin_fmaf(gu, d.x, dA[j]);
-                dB[j] = g * d.y;
-                dC[j] = dy * h[t][j];
+                f2 = __builtin_fmaf(g, k.B[j], f2);
+                dAc[j] = __builtin_fmaf(gu, k.d.x, dAc[j]);
+                dB[j] = g * k.d.y;
+                dC[j] = dv * h[t][j];
             }
-            f1 = quad_sum(f1);
-            f2 = quad_sum(f2);
-            if ((t & 3) == p.q) e1[t >> 2] = f1, e2[t >> 2] = f2;
+            join_token<NS>(dB, lane);
+            join_token<NS>(dC, lane);
 #pragma unroll
-            for (int j = 0; j < NS; ++j)
+            for (int j = 0; j < kHeld; ++j) {
+                pin(dB[j]);
+                pin(dC[j]);
+                gB[t % GT * kHeld + j] = dB[j];
+                gC[t % GT * kHeld + j] = dC[j];
+            }
+            pin(f1);
+            pin(f2);
+            // In the places of this token's decay and state, which are done with.
+            dec[t][0] = f1;
+            h[t][0] = f2;
+            if (t % GT == 0)
 #pragma unroll
-                for (int o = 4; o < 64; o *= 2) {
-                    dB[j] += __shfl_xor(dB[j], o);
-                    dC[j] += __shfl_xor(dC[j], o);
+                for (int k0 = 0; k0 < kHeld * GT; k0 += 16 >> levels_of(NS)) {
+                    const float sB = join_group<NS>(gB + k0, lane);
+                    const float sC = join_group<NS>(gC + k0, lane);
+                    const int i = (k0 << levels_of(NS)) + ((lane >> 5) & 1) + ((lane >> 3) & 2) +
+                                  ((lane >> 1) & 4) + ((lane << 1) & 8);
+                    const int u = t + i / NS, n = p.q * NS + i % NS;
+                    if (l + u < p.hi) {
+                        float* o = b.part_bc + (((int64_t)p.block * a.seqs.rows + p.start + l + u) *
+                                                2) * (4 * NS) + n;
+                        o[0] = sB;
+                        o[4 * NS] = sC;
+                    }
                 }
-            if (p.cl == 0 && l0 + t < p.len) {
-                float* o = b.part_bc +
-                           (((int64_t)p.block * a.seqs.rows + row0 + l0 + t) * 2) * (4 * NS) +
-                           p.q * NS;
+            // The next tokens' loads, with enough time left to arrive and no
+            // sooner: they take the registers of states that are done with.
+            if (t == TT / 2 && chunk > 0) fetch(l - W * TT);
+        });
 #pragma unroll
-                for (int j = 0; j < NS; ++j) o[j] = dB[j], o[4 * NS + j] = dC[j];
-            }
+        for (int i = 0; i < kItems; ++i) {
+            e1[i] = quad_sums(dec[4 * i][0], dec[4 * i + 1][0], dec[4 * i + 2][0],
+                              dec[4 * i + 3][0], p.q);
+            e2[i] = quad_sums(h[4 * i][0], h[4 * i + 1][0], h[4 * i + 2][0], h[4 * i + 3][0], p.q);
+        }
+        // The sum over all tokens is long: what each addition drops is kept
+        // (Kahan), so that it is as exact as a chunk's own sum.
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            const float add = dAc[j] - lost[j], s = dA[j] + add;
+            lost[j] = (s - dA[j]) - add;
+            dA[j] = s;
+            if (!SPLIT) carry[j] = c[j];
         }
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const int t = p.q + 4 * i, l = l0 + t;
-            const float dy = tile.dy[t][p.cl];
-            if (l < p.len && p.in) {
-                float ddl = __builtin_fmaf(e2[i], x[i], e1[i] * kLn2);
-                if (a.softplus) ddl *= sigmoid_f32(raw[i]);
-                row_of<T>(b.ddt, a.seqs, p.s, p.start, l)[p.ch] = (T)ddl;
-                row_of<T>(b.dx, a.seqs, p.s, p.start, l)[p.ch] =
-                    (T)__builtin_fmaf(e2[i], dl[i], skip * dy);
+            const int t = p.q + 4 * i;
+            if (l + t < p.hi && p.in) {
+                const float4 it = both.item[i][lane];  // x, dt + bias, z, dy
+                const float dv = both.dv[t][p.cl];
+                float ddl = __builtin_fmaf(e2[i], it.x, e1[i] * kLn2);
+                if (a.softplus) ddl *= sigmoid_f32(it.y);
+                store_item(cddt, p, l, i, ddl);
+                store_item(cdx, p, l, i, __builtin_fmaf(e2[i], tile.d[t][p.cl].x, skip * dv));
                 if (a.z.p) {
-                    const float sg = sigmoid_f32(z[i]), y = __builtin_fmaf(skip, x[i], v[i]);
-                    row_of<T>(b.dz, a.seqs, p.s, p.start, l)[p.ch] =
-                        (T)(dout[i] * y * sg * __builtin_fmaf(z[i], 1.0f - sg, 1.0f));
+                    const float sg = sigmoid_f32(it.z), y = __builtin_fmaf(skip, it.x, v[i]);
+                    store_item(cdz, p, l, i,
+                               it.w * y * sg * __builtin_fmaf(it.z, 1.0f - sg, 1.0f));
                 }
                 dbias += ddl;
-                dD = __builtin_fmaf(dy, x[i], dD);
+                dD = __builtin_fmaf(dv, it.x, dD);
             }
         }
-        __syncthreads();
+        wave_sync();
     }
     dD = quad_sum(dD);
     dbias = quad_sum(dbias);
-    if (!p.in) return;
-    if (p.q == 0) {
-        b.part_d[(int64_t)p.s * 2 * a.D + p.ch] = dD;
-        b.part_d[((int64_t)p.s * 2 + 1) * a.D + p.ch] = dbias;
+    if constexpr (SPLIT) {
+        // The waves' sums, one after another.
+        __syncthreads();
+        float* const ex = exchange;
+        put<NS>(exchange_at<NS>(ex, p.w, 0), dA);
+        exchange_at<NS>(ex, p.w, 1)[0] = p.q == 0 ? dD : dbias;
+        __syncthreads();
+        if (p.w == 0)
+            for (int k = 1; k < W; ++k) {
+                float e[NS];
+                get<NS>(exchange_at<NS>(ex, k, 0), e);
+#pragma unroll
+                for (int j = 0; j < NS; ++j) dA[j] += e[j];
+                const float o = exchange_at<NS>(ex, k, 1)[0];
+                dD += o;
+                dbias += o;
+            }
     }
+    if (p.w != 0 || !p.in) return;
+    const int64_t out = a.PL ? p.part0 + p.part(a.PL) : p.s;
+    if (p.q < 2) b.part_d[(out * 2 + p.q) * a.D + p.ch] = p.q == 0 ? dD : dbias;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
         const int n = p.q * NS + j;
-        if (n < a.N) {
-            const int64_t o = ((int64_t)p.s * a.D + p.ch) * a.N + n;
-            b.part_a[o] = dA[j];
-            if (b.dinitial) b.dinitial[o] = carry[j];
-        }
+        if (n < a.N) b.part_a[(out * a.D + p.ch) * a.N + n] = dA[j];
     }
+    if (p.lo == 0) store_state<NS>(b.dinitial, a, p, carry);
+}
+
+// What the parts but a sequence's first pass to the tokens before them, from
+// zero, and their decays.
+template <typename T, int NS, int TT>
+__global__ __launch_bounds__(64 * waves_for(NS)) void scan_bwd_parts(const ScanArgs a,
+                                                                     const ScanGrads b) {
+    extern __shared__ float4 lds[];
+    const int W = blockDim.x >> 6;
+    const Place p(a);
+    if (p.lo <= 0) return;
+    Tile<NS, TT>& tile = ((Tile<NS, TT>*)lds)[p.w];
+    float* const ex = (float*)((Tile<NS, TT>*)lds + W);
+    float A2[NS], c[NS], sum = 0.0f;
+    load_A2<NS>(a, p, A2);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) c[j] = 0.0f;
+    const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
+    const int run = a.PL / W;
+    const Col<const T> cdt(a.dt, a.seqs, p), cz(a.z, a.seqs, p), cdy(b.dy, a.seqs, p),
+        cC(a.C, a.seqs, p, p.g * a.N);
+    Items<T, TT> rdt, rz, rdy;
+    Shared<T, NS, TT> rC;
+    const auto fetch = [&](int l) {
+        rdt.load(cdt, p, l);
+        if (a.z.p) rz.load(cz, p, l);
+        rdy.load(cdy, p, l);
+        rC.load(cC, p, a.N, l);
+    };
+    const int first = p.lo + p.w * run;
+    fetch(first + run - TT);
+    for (int l = first + run - TT; l >= first; l -= TT) {
+#pragma unroll
+        for (int i = 0; i < TT / 4; ++i) {
+            const int t = p.q + 4 * i;
+            const float d = l + t < p.hi ? step_size(a, (float)rdt.v[i] + bias) : 0.0f;
+            const float dy = (float)rdy.v[i];
+            tile.d[t][p.cl] = make_float2(d, a.z.p ? dy * silu_f32((float)rz.v[i]) : dy);
+        }
+        rC.put(tile.C);
+        wave_sync();
+        if (l > first) fetch(l - TT);
+        for_tokens<NS, TT, false, true, false>(tile, p.cl, p.q, [&](int, const Token<NS>& k) {
+            sum += k.d.x;
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+                c[j] = __builtin_fmaf(k.d.y, k.C[j], c[j]) * __builtin_amdgcn_exp2f(k.d.x * A2[j]);
+        });
+        wave_sync();
+    }
+    float P[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) P[j] = __builtin_amdgcn_exp2f(sum * A2[j]);
+    put<NS>(exchange_at<NS>(ex, p.w, 0), P);
+    put<NS>(exchange_at<NS>(ex, p.w, 1), c);
+    __syncthreads();
+    if (p.w != W - 1) return;
+    for (int k = W - 2; k >= 0; --k) {
+        float Q[NS], e[NS];
+        get<NS>(exchange_at<NS>(ex, k, 0), Q);
+        get<NS>(exchange_at<NS>(ex, k, 1), e);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) c[j] = __builtin_fmaf(Q[j], c[j], e[j]), P[j] *= Q[j];
+    }
+    if (!p.in) return;
+    put<NS>(part_at<NS>(a, p, p.part(a.PL), 0), P);
+    put<NS>(part_at<NS>(a, p, p.part(a.PL), 1), c);
 }
 
 // dB and dC of the rows that the sequences cover: sums over a group's blocks
@@ -378,26 +927,56 @@ __global__ __launch_bounds__(256) void scan_step(const StepArgs b) {
     }
 }
 
-// States of a lane for N, and tokens of a chunk: as many as the registers
-// hold decays for.
+// States of a lane: 4 lanes hold N.
 int states_for(int N) {
     int ns = 1;
     while (4 * ns < N) ns *= 2;
     return ns;
 }
-constexpr int chunk_for(int ns) { return ns <= 4 ? 16 : 64 / ns < 4 ? 4 : 64 / ns; }
 
-ScanArgs args_of(const tg_scan_args& a, float* saved) {
+// How a call is cut up, by its sizes alone.
+struct Plan {
+    int ns, tt, waves, PL;  // waves 1: whole sequences by single waves
+    int64_t slots, nb;      // workgroups: slots * nb
+};
+Plan plan_of(const tg_scan_args& a) {
+    Plan p;
+    p.ns = states_for(a.N);
+    p.tt = chunk_for(p.ns);
+    p.nb = (int64_t)a.G * ceil_div(a.D / a.G, kCh);
+    const int64_t groups = a.seqs.seqs * p.nb;
+    p.waves = groups >= 4096 ? 1 : waves_for(p.ns);
+    p.PL = 0;
+    p.slots = a.seqs.seqs;
+    // Fewer than four waves for each compute unit: parts of the sequences, so
+    // many that there would be eight, and not shorter than two rounds of a workgroup.
+    if (p.waves > 1 && groups * p.waves < 1024) {
+        const int64_t round = (int64_t)p.waves * p.tt;
+        int64_t pl = a.seqs.rows * p.nb * p.waves / 2048 / round * round;
+        if (pl < 2 * round) pl = 2 * round;
+        const int64_t longest = a.seqs.offsets ? a.seqs.rows : a.seqs.rows / a.seqs.seqs;
+        if (pl < longest) {
+            p.PL = (int)pl;
+            p.slots = a.seqs.rows / pl + a.seqs.seqs;
+        }
+    }
+    return p;
+}
+size_t parts_bytes(const tg_scan_args& a, const Plan& p) {
+    return p.PL ? (size_t)p.slots * 2 * a.D * 4 * p.ns * sizeof(float) : 0;
+}
+
+ScanArgs args_of(const tg_scan_args& a, const Plan& p, float* saved, void* parts) {
     const int Dg = a.D / a.G;
-    return {map_of(a.seqs), a.D, a.N, a.G, Dg, (int)ceil_div(Dg, kCh), a.softplus,
+    return {map_of(a.seqs), a.D, a.N, a.G, Dg, (int)ceil_div(Dg, kCh), a.softplus, p.PL,
             rows_of<const void>(a.x), rows_of<const void>(a.dt), rows_of<const void>(a.B),
             rows_of<const void>(a.C), rows_of<const void>(a.z), rows_of<void>(a.y), a.A, a.D_skip,
-            a.dt_bias, a.initial, a.final, saved};
+            a.dt_bias, a.initial, a.final, saved, (float*)parts};
 }
 
 #define TG_SCAN_NS(X, T)                           \
     do {                                           \
-        switch (states_for(N)) {                   \
+        switch (p.ns) {                            \
             case 1: X(T, 1); break;                \
             case 2: X(T, 2); break;                \
             case 4: X(T, 4); break;                \
@@ -413,56 +992,110 @@ ScanArgs args_of(const tg_scan_args& a, float* saved) {
         else TG_SCAN_NS(X, f16);                   \
     } while (0)
 
+// Tiles of `tile` bytes for each wave, and `buffers` exchange buffers.
+template <typename Kernel, typename... Args>
+hipError_t launch_waves(Kernel kernel, const Plan& p, size_t tile, int buffers, hipStream_t st,
+                        const Args&... args) {
+    const size_t bytes = p.waves * (tile + (p.waves > 1 ? buffers * 128 * p.ns * sizeof(float) : 0));
+    const hipError_t e = ensure_dynamic_lds((const void*)kernel, bytes);
+    if (e != hipSuccess) return e;
+    kernel<<<(unsigned)(p.slots * p.nb), 64 * p.waves, bytes, st>>>(args...);
+    return hipGetLastError();
+}
+
+template <typename T, int NS>
+hipError_t fwd_typed(const Plan& p, const ScanArgs& f, hipStream_t st) {
+    constexpr int TT = chunk_for(NS);
+    constexpr size_t tile = sizeof(Tile<NS, TT>);
+    if (p.PL) {
+        const hipError_t e = launch_waves(scan_parts<T, NS, TT>, p, tile, 1, st, f);
+        if (e != hipSuccess) return e;
+    }
+    if (p.waves > 1) return launch_waves(scan_fwd<T, NS, TT, true>, p, tile, 2, st, f);
+    return launch_waves(scan_fwd<T, NS, TT, false>, p, tile, 0, st, f);
+}
+template <typename T, int NS>
+hipError_t bwd_typed(const Plan& p, const ScanArgs& f, const ScanGrads& b, hipStream_t st) {
+    constexpr int TT = chunk_for(NS);
+    constexpr size_t tile = sizeof(Tile<NS, TT>), both = sizeof(BackTile<NS, TT>);
+    if (p.PL) {
+        const hipError_t e = launch_waves(scan_bwd_parts<T, NS, TT>, p, tile, 1, st, f, b);
+        if (e != hipSuccess) return e;
+    }
+    if (p.waves > 1) return launch_waves(scan_bwd<T, NS, TT, true>, p, both, 2, st, f, b);
+    return launch_waves(scan_bwd<T, NS, TT, false>, p, both, 0, st, f, b);
+}
+
 struct BackwardWs {
-    size_t bc, a, d, total;
+    size_t a, d, bc, parts, total;  // [a][d]: zeroed, see launch_scan_backward
 };
-BackwardWs backward_ws(const tg_scan_args& a) {
-    const int np = 4 * states_for(a.N), blocks = a.G * (int)ceil_div(a.D / a.G, kCh);
+BackwardWs backward_ws(const tg_scan_args& a, const Plan& p) {
     BackwardWs w;
-    w.bc = 0;
-    w.a = up256((size_t)blocks * a.seqs.rows * 2 * np * sizeof(float));
-    w.d = w.a + up256((size_t)a.seqs.seqs * a.D * a.N * sizeof(float));
-    w.total = w.d + up256((size_t)a.seqs.seqs * 2 * a.D * sizeof(float));
+    w.a = 0;
+    w.d = w.a + up256((size_t)p.slots * a.D * a.N * sizeof(float));
+    w.bc = w.d + up256((size_t)p.slots * 2 * a.D * sizeof(float));
+    w.parts = w.bc + up256((size_t)p.nb * a.seqs.rows * 2 * 4 * p.ns * sizeof(float));
+    w.total = w.parts + parts_bytes(a, p);
     return w;
+}
+
+// Slots that no part of a sequence owns count as zero in the sums.
+__global__ __launch_bounds__(256) void scan_clear_slots(const ScanArgs a, int slots, float* part_a,
+                                                        float* part_d) {
+    const int slot = blockIdx.y, s = a.seqs.owner(slot, a.PL);
+    const int len = a.seqs.end(s) - a.seqs.start(s), first = a.seqs.slot0(s, a.PL);
+    if (slot == first || (int64_t)(slot - first) * a.PL < len) return;
+    const int64_t n = (int64_t)a.D * a.N;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n + 2 * a.D;
+         i += (int64_t)gridDim.x * 256) {
+        if (i < n) part_a[slot * n + i] = 0.0f;
+        else part_d[(int64_t)slot * 2 * a.D + (i - n)] = 0.0f;
+    }
 }
 
 }  // namespace
 
 void scan_sizes(const tg_scan_args& a, size_t* work, size_t* saved, size_t* backward) {
-    const int ns = states_for(a.N);
-    const int64_t slots = a.seqs.rows / chunk_for(ns) + a.seqs.seqs;
-    if (work) *work = 0;
-    if (saved) *saved = (size_t)slots * a.D * 4 * ns * sizeof(float);
-    if (backward) *backward = backward_ws(a).total;
+    const Plan p = plan_of(a);
+    const int64_t slots = a.seqs.rows / p.tt + a.seqs.seqs;
+    if (work) *work = parts_bytes(a, p);
+    if (saved) *saved = (size_t)slots * a.D * 4 * p.ns * sizeof(float);
+    if (backward) *backward = backward_ws(a, p).total;
 }
 
-hipError_t launch_scan(const tg_scan_args& a, void*, void* saved, hipStream_t st) {
+hipError_t launch_scan(const tg_scan_args& a, void* ws, void* saved, hipStream_t st) {
     const tg_dtype dtype = a.dtype;
-    const int N = a.N;
-    const ScanArgs f = args_of(a, (float*)saved);
-    const unsigned grid = (unsigned)(f.G * f.bpg * a.seqs.seqs);
-#define TG_X(T, NS) scan_fwd<T, NS, chunk_for(NS)><<<grid, 64, 0, st>>>(f)
+    const Plan p = plan_of(a);
+    const ScanArgs f = args_of(a, p, (float*)saved, ws);
+#define TG_X(T, NS) return fwd_typed<T, NS>(p, f, st)
     TG_SCAN_DISPATCH(TG_X);
 #undef TG_X
-    return hipGetLastError();
+    return hipErrorInvalidValue;
 }
 
 hipError_t launch_scan_backward(const tg_scan_args& a, const tg_scan_grads& g, const void* saved,
                                 void* ws, hipStream_t st) {
     const tg_dtype dtype = a.dtype;
-    const int N = a.N, np = 4 * states_for(N);
-    const BackwardWs w = backward_ws(a);
-    const ScanArgs f = args_of(a, nullptr);
+    const Plan p = plan_of(a);
+    const BackwardWs w = backward_ws(a, p);
+    char* const base = (char*)ws;
+    const ScanArgs f = args_of(a, p, nullptr, base + w.parts);
     const ScanGrads b{rows_of<const void>(g.dy), g.dfinal, (const float*)saved,
                       rows_of<void>(g.dx), rows_of<void>(g.ddt), rows_of<void>(g.dz), g.dinitial,
-                      (float*)ws, (float*)((char*)ws + w.a), (float*)((char*)ws + w.d)};
-    const unsigned grid = (unsigned)(f.G * f.bpg * a.seqs.seqs);
-#define TG_X(T, NS) scan_bwd<T, NS, chunk_for(NS)><<<grid, 64, 0, st>>>(f, b)
+                      (float*)(base + w.bc), (float*)(base + w.a), (float*)(base + w.d)};
+    hipError_t e = hipSuccess;
+    if (p.PL) {
+        scan_clear_slots<<<dim3(16, (unsigned)p.slots), 256, 0, st>>>(f, (int)p.slots, b.part_a,
+                                                                      b.part_d);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+#define TG_X(T, NS) e = bwd_typed<T, NS>(p, f, b, st)
     TG_SCAN_DISPATCH(TG_X);
 #undef TG_X
-    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (a.seqs.rows > 0) {
+        const int np = 4 * p.ns;
         const int64_t need = ceil_div(a.seqs.rows * a.G * 2 * np, 256);
         const unsigned sums = (unsigned)(need < 4096 ? need : 4096);
         const Rows<void> dB = rows_of<void>(g.dB), dC = rows_of<void>(g.dC);
@@ -472,15 +1105,16 @@ hipError_t launch_scan_backward(const tg_scan_args& a, const tg_scan_grads& g, c
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const int seqs = (int)a.seqs.seqs;
-    e = launch_column_sums(b.part_a, seqs, (int64_t)a.D * N, g.dA, (int64_t)a.D * N, nullptr, st);
+    const int slots = (int)p.slots;
+    const int64_t dn = (int64_t)a.D * a.N;
+    e = launch_column_sums(b.part_a, slots, dn, g.dA, dn, nullptr, st);
     if (e != hipSuccess || (!g.dD && !g.ddt_bias)) return e;
-    return launch_column_sums(b.part_d, seqs, 2 * (int64_t)a.D, g.dD, a.D, g.ddt_bias, st);
+    return launch_column_sums(b.part_d, slots, 2 * (int64_t)a.D, g.dD, a.D, g.ddt_bias, st);
 }
 
 hipError_t launch_scan_step(const tg_scan_args& a, float* state, int64_t num_slots,
                             const int32_t* slots, hipStream_t st) {
-    const StepArgs b{args_of(a, nullptr), state, num_slots, slots};
+    const StepArgs b{args_of(a, Plan{}, nullptr, nullptr), state, num_slots, slots};
     const unsigned grid = (unsigned)(ceil_div(a.D, 64) * a.seqs.seqs);
     const bool v4 = a.N % 4 == 0 && ((uintptr_t)state & 15) == 0 && ((uintptr_t)a.A & 15) == 0;
 #define TG_X(T)                                                  \
