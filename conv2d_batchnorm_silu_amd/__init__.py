@@ -29,5 +29,5 @@ def __getattr__(name):
         return getattr(binding, name)
     if name in _SEQUENCE_NAMES:
         from . import sequence
-        return getattr(sequence, name)
+        return globals().setdefault(name, getattr(sequence, name))
     raise AttributeError(name)

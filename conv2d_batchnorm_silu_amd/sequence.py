@@ -22,9 +22,15 @@ from __future__ import annotations
 import collections
 import ctypes
 
+import torch
+
 from .binding import Activation, Dtype, _check, library
 
 i32, i64, vp, sz = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+
+_F32, _I32, _DENSE = torch.float32, torch.int32, torch.contiguous_format
+_DTYPES = {torch.float16: int(Dtype.F16), torch.bfloat16: int(Dtype.BF16),
+           torch.float32: int(Dtype.F32)}
 
 
 class _Rows(ctypes.Structure):
@@ -57,46 +63,34 @@ class _ScanGrads(ctypes.Structure):
 ScanGradients = collections.namedtuple(
     "ScanGradients", "dx ddt dA dB dC dD dz ddt_bias dinitial_state")
 
-_ready = False
+_loaded = None
 
 
 def _lib():
-    global _ready
+    global _loaded
+    if _loaded is not None:
+        return _loaded
     lib = library()
-    if not _ready:
-        f = ctypes.c_float
-        psz = ctypes.POINTER(sz)
-        conv, scan, grads = (ctypes.POINTER(t) for t in (_ConvArgs, _ScanArgs, _ScanGrads))
-        lib.tg_layer_norm.argtypes = [vp, i64, vp, i64, vp, vp, f, i64, i32, i32, vp, vp, vp, vp, vp]
-        lib.tg_layer_norm_backward_workspace.argtypes = [i64, i32, i32, psz]
-        lib.tg_layer_norm_backward.argtypes = ([vp, i64, vp, i64, vp, vp, vp, vp, i64, i64, i32, i32]
-                                               + [vp] * 4 + [sz, vp])
-        lib.tg_causal_conv.argtypes = [conv, vp]
-        lib.tg_causal_conv_backward_workspace.argtypes = [conv, psz]
-        lib.tg_causal_conv_backward.argtypes = [conv, _Rows, _Rows, vp, vp, vp, vp, vp, sz, vp]
-        lib.tg_causal_conv_step.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, i32, i32, i32, i32,
-                                            vp, vp]
-        lib.tg_selective_scan_sizes.argtypes = [scan, psz, psz, psz]
-        lib.tg_selective_scan.argtypes = [scan, vp, sz, vp, sz, vp]
-        lib.tg_selective_scan_backward.argtypes = [scan, grads, vp, sz, vp, sz, vp]
-        lib.tg_selective_scan_step.argtypes = [scan, vp, i64, vp, vp]
-        _ready = True
+    f, psz = ctypes.c_float, ctypes.POINTER(sz)
+    conv, scan, grads = (ctypes.POINTER(t) for t in (_ConvArgs, _ScanArgs, _ScanGrads))
+    lib.tg_layer_norm.argtypes = [vp, i64, vp, i64, vp, vp, f, i64, i32, i32, vp, vp, vp, vp, vp]
+    lib.tg_layer_norm_backward_workspace.argtypes = [i64, i32, i32, psz]
+    lib.tg_layer_norm_backward.argtypes = ([vp, i64, vp, i64, vp, vp, vp, vp, i64, i64, i32, i32]
+                                           + [vp] * 4 + [sz, vp])
+    lib.tg_causal_conv.argtypes = [conv, vp]
+    lib.tg_causal_conv_backward_workspace.argtypes = [conv, psz]
+    lib.tg_causal_conv_backward.argtypes = [conv, _Rows, _Rows, vp, vp, vp, vp, vp, sz, vp]
+    lib.tg_causal_conv_step.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, i32, i32, i32, i32,
+                                        vp, vp]
+    lib.tg_selective_scan_sizes.argtypes = [scan, psz, psz, psz]
+    lib.tg_selective_scan.argtypes = [scan, vp, sz, vp, sz, vp]
+    lib.tg_selective_scan_backward.argtypes = [scan, grads, vp, sz, vp, sz, vp]
+    lib.tg_selective_scan_step.argtypes = [scan, vp, i64, vp, vp]
+    _loaded = lib
     return lib
 
 
-def _dtypes():
-    import torch
-    return {torch.float16: int(Dtype.F16), torch.bfloat16: int(Dtype.BF16),
-            torch.float32: int(Dtype.F32)}
-
-
-_DTYPES = None
-
-
 def _dtype(t, name):
-    global _DTYPES
-    if _DTYPES is None:
-        _DTYPES = _dtypes()
     d = _DTYPES.get(t.dtype)
     if d is None:
         raise ValueError("%s must be float16, bfloat16 or float32, got %s" % (name, t.dtype))
@@ -104,187 +98,180 @@ def _dtype(t, name):
 
 
 def _device(t, name):
+    """The device number of the tensor that the others are held against."""
     if not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
-    return t.device
+    return t.get_device()
 
 
-def _tensor(t, name, like, shape, dtype=None):
-    """Device, type and shape of an argument; its last dimension contiguous."""
-    if t.device != like.device:
-        raise ValueError("%s must be on %s, got %s" % (name, like.device, t.device))
-    want = like.dtype if dtype is None else dtype
-    if t.dtype != want:
-        raise ValueError("%s must be %s, got %s" % (name, want, t.dtype))
+def _refuse(t, name, dev, shape, dtype, contiguous):
+    """Say what is wrong with an argument; the checks before only saw that
+    something is."""
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, dev, t.device))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if contiguous and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError("%s must be contiguous in its last dimension" % name)
 
 
-def _flat(t, name, like, shape, dtype):
+def _flat(t, name, dev, shape, dtype=_F32):
     """A dense argument's address; None gives 0."""
     if t is None:
         return 0
-    _tensor(t, name, like, shape, dtype)
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    if not (t.dtype is dtype and t.is_cuda and t.get_device() == dev and t.shape == shape
+            and t.is_contiguous()):
+        _refuse(t, name, dev, shape, dtype, True)
     return t.data_ptr()
 
 
-def _param(t, name, like, *shape):
-    import torch
-    return _flat(t, name, like, shape, torch.float32)
+def _some(t, name):
+    if t is None:
+        raise ValueError("%s is required" % name)
+    return t
 
 
-def _row_stride(t, width):
-    return t.stride(-2) if t.shape[-2] > 1 else width
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-class _Launch:
-    """The stream of a call, and its device and stream as torch's current ones
-    while outputs are allocated (only entered where they are not already)."""
-
-    def __init__(self, x, stream):
-        import torch
-        cur = torch.cuda.current_stream(x.device)
-        self.contexts = []
-        if stream is not None and stream != cur:
-            if stream.device != x.device:
-                raise ValueError("stream is on %s, the tensors on %s" % (stream.device, x.device))
-            self.contexts.append(torch.cuda.stream(stream))
-            cur = stream
-        elif x.device.index != torch.cuda.current_device():
-            self.contexts.append(torch.cuda.device(x.device))
-        self.handle = cur.cuda_stream
-
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
+def _elsewhere(dev, stream):
+    """A context that makes ``stream``, or device ``dev``, torch's current one
+    if it is not: the call then starts over inside, so that outputs and
+    scratch are allocated for that stream."""
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError("stream is on %s, the tensors on cuda:%d" % (stream.device, dev))
+        return torch.cuda.stream(stream)
+    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _batch(x, offsets, name="x"):
-    """(_Seqs, leading shape, number of sequences) of a dense or packed batch."""
-    import torch
-    _device(x, name)
+def _batch(x, offsets, dev):
+    """(seqs, rows, offsets address) of a dense or packed batch."""
     if offsets is None:
         if x.dim() != 3:
-            raise ValueError("%s must be [S, L, C], or [T, C] with offsets; got %s"
-                             % (name, tuple(x.shape)))
+            raise ValueError("x must be [S, L, C], or [T, C] with offsets; got %s"
+                             % (tuple(x.shape),))
         S, L = x.shape[0], x.shape[1]
         if S < 1:
-            raise ValueError("%s must hold at least one sequence" % name)
-        return _Seqs(S, S * L, 0), x.shape[:2], S
+            raise ValueError("x must hold at least one sequence")
+        return S, S * L, 0
     if x.dim() != 2:
-        raise ValueError("%s must be [T, C] with offsets, got %s" % (name, tuple(x.shape)))
-    if (offsets.device != x.device or offsets.dtype != torch.int32 or offsets.dim() != 1
-            or offsets.numel() < 2 or not offsets.is_contiguous()):
-        raise ValueError("offsets must be a contiguous int32 tensor of at least 2 elements on %s"
-                         % x.device)
-    S = offsets.numel() - 1
-    return _Seqs(S, x.shape[0], offsets.data_ptr()), x.shape[:1], S
+        raise ValueError("x must be [T, C] with offsets, got %s" % (tuple(x.shape),))
+    if (not offsets.is_cuda or offsets.get_device() != dev or offsets.dtype != _I32
+            or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous()):
+        raise ValueError("offsets must be a contiguous int32 tensor of at least 2 elements on "
+                         "cuda:%d" % dev)
+    return offsets.numel() - 1, x.shape[0], offsets.data_ptr()
 
 
-def _rows(t, name, like, shape, packed, width=None):
-    """_Rows of a batch's tensor; ``width``: elements of a row."""
+_NO_ROWS = (0, 0, 0)
+
+
+def _rows(t, name, dev, shape, dtype, packed, width):
+    """The tg_rows of a batch's tensor, as a tuple; ``width``: elements of a row."""
     if t is None:
-        return _Rows(0, 0, 0)
-    _tensor(t, name, like, shape)
-    return _rows_unchecked(t, packed, width or shape[-1], len(shape) - (1 if packed else 2))
+        return _NO_ROWS
+    st = t.stride()
+    if not (t.dtype is dtype and t.is_cuda and t.get_device() == dev and t.shape == shape
+            and (st[-1] == 1 or shape[-1] == 1)):
+        _refuse(t, name, dev, shape, dtype, False)
+    return _place(t, st, packed, width)
 
 
-def _rows_unchecked(t, packed, width, inner=1):
+def _place(t, st, packed, width):
+    # The stride of a dimension of one element means nothing.
     if packed:
-        return _Rows(t.data_ptr(), 0, t.stride(0) if t.shape[0] > 1 else width)
-    row = t.stride(1) if t.shape[1] > 1 else width
-    return _Rows(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else row * t.shape[1], row)
+        return t.data_ptr(), 0, st[0] if t.shape[0] > 1 else width
+    row = st[1] if t.shape[1] > 1 else width
+    return t.data_ptr(), st[0] if t.shape[0] > 1 else row * t.shape[1], row
 
 
-def _out(out, like, name, shape):
-    import torch
+def _new_or(out, like, dev, dense):
+    """A new tensor like ``like``, dense, or ``out`` if it fits."""
     if out is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
-    _tensor(out, name, like, shape)
+        return torch.empty_like(like, memory_format=_DENSE)
+    _refuse(out, "out", dev, like.shape, like.dtype, dense)
     return out
-
-
-def _slots(slots, like, n):
-    import torch
-    if slots is None:
-        return 0
-    return _flat(slots, "slots", like, (n,), torch.int32)
 
 
 # -------------------------------------------------------------- layer norm
 
-def _norm_rows(t, name, like):
+def _norm_rows(t, name, dev, shape, dtype):
     """(address, row stride) of [..., C] whose leading dimensions are one row
     stride apart."""
-    _tensor(t, name, like, like.shape)
-    C = t.shape[-1]
+    if t is None:
+        return 0, 0
+    if not (t.dtype is dtype and t.is_cuda and t.get_device() == dev and t.shape == shape):
+        _refuse(t, name, dev, shape, dtype, False)
+    C = shape[-1]
     if t.is_contiguous():
         return t.data_ptr(), C
-    if t.numel() == 0:
-        return t.data_ptr(), C
-    stride, step = None, 0
-    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-        if n == 1:
-            continue
-        if stride is None:
-            stride = s
-            step = s * n
-        elif s != step:
-            raise ValueError("%s: the rows must be one stride apart (make it contiguous)" % name)
-        else:
-            step = s * n
+    _refuse(t, name, dev, shape, dtype, False)
+    stride = step = None
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n != 1:
+            if step is not None and st != step:
+                raise ValueError("%s: the rows must be one stride apart (make it contiguous)" % name)
+            stride = st if stride is None else stride
+            step = st * n
     return t.data_ptr(), C if stride is None else stride
 
 
-def _norm_forward(x, gamma, beta, eps, residual, train, out, stream):
-    import torch
-    _device(x, "x")
-    dt = _dtype(x, "x")
+def _norm_shape(x, name):
     if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("x must be [..., C] with C >= 1, got %s" % (tuple(x.shape),))
-    C = x.shape[-1]
-    rows = x.numel() // C
-    xp, xs = _norm_rows(x, "x", x)
-    rp, rs = (0, 0) if residual is None else _norm_rows(residual, "residual", x)
-    if gamma is None:
-        raise ValueError("gamma is required")
-    gp, bp = _param(gamma, "gamma", x, C), _param(beta, "beta", x, C)
-    lib = _lib()
-    with _Launch(x, stream) as st:
-        y = _out(out, x, "out", x.shape)
-        if out is not None and not y.is_contiguous():
-            raise ValueError("out must be contiguous")
-        total = None if residual is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        mean = rstd = None
-        if train:
-            mean, rstd = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=x.device)
-        _check(lib.tg_layer_norm(
-            xp, xs, rp, rs, gp, bp, eps, rows, C, dt, y.data_ptr(),
-            0 if total is None else total.data_ptr(), 0 if mean is None else mean.data_ptr(),
-            0 if rstd is None else rstd.data_ptr(), st), "tg_layer_norm")
+        raise ValueError("%s must be [..., C] with C >= 1, got %s" % (name, tuple(x.shape)))
+    shape, C = x.shape, x.shape[-1]
+    return shape, C, x.numel() // C, x.dtype
+
+
+def _norm_forward(x, gamma, beta, eps, residual, train, out, dev):
+    dt = _dtype(x, "x")
+    shape, C, rows, dtype = _norm_shape(x, "x")
+    xp, xs = _norm_rows(x, "x", dev, shape, dtype)
+    rp, rs = _norm_rows(residual, "residual", dev, shape, dtype)
+    gp = _flat(_some(gamma, "gamma"), "gamma", dev, (C,))
+    bp = _flat(beta, "beta", dev, (C,))
+    y = _new_or(out, x, dev, True)
+    total, tp, mean, rstd, mp, qp = None, 0, None, None, 0, 0
+    if residual is not None:
+        total = torch.empty_like(x, memory_format=_DENSE)
+        tp = total.data_ptr()
+    if train:
+        mean, rstd = torch.empty((2,) + shape[:-1], dtype=_F32, device=x.device)
+        mp, qp = mean.data_ptr(), rstd.data_ptr()
+    st = _lib().tg_layer_norm(xp, xs, rp, rs, gp, bp, eps, rows, C, dt, y.data_ptr(), tp, mp, qp,
+                              _raw_stream(dev))
+    if st:
+        _check(st, "tg_layer_norm")
     return y, total, mean, rstd
 
 
 def layer_norm(x, gamma, beta=None, eps=1e-5, residual=None, out=None, stream=None):
     """Layer norm over the last dimension: y, or with ``residual`` (x's shape
     and type) the pair (y, x + residual), the norm taken of the sum."""
-    y, total, _, _ = _norm_forward(x, gamma, beta, eps, residual, False, out, stream)
+    dev = _device(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return layer_norm(x, gamma, beta, eps, residual, out)
+    y, total, _, _ = _norm_forward(x, gamma, beta, eps, residual, False, out, dev)
     return y if residual is None else (y, total)
 
 
 def layer_norm_train(x, gamma, beta=None, eps=1e-5, residual=None, out=None, stream=None):
     """(y, s, mean, rstd): layer norm and what its backward pass takes. s is
     the normalised input: x itself, or x + residual."""
-    y, total, mean, rstd = _norm_forward(x, gamma, beta, eps, residual, True, out, stream)
+    dev = _device(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return layer_norm_train(x, gamma, beta, eps, residual, out)
+    y, total, mean, rstd = _norm_forward(x, gamma, beta, eps, residual, True, out, dev)
     return y, x if residual is None else total, mean, rstd
 
 
@@ -292,58 +279,62 @@ def layer_norm_backward(dy, s, gamma, mean, rstd, dsum=None, out=None, stream=No
     """(dx, dgamma, dbeta) from dy and layer_norm_train's s, mean and rstd.
     ``dsum``: a gradient that reaches s past the norm (the residual stream's),
     added to dx. dx is the gradient of x and of the residual alike."""
-    import torch
-    _device(s, "s")
+    dev = _device(s, "s")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return layer_norm_backward(dy, s, gamma, mean, rstd, dsum, out)
     dt = _dtype(s, "s")
-    C = s.shape[-1]
-    rows = s.numel() // C
-    sp, ss = _norm_rows(s, "s", s)
-    gp, gs = _norm_rows(dy, "dy", s)
-    dp, ds = (0, 0) if dsum is None else _norm_rows(dsum, "dsum", s)
-    if gamma is None:
-        raise ValueError("gamma is required")
-    wp = _param(gamma, "gamma", s, C)
-    mp = _param(mean, "mean", s, *s.shape[:-1])
-    qp = _param(rstd, "rstd", s, *s.shape[:-1])
+    shape, C, rows, dtype = _norm_shape(s, "s")
+    sp, ss = _norm_rows(s, "s", dev, shape, dtype)
+    gp, gs = _norm_rows(_some(dy, "dy"), "dy", dev, shape, dtype)
+    dp, ds = _norm_rows(dsum, "dsum", dev, shape, dtype)
+    wp = _flat(_some(gamma, "gamma"), "gamma", dev, (C,))
+    mp = _flat(_some(mean, "mean"), "mean", dev, shape[:-1])
+    qp = _flat(_some(rstd, "rstd"), "rstd", dev, shape[:-1])
     lib = _lib()
     need = sz()
     _check(lib.tg_layer_norm_backward_workspace(rows, C, dt, ctypes.byref(need)),
            "tg_layer_norm_backward_workspace")
-    with _Launch(s, stream) as st:
-        dx = _out(out, s, "out", s.shape)
-        if out is not None and not dx.is_contiguous():
-            raise ValueError("out must be contiguous")
-        dw = torch.empty((2, C), dtype=torch.float32, device=s.device)
-        ws = torch.empty(need.value, dtype=torch.uint8, device=s.device)
-        _check(lib.tg_layer_norm_backward(
-            gp, gs, sp, ss, wp, mp, qp, dp, ds, rows, C, dt, dx.data_ptr(), dw[0].data_ptr(),
-            dw[1].data_ptr(), ws.data_ptr(), need.value, st), "tg_layer_norm_backward")
+    dx = _new_or(out, s, dev, True)
+    dw = torch.empty((2, C), dtype=_F32, device=s.device)
+    ws = torch.empty(need.value, dtype=torch.uint8, device=s.device)
+    _check(lib.tg_layer_norm_backward(
+        gp, gs, sp, ss, wp, mp, qp, dp, ds, rows, C, dt, dx.data_ptr(), dw.data_ptr(),
+        dw.data_ptr() + 4 * C, ws.data_ptr(), need.value, _raw_stream(dev)),
+        "tg_layer_norm_backward")
     return dx, dw[0], dw[1]
 
 
 # -------------------------------------------------- short causal convolution
 
+_ACTS = {"silu": int(Activation.SILU), "none": int(Activation.NONE),
+         Activation.SILU: int(Activation.SILU), Activation.NONE: int(Activation.NONE)}
+
+
 def _activation(act):
-    a = act if isinstance(act, Activation) else Activation[str(act).upper()]
-    if a not in (Activation.SILU, Activation.NONE):
-        raise ValueError("act must be silu or none, got %s" % act)
-    return int(a)
+    a = _ACTS.get(act.lower() if isinstance(act, str) else act)
+    if a is None:
+        raise ValueError("act must be silu or none, got %s" % (act,))
+    return a
 
 
-def _conv_args(x, w, bias, act, initial_state, offsets):
-    import torch
-    dt = _dtype(x, "x")
-    seqs, lead, S = _batch(x, offsets)
-    packed = offsets is not None
-    D = x.shape[-1]
+def _taps(w):
     if w is None or w.dim() != 2:
         raise ValueError("w must be [K, D]")
-    K = w.shape[0]
-    a = _ConvArgs(seqs, D, K, dt, _activation(act))
-    a.x = _rows(x, "x", x, x.shape, packed)
-    a.w, a.bias = _param(w, "w", x, K, D), _param(bias, "bias", x, D)
-    a.initial = _flat(initial_state, "initial_state", x, (S, K - 1, D), x.dtype)
-    return a, packed, (S, K - 1, D)
+    return w.shape[0]
+
+
+def _conv_args(x, w, bias, act, initial_state, offsets, dev):
+    dt = _dtype(x, "x")
+    S, rows, off = _batch(x, offsets, dev)
+    packed, D, K = offsets is not None, x.shape[-1], _taps(w)
+    held = (S, K - 1, D)
+    a = _ConvArgs((S, rows, off), D, K, dt, _activation(act),
+                  _rows(x, "x", dev, x.shape, x.dtype, packed, D), _NO_ROWS,
+                  _flat(w, "w", dev, (K, D)), _flat(bias, "bias", dev, (D,)),
+                  _flat(initial_state, "initial_state", dev, held, x.dtype), 0)
+    return a, packed, held
 
 
 def causal_conv(x, w, bias=None, act="silu", initial_state=None, offsets=None, return_state=False,
@@ -355,16 +346,19 @@ def causal_conv(x, w, bias=None, act="silu", initial_state=None, offsets=None, r
     the rows before each sequence (default zeros). Returns y, or with
     ``return_state`` (y, state): the last K-1 rows of each sequence, as a
     next chunk's initial state or causal_conv_step's state."""
-    import torch
-    a, packed, held = _conv_args(x, w, bias, act, initial_state, offsets)
-    lib = _lib()
-    with _Launch(x, stream) as st:
-        y = _out(out, x, "out", x.shape)
-        a.y = _rows_unchecked(y, packed, a.D)
-        state = torch.empty(held, dtype=x.dtype, device=x.device) if return_state else None
-        if return_state:
-            a.final = state.data_ptr()
-        _check(lib.tg_causal_conv(ctypes.byref(a), st), "tg_causal_conv")
+    dev = _device(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return causal_conv(x, w, bias, act, initial_state, offsets, return_state, out)
+    a, packed, held = _conv_args(x, w, bias, act, initial_state, offsets, dev)
+    y = _new_or(out, x, dev, False)
+    a.y = _place(y, y.stride(), packed, a.D)
+    state = None
+    if return_state:
+        state = torch.empty(held, dtype=x.dtype, device=x.device)
+        a.final = state.data_ptr()
+    _check(_lib().tg_causal_conv(ctypes.byref(a), _raw_stream(dev)), "tg_causal_conv")
     return (y, state) if return_state else y
 
 
@@ -373,25 +367,31 @@ def causal_conv_backward(dy, x, w, bias=None, act="silu", initial_state=None, of
     """(dx, dw, dbias, dinitial_state) of causal_conv's y with the same x, w,
     bias, act, initial_state and offsets. ``dstate`` [S, K-1, D]: the gradient
     of the returned state. dinitial_state is None without an initial_state."""
-    import torch
-    a, packed, held = _conv_args(x, w, bias, act, initial_state, offsets)
-    g = _rows(dy, "dy", x, x.shape, packed)
-    df = _flat(dstate, "dstate", x, held, x.dtype)
+    dev = _device(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return causal_conv_backward(dy, x, w, bias, act, initial_state, offsets, dstate)
+    a, packed, held = _conv_args(x, w, bias, act, initial_state, offsets, dev)
+    K, D = a.K, a.D
+    g = _rows(_some(dy, "dy"), "dy", dev, x.shape, x.dtype, packed, D)
+    df = _flat(dstate, "dstate", dev, held, x.dtype)
     lib = _lib()
     need = sz()
     _check(lib.tg_causal_conv_backward_workspace(ctypes.byref(a), ctypes.byref(need)),
            "tg_causal_conv_backward_workspace")
-    with _Launch(x, stream) as st:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty((a.K + 1, a.D), dtype=torch.float32, device=x.device)
-        d0 = (None if initial_state is None
-              else torch.empty(held, dtype=x.dtype, device=x.device))
-        ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-        _check(lib.tg_causal_conv_backward(
-            ctypes.byref(a), g, _rows_unchecked(dx, packed, a.D), dw.data_ptr(),
-            dw[a.K].data_ptr(), df, 0 if d0 is None else d0.data_ptr(), ws.data_ptr(), need.value,
-            st), "tg_causal_conv_backward")
-    return dx, dw[:a.K], dw[a.K], d0
+    dx = torch.empty_like(x, memory_format=_DENSE)
+    dw = torch.empty((K + 1, D), dtype=_F32, device=x.device)
+    d0, d0p = None, 0
+    if initial_state is not None:
+        d0 = torch.empty(held, dtype=x.dtype, device=x.device)
+        d0p = d0.data_ptr()
+    ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+    _check(lib.tg_causal_conv_backward(
+        ctypes.byref(a), _Rows(*g), _Rows(*_place(dx, dx.stride(), packed, D)), dw.data_ptr(),
+        dw.data_ptr() + 4 * K * D, df, d0p, ws.data_ptr(), need.value,
+        _raw_stream(dev)), "tg_causal_conv_backward")
+    return dx, dw[:K], dw[K], d0
 
 
 def causal_conv_step(x, state, w, bias=None, act="silu", slots=None, out=None, stream=None):
@@ -399,86 +399,81 @@ def causal_conv_step(x, state, w, bias=None, act="silu", slots=None, out=None, s
     [num_slots, K-1, D] moves on in place. ``slots`` (int32 [n]): each
     sequence's place in ``state`` (default: its number); a slot outside the
     state marks a row without a sequence (y zero, nothing updated)."""
-    _device(x, "x")
-    dt = _dtype(x, "x")
+    dev = _device(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return causal_conv_step(x, state, w, bias, act, slots, out)
+    dt, dtype = _dtype(x, "x"), x.dtype
     if x.dim() != 2:
         raise ValueError("x must be [n, D], got %s" % (tuple(x.shape),))
-    n, D = x.shape
-    if w is None or w.dim() != 2:
-        raise ValueError("w must be [K, D]")
-    K = w.shape[0]
-    if state.dim() != 3:
-        raise ValueError("state must be [num_slots, K-1, D]")
-    num = state.shape[0]
-    _tensor(x, "x", x, x.shape)
-    hp = _flat(state, "state", x, (num, K - 1, D), x.dtype)
-    sp = _slots(slots, x, n)
-    wp, bp = _param(w, "w", x, K, D), _param(bias, "bias", x, D)
-    a = _activation(act)
-    lib = _lib()
-    with _Launch(x, stream) as st:
-        y = _out(out, x, "out", x.shape)
-        if out is not None and not y.is_contiguous():
-            raise ValueError("out must be contiguous")
-        _check(lib.tg_causal_conv_step(x.data_ptr(), _row_stride(x, D), hp, num, sp, wp, bp, n, D,
-                                       K, dt, a, y.data_ptr(), st), "tg_causal_conv_step")
+    (n, D), K, num = x.shape, _taps(w), state.shape[0]
+    xp, _, xs = _rows(x, "x", dev, x.shape, dtype, True, D)
+    hp = _flat(state, "state", dev, (num, K - 1, D), dtype)
+    sp = _flat(slots, "slots", dev, (n,), _I32)
+    wp, bp = _flat(w, "w", dev, (K, D)), _flat(bias, "bias", dev, (D,))
+    y = _new_or(out, x, dev, True)
+    st = _lib().tg_causal_conv_step(xp, xs, hp, num, sp, wp, bp, n, D, K, dt, _activation(act),
+                                    y.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "tg_causal_conv_step")
     return y
 
 
 # ---------------------------------------------------------- selective scan
 
-def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, seqs, lead, S, packed):
-    import torch
-    d = _dtype(x, "x")
-    width = x.shape[-1]
+def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, seqs, packed, dev):
+    d, dtype, shape = _dtype(x, "x"), x.dtype, x.shape
+    lead, width = shape[:-1], shape[-1]
     if A is None or A.dim() != 2:
-        raise ValueError("A must be [D, N]")
+        raise ValueError("A must be [channels, N]")
     N = A.shape[1]
     if B.dim() != len(lead) + 2:
         raise ValueError("B must be %s + [G, N], got %s" % (tuple(lead), tuple(B.shape)))
     G = B.shape[-2]
     if G < 1 or width % G:
         raise ValueError("the %d groups of B must divide the %d channels" % (G, width))
-    a = _ScanArgs(seqs, width, N, G, d, 1 if softplus else 0)
-    a.x = _rows(x, "x", x, x.shape, packed)
-    a.dt = _rows(dt, "dt", x, x.shape, packed)
     gn = lead + (G, N)
-    for name, t in (("B", B), ("C", C)):
-        if t.dim() == len(gn) and G > 1 and t.stride(-2) != N:
-            raise ValueError("%s: the groups of a row must lie one after another" % name)
-        setattr(a, name, _rows(t, name, x, gn, packed, G * N))
-    a.z = _rows(z, "z", x, x.shape, packed)
-    a.A, a.D_skip = _param(A, "A", x, width, N), _param(D, "D", x, width)
-    a.dt_bias = _param(dt_bias, "dt_bias", x, width)
-    a.initial = _param(initial_state, "initial_state", x, S, width, N)
-    return a
+    if G > 1:
+        for name, t in (("B", B), ("C", C)):
+            if t.dim() == len(gn) and t.stride(-2) != N:
+                raise ValueError("%s: the groups of a row must lie one after another" % name)
+    return _ScanArgs(
+        seqs, width, N, G, d, 1 if softplus else 0,
+        _rows(x, "x", dev, shape, dtype, packed, width),
+        _rows(dt, "dt", dev, shape, dtype, packed, width),
+        _rows(B, "B", dev, gn, dtype, packed, G * N),
+        _rows(C, "C", dev, gn, dtype, packed, G * N),
+        _rows(z, "z", dev, shape, dtype, packed, width), _NO_ROWS,
+        _flat(A, "A", dev, (width, N)), _flat(D, "D", dev, (width,)),
+        _flat(dt_bias, "dt_bias", dev, (width,)),
+        _flat(initial_state, "initial_state", dev, (seqs[0], width, N)), 0)
 
 
 def _scan_forward(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, offsets, want_state,
-                  train, out, stream):
-    import torch
-    seqs, lead, S = _batch(x, offsets)
+                  train, out, dev):
     packed = offsets is not None
-    a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, seqs, lead, S, packed)
+    a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state,
+                   _batch(x, offsets, dev), packed, dev)
     lib = _lib()
     work, keep = sz(), sz()
     _check(lib.tg_selective_scan_sizes(ctypes.byref(a), ctypes.byref(work), ctypes.byref(keep),
                                        None), "tg_selective_scan_sizes")
-    with _Launch(x, stream) as st:
-        y = _out(out, x, "out", x.shape)
-        a.y = _rows_unchecked(y, packed, a.D)
-        state = saved = ws = None
-        if want_state:
-            state = torch.empty((S, a.D, a.N), dtype=torch.float32, device=x.device)
-            a.final = state.data_ptr()
-        if train:
-            saved = torch.empty(keep.value // 4, dtype=torch.float32, device=x.device)
-        if work.value:
-            ws = torch.empty(work.value, dtype=torch.uint8, device=x.device)
-        _check(lib.tg_selective_scan(
-            ctypes.byref(a), 0 if ws is None else ws.data_ptr(), work.value,
-            0 if saved is None else saved.data_ptr(), keep.value if train else 0, st),
-            "tg_selective_scan")
+    y = _new_or(out, x, dev, False)
+    a.y = _place(y, y.stride(), packed, a.D)
+    state = saved = ws = None
+    wp = kp = 0
+    if want_state:
+        state = torch.empty((a.seqs.seqs, a.D, a.N), dtype=_F32, device=x.device)
+        a.final = state.data_ptr()
+    if train:
+        saved = torch.empty(keep.value // 4, dtype=_F32, device=x.device)
+        kp = saved.data_ptr()
+    if work.value:
+        ws = torch.empty(work.value, dtype=torch.uint8, device=x.device)
+        wp = ws.data_ptr()
+    _check(lib.tg_selective_scan(ctypes.byref(a), wp, work.value, kp, keep.value if train else 0,
+                                 _raw_stream(dev)), "tg_selective_scan")
     return y, state, saved
 
 
@@ -494,8 +489,14 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=True, 
     128; B, C [..., G, N], each group shared by channels/G neighbouring channels;
     D, dt_bias [channels]. ``initial_state`` fp32 [S, channels, N] (default
     zeros). Returns y, or with ``return_state`` (y, state)."""
+    dev = _device(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return selective_scan(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, offsets,
+                                  return_state, out)
     y, state, _ = _scan_forward(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, offsets,
-                                return_state, False, out, stream)
+                                return_state, False, out, dev)
     return (y, state) if return_state else y
 
 
@@ -504,8 +505,14 @@ def selective_scan_train(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=
                          stream=None):
     """selective_scan for training: (y, saved) or (y, state, saved); ``saved``
     holds the states that selective_scan_backward starts from."""
+    dev = _device(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return selective_scan_train(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state,
+                                        offsets, return_state, out)
     y, state, saved = _scan_forward(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state,
-                                    offsets, return_state, True, out, stream)
+                                    offsets, return_state, True, out, dev)
     return (y, state, saved) if return_state else (y, saved)
 
 
@@ -515,40 +522,53 @@ def selective_scan_backward(dy, x, dt, A, B, C, saved, D=None, z=None, dt_bias=N
     selective_scan_train's y with the same arguments and its ``saved``;
     entries are None for arguments that were not given. ``dstate`` fp32 [S,
     channels, N]: the gradient of the returned state."""
-    import torch
-    seqs, lead, S = _batch(x, offsets)
+    dev = _device(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return selective_scan_backward(dy, x, dt, A, B, C, saved, D, z, dt_bias, softplus,
+                                           initial_state, offsets, dstate)
     packed = offsets is not None
-    a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, seqs, lead, S, packed)
-    g = _ScanGrads()
-    g.dy = _rows(dy, "dy", x, x.shape, packed)
-    g.dfinal = _param(dstate, "dstate", x, S, a.D, a.N)
+    a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state,
+                   _batch(x, offsets, dev), packed, dev)
+    S, width, N, gn = a.seqs.seqs, a.D, a.N, a.G * a.N
+    g = _ScanGrads(_rows(_some(dy, "dy"), "dy", dev, x.shape, x.dtype, packed, width),
+                   _flat(dstate, "dstate", dev, (S, width, N)))
     lib = _lib()
     keep, need = sz(), sz()
     _check(lib.tg_selective_scan_sizes(ctypes.byref(a), None, ctypes.byref(keep),
                                        ctypes.byref(need)), "tg_selective_scan_sizes")
-    sp = _flat(saved, "saved", x, (keep.value // 4,), torch.float32)
-    with _Launch(x, stream) as st:
-        def new(shape, dtype=torch.float32):
-            return torch.empty(shape, dtype=dtype, device=x.device)
-        dx, ddt = new(x.shape, x.dtype), new(x.shape, x.dtype)
-        dz = None if z is None else new(x.shape, x.dtype)
-        dB, dC = new(B.shape, x.dtype), new(C.shape, x.dtype)
-        dA = new((a.D, a.N))
-        dD = None if D is None else new((a.D,))
-        db = None if dt_bias is None else new((a.D,))
-        d0 = None if initial_state is None else new((S, a.D, a.N))
-        ws = new((need.value,), torch.uint8)
-        for name, t, w in (("dx", dx, a.D), ("ddt", ddt, a.D), ("dz", dz, a.D),
-                           ("dB", dB, a.G * a.N), ("dC", dC, a.G * a.N)):
-            if t is not None:
-                setattr(g, name, _rows_unchecked(t, packed, w))
-        g.dA = dA.data_ptr()
-        g.dD = 0 if dD is None else dD.data_ptr()
-        g.ddt_bias = 0 if db is None else db.data_ptr()
-        g.dinitial = 0 if d0 is None else d0.data_ptr()
-        _check(lib.tg_selective_scan_backward(ctypes.byref(a), ctypes.byref(g), sp, keep.value,
-                                              ws.data_ptr(), need.value, st),
-               "tg_selective_scan_backward")
+    sp = _flat(_some(saved, "saved"), "saved", dev, (keep.value // 4,))
+
+    def rows_like(t, w):
+        o = torch.empty_like(t, memory_format=_DENSE)
+        return o, _place(o, o.stride(), packed, w)
+
+    def params(*shape):
+        return torch.empty(shape, dtype=_F32, device=x.device)
+
+    dx, g.dx = rows_like(x, width)
+    ddt, g.ddt = rows_like(x, width)
+    dB, g.dB = rows_like(B, gn)
+    dC, g.dC = rows_like(C, gn)
+    dz = dD = db = d0 = None
+    if z is not None:
+        dz, g.dz = rows_like(x, width)
+    dA = params(width, N)
+    g.dA = dA.data_ptr()
+    if D is not None:
+        dD = params(width)
+        g.dD = dD.data_ptr()
+    if dt_bias is not None:
+        db = params(width)
+        g.ddt_bias = db.data_ptr()
+    if initial_state is not None:
+        d0 = params(S, width, N)
+        g.dinitial = d0.data_ptr()
+    ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+    _check(lib.tg_selective_scan_backward(ctypes.byref(a), ctypes.byref(g), sp, keep.value,
+                                          ws.data_ptr(), need.value, _raw_stream(dev)),
+           "tg_selective_scan_backward")
     return ScanGradients(dx, ddt, dA, dB, dC, dD, dz, db, d0)
 
 
@@ -557,22 +577,21 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, sof
     """One token of each of n sequences: x, dt, z [n, channels], B, C [n, G, N]
     -> y [n, channels]; ``state`` fp32 [num_slots, channels, N] is updated in
     place. ``slots`` as in causal_conv_step."""
-    import torch
-    _device(x, "x")
+    dev = _device(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return selective_scan_step(x, dt, A, B, C, state, D, z, dt_bias, softplus, slots, out)
     if x.dim() != 2:
         raise ValueError("x must be [n, channels], got %s" % (tuple(x.shape),))
     n = x.shape[0]
-    a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, None, _Seqs(n, n, 0), x.shape[:1], n,
-                   True)
-    if state.dim() != 3:
-        raise ValueError("state must be [num_slots, channels, N]")
+    a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, None, (n, n, 0), True, dev)
     num = state.shape[0]
-    hp = _param(state, "state", x, num, a.D, a.N)
-    sp = _slots(slots, x, n)
-    lib = _lib()
-    with _Launch(x, stream) as st:
-        y = _out(out, x, "out", x.shape)
-        a.y = _rows_unchecked(y, True, a.D)
-        _check(lib.tg_selective_scan_step(ctypes.byref(a), hp, num, sp, st),
-               "tg_selective_scan_step")
+    hp = _flat(state, "state", dev, (num, a.D, a.N))
+    sp = _flat(slots, "slots", dev, (n,), _I32)
+    y = _new_or(out, x, dev, False)
+    a.y = _place(y, y.stride(), True, a.D)
+    st = _lib().tg_selective_scan_step(ctypes.byref(a), hp, num, sp, _raw_stream(dev))
+    if st:
+        _check(st, "tg_selective_scan_step")
     return y
