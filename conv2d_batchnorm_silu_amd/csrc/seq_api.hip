@@ -12,6 +12,8 @@ namespace {
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 constexpr int kMaxChannels = 1 << 20;
 constexpr int64_t kMaxGroups = ((int64_t)1 << 31) - 1;
+// The scan addresses 16 rows by 31-bit byte offsets.
+constexpr int64_t kMaxScanStride = (int64_t)1 << 25;
 
 bool dtype_ok(int d) { return d == TG_F16 || d == TG_BF16 || d == TG_F32; }
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -42,6 +44,11 @@ tg_status check_rows(const tg_rows& r, const tg_seqs& s, int64_t width, size_t e
         TG_REQUIRE(r.seq_stride >= least || (written && s.seqs == 1), TG_ERR_INVALID_ARGUMENT);
     TG_REQUIRE(aligned(r.p, elem), TG_ERR_ALIGNMENT);
     return TG_OK;
+}
+tg_status check_scan_rows(const tg_rows& r, const tg_seqs& s, int64_t width, size_t elem,
+                          bool written) {
+    TG_REQUIRE(s.rows == 0 || r.row_stride < kMaxScanStride, TG_ERR_UNSUPPORTED);
+    return check_rows(r, s, width, elem, written);
 }
 
 #define TG_CHECK(expr)                     \
@@ -77,11 +84,11 @@ tg_status check_scan_inputs(const tg_scan_args* a) {
     TG_REQUIRE(a->A, TG_ERR_INVALID_ARGUMENT);
     TG_REQUIRE(aligned(a->A, 4) && aligned(a->D_skip, 4) && aligned(a->dt_bias, 4) &&
                    aligned(a->initial, 4) && aligned(a->final, 4), TG_ERR_ALIGNMENT);
-    TG_CHECK(check_rows(a->x, a->seqs, a->D, e, false));
-    TG_CHECK(check_rows(a->dt, a->seqs, a->D, e, false));
-    TG_CHECK(check_rows(a->B, a->seqs, (int64_t)a->G * a->N, e, false));
-    TG_CHECK(check_rows(a->C, a->seqs, (int64_t)a->G * a->N, e, false));
-    if (a->z.p) TG_CHECK(check_rows(a->z, a->seqs, a->D, e, false));
+    TG_CHECK(check_scan_rows(a->x, a->seqs, a->D, e, false));
+    TG_CHECK(check_scan_rows(a->dt, a->seqs, a->D, e, false));
+    TG_CHECK(check_scan_rows(a->B, a->seqs, (int64_t)a->G * a->N, e, false));
+    TG_CHECK(check_scan_rows(a->C, a->seqs, (int64_t)a->G * a->N, e, false));
+    if (a->z.p) TG_CHECK(check_scan_rows(a->z, a->seqs, a->D, e, false));
     return TG_OK;
 }
 
@@ -199,7 +206,7 @@ tg_status tg_selective_scan(const tg_scan_args* a, void* workspace, size_t works
                             void* saved, size_t saved_bytes, void* stream) {
     TG_CHECK(check_scan(a));
     TG_CHECK(check_scan_inputs(a));
-    TG_CHECK(check_rows(a->y, a->seqs, a->D, elem_bytes(a->dtype), true));
+    TG_CHECK(check_scan_rows(a->y, a->seqs, a->D, elem_bytes(a->dtype), true));
     size_t work = 0, keep = 0;
     scan_sizes(*a, &work, &keep, nullptr);
     TG_REQUIRE(aligned(workspace, 16) && aligned(saved, 16), TG_ERR_ALIGNMENT);
@@ -216,12 +223,12 @@ tg_status tg_selective_scan_backward(const tg_scan_args* a, const tg_scan_grads*
     TG_REQUIRE(g && g->dA && (!g->dz.p == !a->z.p), TG_ERR_INVALID_ARGUMENT);
     const size_t e = elem_bytes(a->dtype);
     const int64_t gn = (int64_t)a->G * a->N;
-    TG_CHECK(check_rows(g->dy, a->seqs, a->D, e, false));
-    TG_CHECK(check_rows(g->dx, a->seqs, a->D, e, true));
-    TG_CHECK(check_rows(g->ddt, a->seqs, a->D, e, true));
-    TG_CHECK(check_rows(g->dB, a->seqs, gn, e, true));
-    TG_CHECK(check_rows(g->dC, a->seqs, gn, e, true));
-    if (g->dz.p) TG_CHECK(check_rows(g->dz, a->seqs, a->D, e, true));
+    TG_CHECK(check_scan_rows(g->dy, a->seqs, a->D, e, false));
+    TG_CHECK(check_scan_rows(g->dx, a->seqs, a->D, e, true));
+    TG_CHECK(check_scan_rows(g->ddt, a->seqs, a->D, e, true));
+    TG_CHECK(check_scan_rows(g->dB, a->seqs, gn, e, true));
+    TG_CHECK(check_scan_rows(g->dC, a->seqs, gn, e, true));
+    if (g->dz.p) TG_CHECK(check_scan_rows(g->dz, a->seqs, a->D, e, true));
     TG_REQUIRE(aligned(g->dA, 4) && aligned(g->dD, 4) && aligned(g->ddt_bias, 4) &&
                    aligned(g->dfinal, 4) && aligned(g->dinitial, 4) && aligned(saved, 16) &&
                    aligned(workspace, 16), TG_ERR_ALIGNMENT);
@@ -242,7 +249,7 @@ tg_status tg_selective_scan_step(const tg_scan_args* a, float* state, int64_t nu
     tg_scan_args b = *a;
     for (tg_rows* r : {&b.x, &b.dt, &b.B, &b.C, &b.z, &b.y}) r->seq_stride = r->row_stride;
     TG_CHECK(check_scan_inputs(&b));
-    TG_CHECK(check_rows(b.y, b.seqs, b.D, elem_bytes(b.dtype), true));
+    TG_CHECK(check_scan_rows(b.y, b.seqs, b.D, elem_bytes(b.dtype), true));
     TG_REQUIRE((slots || a->seqs.seqs <= num_slots) && (state || num_slots == 0),
                TG_ERR_INVALID_ARGUMENT);
     TG_REQUIRE(num_slots < kMaxRows, TG_ERR_UNSUPPORTED);

@@ -26,8 +26,6 @@
 // kernel computes the parts' P and last states.
 //
 // Tokens past the end count as d = x = B = C = 0: a = 1, and the state stays.
-#include <type_traits>
-
 #include "seq_device.hpp"
 #include "seq_internal.hpp"
 #include "tg_internal.hpp"
@@ -38,9 +36,13 @@ namespace {
 constexpr int kCh = 16;  // channels of a wave
 constexpr float kLn2 = 0.69314718055994531f;
 
-// Tokens that a wave takes at a time: the decays of TT tokens and NS states
-// stay in registers.
+// Tokens that a wave takes at a time. The backward pass holds TT tokens'
+// decays and states (for NS = 4 two waves on a SIMD with 16 tokens; 8 tokens
+// and three waves took 5% longer, with the joins twice as often). The forward
+// pass holds decays only: 8 tokens leave room for four waves on a SIMD, which
+// took 203 us where two waves of 16 tokens took 241 (4 x 4096 tokens, 2048 channels, bf16).
 constexpr int chunk_for(int ns) { return ns <= 4 ? 16 : 64 / ns < 4 ? 4 : 64 / ns; }
+constexpr int fwd_chunk_for(int ns) { return ns <= 4 ? 8 : chunk_for(ns); }
 // Waves of a workgroup side by side: what they exchange (2*NS values for
 // each lane, in two buffers) stays within 64 KB of LDS.
 constexpr int waves_for(int ns) { return ns <= 8 ? 8 : 64 / ns; }
@@ -202,7 +204,9 @@ struct Place {
     int s, start, len, lo, hi, block, g, cl, q, ch, w;
     int64_t part0;  // the slot of the sequence's first part
     bool in;
-    __device__ __forceinline__ explicit Place(const ScanArgs& a) {
+    // by_rows: lane q*16 + channel (what the matrix instructions give), else
+    // lane channel*4 + q (what the sums over channels join best).
+    __device__ __forceinline__ Place(const ScanArgs& a, bool by_rows) {
         const SeqMap& m = a.seqs;
         const int tile = xcd_contiguous_tile(blockIdx.x, gridDim.x), nb = a.G * a.bpg;
         const int slot = tile / nb;
@@ -222,79 +226,116 @@ struct Place {
         g = block / a.bpg;
         const int c0 = (block - g * a.bpg) * kCh;
         w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        cl = (threadIdx.x & 63) >> 2;
-        q = threadIdx.x & 3;
+        const int lane = threadIdx.x & 63;
+        cl = by_rows ? lane & 15 : lane >> 2;
+        q = by_rows ? lane >> 4 : lane & 3;
         in = c0 + cl < a.Dg;
         ch = g * a.Dg + c0 + (in ? cl : 0);
     }
     __device__ __forceinline__ int part(int PL) const { return PL ? lo / PL : 0; }
 };
 
-// A tensor's rows of one sequence: uniform, and a row stride of 32 bits (the
-// host checks it), so that addresses are scalar plus a 32-bit lane offset.
-template <typename T>
+// A tensor's rows of one sequence. A chunk's rows are read and written through a
+// buffer descriptor that ends with the last token: what lies past it reads
+// as zero and is not written, so the tail of a sequence takes no branch. The host
+// keeps row strides below 2^25 elements, so that a chunk's offsets fit 31 bits.
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset past any chunk
 struct Col {
-    T* base;
-    int row;
+    char* base;
+    uint32_t row, width;  // bytes from row to row, bytes of a row
     template <typename P>
-    __device__ __forceinline__ Col(const Rows<P>& r, const SeqMap& m, const Place& p, int at = 0)
-        : base(row_of<T>(r, m, p.s, p.start, 0) + at), row((int)r.row) {}
-    __device__ __forceinline__ T* at(int l) const { return base + (int64_t)l * row; }
-};
-// Element `off` of a uniform address; the offset's bytes fit 32 bits.
-template <typename T>
-__device__ __forceinline__ T& elem(T* base, uint32_t off) {
-    typedef typename std::conditional<std::is_const<T>::value, const char, char>::type Byte;
-    return *(T*)((Byte*)base + off * (uint32_t)sizeof(T));
-}
-
-// The items of a lane in one tensor, as loaded: token q + 4*i of the chunk at
-// l, the lane's channel. Tokens past hi are not read.
-template <typename T, int TT>
-struct Items {
-    T v[TT / 4];
-    __device__ __forceinline__ void load(const Col<const T>& r, const Place& p, int l) {
-        const uint32_t off = (uint32_t)p.q * (uint32_t)r.row + (uint32_t)p.ch;
-        const T* const base = r.at(l);
-        const int64_t step = 4 * (int64_t)r.row;
-        if (l + TT <= p.hi) {
-#pragma unroll
-            for (int i = 0; i < TT / 4; ++i) v[i] = elem(base + i * step, off);
-        } else {
-#pragma unroll
-            for (int i = 0; i < TT / 4; ++i) {
-                v[i] = (T)0.0f;
-                if (l + p.q + 4 * i < p.hi) v[i] = elem(base + i * step, off);
-            }
-        }
+    __device__ __forceinline__ Col(const Rows<P>& r, const SeqMap& m, const Place& p, int elem,
+                                   int width_)
+        : base((char*)r.p + (m.offsets ? (int64_t)p.start * r.row : (int64_t)p.s * r.seq) * elem),
+          row((uint32_t)r.row * elem),
+          width((uint32_t)width_ * elem) {}
+    // Up to n rows from token l, not past hi.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(int l, int hi, int n) const {
+        const int have = imin(hi - l, n);
+        const uint32_t bytes = have > 0 ? (uint32_t)(have - 1) * row + width : 0;
+        return __builtin_amdgcn_make_buffer_rsrc(base + (int64_t)l * row, 0, bytes, 0x00027000);
     }
 };
+// An element as loaded, and its value.
 template <typename T>
-__device__ __forceinline__ void store_item(const Col<T>& r, const Place& p, int l, int i, float v) {
-    elem(r.at(l) + i * (4 * (int64_t)r.row), (uint32_t)p.q * (uint32_t)r.row + (uint32_t)p.ch) = (T)v;
+struct Raw {
+    typedef uint16_t type;
+};
+template <>
+struct Raw<float> {
+    typedef uint32_t type;
+};
+template <typename T>
+__device__ __forceinline__ typename Raw<T>::type buf_load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    if constexpr (sizeof(T) == 2) return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+}
+template <typename T>
+__device__ __forceinline__ float raw_value(typename Raw<T>::type v) {
+    return (float)__builtin_bit_cast(T, v);
+}
+template <typename T>
+__device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t r, uint32_t off, float v) {
+    const T t = (T)v;
+    const typename Raw<T>::type u = __builtin_bit_cast(typename Raw<T>::type, t);
+    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(u, r, off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(u, r, off, 0, 0);
+}
+
+// The items of a lane in one tensor: token q + 4*i of the chunk at l, the
+// lane's channel.
+template <typename T>
+__device__ __forceinline__ uint32_t item_offset(const Col& c, const Place& p) {
+    return p.in ? (uint32_t)p.q * c.row + (uint32_t)p.ch * (uint32_t)sizeof(T) : kNowhere;
+}
+// An offset that is added up where it is used: the compiler would keep every sum.
+__device__ __forceinline__ uint32_t here(uint32_t off) {
+    asm volatile("" : "+v"(off));
+    return off;
+}
+template <typename T, int TT>
+struct Items {
+    typename Raw<T>::type v[TT / 4];
+    __device__ __forceinline__ void load(const Col& c, const Place& p, int l) {
+        const __amdgpu_buffer_rsrc_t r = c.rows(l, p.hi, TT);
+        const uint32_t off = here(item_offset<T>(c, p));
+#pragma unroll
+        for (int i = 0; i < TT / 4; ++i) v[i] = buf_load<T>(r, off + i * (4 * c.row));
+    }
+    __device__ __forceinline__ float operator[](int i) const { return raw_value<T>(v[i]); }
+};
+template <typename T, int TT>
+__device__ __forceinline__ void store_items(const Col& c, const Place& p, int l,
+                                            const float (&v)[TT / 4]) {
+    const __amdgpu_buffer_rsrc_t r = c.rows(l, p.hi, TT);
+    const uint32_t off = here(item_offset<T>(c, p));
+#pragma unroll
+    for (int i = 0; i < TT / 4; ++i) buf_store<T>(r, off + i * (4 * c.row), v[i]);
 }
 
 // A wave's share of TT tokens' B or C: element lane + 64*k of [TT][4*NS].
 template <typename T, int NS, int TT>
 struct Shared {
     static constexpr int kN = 4 * NS, kPer = TT * kN / 64;
-    T v[kPer];
-    __device__ __forceinline__ void load(const Col<const T>& r, const Place& p, int N, int l) {
+    typename Raw<T>::type v[kPer];
+    __device__ __forceinline__ void load(const Col& c, const Place& p, int N, int l) {
+        const __amdgpu_buffer_rsrc_t r = c.rows(l, p.hi, TT);
         const int lane = threadIdx.x & 63;
-        const T* const base = r.at(l);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             // Rows k*64/kN (the same for all lanes) and lane/kN (for short rows).
             const int t0 = k * 64 / kN, t = kN < 64 ? lane / kN : 0;
             const int n = kN < 64 ? lane % kN : (k * 64 % kN) + lane;
-            v[k] = (T)0.0f;
-            if (n < N && l + t0 + t < p.hi)
-                v[k] = elem(base + t0 * (int64_t)r.row, (uint32_t)t * (uint32_t)r.row + (uint32_t)n);
+            const uint32_t off = n < N ? (uint32_t)t * c.row +
+                                             (uint32_t)(p.g * N + n) * (uint32_t)sizeof(T)
+                                       : kNowhere;
+            v[k] = buf_load<T>(r, here(off) + t0 * c.row);
         }
     }
     __device__ __forceinline__ void put(float (&to)[TT][kN]) const {
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) (&to[0][0])[k * 64 + (threadIdx.x & 63)] = (float)v[k];
+        for (int k = 0; k < kPer; ++k)
+            (&to[0][0])[k * 64 + (threadIdx.x & 63)] = raw_value<T>(v[k]);
     }
 };
 
@@ -305,32 +346,39 @@ __device__ __forceinline__ float* exchange_at(float* ex, int w, int which) {
     return ex + ((w * 2 + which) * 64 + (threadIdx.x & 63)) * NS;
 }
 
+// State j of a lane, with lanes by rows: the rows of a 16 x 16 matrix that the
+// lane holds, 4q to 4q+3 (with NS < 4 only NS of them are used).
+template <int NS, bool ROWS>
+__device__ __forceinline__ int state_of(int q, int j) {
+    return !ROWS || NS < 4 ? q * NS + j : (j & ~3) * 4 + q * 4 + (j & 3);
+}
+
 // log2(a) = d * A2 of the lane's states, zero past N and for lanes without a
 // channel.
-template <int NS>
+template <int NS, bool ROWS>
 __device__ __forceinline__ void load_A2(const ScanArgs& a, const Place& p, float (&A2)[NS]) {
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-        const int n = p.q * NS + j;
+        const int n = state_of<NS, ROWS>(p.q, j);
         A2[j] = p.in && n < a.N ? a.A[(int64_t)p.ch * a.N + n] * kLog2e : 0.0f;
     }
 }
-template <int NS>
+template <int NS, bool ROWS>
 __device__ __forceinline__ void load_state(const float* st, const ScanArgs& a, const Place& p,
                                            float (&h)[NS]) {
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-        const int n = p.q * NS + j;
+        const int n = state_of<NS, ROWS>(p.q, j);
         h[j] = st && p.in && n < a.N ? st[((int64_t)p.s * a.D + p.ch) * a.N + n] : 0.0f;
     }
 }
-template <int NS>
+template <int NS, bool ROWS>
 __device__ __forceinline__ void store_state(float* st, const ScanArgs& a, const Place& p,
                                             const float (&h)[NS]) {
     if (!st || !p.in) return;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-        const int n = p.q * NS + j;
+        const int n = state_of<NS, ROWS>(p.q, j);
         if (n < a.N) st[((int64_t)p.s * a.D + p.ch) * a.N + n] = h[j];
     }
 }
@@ -343,18 +391,88 @@ __device__ __forceinline__ float step_size(const ScanArgs& a, float raw) {
     return a.softplus ? softplus_f32(raw) : raw;
 }
 
+// The forward kernels have lanes by rows: lane q*16 + c holds channel c and states
+// 4q .. 4q+3 (and the same of each further 16). That is how
+// v_mfma_f32_16x16x1_4b_f32 leaves four 16 x 16 outer products, one for each of four tokens:
+// (d*x)[c] * B[n] of four tokens and four states comes from one matrix
+// instruction (exact fp32 products), beside the vector units, with operands as the lanes loaded
+// them: lane (token, channel) its own item's d*x, and lane (token, n) B. C in
+// every lane that needs it is the product with ones.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+constexpr int blocks_of(int ns) { return ns <= 4 ? 1 : ns / 4; }  // of 16 states
+
+// A lane's elements of B or C: token 4*g + (lane >> 4), state row lane & 15 of
+// each block of 16 (zero where that is no state).
+template <typename T, int NS, int TT>
+struct RowVals {
+    typename Raw<T>::type v[TT / 4][blocks_of(NS)];
+    __device__ __forceinline__ void load(const Col& c, const Place& p, int N, int l) {
+        const __amdgpu_buffer_rsrc_t r = c.rows(l, p.hi, TT);
+        const int row = threadIdx.x & 15;
+        const int n = NS >= 4 ? row : (row >> 2) * NS + (row & 3);
+#pragma unroll
+        for (int m = 0; m < blocks_of(NS); ++m) {
+            const bool in = n + 16 * m < N && (NS >= 4 || (row & 3) < NS);
+            const uint32_t off = in ? (uint32_t)p.q * c.row +
+                                          (uint32_t)(p.g * N + n + 16 * m) * (uint32_t)sizeof(T)
+                                    : kNowhere;
+            const uint32_t o = here(off);
+#pragma unroll
+            for (int g = 0; g < TT / 4; ++g) v[g][m] = buf_load<T>(r, o + g * (4 * c.row));
+        }
+    }
+    // out[token][j]: value of tokens 4*g to 4*g+3 times x (a lane's item of
+    // token 4*g + q, or one) for the lane's states.
+    __device__ __forceinline__ void outer(int g, float x, float (&out)[4][NS]) const {
+        const f32x16 zero = {};
+#pragma unroll
+        for (int m = 0; m < blocks_of(NS); ++m) {
+            const f32x16 d =
+                __builtin_amdgcn_mfma_f32_16x16x1f32(raw_value<T>(v[g][m]), x, zero, 0, 0, 0);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4 && j < NS; ++j) out[t][4 * m + j] = d[4 * t + j];
+        }
+    }
+};
+
+// The step sizes of a wave's tokens, for all lanes of a channel.
+template <int TT>
+struct alignas(16) Steps {
+    float d[kCh][TT + 4];
+};
+
+// The sums of y[0..3] over the 4 lanes of a channel, token q's in lane q.
+__device__ __forceinline__ float row_sums(const float (&y)[4], int lane) {
+    return join<4>(join<5>(y[0], y[2], lane), join<5>(y[1], y[3], lane), lane);
+}
+
+// Run body(g) over the groups of 4 tokens, in order, without moving work
+// from one to another: otherwise all groups' products are held at once.
+template <int TT, typename Body>
+__device__ __forceinline__ void for_groups(Body body) {
+#pragma unroll
+    for (int g = 0; g < TT / 4; ++g) {
+        body(g);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 template <typename T, int NS, int TT, bool SPLIT>
-__global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_fwd(const ScanArgs a) {
+__global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64)
+    __attribute__((amdgpu_waves_per_eu(NS <= 4 ? 4 : 1))) void scan_fwd(const ScanArgs a) {
     constexpr int kItems = TT / 4;
     extern __shared__ float4 lds[];
     const int W = SPLIT ? blockDim.x >> 6 : 1;
-    const Place p(a);
+    const Place p(a, true);
     if (p.lo < 0) return;
-    Tile<NS, TT>& tile = ((Tile<NS, TT>*)lds)[p.w];
-    float* const exchange = (float*)((Tile<NS, TT>*)lds + W);
+    const int lane = threadIdx.x & 63;
+    Steps<TT>& steps = ((Steps<TT>*)lds)[p.w];
+    float* const exchange = (float*)((Steps<TT>*)lds + W);
     float A2[NS], h[NS];
-    load_A2<NS>(a, p, A2);
-    load_state<NS>(a.initial, a, p, h);
+    load_A2<NS, true>(a, p, A2);
+    load_state<NS, true>(a.initial, a, p, h);
     for (int k = 0; k < p.part(a.PL); ++k) {
         float P[NS], e[NS];
         get<NS>(part_at<NS>(a, p, k, 0), P);
@@ -364,12 +482,12 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_fwd(cons
     }
     const float skip = a.D_skip ? a.D_skip[p.ch] : 0.0f;
     const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
-    int64_t slot = a.seqs.slot0(p.s, TT) + p.lo / TT + p.w;
-    const Col<const T> cx(a.x, a.seqs, p), cdt(a.dt, a.seqs, p), cz(a.z, a.seqs, p),
-        cB(a.B, a.seqs, p, p.g * a.N), cC(a.C, a.seqs, p, p.g * a.N);
-    const Col<T> cy(a.y, a.seqs, p);
+    constexpr int E = sizeof(T);
+    const Col cx(a.x, a.seqs, p, E, a.D), cdt(a.dt, a.seqs, p, E, a.D), cz(a.z, a.seqs, p, E, a.D),
+        cB(a.B, a.seqs, p, E, a.G * a.N), cC(a.C, a.seqs, p, E, a.G * a.N),
+        cy(a.y, a.seqs, p, E, a.D);
     Items<T, TT> rx, rdt, rz;
-    Shared<T, NS, TT> rB, rC;
+    RowVals<T, NS, TT> rB, rC;
     const auto fetch = [&](int l) {
         rx.load(cx, p, l);
         rdt.load(cdt, p, l);
@@ -377,40 +495,54 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_fwd(cons
         rB.load(cB, p, a.N, l);
         rC.load(cC, p, a.N, l);
     };
+    // The state at the start of a wave's tokens, for the backward pass.
+    const auto save = [&](int l, const float (&r)[NS]) {
+        constexpr int every = chunk_for(NS);
+        if (!a.saved || !p.in || l >= p.hi || l % every) return;
+        float* const to =
+            a.saved + ((a.seqs.slot0(p.s, every) + (int64_t)(l / every)) * a.D + p.ch) * (4 * NS);
+        constexpr int V = NS < 4 ? NS : 4;
+#pragma unroll
+        for (int j = 0; j < NS; j += V)
+            store_f32<float, V>(to + state_of<NS, true>(p.q, j), *(const float (*)[V])(r + j));
+    };
     int flip = 0;
     if (p.lo < p.hi) fetch(p.lo + p.w * TT);
-    for (int l0 = p.lo; l0 < p.hi; l0 += W * TT, slot += W) {
+    for (int l0 = p.lo; l0 < p.hi; l0 += W * TT) {
         const int l = l0 + p.w * TT;
-        float x[kItems], z[kItems], v[kItems];
+        float x[kItems], u[kItems], z[kItems], v[kItems];
+        RowVals<T, NS, TT> tB = rB, tC = rC;
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const int t = p.q + 4 * i;
-            x[i] = (float)rx.v[i];
-            z[i] = a.z.p ? (float)rz.v[i] : 0.0f;
-            const float d = l + t < p.hi ? step_size(a, (float)rdt.v[i] + bias) : 0.0f;
-            tile.d[t][p.cl] = make_float2(d, d * x[i]);
+            x[i] = rx[i];
+            z[i] = a.z.p ? rz[i] : 0.0f;
+            float d = step_size(a, rdt[i] + bias);
+            if (l + TT > p.hi) d = l + p.q + 4 * i < p.hi ? d : 0.0f;
+            u[i] = d * x[i];
+            steps.d[p.cl][4 * i + p.q] = d;
         }
-        rB.put(tile.B);
-        rC.put(tile.C);
         wave_sync();
         // The next tokens arrive while these are computed.
         if (l0 + W * TT < p.hi) fetch(l + W * TT);
         if constexpr (SPLIT) {
-            float dec[TT][NS], e[NS], y[TT], sum = 0.0f;
+            float dec[TT][NS], e[NS], sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < NS; ++j) e[j] = 0.0f;
-            for_tokens<NS, TT, true, true, true>(tile, p.cl, p.q, [&](int t, const Token<NS>& k) {
-                sum += k.d.x;
-                y[t] = 0.0f;
+            for_groups<TT>([&](int g) {
+                float d[4], b[4][NS];
+                load_f32<float, 4>(&steps.d[p.cl][4 * g], d);
+                tB.outer(g, u[g], b);
 #pragma unroll
-                for (int j = 0; j < NS; ++j) {
-                    dec[t][j] = __builtin_amdgcn_exp2f(k.d.x * A2[j]);
-                    e[j] = __builtin_fmaf(dec[t][j], e[j], k.d.y * k.B[j]);
-                    y[t] = __builtin_fmaf(e[j], k.C[j], y[t]);
+                for (int t = 0; t < 4; ++t) {
+                    sum += d[t];
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) {
+                        dec[4 * g + t][j] = __builtin_amdgcn_exp2f(d[t] * A2[j]);
+                        e[j] = __builtin_fmaf(dec[4 * g + t][j], e[j], b[t][j]);
+                    }
                 }
-                pin(y[t]);
             });
-            float P[NS];
+            float P[NS], r[NS];
 #pragma unroll
             for (int j = 0; j < NS; ++j) P[j] = __builtin_amdgcn_exp2f(sum * A2[j]);
             float* const ex = exchange + flip * (W * 128 * NS);
@@ -420,7 +552,6 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_fwd(cons
             __syncthreads();
             // The other buffer is written next, past this barrier of the next
             // round: nobody still reads it then.
-            float r[NS];
             for (int k = 0; k < W; ++k) {
                 if (k == p.w)
 #pragma unroll
@@ -430,49 +561,53 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_fwd(cons
 #pragma unroll
                 for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(P[j], h[j], e[j]);
             }
-            if (a.saved && p.in && l < p.hi)
-                put<NS>(a.saved + (slot * a.D + p.ch) * (4 * NS) + p.q * NS, r);
-            // What the state before the segment adds: it decays, token by token.
-            for_tokens<NS, TT, false, true, true>(tile, p.cl, p.q, [&](int t, const Token<NS>& k) {
+            save(l, r);
+            // The second run, from the true state. Its products d*x*B are made
+            // again: holding them would take as many registers as the decays.
+            for_groups<TT>([&](int g) {
+                float b[4][NS], C[4][NS], y[4];
+                tB.outer(g, u[g], b);
+                tC.outer(g, 1.0f, C);
 #pragma unroll
-                for (int j = 0; j < NS; ++j) {
-                    r[j] *= dec[t][j];
-                    y[t] = __builtin_fmaf(r[j], k.C[j], y[t]);
+                for (int t = 0; t < 4; ++t) {
+                    y[t] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) {
+                        r[j] = __builtin_fmaf(dec[4 * g + t][j], r[j], b[t][j]);
+                        y[t] = __builtin_fmaf(r[j], C[t][j], y[t]);
+                    }
                 }
-                pin(y[t]);
+                v[g] = row_sums(y, lane);
             });
-#pragma unroll
-            for (int i = 0; i < kItems; ++i)
-                v[i] = quad_sums(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3], p.q);
         } else {
-            if (a.saved && p.in) put<NS>(a.saved + (slot * a.D + p.ch) * (4 * NS) + p.q * NS, h);
-            float y[4];
-            for_tokens<NS, TT, true, true, true>(tile, p.cl, p.q, [&](int t, const Token<NS>& k) {
-                float s = 0.0f;
+            save(l, h);
+            for_groups<TT>([&](int g) {
+                float d[4], b[4][NS], C[4][NS], y[4];
+                load_f32<float, 4>(&steps.d[p.cl][4 * g], d);
+                tB.outer(g, u[g], b);
+                tC.outer(g, 1.0f, C);
 #pragma unroll
-                for (int j = 0; j < NS; ++j) {
-                    const float e = __builtin_amdgcn_exp2f(k.d.x * A2[j]);
-                    h[j] = __builtin_fmaf(e, h[j], k.d.y * k.B[j]);
-                    s = __builtin_fmaf(h[j], k.C[j], s);
+                for (int t = 0; t < 4; ++t) {
+                    y[t] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) {
+                        const float e = __builtin_amdgcn_exp2f(d[t] * A2[j]);
+                        h[j] = __builtin_fmaf(e, h[j], b[t][j]);
+                        y[t] = __builtin_fmaf(h[j], C[t][j], y[t]);
+                    }
                 }
-                y[t & 3] = s;
-                pin(y[t & 3]);
-                if ((t & 3) == 3) {
-                    v[t >> 2] = quad_sums(y[0], y[1], y[2], y[3], p.q);
-                    pin(v[t >> 2]);
-                }
+                v[g] = row_sums(y, lane);
             });
         }
 #pragma unroll
-        for (int i = 0; i < kItems; ++i)
-            if (l + p.q + 4 * i < p.hi && p.in) {
-                float o = __builtin_fmaf(skip, x[i], v[i]);
-                if (a.z.p) o *= silu_f32(z[i]);
-                store_item(cy, p, l, i, o);
-            }
+        for (int i = 0; i < kItems; ++i) {
+            v[i] = __builtin_fmaf(skip, x[i], v[i]);
+            if (a.z.p) v[i] *= silu_f32(z[i]);
+        }
+        store_items<T, TT>(cy, p, l, v);
         wave_sync();
     }
-    if (p.w == 0 && p.hi == p.len) store_state<NS>(a.final, a, p, h);
+    if (p.w == 0 && p.hi == p.len) store_state<NS, true>(a.final, a, p, h);
 }
 
 // The parts' decays and last states from zero, for all parts but a sequence's
@@ -481,19 +616,21 @@ template <typename T, int NS, int TT>
 __global__ __launch_bounds__(64 * waves_for(NS)) void scan_parts(const ScanArgs a) {
     extern __shared__ float4 lds[];
     const int W = blockDim.x >> 6;
-    const Place p(a);
+    const Place p(a, true);
     if (p.lo < 0 || p.hi == p.len) return;
-    Tile<NS, TT>& tile = ((Tile<NS, TT>*)lds)[p.w];
-    float* const ex = (float*)((Tile<NS, TT>*)lds + W);
+    Steps<TT>& steps = ((Steps<TT>*)lds)[p.w];
+    float* const ex = (float*)((Steps<TT>*)lds + W);
     float A2[NS], h[NS], sum = 0.0f;
-    load_A2<NS>(a, p, A2);
+    load_A2<NS, true>(a, p, A2);
 #pragma unroll
     for (int j = 0; j < NS; ++j) h[j] = 0.0f;
     const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
     const int run = a.PL / W;  // PL is a multiple of W * TT
-    const Col<const T> cx(a.x, a.seqs, p), cdt(a.dt, a.seqs, p), cB(a.B, a.seqs, p, p.g * a.N);
+    constexpr int E = sizeof(T);
+    const Col cx(a.x, a.seqs, p, E, a.D), cdt(a.dt, a.seqs, p, E, a.D),
+        cB(a.B, a.seqs, p, E, a.G * a.N);
     Items<T, TT> rx, rdt;
-    Shared<T, NS, TT> rB;
+    RowVals<T, NS, TT> rB;
     const auto fetch = [&](int l) {
         rx.load(cx, p, l);
         rdt.load(cdt, p, l);
@@ -502,19 +639,27 @@ __global__ __launch_bounds__(64 * waves_for(NS)) void scan_parts(const ScanArgs 
     const int first = p.lo + p.w * run;
     fetch(first);
     for (int l = first; l < first + run; l += TT) {
+        float u[TT / 4];
+        RowVals<T, NS, TT> tB = rB;
 #pragma unroll
         for (int i = 0; i < TT / 4; ++i) {
-            const float d = step_size(a, (float)rdt.v[i] + bias);
-            tile.d[p.q + 4 * i][p.cl] = make_float2(d, d * (float)rx.v[i]);
+            const float d = step_size(a, rdt[i] + bias);
+            u[i] = d * rx[i];
+            steps.d[p.cl][4 * i + p.q] = d;
         }
-        rB.put(tile.B);
         wave_sync();
         if (l + TT < first + run) fetch(l + TT);
-        for_tokens<NS, TT, true, false, true>(tile, p.cl, p.q, [&](int, const Token<NS>& k) {
-            sum += k.d.x;
+        for_groups<TT>([&](int g) {
+            float d[4], b[4][NS];
+            load_f32<float, 4>(&steps.d[p.cl][4 * g], d);
+            tB.outer(g, u[g], b);
 #pragma unroll
-            for (int j = 0; j < NS; ++j)
-                h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(k.d.x * A2[j]), h[j], k.d.y * k.B[j]);
+            for (int t = 0; t < 4; ++t) {
+                sum += d[t];
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[t] * A2[j]), h[j], b[t][j]);
+            }
         });
         wave_sync();
     }
@@ -562,15 +707,15 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
     constexpr int kItems = TT / 4, kHeld = NS >> levels_of(NS), GT = NS < 16 ? 16 / NS : 1;
     extern __shared__ float4 lds[];
     const int W = SPLIT ? blockDim.x >> 6 : 1;
-    const Place p(a);
+    const Place p(a, false);
     if (p.lo < 0) return;
     BackTile<NS, TT>& both = ((BackTile<NS, TT>*)lds)[p.w];
     Tile<NS, TT>& tile = both.f;
     float* const exchange = (float*)((BackTile<NS, TT>*)lds + W);
     const int lane = threadIdx.x & 63;
     float A2[NS], carry[NS], dA[NS], lost[NS];
-    load_A2<NS>(a, p, A2);
-    load_state<NS>(b.dfinal, a, p, carry);
+    load_A2<NS, false>(a, p, A2);
+    load_state<NS, false>(b.dfinal, a, p, carry);
     if (a.PL)
         for (int k = (p.len - 1) / a.PL; k > p.part(a.PL); --k) {
             float P[NS], e[NS];
@@ -585,9 +730,11 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
     const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
     float dD = 0.0f, dbias = 0.0f;
     const int64_t slot0 = a.seqs.slot0(p.s, TT);
-    const Col<const T> cx(a.x, a.seqs, p), cdt(a.dt, a.seqs, p), cz(a.z, a.seqs, p),
-        cdy(b.dy, a.seqs, p), cB(a.B, a.seqs, p, p.g * a.N), cC(a.C, a.seqs, p, p.g * a.N);
-    const Col<T> cdx(b.dx, a.seqs, p), cddt(b.ddt, a.seqs, p), cdz(b.dz, a.seqs, p);
+    constexpr int E = sizeof(T);
+    const Col cx(a.x, a.seqs, p, E, a.D), cdt(a.dt, a.seqs, p, E, a.D), cz(a.z, a.seqs, p, E, a.D),
+        cdy(b.dy, a.seqs, p, E, a.D), cB(a.B, a.seqs, p, E, a.G * a.N),
+        cC(a.C, a.seqs, p, E, a.G * a.N), cdx(b.dx, a.seqs, p, E, a.D),
+        cddt(b.ddt, a.seqs, p, E, a.D), cdz(b.dz, a.seqs, p, E, a.D);
     Items<T, TT> rx, rdt, rz, rdy;
     Shared<T, NS, TT> rB, rC;
     const auto fetch = [&](int l) {
@@ -611,11 +758,10 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
             const int t = p.q + 4 * i;
-            const float x = (float)rx.v[i], raw = (float)rdt.v[i] + bias;
-            const float d = l + t < p.hi ? step_size(a, raw) : 0.0f;
-            const float z = a.z.p ? (float)rz.v[i] : 0.0f;
-            const float dout = p.in ? (float)rdy.v[i] : 0.0f;
-            tile.d[t][p.cl] = make_float2(d, p.in ? d * x : 0.0f);
+            const float x = rx[i], raw = rdt[i] + bias, z = a.z.p ? rz[i] : 0.0f, dout = rdy[i];
+            float d = step_size(a, raw);
+            if (l + TT > p.hi) d = l + t < p.hi ? d : 0.0f;
+            tile.d[t][p.cl] = make_float2(d, d * x);
             both.dv[t][p.cl] = a.z.p ? dout * silu_f32(z) : dout;
             both.item[i][lane] = make_float4(x, raw, z, dout);
         }
@@ -738,25 +884,26 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
             dA[j] = s;
             if (!SPLIT) carry[j] = c[j];
         }
+        float dt[kItems], dx[kItems], dz[kItems];
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
             const int t = p.q + 4 * i;
-            if (l + t < p.hi && p.in) {
-                const float4 it = both.item[i][lane];  // x, dt + bias, z, dy
-                const float dv = both.dv[t][p.cl];
-                float ddl = __builtin_fmaf(e2[i], it.x, e1[i] * kLn2);
-                if (a.softplus) ddl *= sigmoid_f32(it.y);
-                store_item(cddt, p, l, i, ddl);
-                store_item(cdx, p, l, i, __builtin_fmaf(e2[i], tile.d[t][p.cl].x, skip * dv));
-                if (a.z.p) {
-                    const float sg = sigmoid_f32(it.z), y = __builtin_fmaf(skip, it.x, v[i]);
-                    store_item(cdz, p, l, i,
-                               it.w * y * sg * __builtin_fmaf(it.z, 1.0f - sg, 1.0f));
-                }
-                dbias += ddl;
-                dD = __builtin_fmaf(dv, it.x, dD);
-            }
+            const float4 it = both.item[i][lane];  // x, dt + bias, z, dy
+            const float dv = both.dv[t][p.cl];
+            dt[i] = __builtin_fmaf(e2[i], it.x, e1[i] * kLn2);
+            if (a.softplus) dt[i] *= sigmoid_f32(it.y);
+            dx[i] = __builtin_fmaf(e2[i], tile.d[t][p.cl].x, skip * dv);
+            const float sg = sigmoid_f32(it.z), y = __builtin_fmaf(skip, it.x, v[i]);
+            dz[i] = it.w * y * sg * __builtin_fmaf(it.z, 1.0f - sg, 1.0f);
+            // Past the end the state and its adjoint only pass through, but their
+            // product is not zero.
+            if (l + TT > p.hi) dt[i] = l + t < p.hi ? dt[i] : 0.0f;
+            dbias += dt[i];
+            dD = __builtin_fmaf(dv, it.x, dD);
         }
+        store_items<T, TT>(cddt, p, l, dt);
+        store_items<T, TT>(cdx, p, l, dx);
+        if (a.z.p) store_items<T, TT>(cdz, p, l, dz);
         wave_sync();
     }
     dD = quad_sum(dD);
@@ -787,7 +934,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
         const int n = p.q * NS + j;
         if (n < a.N) b.part_a[(out * a.D + p.ch) * a.N + n] = dA[j];
     }
-    if (p.lo == 0) store_state<NS>(b.dinitial, a, p, carry);
+    if (p.lo == 0) store_state<NS, false>(b.dinitial, a, p, carry);
 }
 
 // What the parts but a sequence's first pass to the tokens before them, from
@@ -797,18 +944,19 @@ __global__ __launch_bounds__(64 * waves_for(NS)) void scan_bwd_parts(const ScanA
                                                                      const ScanGrads b) {
     extern __shared__ float4 lds[];
     const int W = blockDim.x >> 6;
-    const Place p(a);
+    const Place p(a, false);
     if (p.lo <= 0) return;
     Tile<NS, TT>& tile = ((Tile<NS, TT>*)lds)[p.w];
     float* const ex = (float*)((Tile<NS, TT>*)lds + W);
     float A2[NS], c[NS], sum = 0.0f;
-    load_A2<NS>(a, p, A2);
+    load_A2<NS, false>(a, p, A2);
 #pragma unroll
     for (int j = 0; j < NS; ++j) c[j] = 0.0f;
     const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
     const int run = a.PL / W;
-    const Col<const T> cdt(a.dt, a.seqs, p), cz(a.z, a.seqs, p), cdy(b.dy, a.seqs, p),
-        cC(a.C, a.seqs, p, p.g * a.N);
+    constexpr int E = sizeof(T);
+    const Col cdt(a.dt, a.seqs, p, E, a.D), cz(a.z, a.seqs, p, E, a.D),
+        cdy(b.dy, a.seqs, p, E, a.D), cC(a.C, a.seqs, p, E, a.G * a.N);
     Items<T, TT> rdt, rz, rdy;
     Shared<T, NS, TT> rC;
     const auto fetch = [&](int l) {
@@ -823,9 +971,10 @@ __global__ __launch_bounds__(64 * waves_for(NS)) void scan_bwd_parts(const ScanA
 #pragma unroll
         for (int i = 0; i < TT / 4; ++i) {
             const int t = p.q + 4 * i;
-            const float d = l + t < p.hi ? step_size(a, (float)rdt.v[i] + bias) : 0.0f;
-            const float dy = (float)rdy.v[i];
-            tile.d[t][p.cl] = make_float2(d, a.z.p ? dy * silu_f32((float)rz.v[i]) : dy);
+            float d = step_size(a, rdt[i] + bias);
+            if (l + TT > p.hi) d = l + t < p.hi ? d : 0.0f;
+            const float dy = rdy[i];
+            tile.d[t][p.cl] = make_float2(d, a.z.p ? dy * silu_f32(rz[i]) : dy);
         }
         rC.put(tile.C);
         wave_sync();
@@ -858,23 +1007,33 @@ __global__ __launch_bounds__(64 * waves_for(NS)) void scan_bwd_parts(const ScanA
 }
 
 // dB and dC of the rows that the sequences cover: sums over a group's blocks
-// of channels.
+// of channels, each by kPhases threads.
+constexpr int kPhases = 4;
 template <typename T>
-__global__ __launch_bounds__(256) void scan_bc_sums(const ScanArgs a, const float* part, int NP,
-                                                    Rows<void> dB, Rows<void> dC) {
+__global__ __launch_bounds__(64 * kPhases) void scan_bc_sums(const ScanArgs a, const float* part,
+                                                             int NP, Rows<void> dB, Rows<void> dC) {
+    __shared__ float red[kPhases][64];
     const SeqMap& m = a.seqs;
+    const int lane = threadIdx.x & 63, ph = threadIdx.x >> 6;
     const int64_t per = (int64_t)a.G * 2 * NP, last = m.end(m.seqs - 1) * per;
-    for (int64_t i = m.start(0) * per + (int64_t)blockIdx.x * 256 + threadIdx.x; i < last;
-         i += (int64_t)gridDim.x * 256) {
-        const int row = (int)(i / per), r = (int)(i - row * per);
-        const int g = r / (2 * NP), k = r - g * 2 * NP, c = k / NP, n = k - c * NP;
-        if (n >= a.N) continue;
-        float v = 0.0f;
-        for (int blk = 0; blk < a.bpg; ++blk)
-            v += part[(((int64_t)(g * a.bpg + blk) * m.rows + row) * 2 + c) * NP + n];
-        const int s = m.offsets ? 0 : row / m.L;
-        row_of<T>(c ? dC : dB, m, s, 0, m.offsets ? row : row - s * m.L)[g * a.N + n] = (T)v;
+    const int64_t i = m.start(0) * per + (int64_t)blockIdx.x * 64 + lane;
+    const int row = (int)(i / per), r = (int)(i - row * per);
+    const int g = r / (2 * NP), k = r - g * 2 * NP, c = k / NP, n = k - c * NP;
+    const bool in = i < last && n < a.N;
+    float v = 0.0f;
+    if (in) {
+        const float* p = part + (((int64_t)g * a.bpg * m.rows + row) * 2 + c) * NP + n;
+        const int64_t step = (int64_t)m.rows * 2 * NP;
+#pragma unroll 8
+        for (int blk = ph; blk < a.bpg; blk += kPhases) v += p[blk * step];
     }
+    red[ph][lane] = v;
+    __syncthreads();
+    if (ph != 0 || !in) return;
+#pragma unroll
+    for (int j = 1; j < kPhases; ++j) v += red[j][lane];
+    const int s = m.offsets ? 0 : row / m.L;
+    row_of<T>(c ? dC : dB, m, s, 0, m.offsets ? row : row - s * m.L)[g * a.N + n] = (T)v;
 }
 
 struct StepArgs {
@@ -948,11 +1107,11 @@ Plan plan_of(const tg_scan_args& a) {
     p.waves = groups >= 4096 ? 1 : waves_for(p.ns);
     p.PL = 0;
     p.slots = a.seqs.seqs;
-    // Fewer than four waves for each compute unit: parts of the sequences, so
-    // many that there would be eight, and not shorter than two rounds of a workgroup.
-    if (p.waves > 1 && groups * p.waves < 1024) {
+    // Fewer than eight waves for each compute unit: parts of the sequences, so
+    // many that there would be sixteen, and not shorter than two rounds of a workgroup.
+    if (p.waves > 1 && groups * p.waves < 2048) {
         const int64_t round = (int64_t)p.waves * p.tt;
-        int64_t pl = a.seqs.rows * p.nb * p.waves / 2048 / round * round;
+        int64_t pl = a.seqs.rows * p.nb * p.waves / 4096 / round * round;
         if (pl < 2 * round) pl = 2 * round;
         const int64_t longest = a.seqs.offsets ? a.seqs.rows : a.seqs.rows / a.seqs.seqs;
         if (pl < longest) {
@@ -1005,8 +1164,8 @@ hipError_t launch_waves(Kernel kernel, const Plan& p, size_t tile, int buffers, 
 
 template <typename T, int NS>
 hipError_t fwd_typed(const Plan& p, const ScanArgs& f, hipStream_t st) {
-    constexpr int TT = chunk_for(NS);
-    constexpr size_t tile = sizeof(Tile<NS, TT>);
+    constexpr int TT = fwd_chunk_for(NS);
+    constexpr size_t tile = sizeof(Steps<TT>);
     if (p.PL) {
         const hipError_t e = launch_waves(scan_parts<T, NS, TT>, p, tile, 1, st, f);
         if (e != hipSuccess) return e;
@@ -1096,12 +1255,12 @@ hipError_t launch_scan_backward(const tg_scan_args& a, const tg_scan_grads& g, c
     if (e != hipSuccess) return e;
     if (a.seqs.rows > 0) {
         const int np = 4 * p.ns;
-        const int64_t need = ceil_div(a.seqs.rows * a.G * 2 * np, 256);
-        const unsigned sums = (unsigned)(need < 4096 ? need : 4096);
+        const unsigned sums = (unsigned)ceil_div(a.seqs.rows * a.G * 2 * np, 64);
+        constexpr int threads = 64 * kPhases;
         const Rows<void> dB = rows_of<void>(g.dB), dC = rows_of<void>(g.dC);
-        if (dtype == TG_F32) scan_bc_sums<float><<<sums, 256, 0, st>>>(f, b.part_bc, np, dB, dC);
-        else if (dtype == TG_BF16) scan_bc_sums<bf16><<<sums, 256, 0, st>>>(f, b.part_bc, np, dB, dC);
-        else scan_bc_sums<f16><<<sums, 256, 0, st>>>(f, b.part_bc, np, dB, dC);
+        if (dtype == TG_F32) scan_bc_sums<float><<<sums, threads, 0, st>>>(f, b.part_bc, np, dB, dC);
+        else if (dtype == TG_BF16) scan_bc_sums<bf16><<<sums, threads, 0, st>>>(f, b.part_bc, np, dB, dC);
+        else scan_bc_sums<f16><<<sums, threads, 0, st>>>(f, b.part_bc, np, dB, dC);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

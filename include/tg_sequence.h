@@ -138,7 +138,8 @@ tg_status tg_causal_conv_step(const void *x, int64_t x_stride, void *state, int6
  * B and C are shared by the D/G channels of a group g = c / (D/G); a row of
  * B or C is [G][N], contiguous. A fp32 [D][N]; D_skip, dt_bias fp32 [D] or
  * NULL; initial, final fp32 [seqs][D][N] or NULL; final may alias initial
- * only if it is the same buffer. */
+ * only if it is the same buffer. Row strides here stay below 2^25 elements
+ * (else TG_ERR_UNSUPPORTED). */
 typedef struct {
     tg_seqs seqs;
     int D, N, G;
