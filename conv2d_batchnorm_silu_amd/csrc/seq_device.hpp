@@ -119,14 +119,22 @@ Rows<P> rows_of(const tg_rows& r) {
 // drop u's bits. log(1 + u) = 2 atanh(s) with s = u / (2 + u) <= 1/3, and
 // atanh(s) / s as a polynomial in s^2 <= 1/9 through the function's values at the
 // five Chebyshev points there (off by at most 2^-27).
-__device__ __forceinline__ float softplus_f32(float v) {
-    const float u = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e);
+__device__ __forceinline__ float softplus_from(float v, float u) {
     const float s = u * __builtin_amdgcn_rcpf(2.0f + u), q = s * s;
     float r = __builtin_fmaf(0.14078889f, q, 0.13982579f);
     r = __builtin_fmaf(r, q, 0.20012298f);
     r = __builtin_fmaf(r, q, 0.33333161f);
     r = __builtin_fmaf(r, q, 1.0f);
     return __builtin_fmaf(s + s, r, fmaxf(v, 0.0f));
+}
+__device__ __forceinline__ float softplus_f32(float v) {
+    return softplus_from(v, __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e));
+}
+// And its slope, the logistic function.
+__device__ __forceinline__ void softplus_grad_f32(float v, float& d, float& slope) {
+    const float u = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e);
+    d = softplus_from(v, u);
+    slope = (v < 0.0f ? u : 1.0f) * __builtin_amdgcn_rcpf(1.0f + u);
 }
 __device__ __forceinline__ float sigmoid_f32(float v) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));

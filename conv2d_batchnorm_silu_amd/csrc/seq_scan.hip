@@ -132,8 +132,8 @@ struct alignas(16) Tile {
     float B[TT][4 * NS];
     float C[TT][4 * NS];
 };
-// The backward pass: dL/dv too, and the items' x, dt + bias, z and dy, which
-// would take 16 registers until the end of the chunk.
+// The backward pass: dL/dv too, and the items' x, slope of softplus and dz for
+// v = 1, which would take registers until the end of the chunk.
 template <int NS, int TT>
 struct alignas(16) BackTile {
     Tile<NS, TT> f;
@@ -340,11 +340,13 @@ struct Shared {
 };
 
 // A wave's states (or their adjoints) after its segment from zero, and the decay over it:
-// LDS [W][2][64][NS] floats.
+// LDS [W][2][64][NS] floats, and after them [64][NS]: the true state that the round
+// before left.
 template <int NS>
 __device__ __forceinline__ float* exchange_at(float* ex, int w, int which) {
     return ex + ((w * 2 + which) * 64 + (threadIdx.x & 63)) * NS;
 }
+constexpr int exchange_floats(int W, int ns) { return (2 * W + 1) * 64 * ns; }
 
 // State j of a lane, with lanes by rows: the rows of a 16 x 16 matrix that the
 // lane holds, 4q to 4q+3 (with NS < 4 only NS of them are used).
@@ -507,6 +509,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64)
             store_f32<float, V>(to + state_of<NS, true>(p.q, j), *(const float (*)[V])(r + j));
     };
     int flip = 0;
+    if (SPLIT && p.w == W - 1) put<NS>(exchange_at<NS>(exchange, W, 0), h);
     if (p.lo < p.hi) fetch(p.lo + p.w * TT);
     for (int l0 = p.lo; l0 < p.hi; l0 += W * TT) {
         const int l = l0 + p.w * TT;
@@ -545,21 +548,19 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64)
             float P[NS], r[NS];
 #pragma unroll
             for (int j = 0; j < NS; ++j) P[j] = __builtin_amdgcn_exp2f(sum * A2[j]);
-            float* const ex = exchange + flip * (W * 128 * NS);
+            float* const ex = exchange + flip * exchange_floats(W, NS);
             flip ^= 1;
             put<NS>(exchange_at<NS>(ex, p.w, 0), P);
             put<NS>(exchange_at<NS>(ex, p.w, 1), e);
             __syncthreads();
             // The other buffer is written next, past this barrier of the next
             // round: nobody still reads it then.
-            for (int k = 0; k < W; ++k) {
-                if (k == p.w)
-#pragma unroll
-                    for (int j = 0; j < NS; ++j) r[j] = h[j];
+            get<NS>(exchange_at<NS>(ex, W, 0), r);
+            for (int k = 0; k < p.w; ++k) {
                 get<NS>(exchange_at<NS>(ex, k, 0), P);
                 get<NS>(exchange_at<NS>(ex, k, 1), e);
 #pragma unroll
-                for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(P[j], h[j], e[j]);
+                for (int j = 0; j < NS; ++j) r[j] = __builtin_fmaf(P[j], r[j], e[j]);
             }
             save(l, r);
             // The second run, from the true state. Its products d*x*B are made
@@ -579,6 +580,12 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64)
                 }
                 v[g] = row_sums(y, lane);
             });
+            // The last wave has reached the state that the next round starts from.
+            if (p.w == W - 1) {
+                put<NS>(exchange_at<NS>(exchange + flip * exchange_floats(W, NS), W, 0), r);
+#pragma unroll
+                for (int j = 0; j < NS; ++j) h[j] = r[j];
+            }
         } else {
             save(l, h);
             for_groups<TT>([&](int g) {
@@ -607,7 +614,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64)
         store_items<T, TT>(cy, p, l, v);
         wave_sync();
     }
-    if (p.w == 0 && p.hi == p.len) store_state<NS, true>(a.final, a, p, h);
+    if (p.w == W - 1 && p.hi == p.len) store_state<NS, true>(a.final, a, p, h);
 }
 
 // The parts' decays and last states from zero, for all parts but a sequence's
@@ -713,16 +720,17 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
     Tile<NS, TT>& tile = both.f;
     float* const exchange = (float*)((BackTile<NS, TT>*)lds + W);
     const int lane = threadIdx.x & 63;
-    float A2[NS], carry[NS], dA[NS], lost[NS];
+    // c: a[t+1]*g[t+1] of the next token.
+    float A2[NS], c[NS], dA[NS], lost[NS];
     load_A2<NS, false>(a, p, A2);
-    load_state<NS, false>(b.dfinal, a, p, carry);
+    load_state<NS, false>(b.dfinal, a, p, c);
     if (a.PL)
         for (int k = (p.len - 1) / a.PL; k > p.part(a.PL); --k) {
             float P[NS], e[NS];
             get<NS>(part_at<NS>(a, p, k, 0), P);
             get<NS>(part_at<NS>(a, p, k, 1), e);
 #pragma unroll
-            for (int j = 0; j < NS; ++j) carry[j] = __builtin_fmaf(P[j], carry[j], e[j]);
+            for (int j = 0; j < NS; ++j) c[j] = __builtin_fmaf(P[j], c[j], e[j]);
         }
 #pragma unroll
     for (int j = 0; j < NS; ++j) dA[j] = lost[j] = 0.0f;
@@ -737,6 +745,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
         cddt(b.ddt, a.seqs, p, E, a.D), cdz(b.dz, a.seqs, p, E, a.D);
     Items<T, TT> rx, rdt, rz, rdy;
     Shared<T, NS, TT> rB, rC;
+    float rh[NS];
     const auto fetch = [&](int l) {
         rx.load(cx, p, l);
         rdt.load(cdt, p, l);
@@ -744,26 +753,40 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
         rdy.load(cdy, p, l);
         rB.load(cB, p, a.N, l);
         rC.load(cC, p, a.N, l);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) rh[j] = 0.0f;
+        if (p.in && l < p.hi)
+            get<NS>(b.saved + ((slot0 + l / TT) * a.D + p.ch) * (4 * NS) + p.q * NS, rh);
     };
     int flip = 0;
+    if (SPLIT && p.w == 0) put<NS>(exchange_at<NS>(exchange, W, 0), c);
     const int chunks = (p.hi - p.lo + W * TT - 1) / (W * TT);
     if (chunks > 0) fetch(p.lo + ((chunks - 1) * W + p.w) * TT);
     for (int chunk = chunks - 1; chunk >= 0; --chunk) {
         const int l = p.lo + (chunk * W + p.w) * TT;
         float h0[NS];
 #pragma unroll
-        for (int j = 0; j < NS; ++j) h0[j] = 0.0f;
-        if (p.in && l < p.hi)
-            get<NS>(b.saved + ((slot0 + l / TT) * a.D + p.ch) * (4 * NS) + p.q * NS, h0);
+        for (int j = 0; j < NS; ++j) h0[j] = rh[j];
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
             const int t = p.q + 4 * i;
-            const float x = rx[i], raw = rdt[i] + bias, z = a.z.p ? rz[i] : 0.0f, dout = rdy[i];
-            float d = step_size(a, raw);
-            if (l + TT > p.hi) d = l + t < p.hi ? d : 0.0f;
+            const float x = rx[i], raw = rdt[i] + bias, dout = rdy[i];
+            float d = raw, slope = 1.0f, dv = dout, w = 0.0f;  // w: dz for v = 1
+            if (a.softplus) softplus_grad_f32(raw, d, slope);
+            if (a.z.p) {
+                const float z = rz[i], sg = sigmoid_f32(z);
+                dv = dout * (z * sg);
+                w = dout * (sg * __builtin_fmaf(z, 1.0f - sg, 1.0f));
+            }
+            if (l + TT > p.hi) {
+                // Past the end the state and its adjoint only pass through, but
+                // their product, which dL/dd holds, is not zero.
+                d = l + t < p.hi ? d : 0.0f;
+                slope = l + t < p.hi ? slope : 0.0f;
+            }
             tile.d[t][p.cl] = make_float2(d, d * x);
-            both.dv[t][p.cl] = a.z.p ? dout * silu_f32(z) : dout;
-            both.item[i][lane] = make_float4(x, raw, z, dout);
+            both.dv[t][p.cl] = dv;
+            both.item[i][lane] = make_float4(x, slope, w, 0.0f);
         }
         rB.put(tile.B);
         rC.put(tile.C);
@@ -788,7 +811,6 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
                 }
             });
         }
-        float c[NS];  // a[t+1]*g[t+1] of the next token
         if constexpr (SPLIT) {
             float P[NS], e[NS];
 #pragma unroll
@@ -800,23 +822,18 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
             });
 #pragma unroll
             for (int j = 0; j < NS; ++j) P[j] = __builtin_amdgcn_exp2f(sum * A2[j]);
-            float* const ex = exchange + flip * (W * 128 * NS);
+            float* const ex = exchange + flip * exchange_floats(W, NS);
             flip ^= 1;
             put<NS>(exchange_at<NS>(ex, p.w, 0), P);
             put<NS>(exchange_at<NS>(ex, p.w, 1), e);
             __syncthreads();
-            for (int m = W - 1; m >= 0; --m) {
-                if (m == p.w)
-#pragma unroll
-                    for (int j = 0; j < NS; ++j) c[j] = carry[j];
+            get<NS>(exchange_at<NS>(ex, W, 0), c);
+            for (int m = W - 1; m > p.w; --m) {
                 get<NS>(exchange_at<NS>(ex, m, 0), P);
                 get<NS>(exchange_at<NS>(ex, m, 1), e);
 #pragma unroll
-                for (int j = 0; j < NS; ++j) carry[j] = __builtin_fmaf(P[j], carry[j], e[j]);
+                for (int j = 0; j < NS; ++j) c[j] = __builtin_fmaf(P[j], c[j], e[j]);
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < NS; ++j) c[j] = carry[j];
         }
         float dAc[NS];
 #pragma unroll
@@ -867,7 +884,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
                 }
             // The next tokens' loads, with enough time left to arrive and no
             // sooner: they take the registers of states that are done with.
-            if (t == TT / 2 && chunk > 0) fetch(l - W * TT);
+            if (t == TT / 4 && chunk > 0) fetch(l - W * TT);
         });
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
@@ -882,22 +899,18 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
             const float add = dAc[j] - lost[j], s = dA[j] + add;
             lost[j] = (s - dA[j]) - add;
             dA[j] = s;
-            if (!SPLIT) carry[j] = c[j];
         }
+        if (SPLIT && p.w == 0)
+            put<NS>(exchange_at<NS>(exchange + flip * exchange_floats(W, NS), W, 0), c);
         float dt[kItems], dx[kItems], dz[kItems];
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
             const int t = p.q + 4 * i;
-            const float4 it = both.item[i][lane];  // x, dt + bias, z, dy
+            const float4 it = both.item[i][lane];
             const float dv = both.dv[t][p.cl];
-            dt[i] = __builtin_fmaf(e2[i], it.x, e1[i] * kLn2);
-            if (a.softplus) dt[i] *= sigmoid_f32(it.y);
+            dt[i] = __builtin_fmaf(e2[i], it.x, e1[i] * kLn2) * it.y;
             dx[i] = __builtin_fmaf(e2[i], tile.d[t][p.cl].x, skip * dv);
-            const float sg = sigmoid_f32(it.z), y = __builtin_fmaf(skip, it.x, v[i]);
-            dz[i] = it.w * y * sg * __builtin_fmaf(it.z, 1.0f - sg, 1.0f);
-            // Past the end the state and its adjoint only pass through, but their
-            // product is not zero.
-            if (l + TT > p.hi) dt[i] = l + t < p.hi ? dt[i] : 0.0f;
+            dz[i] = it.z * __builtin_fmaf(skip, it.x, v[i]);
             dbias += dt[i];
             dD = __builtin_fmaf(dv, it.x, dD);
         }
@@ -934,7 +947,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
         const int n = p.q * NS + j;
         if (n < a.N) b.part_a[(out * a.D + p.ch) * a.N + n] = dA[j];
     }
-    if (p.lo == 0) store_state<NS, false>(b.dinitial, a, p, carry);
+    if (p.lo == 0) store_state<NS, false>(b.dinitial, a, p, c);
 }
 
 // What the parts but a sequence's first pass to the tokens before them, from
@@ -1098,10 +1111,10 @@ struct Plan {
     int ns, tt, waves, PL;  // waves 1: whole sequences by single waves
     int64_t slots, nb;      // workgroups: slots * nb
 };
-Plan plan_of(const tg_scan_args& a) {
+Plan plan_of(const tg_scan_args& a, bool forward) {
     Plan p;
     p.ns = states_for(a.N);
-    p.tt = chunk_for(p.ns);
+    p.tt = forward ? fwd_chunk_for(p.ns) : chunk_for(p.ns);
     p.nb = (int64_t)a.G * ceil_div(a.D / a.G, kCh);
     const int64_t groups = a.seqs.seqs * p.nb;
     p.waves = groups >= 4096 ? 1 : waves_for(p.ns);
@@ -1155,7 +1168,7 @@ ScanArgs args_of(const tg_scan_args& a, const Plan& p, float* saved, void* parts
 template <typename Kernel, typename... Args>
 hipError_t launch_waves(Kernel kernel, const Plan& p, size_t tile, int buffers, hipStream_t st,
                         const Args&... args) {
-    const size_t bytes = p.waves * (tile + (p.waves > 1 ? buffers * 128 * p.ns * sizeof(float) : 0));
+    const size_t bytes = p.waves * tile + (p.waves > 1 ? buffers * exchange_floats(p.waves, p.ns) * sizeof(float) : 0);
     const hipError_t e = ensure_dynamic_lds((const void*)kernel, bytes);
     if (e != hipSuccess) return e;
     kernel<<<(unsigned)(p.slots * p.nb), 64 * p.waves, bytes, st>>>(args...);
@@ -1215,16 +1228,16 @@ __global__ __launch_bounds__(256) void scan_clear_slots(const ScanArgs a, int sl
 }  // namespace
 
 void scan_sizes(const tg_scan_args& a, size_t* work, size_t* saved, size_t* backward) {
-    const Plan p = plan_of(a);
+    const Plan f = plan_of(a, true), p = plan_of(a, false);
     const int64_t slots = a.seqs.rows / p.tt + a.seqs.seqs;
-    if (work) *work = parts_bytes(a, p);
+    if (work) *work = parts_bytes(a, f);
     if (saved) *saved = (size_t)slots * a.D * 4 * p.ns * sizeof(float);
     if (backward) *backward = backward_ws(a, p).total;
 }
 
 hipError_t launch_scan(const tg_scan_args& a, void* ws, void* saved, hipStream_t st) {
     const tg_dtype dtype = a.dtype;
-    const Plan p = plan_of(a);
+    const Plan p = plan_of(a, true);
     const ScanArgs f = args_of(a, p, (float*)saved, ws);
 #define TG_X(T, NS) return fwd_typed<T, NS>(p, f, st)
     TG_SCAN_DISPATCH(TG_X);
@@ -1235,7 +1248,7 @@ hipError_t launch_scan(const tg_scan_args& a, void* ws, void* saved, hipStream_t
 hipError_t launch_scan_backward(const tg_scan_args& a, const tg_scan_grads& g, const void* saved,
                                 void* ws, hipStream_t st) {
     const tg_dtype dtype = a.dtype;
-    const Plan p = plan_of(a);
+    const Plan p = plan_of(a, false);
     const BackwardWs w = backward_ws(a, p);
     char* const base = (char*)ws;
     const ScanArgs f = args_of(a, p, nullptr, base + w.parts);
