@@ -33,6 +33,20 @@ __device__ __forceinline__ void load_f32(const T* p, float (&v)[V]) {
         for (int i = 0; i < V; ++i) v[i] = (float)r[i];
     }
 }
+// The same in two steps: the load, and the values once they are needed.
+template <typename T, int V>
+struct Vec {
+    typename VecOf<T, V>::type r;
+    __device__ __forceinline__ void load(const T* p) { r = *(const typename VecOf<T, V>::type*)p; }
+    __device__ __forceinline__ void values(float (&v)[V]) const {
+        if constexpr (V == 1) {
+            v[0] = (float)r;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = (float)r[i];
+        }
+    }
+};
 template <typename T, int V>
 __device__ __forceinline__ void store_f32(T* p, const float (&v)[V]) {
     if constexpr (V == 1) {

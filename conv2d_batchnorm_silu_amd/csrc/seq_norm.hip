@@ -3,7 +3,7 @@
 //
 // Both passes are bound by HBM: a few operations for each element read or
 // written. So each element is read once and held in registers: TPR threads
-// (one wave, four or sixteen) share a row, a thread holds NV vectors of V
+// (one wave to sixteen) share a row, a thread holds NV vectors of V
 // elements of it, V as wide (up to 16 bytes) as the alignment of C, the
 // strides and the pointers allows. The statistics are two sums over the
 // held values, the mean first and then the squared distances from it: the
@@ -37,12 +37,12 @@ template <int TPR>
 __device__ __forceinline__ float row_total(float v, float* red) {
     v = wave_sum(v);
     if constexpr (TPR > 64) {
-        const int w = threadIdx.x >> 6;
+        const int w = threadIdx.x >> 6, first = w & ~(TPR / 64 - 1);
         if ((threadIdx.x & 63) == 0) red[w] = v;
         __syncthreads();
         v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < TPR / 64; ++i) v += red[i];
+        for (int i = 0; i < TPR / 64; ++i) v += red[first + i];
     }
     return v;
 }
@@ -53,12 +53,12 @@ __device__ __forceinline__ void row_totals(float& u, float& v, float (*red)[16])
     u = wave_sum(u);
     v = wave_sum(v);
     if constexpr (TPR > 64) {
-        const int w = threadIdx.x >> 6;
+        const int w = threadIdx.x >> 6, first = w & ~(TPR / 64 - 1);
         if ((threadIdx.x & 63) == 0) red[0][w] = u, red[1][w] = v;
         __syncthreads();
         u = v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < TPR / 64; ++i) u += red[0][i], v += red[1][i];
+        for (int i = 0; i < TPR / 64; ++i) u += red[0][first + i], v += red[1][first + i];
     }
 }
 
@@ -90,38 +90,48 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(const NormFwd 
         }
     }
     const float inv = 1.0f / (float)C;
-    // All threads of a workgroup that shares a row (TPR > 64) run the same
-    // number of rows, so the barriers inside match.
-    for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows;
-         row += (int64_t)gridDim.x * RPB) {
-        const T* xp = (const T*)a.x + row * a.xs;
-        const T* rp = (const T*)a.res + row * a.rs;
-        float v[NV][V], s = 0.0f;
+    Vec<T, V> rx[NV], rr[NV];
+    const auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + i) * V;
             if (c < C) {
-                load_f32<T, V>(xp + c, v[j]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[j][e] = 0.0f;
+                rx[j].load((const T*)a.x + row * a.xs + c);
+                if (a.res) rr[j].load((const T*)a.res + row * a.rs + c);
             }
         }
-        if (a.res) {
+    };
+    // The barriers of a row that several waves share have to match: all groups of the
+    // workgroup go round as often as its first, those past the last row idly.
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    const int grp = threadIdx.x / TPR;
+    int64_t first = (int64_t)blockIdx.x * RPB;
+    if (first + grp < a.rows) fetch(first + grp);
+    for (; first < a.rows; first += step) {
+        const int64_t row = first + grp;
+        const int D = row < a.rows ? C : 0;  // this group's channels
+        float v[NV][V], s = 0.0f;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * TPR + i) * V;
-                if (c < C) {
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + i) * V;
+            if (c < D) {
+                rx[j].values(v[j]);
+                if (a.res) {
                     float r[V];
-                    load_f32<T, V>(rp + c, r);
+                    rr[j].values(r);
                     // The statistics are those of the rounded sum: it is what the next
                     // block and the backward pass read.
 #pragma unroll
                     for (int e = 0; e < V; ++e) v[j][e] = (float)(T)(v[j][e] + r[e]);
                     store_f32<T, V>((T*)a.sum + row * C + c, v[j]);
                 }
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[j][e] = 0.0f;
             }
         }
+        // The next row arrives while this one is reduced and written.
+        if (row + step < a.rows) fetch(row + step);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -130,7 +140,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(const NormFwd 
         float q = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const bool in = (j * TPR + i) * V < C;
+            const bool in = (j * TPR + i) * V < D;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float d = in ? v[j][e] - mean : 0.0f;
@@ -140,14 +150,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(const NormFwd 
         }
         const float var = row_total<TPR>(q, red[1]) * inv;
         const float rstd = 1.0f / sqrtf(var + a.eps);
-        if (i == 0 && a.mean) {
+        if (i < D && i == 0 && a.mean) {
             a.mean[row] = mean;
             a.rstd[row] = rstd;
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + i) * V;
-            if (c < C) {
+            if (c < D) {
                 float o[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e)
@@ -223,23 +233,44 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(const NormBwd 
     }
     const float inv = 1.0f / (float)C;
     int flip = 0;  // two sets of sums: one row's are read while the next's are written
-    for (int64_t row = (int64_t)blockIdx.x * RPB + grp; row < a.rows;
-         row += (int64_t)gridDim.x * RPB) {
-        const T* gp = (const T*)a.dy + row * a.dys;
-        const T* sp = (const T*)a.s + row * a.ss;
-        const float mean = a.mean[row], rstd = a.rstd[row];
-        float g[NV][V], h[NV][V], s1 = 0.0f, s2 = 0.0f;
+    Vec<T, V> rg[NV], rs[NV], rd[NV];
+    float rmean = 0.0f, rrstd = 0.0f;
+    const auto fetch = [&](int64_t row) {
+        rmean = a.mean[row];
+        rrstd = a.rstd[row];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + i) * V;
             if (c < C) {
-                load_f32<T, V>(gp + c, g[j]);
-                load_f32<T, V>(sp + c, h[j]);
+                rg[j].load((const T*)a.dy + row * a.dys + c);
+                rs[j].load((const T*)a.s + row * a.ss + c);
+                if (a.dsum) rd[j].load((const T*)a.dsum + row * a.dss + c);
+            }
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t first = (int64_t)blockIdx.x * RPB;
+    if (first + grp < a.rows) fetch(first + grp);
+    for (; first < a.rows; first += step) {  // barriers as in the forward pass
+        const int64_t row = first + grp;
+        const int D = row < a.rows ? C : 0;
+        const float mean = rmean, rstd = rrstd;
+        float g[NV][V], h[NV][V], s1 = 0.0f, s2 = 0.0f;
+        Vec<T, V> add[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * TPR + i) * V;
+            add[j] = rd[j];
+            if (c < D) {
+                rg[j].values(g[j]);
+                rs[j].values(h[j]);
             } else {
 #pragma unroll
                 for (int e = 0; e < V; ++e) g[j][e] = 0.0f, h[j][e] = mean;
             }
         }
+        // The next row arrives while this one is reduced and written.
+        if (row + step < a.rows) fetch(row + step);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -257,14 +288,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(const NormBwd 
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * TPR + i) * V;
-            if (c < C) {
+            if (c < D) {
                 float o[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e)
                     o[e] = rstd * (g[j][e] - __builtin_fmaf(h[j][e], m2, m1));
                 if (a.dsum) {
                     float r[V];
-                    load_f32<T, V>((const T*)a.dsum + row * a.dss + c, r);
+                    add[j].values(r);
 #pragma unroll
                     for (int e = 0; e < V; ++e) o[e] += r[e];
                 }
@@ -351,6 +382,7 @@ __global__ __launch_bounds__(64 * kColThreads) void column_sums(const float* par
     const int64_t m = (int64_t)blockIdx.x * 64 + l;
     float s = 0.0f;
     if (m < M)
+#pragma unroll 8
         for (int p = ph; p < P; p += kColThreads) s += part[(int64_t)p * M + m];
     red[ph][l] = s;
     __syncthreads();
@@ -363,40 +395,39 @@ __global__ __launch_bounds__(64 * kColThreads) void column_sums(const float* par
     }
 }
 
-// Most vectors that a thread holds. 32 values and their gamma and beta, or
-// (backward) five such sets, stay within the registers of four workgroups of
-// 256 threads on a compute unit; 1024 threads leave 128 registers each, which
-// the backward pass fills with 16 values.
-constexpr int nv_most(int V, int tpr, bool bwd) {
-    const int n = tpr < 1024 ? 4 : (bwd ? 16 : 32) / V;
-    return V == 1 || n > 8 ? 8 : n;
+// Which numbers of threads for a row (tpr) and of vectors in a thread (nv) are
+// built. A thread holds at most 8 values (16 for the longest rows): with their
+// gamma and beta, or (backward) five such sets, and the next row on its way,
+// that leaves five to eight waves on a SIMD, which counts for more than a row's
+// barriers: 16384 x 2048 bf16 forward and backward took 165 us with a wave and 32
+// values for each row, 113 us with 256 threads and 8 values.
+constexpr bool shape_used(int V, int tpr, int nv, bool bwd) {
+    if (V >= 4) return tpr < 1024 ? nv == 1 : nv * V <= (bwd ? 8 : 16);
+    if (tpr == 128 || tpr == 512) return false;
+    const int most = V == 1 ? 8 : tpr == 1024 && !bwd ? 8 : 4;
+    return nv <= most && (tpr == 64 || nv >= (V == 1 ? 4 : 2));
 }
-// The least that norm_shape asks of tpr threads: below it fewer threads do.
-constexpr int nv_least(int V, int tpr) { return tpr == 64 ? 1 : (V == 1 ? 4 : 2); }
 
-// Threads for each row and vectors for each thread that hold C elements in
-// vectors of V; tpr 0: too long for the held form.
+// The fewest threads that hold C elements in vectors of V; tpr 0: too long
+// for the held form.
 struct Shape {
     int tpr, nv;
 };
 Shape norm_shape(int C, int V, bool bwd) {
     const int64_t n = ceil_div(C, V);
-    for (int tpr : {64, 256, 1024})
-        for (int nv = 1; nv <= nv_most(V, tpr, bwd); nv *= 2)
-            if (n <= (int64_t)tpr * nv) return {tpr, nv};
+    for (int tpr : {64, 128, 256, 512, 1024})
+        for (int nv = 1; nv <= 8; nv *= 2)
+            if (shape_used(V, tpr, nv, bwd) && n <= (int64_t)tpr * nv) return {tpr, nv};
     return {0, 0};
 }
 
-int norm_grid(int64_t rows, int tpr, int per_cu) {
+// Workgroups of the forward pass: 2048 where a wave holds a row (25088 x 363
+// fp32: 13 us; 1024 take 19), else 1024 threads on each compute unit (8192 x
+// 4096 bf16: 57 us; half as many take 64, twice as many 61).
+int norm_grid(int64_t rows, int tpr) {
     const int rpb = tpr >= 256 ? 1 : 256 / tpr;
-    const int64_t need = ceil_div(rows, rpb), most = 256 * (int64_t)per_cu;
+    const int64_t need = ceil_div(rows, rpb), most = tpr == 64 ? 2048 : tpr < 256 ? 1024 : 256 * (1024 / tpr);
     return (int)(need < most ? need : most);
-}
-
-// Whether norm_shape gives nv vectors for TPR threads.
-template <int V, int TPR, typename Args>
-constexpr bool nv_used(int nv) {
-    return nv >= nv_least(V, TPR) && nv <= nv_most(V, TPR, std::is_same<Args, NormBwd>::value);
 }
 
 template <typename T, int V, int TPR, int NV>
@@ -407,22 +438,26 @@ template <typename T, int V, int TPR, int NV>
 void norm_one(int grid, const NormBwd& a, hipStream_t st) {
     norm_bwd<T, V, TPR, NV><<<grid, TPR > 256 ? TPR : 256, 0, st>>>(a);
 }
+// The kernel for tpr threads and nv vectors, if it is built.
+template <typename T, int V, int TPR, int NV, typename Args>
+void norm_try(const Shape& sh, int grid, const Args& a, hipStream_t st) {
+    if constexpr (shape_used(V, TPR, NV, std::is_same<Args, NormBwd>::value))
+        if (sh.tpr == TPR && sh.nv == NV) norm_one<T, V, TPR, NV>(grid, a, st);
+}
 template <typename T, int V, int TPR, typename Args>
-void norm_nv(int nv, int grid, const Args& a, hipStream_t st) {
-    if constexpr (nv_used<V, TPR, Args>(1))
-        if (nv == 1) return norm_one<T, V, TPR, 1>(grid, a, st);
-    if constexpr (nv_used<V, TPR, Args>(2))
-        if (nv == 2) return norm_one<T, V, TPR, 2>(grid, a, st);
-    if constexpr (nv_used<V, TPR, Args>(8))
-        if (nv == 8) return norm_one<T, V, TPR, 8>(grid, a, st);
-    if constexpr (nv_used<V, TPR, Args>(4))
-        if (nv == 4) return norm_one<T, V, TPR, 4>(grid, a, st);
+void norm_nv(const Shape& sh, int grid, const Args& a, hipStream_t st) {
+    norm_try<T, V, TPR, 1>(sh, grid, a, st);
+    norm_try<T, V, TPR, 2>(sh, grid, a, st);
+    norm_try<T, V, TPR, 4>(sh, grid, a, st);
+    norm_try<T, V, TPR, 8>(sh, grid, a, st);
 }
 template <typename T, int V, typename Args>
 void norm_tpr(const Shape& sh, int grid, const Args& a, hipStream_t st) {
-    if (sh.tpr == 64) norm_nv<T, V, 64>(sh.nv, grid, a, st);
-    else if (sh.tpr == 256) norm_nv<T, V, 256>(sh.nv, grid, a, st);
-    else norm_nv<T, V, 1024>(sh.nv, grid, a, st);
+    norm_nv<T, V, 64>(sh, grid, a, st);
+    norm_nv<T, V, 128>(sh, grid, a, st);
+    norm_nv<T, V, 256>(sh, grid, a, st);
+    norm_nv<T, V, 512>(sh, grid, a, st);
+    norm_nv<T, V, 1024>(sh, grid, a, st);
 }
 template <typename T, typename Args>
 void norm_launch(int V, const Shape& sh, int grid, const Args& a, hipStream_t st) {
@@ -437,10 +472,10 @@ template <typename T>
 void fwd_typed(int V, const NormFwd& a, hipStream_t st) {
     const Shape sh = norm_shape(a.C, V, false);
     if (!sh.tpr) {
-        norm_fwd_long<T><<<norm_grid(a.rows, 1024, 2), 1024, 0, st>>>(a);
+        norm_fwd_long<T><<<norm_grid(a.rows, 1024), 1024, 0, st>>>(a);
         return;
     }
-    const int grid = norm_grid(a.rows, sh.tpr, sh.tpr == 1024 ? 2 : 8);
+    const int grid = norm_grid(a.rows, sh.tpr);
     norm_launch<T>(V, sh, grid, a, st);
 }
 template <typename T>
@@ -450,7 +485,8 @@ void bwd_typed(int V, int grid, const NormBwd& a, hipStream_t st) {
     else norm_launch<T>(V, sh, grid, a, st);
 }
 
-// Workgroups of the backward pass: one row of partial sums each.
+// Workgroups of the backward pass, one row of partial sums each (16384 x 2048
+// bf16, forward and backward: 111 us; 384 workgroups 123, 768 and 1024: 115, 128).
 int bwd_grid(int64_t rows) {
     const int64_t need = ceil_div(rows, 4);
     return (int)(need < 512 ? need : 512);
