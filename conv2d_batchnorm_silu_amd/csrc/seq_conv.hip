@@ -43,24 +43,30 @@ __device__ __forceinline__ void row_or_state(const A& a, int s, int start, int l
     }
 }
 
-// The sequence that holds flat row t (t < rows), skipping empty ones: the
-// last one that starts at or before t. Rows that wrong offsets leave uncovered
-// belong to a sequence that ended before them.
-__device__ __forceinline__ int seq_at(const SeqMap& m, int t) {
-    if (!m.offsets) return t / m.L;
-    int lo = 0, hi = m.seqs - 1;
-    while (lo < hi) {
-        const int k = (lo + hi + 1) >> 1;
-        if (m.start(k) <= t) lo = k;
-        else hi = k - 1;
-    }
-    return lo;
-}
-
 template <int V>
 __device__ __forceinline__ void load_consts(const float* p, int c, float (&v)[V]) {
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = p ? p[c + e] : 0.0f;
+}
+
+// Rows that a thread has on their way while it computes: one row of a wave is 512
+// bytes, and some thousand waves of one row each do not fill the memory's pipe.
+constexpr int kAhead = 4;
+template <typename T, int V>
+struct Ahead {
+    Vec<T, V> r[kAhead];
+    // Rows l .. l+3 of the sequence, the last one (end - 1) again past the end.
+    __device__ __forceinline__ void load(const Rows<const void>& x, const SeqMap& m, int s, int b,
+                                         int l, int end, int c) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            r[k].load(row_of<const T>(x, m, s, b, imin(l + k, end - 1)) + c);
+    }
+};
+
+// A wave's threads share a strip, so what goes by it is uniform.
+__device__ __forceinline__ int wave_piece() {
+    return __builtin_amdgcn_readfirstlane(blockIdx.x * blockDim.y + threadIdx.y);
 }
 
 // blockIdx.x: strips, then (with final) one more block row for each sequence.
@@ -68,12 +74,13 @@ __device__ __forceinline__ void load_consts(const float* p, int c, float (&v)[V]
 template <typename T, int V, int K>
 __global__ __launch_bounds__(kBlock) void conv_fwd(const ConvFwd a, int strips) {
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
-    if (c >= a.D) return;
     const SeqMap& m = a.seqs;
-    const int piece = blockIdx.x * blockDim.y + threadIdx.y;
+    const int piece = wave_piece();
+    int t = piece * a.strip, s = piece < strips ? m.holder(t) : 0;
+    if (c >= a.D) return;
     if (piece >= strips) {
         // The last K-1 rows of a sequence, as its next state.
-        const int s = piece - strips;
+        s = piece - strips;
         if (!a.final || s >= m.seqs) return;
         const int b = m.start(s), n = m.end(s) - b;
         for (int r = 0; r < K - 1; ++r) {
@@ -87,30 +94,39 @@ __global__ __launch_bounds__(kBlock) void conv_fwd(const ConvFwd a, int strips) 
 #pragma unroll
     for (int k = 0; k < K; ++k) load_consts<V>(a.w + (int64_t)k * a.D, c, w[k]);
     load_consts<V>(a.bias, c, bias);
-    int t = piece * a.strip;
     const int stop = imin(t + a.strip, m.rows);
-    int s = seq_at(m, t);
     while (t < stop && s < m.seqs) {
         const int b = m.start(s), e = imin(m.end(s), stop);
         if (t < b) t = b;
-#pragma unroll
-        for (int k = 0; k < K - 1; ++k)
-            if (t < e) row_or_state<T, V, K>(a, s, b, t - b - (K - 1) + k, c, win[k]);
-        for (; t < e; ++t) {
-            load_f32<T, V>(row_of<const T>(a.x, m, s, b, t - b) + c, win[K - 1]);
-            float o[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float v = bias[i];
-#pragma unroll
-                for (int k = 0; k < K; ++k) v = __builtin_fmaf(w[k][i], win[k][i], v);
-                o[i] = a.silu ? silu_f32(v) : v;
-            }
-            store_f32<T, V>(row_of<T>(a.y, m, s, b, t - b) + c, o);
+        if (t < e) {
+            Ahead<T, V> next;
+            next.load(a.x, m, s, b, t - b, e - b, c);
 #pragma unroll
             for (int k = 0; k < K - 1; ++k)
+                row_or_state<T, V, K>(a, s, b, t - b - (K - 1) + k, c, win[k]);
+            for (; t < e; t += kAhead) {
+                const Ahead<T, V> cur = next;
+                if (t + kAhead < e) next.load(a.x, m, s, b, t + kAhead - b, e - b, c);
 #pragma unroll
-                for (int i = 0; i < V; ++i) win[k][i] = win[k + 1][i];
+                for (int u = 0; u < kAhead; ++u) {
+                    if (t + u >= e) break;
+                    cur.r[u].values(win[K - 1]);
+                    float o[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        float v = bias[i];
+#pragma unroll
+                        for (int k = 0; k < K; ++k) v = __builtin_fmaf(w[k][i], win[k][i], v);
+                        o[i] = a.silu ? silu_f32(v) : v;
+                    }
+                    store_f32<T, V>(row_of<T>(a.y, m, s, b, t + u - b) + c, o);
+#pragma unroll
+                    for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) win[k][i] = win[k + 1][i];
+                }
+            }
+            t = e;
         }
         ++s;
     }
@@ -161,9 +177,10 @@ __device__ __forceinline__ void add_dfinal(const ConvBwd& a, int s, int n, int p
 template <typename T, int V, int K>
 __global__ __launch_bounds__(kBlock) void conv_bwd(const ConvBwd a, int strips) {
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
-    if (c >= a.D) return;
     const SeqMap& m = a.seqs;
-    const int piece = blockIdx.x * blockDim.y + threadIdx.y;
+    const int piece = wave_piece();
+    int t = piece * a.strip, s = piece < strips ? m.holder(t) : 0;
+    if (c >= a.D) return;
     float w[K][V], bias[V], win[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) load_consts<V>(a.w + (int64_t)k * a.D, c, w[k]);
@@ -171,7 +188,7 @@ __global__ __launch_bounds__(kBlock) void conv_bwd(const ConvBwd a, int strips) 
     if (piece >= strips) {
         // The gradient of a sequence's initial state: position q < 0 takes w[k] * dv[t]
         // for t = q + K-1-k >= 0, and passes on what reaches it as a final state.
-        const int s = piece - strips;
+        s = piece - strips;
         if (!a.dinitial || s >= m.seqs) return;
         const int b = m.start(s), n = m.end(s) - b;
         float acc[K - 1][V];
@@ -207,14 +224,15 @@ __global__ __launch_bounds__(kBlock) void conv_bwd(const ConvBwd a, int strips) 
 #pragma unroll
         for (int k = 0; k < K; ++k) dw[k][i] = 0.0f;
     }
-    int t = piece * a.strip;
     const int stop = imin(t + a.strip, m.rows);
-    int s = seq_at(m, t);
     while (t < stop && s < m.seqs) {
         const int b = m.start(s), end = m.end(s), n = end - b, e = imin(end, stop);
         if (t < b) t = b;
         if (t < e) {
             const int first = t, far = imin(e + K - 1, end);
+            Ahead<T, V> nx, ng;
+            nx.load(a.x, m, s, b, t - b, far - b, c);
+            ng.load(a.dy, m, s, b, t - b, far - b, c);
 #pragma unroll
             for (int k = 0; k < K - 1; ++k)
                 row_or_state<T, V, K>(a, s, b, t - b - (K - 1) + k, c, win[k]);
@@ -223,46 +241,56 @@ __global__ __launch_bounds__(kBlock) void conv_bwd(const ConvBwd a, int strips) 
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[k][i] = 0.0f;
             // Up to K-1 steps past the last row with dv: they only send rows off.
-            for (; t < e + K - 1; ++t) {
-                float g[V];
-                if (t < far) {
-                    load_f32<T, V>(row_of<const T>(a.x, m, s, b, t - b) + c, win[K - 1]);
-                    load_f32<T, V>(row_of<const T>(a.dy, m, s, b, t - b) + c, g);
-                    dpre<V, K>(w, bias, win, a.silu, g);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) g[i] = 0.0f, win[K - 1][i] = 0.0f;
+            for (; t < e + K - 1; t += kAhead) {
+                const Ahead<T, V> cx = nx, cg = ng;
+                if (t + kAhead < far) {
+                    nx.load(a.x, m, s, b, t + kAhead - b, far - b, c);
+                    ng.load(a.dy, m, s, b, t + kAhead - b, far - b, c);
                 }
-                if (t < e) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        db[i] += g[i];
+                for (int u = 0; u < kAhead; ++u) {
+                    const int r = t + u;
+                    if (r >= e + K - 1) break;
+                    float g[V];
+                    if (r < far) {
+                        cx.r[u].values(win[K - 1]);
+                        cg.r[u].values(g);
+                        dpre<V, K>(w, bias, win, a.silu, g);
+                    } else {
 #pragma unroll
-                        for (int k = 0; k < K; ++k)
-                            dw[k][i] = __builtin_fmaf(g[i], win[k][i], dw[k][i]);
+                        for (int i = 0; i < V; ++i) g[i] = 0.0f, win[K - 1][i] = 0.0f;
                     }
+                    if (r < e) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            db[i] += g[i];
+#pragma unroll
+                            for (int k = 0; k < K; ++k)
+                                dw[k][i] = __builtin_fmaf(g[i], win[k][i], dw[k][i]);
+                        }
+                    }
+                    // Row r-j takes w[K-1-j] * dv[r].
+#pragma unroll
+                    for (int j = 0; j < K; ++j)
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            acc[j][i] = __builtin_fmaf(w[K - 1 - j][i], g[i], acc[j][i]);
+                    const int done = r - (K - 1);
+                    if (done >= first && done < e) {
+                        add_dfinal<T, V, K>(a, s, n, done - b, c, acc[K - 1]);
+                        store_f32<T, V>(row_of<T>(a.dx, m, s, b, done - b) + c, acc[K - 1]);
+                    }
+#pragma unroll
+                    for (int j = K - 1; j > 0; --j)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) acc[j][i] = acc[j - 1][i];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[0][i] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) win[k][i] = win[k + 1][i];
                 }
-                // Row t-j takes w[K-1-j] * dv[t].
-#pragma unroll
-                for (int j = 0; j < K; ++j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        acc[j][i] = __builtin_fmaf(w[K - 1 - j][i], g[i], acc[j][i]);
-                const int done = t - (K - 1);
-                if (done >= first && done < e) {
-                    add_dfinal<T, V, K>(a, s, n, done - b, c, acc[K - 1]);
-                    store_f32<T, V>(row_of<T>(a.dx, m, s, b, done - b) + c, acc[K - 1]);
-                }
-#pragma unroll
-                for (int j = K - 1; j > 0; --j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) acc[j][i] = acc[j - 1][i];
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[0][i] = 0.0f;
-#pragma unroll
-                for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) win[k][i] = win[k + 1][i];
             }
             t = e;
         }
@@ -374,13 +402,13 @@ void widest_rows(Widest& w, const tg_causal_conv_args& a, const tg_rows& r) {
     if (!a.seqs.offsets) w.len(r.seq_stride);
 }
 
-// Rows for each strip. The K-1 rows in front of a strip are read twice (from
-// the cache), so strips are long where that still leaves some 2000 waves.
-int strip_of(int64_t rows, int D, int V, int most) {
-    int strip = most;
-    const int64_t waves = ceil_div(ceil_div(D, V), 64);
-    while (strip > 4 && waves * ceil_div(rows, strip) < 2048) strip /= 2;
-    return strip;
+// Rows for each strip: the K-1 rows in front of a strip are read twice (from
+// the cache), so no more strips than `waves` waves want, of 4 to `most` rows.
+// Forward 4096 waves (16384 x 2048 bf16: 28 us, 9001 x 1000 f16: 12; 8192 waves 30 and
+// 14), backward 2048 (9001 x 1000 f16 with its sums: 28 us; 1536 waves 30, 3072: 29).
+int strip_of(int64_t rows, int D, int V, int most, int waves) {
+    const int64_t strip = ceil_div(rows * ceil_div(ceil_div(D, V), 64), waves);
+    return (int)(strip < 4 ? 4 : strip > most ? most : strip);
 }
 
 }  // namespace
@@ -397,7 +425,7 @@ hipError_t launch_causal_conv(const tg_causal_conv_args& a, hipStream_t st) {
     if (a.final) w.ptr(a.final, e);
     const int V = vec_for(dtype, w);
     const Block bl = conv_block(a.D, V);
-    const int strip = strip_of(a.seqs.rows, a.D, V, 16);
+    const int strip = strip_of(a.seqs.rows, a.D, V, 32, 4096);
     const int strips = (int)ceil_div(a.seqs.rows, strip);
     const ConvFwd f{map_of(a.seqs), a.D, K, a.act == TG_ACT_SILU, strip, rows_of<const void>(a.x),
                     rows_of<void>(a.y), a.w, a.bias, a.initial, a.final};
@@ -427,7 +455,7 @@ int bwd_vec(const tg_causal_conv_args& a, const tg_rows* dy, const tg_rows* dx, 
 // Strips of the backward pass by the sizes alone (the workspace is asked for
 // before all pointers are known).
 int bwd_strip(const tg_causal_conv_args& a) {
-    return strip_of(a.seqs.rows, a.D, (int)(8 / elem_bytes(a.dtype)), 64);
+        return strip_of(a.seqs.rows, a.D, (int)(8 / elem_bytes(a.dtype)), 64, 2048);
 }
 }  // namespace
 

@@ -89,21 +89,37 @@ struct SeqMap {
     // slots apart, so rows/P + seqs slots serve any lengths, which the host
     // does not know.
     __device__ __forceinline__ int slot0(int s, int P) const { return start(s) / P + s; }
+    // The last sequence s with at(s) <= key (0 if there is none), by all 64
+    // lanes of a wave: each round narrows the range 64 times with one load.
+    template <typename At>
+    __device__ __forceinline__ int last_at(int key, At at) const {
+        const int lane = threadIdx.x & 63;
+        int lo = 0, hi = seqs;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 63) >> 6, s = lo + lane * step;
+            const int n = __popcll(__ballot(s < hi && at(s) <= key));
+            if (n > 1) lo += (n - 1) * step;
+            hi = imin(lo + step, hi);
+        }
+        return __builtin_amdgcn_readfirstlane(lo);
+    }
     // The sequence that owns `slot`: the last one whose slot0 is not past it.
+    // By whole waves, like holder().
     __device__ __forceinline__ int owner(int slot, int P) const {
         if (!offsets) {
-            // start(s)/P + s grows by at least one with s, so s <= slot.
-            const int64_t step = (int64_t)L + P;  // (s*L)/P + s = floor(s*(L+P)/P)
-            int64_t s = (((int64_t)slot + 1) * P - 1) / step;
+            // slot0(s) = floor(s*L/P) + s = floor(s*(L+P) / P)
+            const int64_t step = (int64_t)L + P;
+            const int64_t s = (((int64_t)slot + 1) * P - 1) / step;
             return (int)(s < seqs - 1 ? s : seqs - 1);
         }
-        int lo = 0, hi = seqs - 1;
-        while (lo < hi) {
-            const int m = (lo + hi + 1) >> 1;
-            if (slot0(m, P) <= slot) lo = m;
-            else hi = m - 1;
-        }
-        return lo;
+        return last_at(slot, [&](int s) { return slot0(s, P); });
+    }
+    // The sequence that holds row t < rows, past any empty ones: the last one that
+    // starts at or before t. Rows that wrong offsets leave uncovered belong to a
+    // sequence that ended before them.
+    __device__ __forceinline__ int holder(int t) const {
+        if (!offsets) return t / L;
+        return last_at(t, [&](int s) { return start(s); });
     }
 };
 
