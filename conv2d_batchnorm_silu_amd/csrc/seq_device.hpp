@@ -84,11 +84,13 @@ struct SeqMap {
         return v < b ? b : (v > rows ? rows : v);
     }
     // Pieces of P rows, counted through the batch: sequence s owns the slots
-    // from start(s)/P + s on, one for each P rows of it (the last may be
-    // short). floor(a/P) + floor(b/P) <= floor((a+b)/P) keeps the sequences'
-    // slots apart, so rows/P + seqs slots serve any lengths, which the host
-    // does not know.
-    __device__ __forceinline__ int slot0(int s, int P) const { return start(s) / P + s; }
+    // from slot0(s) on, one for each P rows of it (the last may be short). In
+    // a packed batch slot0 = floor(start/P) + s: floor(a/P) + floor(b/P) <=
+    // floor((a+b)/P) keeps the sequences' slots apart, so rows/P + seqs slots
+    // serve any lengths, which the host does not know.
+    __device__ __forceinline__ int slot0(int s, int P) const {
+        return offsets ? start(s) / P + s : s * ((L + P - 1) / P);
+    }
     // The last sequence s with at(s) <= key (0 if there is none), by all 64
     // lanes of a wave: each round narrows the range 64 times with one load.
     template <typename At>
@@ -106,12 +108,7 @@ struct SeqMap {
     // The sequence that owns `slot`: the last one whose slot0 is not past it.
     // By whole waves, like holder().
     __device__ __forceinline__ int owner(int slot, int P) const {
-        if (!offsets) {
-            // slot0(s) = floor(s*L/P) + s = floor(s*(L+P) / P)
-            const int64_t step = (int64_t)L + P;
-            const int64_t s = (((int64_t)slot + 1) * P - 1) / step;
-            return (int)(s < seqs - 1 ? s : seqs - 1);
-        }
+        if (!offsets) return slot / ((L + P - 1) / P);
         return last_at(slot, [&](int s) { return slot0(s, P); });
     }
     // The sequence that holds row t < rows, past any empty ones: the last one that

@@ -389,6 +389,26 @@ __device__ __forceinline__ float* part_at(const ScanArgs& a, const Place& p, int
     return a.parts + (((p.part0 + part) * 2 + which) * a.D + p.ch) * (4 * NS) + p.q * NS;
 }
 
+// h through parts first, first + step, ... (n of them), from memory four at a time.
+template <int NS>
+__device__ __forceinline__ void fold_parts(const ScanArgs& a, const Place& p, int first, int n,
+                                           int step, float (&h)[NS]) {
+    for (int k = 0; k < n; k += 4) {
+        float P[4][NS], e[4][NS];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int part = first + imin(k + u, n - 1) * step;
+            get<NS>(part_at<NS>(a, p, part, 0), P[u]);
+            get<NS>(part_at<NS>(a, p, part, 1), e[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (k + u < n)
+#pragma unroll
+                for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(P[u][j], h[j], e[u][j]);
+    }
+}
+
 __device__ __forceinline__ float step_size(const ScanArgs& a, float raw) {
     return a.softplus ? softplus_f32(raw) : raw;
 }
@@ -475,13 +495,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64)
     float A2[NS], h[NS];
     load_A2<NS, true>(a, p, A2);
     load_state<NS, true>(a.initial, a, p, h);
-    for (int k = 0; k < p.part(a.PL); ++k) {
-        float P[NS], e[NS];
-        get<NS>(part_at<NS>(a, p, k, 0), P);
-        get<NS>(part_at<NS>(a, p, k, 1), e);
-#pragma unroll
-        for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(P[j], h[j], e[j]);
-    }
+    if (a.PL) fold_parts<NS>(a, p, 0, p.part(a.PL), 1, h);
     const float skip = a.D_skip ? a.D_skip[p.ch] : 0.0f;
     const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
     constexpr int E = sizeof(T);
@@ -724,14 +738,10 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
     float A2[NS], c[NS], dA[NS], lost[NS];
     load_A2<NS, false>(a, p, A2);
     load_state<NS, false>(b.dfinal, a, p, c);
-    if (a.PL)
-        for (int k = (p.len - 1) / a.PL; k > p.part(a.PL); --k) {
-            float P[NS], e[NS];
-            get<NS>(part_at<NS>(a, p, k, 0), P);
-            get<NS>(part_at<NS>(a, p, k, 1), e);
-#pragma unroll
-            for (int j = 0; j < NS; ++j) c[j] = __builtin_fmaf(P[j], c[j], e[j]);
-        }
+    if (a.PL) {
+        const int last = p.len > 0 ? (p.len - 1) / a.PL : 0;
+        fold_parts<NS>(a, p, last, last - p.part(a.PL), -1, c);
+    }
 #pragma unroll
     for (int j = 0; j < NS; ++j) dA[j] = lost[j] = 0.0f;
     const float skip = a.D_skip ? a.D_skip[p.ch] : 0.0f;
@@ -1120,16 +1130,19 @@ Plan plan_of(const tg_scan_args& a, bool forward) {
     p.waves = groups >= 4096 ? 1 : waves_for(p.ns);
     p.PL = 0;
     p.slots = a.seqs.seqs;
-    // Fewer than eight waves for each compute unit: parts of the sequences, so
-    // many that there would be sixteen, and not shorter than two rounds of a workgroup.
-    if (p.waves > 1 && groups * p.waves < 2048) {
+    // Fewer than four waves for each compute unit: parts of the sequences, so
+    // many that there are sixteen, and not shorter than two rounds of a workgroup.
+    // The parts' own pass costs two thirds of the scan and a launch: 9 packed
+    // sequences with 1728 waves take 24 to 33 us whole and 33 to 37 in parts.
+    if (p.waves > 1 && groups * p.waves < 1024) {
         const int64_t round = (int64_t)p.waves * p.tt;
         int64_t pl = a.seqs.rows * p.nb * p.waves / 4096 / round * round;
         if (pl < 2 * round) pl = 2 * round;
         const int64_t longest = a.seqs.offsets ? a.seqs.rows : a.seqs.rows / a.seqs.seqs;
         if (pl < longest) {
             p.PL = (int)pl;
-            p.slots = a.seqs.rows / pl + a.seqs.seqs;
+            p.slots = a.seqs.offsets ? a.seqs.rows / pl + a.seqs.seqs
+                                     : a.seqs.seqs * ceil_div(longest, pl);
         }
     }
     return p;
