@@ -201,7 +201,7 @@ __device__ __forceinline__ void wave_sync() {
 // channels; a lane's channel and states. Neighbouring blocks share the cache lines of
 // x, dt, z and y (16 channels are a quarter of one), so they run on one XCD.
 struct Place {
-    int s, start, len, lo, hi, block, g, cl, q, ch, w;
+    int slot, s, start, len, lo, hi, block, g, cl, q, ch, w;
     int64_t part0;  // the slot of the sequence's first part
     bool in;
     // by_rows: lane q*16 + channel (what the matrix instructions give), else
@@ -209,7 +209,7 @@ struct Place {
     __device__ __forceinline__ Place(const ScanArgs& a, bool by_rows) {
         const SeqMap& m = a.seqs;
         const int tile = xcd_contiguous_tile(blockIdx.x, gridDim.x), nb = a.G * a.bpg;
-        const int slot = tile / nb;
+        slot = tile / nb;
         block = tile - slot * nb;
         s = a.PL ? m.owner(slot, a.PL) : slot;
         start = m.start(s);
@@ -709,8 +709,7 @@ struct ScanGrads {
     Rows<void> dx, ddt, dz;
     float* dinitial;
     float* part_bc;  // [blocks of channels][rows][2][4*NS]: dB, dC of a block
-    float* part_a;   // [slots][D][N]
-    float* part_d;   // [slots][2][D]: dD, ddt_bias
+    float* part_a;   // [slots][D*N + 2*D]: dA, dD, ddt_bias of a sequence or part
 };
 
 // The chunks of a sequence (or part) from the last to the first. In each, the states
@@ -729,7 +728,14 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
     extern __shared__ float4 lds[];
     const int W = SPLIT ? blockDim.x >> 6 : 1;
     const Place p(a, false);
-    if (p.lo < 0) return;
+    float* const sums = b.part_a + (int64_t)p.slot * a.D * (a.N + 2);
+    if (p.lo < 0) {  // nobody's slot adds nothing
+        if (p.w == 0 && p.in) {
+            if (p.q < 2) sums[(int64_t)a.D * a.N + p.q * a.D + p.ch] = 0.0f;
+            for (int n = p.q; n < a.N; n += 4) sums[(int64_t)p.ch * a.N + n] = 0.0f;
+        }
+        return;
+    }
     BackTile<NS, TT>& both = ((BackTile<NS, TT>*)lds)[p.w];
     Tile<NS, TT>& tile = both.f;
     float* const exchange = (float*)((BackTile<NS, TT>*)lds + W);
@@ -950,12 +956,11 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
             }
     }
     if (p.w != 0 || !p.in) return;
-    const int64_t out = a.PL ? p.part0 + p.part(a.PL) : p.s;
-    if (p.q < 2) b.part_d[(out * 2 + p.q) * a.D + p.ch] = p.q == 0 ? dD : dbias;
+    if (p.q < 2) sums[(int64_t)a.D * a.N + p.q * a.D + p.ch] = p.q == 0 ? dD : dbias;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
         const int n = p.q * NS + j;
-        if (n < a.N) b.part_a[(out * a.D + p.ch) * a.N + n] = dA[j];
+        if (n < a.N) sums[(int64_t)p.ch * a.N + n] = dA[j];
     }
     if (p.lo == 0) store_state<NS, false>(b.dinitial, a, p, c);
 }
@@ -1029,34 +1034,56 @@ __global__ __launch_bounds__(64 * waves_for(NS)) void scan_bwd_parts(const ScanA
     put<NS>(part_at<NS>(a, p, p.part(a.PL), 1), c);
 }
 
-// dB and dC of the rows that the sequences cover: sums over a group's blocks
-// of channels, each by kPhases threads.
+// The sums over workgroups, each by kPhases threads in a fixed order. The first
+// `rows_blocks` workgroups: dB and dC of the rows that the sequences cover, over a
+// group's blocks of channels; the others: dA, dD and ddt_bias over the slots.
 constexpr int kPhases = 4;
+struct ScanSums {
+    const float *part_bc, *part_a;
+    int NP, slots, rows_blocks;
+    Rows<void> dB, dC;
+    float *dA, *dD, *ddt_bias;
+};
 template <typename T>
-__global__ __launch_bounds__(64 * kPhases) void scan_bc_sums(const ScanArgs a, const float* part,
-                                                             int NP, Rows<void> dB, Rows<void> dC) {
+__global__ __launch_bounds__(64 * kPhases) void scan_sums(const ScanArgs a, const ScanSums b) {
     __shared__ float red[kPhases][64];
     const SeqMap& m = a.seqs;
-    const int lane = threadIdx.x & 63, ph = threadIdx.x >> 6;
-    const int64_t per = (int64_t)a.G * 2 * NP, last = m.end(m.seqs - 1) * per;
-    const int64_t i = m.start(0) * per + (int64_t)blockIdx.x * 64 + lane;
-    const int row = (int)(i / per), r = (int)(i - row * per);
-    const int g = r / (2 * NP), k = r - g * 2 * NP, c = k / NP, n = k - c * NP;
-    const bool in = i < last && n < a.N;
-    float v = 0.0f;
-    if (in) {
-        const float* p = part + (((int64_t)g * a.bpg * m.rows + row) * 2 + c) * NP + n;
-        const int64_t step = (int64_t)m.rows * 2 * NP;
-#pragma unroll 8
-        for (int blk = ph; blk < a.bpg; blk += kPhases) v += p[blk * step];
+    const int lane = threadIdx.x & 63, ph = threadIdx.x >> 6, NP = b.NP;
+    const bool rows = (int)blockIdx.x < b.rows_blocks;
+    const int64_t M = (int64_t)a.D * (a.N + 2), per = (int64_t)a.G * 2 * NP;
+    const float* p = nullptr;
+    int64_t step = M, i = (int64_t)((int)blockIdx.x - b.rows_blocks) * 64 + lane;
+    int row = 0, g = 0, c = 0, n = 0, count = b.slots;
+    if (rows) {
+        i = m.start(0) * per + (int64_t)blockIdx.x * 64 + lane;
+        row = (int)(i / per);
+        const int r = (int)(i - row * per), k = r % (2 * NP);
+        g = r / (2 * NP), c = k / NP, n = k - c * NP;
+        step = (int64_t)m.rows * 2 * NP;
+        count = a.bpg;
+        if (i < m.end(m.seqs - 1) * per && n < a.N)
+            p = b.part_bc + (((int64_t)g * a.bpg * m.rows + row) * 2 + c) * NP + n;
+    } else if (i < M) {
+        p = b.part_a + i;
     }
+    float v = 0.0f;
+    if (p)
+#pragma unroll 8
+        for (int k = ph; k < count; k += kPhases) v += p[k * step];
     red[ph][lane] = v;
     __syncthreads();
-    if (ph != 0 || !in) return;
+    if (ph != 0 || !p) return;
 #pragma unroll
     for (int j = 1; j < kPhases; ++j) v += red[j][lane];
-    const int s = m.offsets ? 0 : row / m.L;
-    row_of<T>(c ? dC : dB, m, s, 0, m.offsets ? row : row - s * m.L)[g * a.N + n] = (T)v;
+    if (rows) {
+        const int s = m.offsets ? 0 : row / m.L;
+        row_of<T>(c ? b.dC : b.dB, m, s, 0, m.offsets ? row : row - s * m.L)[g * a.N + n] = (T)v;
+        return;
+    }
+    const int64_t dn = (int64_t)a.D * a.N;
+    if (i < dn) b.dA[i] = v;
+    else if (i < dn + a.D && b.dD) b.dD[i - dn] = v;
+    else if (i >= dn + a.D && b.ddt_bias) b.ddt_bias[i - dn - a.D] = v;
 }
 
 struct StepArgs {
@@ -1212,30 +1239,14 @@ hipError_t bwd_typed(const Plan& p, const ScanArgs& f, const ScanGrads& b, hipSt
 }
 
 struct BackwardWs {
-    size_t a, d, bc, parts, total;  // [a][d]: zeroed, see launch_scan_backward
+    size_t bc, parts, total;  // the sums of dA, dD and ddt_bias come first
 };
 BackwardWs backward_ws(const tg_scan_args& a, const Plan& p) {
     BackwardWs w;
-    w.a = 0;
-    w.d = w.a + up256((size_t)p.slots * a.D * a.N * sizeof(float));
-    w.bc = w.d + up256((size_t)p.slots * 2 * a.D * sizeof(float));
+    w.bc = up256((size_t)p.slots * a.D * (a.N + 2) * sizeof(float));
     w.parts = w.bc + up256((size_t)p.nb * a.seqs.rows * 2 * 4 * p.ns * sizeof(float));
     w.total = w.parts + parts_bytes(a, p);
     return w;
-}
-
-// Slots that no part of a sequence owns count as zero in the sums.
-__global__ __launch_bounds__(256) void scan_clear_slots(const ScanArgs a, int slots, float* part_a,
-                                                        float* part_d) {
-    const int slot = blockIdx.y, s = a.seqs.owner(slot, a.PL);
-    const int len = a.seqs.end(s) - a.seqs.start(s), first = a.seqs.slot0(s, a.PL);
-    if (slot == first || (int64_t)(slot - first) * a.PL < len) return;
-    const int64_t n = (int64_t)a.D * a.N;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n + 2 * a.D;
-         i += (int64_t)gridDim.x * 256) {
-        if (i < n) part_a[slot * n + i] = 0.0f;
-        else part_d[(int64_t)slot * 2 * a.D + (i - n)] = 0.0f;
-    }
 }
 
 }  // namespace
@@ -1267,34 +1278,22 @@ hipError_t launch_scan_backward(const tg_scan_args& a, const tg_scan_grads& g, c
     const ScanArgs f = args_of(a, p, nullptr, base + w.parts);
     const ScanGrads b{rows_of<const void>(g.dy), g.dfinal, (const float*)saved,
                       rows_of<void>(g.dx), rows_of<void>(g.ddt), rows_of<void>(g.dz), g.dinitial,
-                      (float*)(base + w.bc), (float*)(base + w.a), (float*)(base + w.d)};
+                      (float*)(base + w.bc), (float*)base};
     hipError_t e = hipSuccess;
-    if (p.PL) {
-        scan_clear_slots<<<dim3(16, (unsigned)p.slots), 256, 0, st>>>(f, (int)p.slots, b.part_a,
-                                                                      b.part_d);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
 #define TG_X(T, NS) e = bwd_typed<T, NS>(p, f, b, st)
     TG_SCAN_DISPATCH(TG_X);
 #undef TG_X
     if (e != hipSuccess) return e;
-    if (a.seqs.rows > 0) {
-        const int np = 4 * p.ns;
-        const unsigned sums = (unsigned)ceil_div(a.seqs.rows * a.G * 2 * np, 64);
-        constexpr int threads = 64 * kPhases;
-        const Rows<void> dB = rows_of<void>(g.dB), dC = rows_of<void>(g.dC);
-        if (dtype == TG_F32) scan_bc_sums<float><<<sums, threads, 0, st>>>(f, b.part_bc, np, dB, dC);
-        else if (dtype == TG_BF16) scan_bc_sums<bf16><<<sums, threads, 0, st>>>(f, b.part_bc, np, dB, dC);
-        else scan_bc_sums<f16><<<sums, threads, 0, st>>>(f, b.part_bc, np, dB, dC);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    const int slots = (int)p.slots;
-    const int64_t dn = (int64_t)a.D * a.N;
-    e = launch_column_sums(b.part_a, slots, dn, g.dA, dn, nullptr, st);
-    if (e != hipSuccess || (!g.dD && !g.ddt_bias)) return e;
-    return launch_column_sums(b.part_d, slots, 2 * (int64_t)a.D, g.dD, a.D, g.ddt_bias, st);
+    const int np = 4 * p.ns;
+    const int64_t row_blocks = ceil_div(a.seqs.rows * a.G * 2 * np, 64);
+    const ScanSums s{b.part_bc, b.part_a, np, (int)p.slots, (int)row_blocks,
+                     rows_of<void>(g.dB), rows_of<void>(g.dC), g.dA, g.dD, g.ddt_bias};
+    const unsigned grid = (unsigned)(row_blocks + ceil_div((int64_t)a.D * (a.N + 2), 64));
+    constexpr int threads = 64 * kPhases;
+    if (dtype == TG_F32) scan_sums<float><<<grid, threads, 0, st>>>(f, s);
+    else if (dtype == TG_BF16) scan_sums<bf16><<<grid, threads, 0, st>>>(f, s);
+    else scan_sums<f16><<<grid, threads, 0, st>>>(f, s);
+    return hipGetLastError();
 }
 
 hipError_t launch_scan_step(const tg_scan_args& a, float* state, int64_t num_slots,
