@@ -570,7 +570,19 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64)
             // The other buffer is written next, past this barrier of the next
             // round: nobody still reads it then.
             get<NS>(exchange_at<NS>(ex, W, 0), r);
-            for (int k = 0; k < p.w; ++k) {
+            // Two segments at a time: one by one the reads' latency adds up.
+            int k = 0;
+            for (; k + 1 < p.w; k += 2) {
+                float P1[NS], e1[NS];
+                get<NS>(exchange_at<NS>(ex, k, 0), P);
+                get<NS>(exchange_at<NS>(ex, k, 1), e);
+                get<NS>(exchange_at<NS>(ex, k + 1, 0), P1);
+                get<NS>(exchange_at<NS>(ex, k + 1, 1), e1);
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    r[j] = __builtin_fmaf(P1[j], __builtin_fmaf(P[j], r[j], e[j]), e1[j]);
+            }
+            if (k < p.w) {
                 get<NS>(exchange_at<NS>(ex, k, 0), P);
                 get<NS>(exchange_at<NS>(ex, k, 1), e);
 #pragma unroll
