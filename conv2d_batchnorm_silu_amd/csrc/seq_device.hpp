@@ -73,12 +73,12 @@ __device__ __forceinline__ float wave_sum(float v) {
 struct SeqMap {
     const int32_t* offsets;
     int seqs, rows, L;
-    __device__ __forceinline__ int start(int s) const {
+    __host__ __device__ __forceinline__ int start(int s) const {
         if (!offsets) return s * L;
         const int v = offsets[s];
         return v < 0 ? 0 : (v > rows ? rows : v);
     }
-    __device__ __forceinline__ int end(int s) const {
+    __host__ __device__ __forceinline__ int end(int s) const {
         if (!offsets) return (s + 1) * L;
         const int b = start(s), v = offsets[s + 1];
         return v < b ? b : (v > rows ? rows : v);
@@ -88,8 +88,19 @@ struct SeqMap {
     // a packed batch slot0 = floor(start/P) + s: floor(a/P) + floor(b/P) <=
     // floor((a+b)/P) keeps the sequences' slots apart, so rows/P + seqs slots
     // serve any lengths, which the host does not know.
-    __device__ __forceinline__ int slot0(int s, int P) const {
+    __host__ __device__ __forceinline__ int slot0(int s, int P) const {
         return offsets ? start(s) / P + s : s * ((L + P - 1) / P);
+    }
+    // The rows lo .. hi-1 of sequence s (len rows) in `slot`, its first slot
+    // being first. False for a slot past the sequence's (or, with wrong offsets,
+    // before them), which belongs to nobody. An empty sequence has one slot.
+    static __host__ __device__ __forceinline__ bool piece(int slot, int first, int len, int P,
+                                                          int& lo, int& hi) {
+        const int64_t l = ((int64_t)slot - first) * P;
+        if (l != 0 && (l < 0 || l >= len)) return false;
+        lo = (int)l;
+        hi = l + P < len ? (int)l + P : len;
+        return true;
     }
     // The last sequence s with at(s) <= key (0 if there is none), by all 64
     // lanes of a wave: each round narrows the range 64 times with one load.

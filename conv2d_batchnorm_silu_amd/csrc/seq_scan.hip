@@ -217,11 +217,7 @@ struct Place {
         lo = 0, hi = len, part0 = 0;
         if (a.PL) {
             part0 = m.slot0(s, a.PL);
-            const int64_t l = (int64_t)(slot - part0) * a.PL;
-            // A slot past the sequence's parts belongs to nobody; an empty
-            // sequence has one part, which passes its state on.
-            lo = l < len || l == 0 ? (int)l : -1;
-            hi = imin(len, lo + a.PL);
+            if (!SeqMap::piece(slot, (int)part0, len, a.PL, lo, hi)) lo = -1;
         }
         g = block / a.bpg;
         const int c0 = (block - g * a.bpg) * kCh;
@@ -1221,8 +1217,12 @@ template <typename Kernel, typename... Args>
 hipError_t launch_waves(Kernel kernel, const Plan& p, size_t tile, int buffers, hipStream_t st,
                         const Args&... args) {
     const size_t bytes = p.waves * tile + (p.waves > 1 ? buffers * exchange_floats(p.waves, p.ns) * sizeof(float) : 0);
-    const hipError_t e = ensure_dynamic_lds((const void*)kernel, bytes);
-    if (e != hipSuccess) return e;
+    try {
+        const hipError_t e = ensure_dynamic_lds((const void*)kernel, bytes);
+        if (e != hipSuccess) return e;
+    } catch (...) {  // its record of kernels could not grow
+        return hipErrorOutOfMemory;
+    }
     kernel<<<(unsigned)(p.slots * p.nb), 64 * p.waves, bytes, st>>>(args...);
     return hipGetLastError();
 }

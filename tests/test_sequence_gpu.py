@@ -478,3 +478,98 @@ def test_refuses_host_and_mismatched_tensors():
         tg.selective_scan_step(x[0], x[0], a, b[0], b[0], torch.zeros(2, 8, 4, device="cuda"))
     with pytest.raises(ValueError, match="saved must have shape"):
         tg.selective_scan_backward(x, x, x, a, b, b, torch.zeros(5, device="cuda"))
+
+
+# ---- many sequences, far rows, wrong offsets
+
+def _many(S, L, D, N, dt=F32, seed=5):
+    r = Rand(seed)
+    dev = lambda *s, **k: r(*s, **k).cuda()  # noqa: E731
+    x = [dev(S, L, D, dtype=dt), dev(S, L, D, dtype=dt, scale=0.5),
+         -torch.arange(1, N + 1).float().repeat(D, 1).cuda(), dev(S, L, 1, N, dtype=dt), dev(S, L, 1, N, dtype=dt)]
+    return x, dict(D=dev(D), z=dev(S, L, D, dtype=dt), dt_bias=dev(D, shift=-3.0), initial_state=dev(S, D, N)), dev(S, L, D, dtype=dt)
+
+
+@pytest.mark.parametrize("N", [3, 8, 16, 30, 64, 128])
+def test_scan_many_sequences(N):
+    """So many sequences that single waves take them whole: against the 64-bit
+    reference for some, and dA, dD and ddt_bias against the sum over small batches."""
+    S, L, D = 4100, 19, 16
+    note("scan of %d sequences, N=%d" % (S, N))
+    args, more, dy = _many(S, L, D, N)
+    y, state, saved = tg.selective_scan_train(*args, return_state=True, **more)
+    g = tg.selective_scan_backward(dy, *args, saved, **more)
+    for i in (0, 1, 2047, S - 1):
+        cut = lambda t: t[i].double().cpu()  # noqa: E731
+        ref = (cut(args[0]), cut(args[1]), args[2].double().cpu(), cut(args[3]), cut(args[4]), more["D"].double().cpu(),
+               cut(more["z"]), more["dt_bias"].double().cpu(), True, cut(more["initial_state"]))
+        (v, b), (h, eh), _ = R.scan(*ref)
+        R.check("y", y[i], v, b)
+        R.check("state", state[i], h, eh)
+        w = R.scan_grads(cut(dy), *ref)
+        for name, got in (("dx", g.dx), ("ddt", g.ddt), ("dz", g.dz), ("dB", g.dB), ("dC", g.dC), ("dinit", g.dinitial_state)):
+            R.check(name, got[i], *w[name])
+    total = None
+    for lo in range(0, S, 205):
+        hi = min(S, lo + 205)
+        part = [t[lo:hi] if t.dim() > 2 else t for t in args]
+        m = {k: t[lo:hi] if t.dim() > 1 else t for k, t in more.items()}
+        _, sv = tg.selective_scan_train(*part, **m)
+        p = tg.selective_scan_backward(dy[lo:hi], *part, sv, **m)
+        three = [p.dA.double(), p.dD.double(), p.ddt_bias.double()]
+        total = three if total is None else [a + b for a, b in zip(total, three)]
+    for name, got, want in zip(("dA", "dD", "ddt_bias"), (g.dA, g.dD, g.ddt_bias), total):
+        # 4100 * 19 terms of either sign, each side's sums in fp32 trees of under 2^11 terms a level.
+        assert float((got.double() - want).norm()) <= 1e-5 * float(want.norm()) + 1e-6, name
+
+
+def test_rows_far_apart():
+    """Row strides that put the last rows past 2^31 elements and 2^32 bytes."""
+    rows, stride, D = 1500, 1500000, 24
+    big = torch.empty(rows, stride, dtype=F16, device="cuda")
+    r = Rand(8)
+    small = [r(rows, D, dtype=F16) for _ in range(3)]
+    view = []
+    for k, t in enumerate(small):
+        view.append(big[:, 1000 * k:1000 * k + D])
+        view[k].copy_(t)
+    near = [t.cuda() for t in small]
+    off = torch.tensor([0, 700, 700, 701, rows], dtype=torch.int32, device="cuda")
+    w, g = r(4, D).cuda(), r(D).cuda()
+    same = lambda f: [(a, b) for a, b in zip(f(near), f(view))]  # noqa: E731
+    A = -torch.ones(D, 4).cuda()
+    bc = lambda t: t[:, :4].unflatten(-1, (1, 4))  # noqa: E731
+
+    def everything(v):
+        y, s, mean, rstd = tg.layer_norm_train(v[0], g, residual=v[1])
+        out = [y, s, *tg.layer_norm_backward(v[2], v[0], g, mean, rstd, dsum=v[1])]
+        out += [tg.causal_conv(v[0], w, offsets=off), *tg.causal_conv_backward(v[1], v[0], w, offsets=off)[:3]]
+        sy, saved = tg.selective_scan_train(v[0], v[1], A, bc(v[1]), bc(v[2]), z=v[2], offsets=off)
+        d = tg.selective_scan_backward(v[1], v[0], v[1], A, bc(v[1]), bc(v[2]), saved, z=v[2], offsets=off)
+        return out + [sy, d.dx, d.ddt, d.dA, d.dB, d.dC, d.dz]
+    for k, (a, b) in enumerate(same(everything)):
+        assert torch.equal(a, b), k
+    with pytest.raises(tg.TgError, match="TG_ERR_UNSUPPORTED"):  # rows too far apart for the scan
+        far = torch.empty(2, 1 << 25, dtype=F16, device="cuda")[:, :D]
+        tg.selective_scan(far, far, A, bc(far), bc(far), offsets=off[:2])
+
+
+@pytest.mark.parametrize("wrong", [[5, 9, 40], [0, 50, 20], [-7, 3, 1000], [30, 10, 0], [40, 40, 40]], ids=str)
+def test_wrong_offsets_stay_inside(wrong):
+    """Offsets that break the contract are cut to the rows: results are not
+    specified, but nothing past the outputs is written."""
+    note("wrong offsets %s" % wrong)
+    rows, D, N = 40, 16, 16
+    c = ScanCase(([rows], True, D, N, 1, "f32", True, True, False, 0))
+    off = torch.tensor(wrong, dtype=torch.int32, device="cuda")
+    guard = torch.full((3 * rows, D), 7.0, device="cuda")
+    out = guard[rows:2 * rows]
+    args, more = c.args(), c.more()
+    more.pop("initial_state"), more.pop("offsets")
+    tg.selective_scan(*args, offsets=off, out=out, **more)
+    y, saved = tg.selective_scan_train(*args, offsets=off, **more)
+    tg.selective_scan_backward(c.dev(c.x), *args, saved, offsets=off, **more)
+    tg.causal_conv(args[0], torch.ones(4, D, device="cuda"), offsets=off, out=out, return_state=True)
+    tg.causal_conv_backward(args[1], args[0], torch.ones(4, D, device="cuda"), offsets=off)
+    torch.cuda.synchronize()
+    assert bool((guard[:rows] == 7).all()) and bool((guard[2 * rows:] == 7).all())
