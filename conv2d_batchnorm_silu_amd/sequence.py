@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import struct
 
 import torch
 
@@ -60,6 +61,12 @@ class _ScanGrads(ctypes.Structure):
                 ("dinitial", vp)]
 
 
+# The same layouts as flat numbers: filling a ctypes structure field by field
+# takes several microseconds, which a single token's call would mostly consist of.
+_CONV = struct.Struct("3q4i10q")
+_SCAN = struct.Struct("3q5i4x23q")
+assert _CONV.size == ctypes.sizeof(_ConvArgs) and _SCAN.size == ctypes.sizeof(_ScanArgs)
+
 ScanGradients = collections.namedtuple(
     "ScanGradients", "dx ddt dA dB dC dD dz ddt_bias dinitial_state")
 
@@ -72,7 +79,8 @@ def _lib():
         return _loaded
     lib = library()
     f, psz = ctypes.c_float, ctypes.POINTER(sz)
-    conv, scan, grads = (ctypes.POINTER(t) for t in (_ConvArgs, _ScanArgs, _ScanGrads))
+    conv = scan = vp  # structures, or bytes of their layout
+    grads = ctypes.POINTER(_ScanGrads)
     lib.tg_layer_norm.argtypes = [vp, i64, vp, i64, vp, vp, f, i64, i32, i32, vp, vp, vp, vp, vp]
     lib.tg_layer_norm_backward_workspace.argtypes = [i64, i32, i32, psz]
     lib.tg_layer_norm_backward.argtypes = ([vp, i64, vp, i64, vp, vp, vp, vp, i64, i64, i32, i32]
@@ -326,15 +334,16 @@ def _taps(w):
 
 
 def _conv_args(x, w, bias, act, initial_state, offsets, dev):
-    dt = _dtype(x, "x")
-    S, rows, off = _batch(x, offsets, dev)
+    """A function of (y's rows, address of the final states) that gives the
+    call's arguments; whether the batch is packed; the states' shape; D."""
+    dt, dtype = _dtype(x, "x"), x.dtype
+    seqs = _batch(x, offsets, dev)
     packed, D, K = offsets is not None, x.shape[-1], _taps(w)
-    held = (S, K - 1, D)
-    a = _ConvArgs((S, rows, off), D, K, dt, _activation(act),
-                  _rows(x, "x", dev, x.shape, x.dtype, packed, D), _NO_ROWS,
-                  _flat(w, "w", dev, (K, D)), _flat(bias, "bias", dev, (D,)),
-                  _flat(initial_state, "initial_state", dev, held, x.dtype), 0)
-    return a, packed, held
+    held = (seqs[0], K - 1, D)
+    head = (*seqs, D, K, dt, _activation(act), *_rows(x, "x", dev, x.shape, dtype, packed, D))
+    tail = (_flat(w, "w", dev, (K, D)), _flat(bias, "bias", dev, (D,)),
+            _flat(initial_state, "initial_state", dev, held, dtype))
+    return (lambda y, final: _CONV.pack(*head, *y, *tail, final)), packed, held, D
 
 
 def causal_conv(x, w, bias=None, act="silu", initial_state=None, offsets=None, return_state=False,
@@ -351,14 +360,14 @@ def causal_conv(x, w, bias=None, act="silu", initial_state=None, offsets=None, r
     if there is not None:
         with there:
             return causal_conv(x, w, bias, act, initial_state, offsets, return_state, out)
-    a, packed, held = _conv_args(x, w, bias, act, initial_state, offsets, dev)
+    args, packed, held, D = _conv_args(x, w, bias, act, initial_state, offsets, dev)
     y = _new_or(out, x, dev, False)
-    a.y = _place(y, y.stride(), packed, a.D)
-    state = None
+    state, final = None, 0
     if return_state:
         state = torch.empty(held, dtype=x.dtype, device=x.device)
-        a.final = state.data_ptr()
-    _check(_lib().tg_causal_conv(ctypes.byref(a), _raw_stream(dev)), "tg_causal_conv")
+        final = state.data_ptr()
+    _check(_lib().tg_causal_conv(args(_place(y, y.stride(), packed, D), final), _raw_stream(dev)),
+           "tg_causal_conv")
     return (y, state) if return_state else y
 
 
@@ -372,13 +381,13 @@ def causal_conv_backward(dy, x, w, bias=None, act="silu", initial_state=None, of
     if there is not None:
         with there:
             return causal_conv_backward(dy, x, w, bias, act, initial_state, offsets, dstate)
-    a, packed, held = _conv_args(x, w, bias, act, initial_state, offsets, dev)
-    K, D = a.K, a.D
+    args, packed, held, D = _conv_args(x, w, bias, act, initial_state, offsets, dev)
+    a, K = args(_NO_ROWS, 0), held[1] + 1
     g = _rows(_some(dy, "dy"), "dy", dev, x.shape, x.dtype, packed, D)
     df = _flat(dstate, "dstate", dev, held, x.dtype)
     lib = _lib()
     need = sz()
-    _check(lib.tg_causal_conv_backward_workspace(ctypes.byref(a), ctypes.byref(need)),
+    _check(lib.tg_causal_conv_backward_workspace(a, ctypes.byref(need)),
            "tg_causal_conv_backward_workspace")
     dx = torch.empty_like(x, memory_format=_DENSE)
     dw = torch.empty((K + 1, D), dtype=_F32, device=x.device)
@@ -388,7 +397,7 @@ def causal_conv_backward(dy, x, w, bias=None, act="silu", initial_state=None, of
         d0p = d0.data_ptr()
     ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
     _check(lib.tg_causal_conv_backward(
-        ctypes.byref(a), _Rows(*g), _Rows(*_place(dx, dx.stride(), packed, D)), dw.data_ptr(),
+        a, _Rows(*g), _Rows(*_place(dx, dx.stride(), packed, D)), dw.data_ptr(),
         dw.data_ptr() + 4 * K * D, df, d0p, ws.data_ptr(), need.value,
         _raw_stream(dev)), "tg_causal_conv_backward")
     return dx, dw[:K], dw[K], d0
@@ -423,6 +432,8 @@ def causal_conv_step(x, state, w, bias=None, act="silu", slots=None, out=None, s
 # ---------------------------------------------------------- selective scan
 
 def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, seqs, packed, dev):
+    """A function of (y's rows, address of the final states) that gives the
+    call's arguments; channels, N, G."""
     d, dtype, shape = _dtype(x, "x"), x.dtype, x.shape
     lead, width = shape[:-1], shape[-1]
     if A is None or A.dim() != 2:
@@ -438,41 +449,42 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, seqs, pac
         for name, t in (("B", B), ("C", C)):
             if t.dim() == len(gn) and t.stride(-2) != N:
                 raise ValueError("%s: the groups of a row must lie one after another" % name)
-    return _ScanArgs(
-        seqs, width, N, G, d, 1 if softplus else 0,
-        _rows(x, "x", dev, shape, dtype, packed, width),
-        _rows(dt, "dt", dev, shape, dtype, packed, width),
-        _rows(B, "B", dev, gn, dtype, packed, G * N),
-        _rows(C, "C", dev, gn, dtype, packed, G * N),
-        _rows(z, "z", dev, shape, dtype, packed, width), _NO_ROWS,
-        _flat(A, "A", dev, (width, N)), _flat(D, "D", dev, (width,)),
-        _flat(dt_bias, "dt_bias", dev, (width,)),
-        _flat(initial_state, "initial_state", dev, (seqs[0], width, N)), 0)
+    head = (*seqs, width, N, G, d, 1 if softplus else 0,
+            *_rows(x, "x", dev, shape, dtype, packed, width),
+            *_rows(dt, "dt", dev, shape, dtype, packed, width),
+            *_rows(B, "B", dev, gn, dtype, packed, G * N),
+            *_rows(C, "C", dev, gn, dtype, packed, G * N),
+            *_rows(z, "z", dev, shape, dtype, packed, width))
+    tail = (_flat(A, "A", dev, (width, N)), _flat(D, "D", dev, (width,)),
+            _flat(dt_bias, "dt_bias", dev, (width,)),
+            _flat(initial_state, "initial_state", dev, (seqs[0], width, N)))
+    return (lambda y, final: _SCAN.pack(*head, *y, *tail, final)), width, N, G
 
 
 def _scan_forward(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, offsets, want_state,
                   train, out, dev):
-    packed = offsets is not None
-    a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state,
-                   _batch(x, offsets, dev), packed, dev)
+    packed, seqs = offsets is not None, _batch(x, offsets, dev)
+    args, width, N, _ = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, seqs,
+                                   packed, dev)
+    y = _new_or(out, x, dev, False)
+    state, final = None, 0
+    if want_state:
+        state = torch.empty((seqs[0], width, N), dtype=_F32, device=x.device)
+        final = state.data_ptr()
+    a = args(_place(y, y.stride(), packed, width), final)
     lib = _lib()
     work, keep = sz(), sz()
-    _check(lib.tg_selective_scan_sizes(ctypes.byref(a), ctypes.byref(work), ctypes.byref(keep),
-                                       None), "tg_selective_scan_sizes")
-    y = _new_or(out, x, dev, False)
-    a.y = _place(y, y.stride(), packed, a.D)
-    state = saved = ws = None
+    _check(lib.tg_selective_scan_sizes(a, ctypes.byref(work), ctypes.byref(keep), None),
+           "tg_selective_scan_sizes")
+    saved = ws = None
     wp = kp = 0
-    if want_state:
-        state = torch.empty((a.seqs.seqs, a.D, a.N), dtype=_F32, device=x.device)
-        a.final = state.data_ptr()
     if train:
         saved = torch.empty(keep.value // 4, dtype=_F32, device=x.device)
         kp = saved.data_ptr()
     if work.value:
         ws = torch.empty(work.value, dtype=torch.uint8, device=x.device)
         wp = ws.data_ptr()
-    _check(lib.tg_selective_scan(ctypes.byref(a), wp, work.value, kp, keep.value if train else 0,
+    _check(lib.tg_selective_scan(a, wp, work.value, kp, keep.value if train else 0,
                                  _raw_stream(dev)), "tg_selective_scan")
     return y, state, saved
 
@@ -528,16 +540,16 @@ def selective_scan_backward(dy, x, dt, A, B, C, saved, D=None, z=None, dt_bias=N
         with there:
             return selective_scan_backward(dy, x, dt, A, B, C, saved, D, z, dt_bias, softplus,
                                            initial_state, offsets, dstate)
-    packed = offsets is not None
-    a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state,
-                   _batch(x, offsets, dev), packed, dev)
-    S, width, N, gn = a.seqs.seqs, a.D, a.N, a.G * a.N
+    packed, seqs = offsets is not None, _batch(x, offsets, dev)
+    args, width, N, G = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, seqs,
+                                   packed, dev)
+    a, S, gn = args(_NO_ROWS, 0), seqs[0], G * N
     g = _ScanGrads(_rows(_some(dy, "dy"), "dy", dev, x.shape, x.dtype, packed, width),
                    _flat(dstate, "dstate", dev, (S, width, N)))
     lib = _lib()
     keep, need = sz(), sz()
-    _check(lib.tg_selective_scan_sizes(ctypes.byref(a), None, ctypes.byref(keep),
-                                       ctypes.byref(need)), "tg_selective_scan_sizes")
+    _check(lib.tg_selective_scan_sizes(a, None, ctypes.byref(keep), ctypes.byref(need)),
+           "tg_selective_scan_sizes")
     sp = _flat(_some(saved, "saved"), "saved", dev, (keep.value // 4,))
 
     def rows_like(t, w):
@@ -566,8 +578,8 @@ def selective_scan_backward(dy, x, dt, A, B, C, saved, D=None, z=None, dt_bias=N
         d0 = params(S, width, N)
         g.dinitial = d0.data_ptr()
     ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-    _check(lib.tg_selective_scan_backward(ctypes.byref(a), ctypes.byref(g), sp, keep.value,
-                                          ws.data_ptr(), need.value, _raw_stream(dev)),
+    _check(lib.tg_selective_scan_backward(a, ctypes.byref(g), sp, keep.value, ws.data_ptr(),
+                                          need.value, _raw_stream(dev)),
            "tg_selective_scan_backward")
     return ScanGradients(dx, ddt, dA, dB, dC, dD, dz, db, d0)
 
@@ -585,13 +597,14 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, sof
     if x.dim() != 2:
         raise ValueError("x must be [n, channels], got %s" % (tuple(x.shape),))
     n = x.shape[0]
-    a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, None, (n, n, 0), True, dev)
+    args, width, N, _ = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, None, (n, n, 0), True,
+                                   dev)
     num = state.shape[0]
-    hp = _flat(state, "state", dev, (num, a.D, a.N))
+    hp = _flat(state, "state", dev, (num, width, N))
     sp = _flat(slots, "slots", dev, (n,), _I32)
     y = _new_or(out, x, dev, False)
-    a.y = _place(y, y.stride(), True, a.D)
-    st = _lib().tg_selective_scan_step(ctypes.byref(a), hp, num, sp, _raw_stream(dev))
+    st = _lib().tg_selective_scan_step(args(_place(y, y.stride(), True, width), 0), hp, num, sp,
+                                       _raw_stream(dev))
     if st:
         _check(st, "tg_selective_scan_step")
     return y
