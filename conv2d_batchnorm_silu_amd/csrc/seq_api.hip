@@ -7,11 +7,11 @@ using namespace tg;
 
 namespace {
 
-// Row numbers, and a strip or chunk past them, are ints in the kernels; the
-// workgroups of a launch are counted in 32 bits.
+// Row numbers, and a strip or chunk past them, are ints in the kernels; a
+// launch has fewer than 2^32 threads, so the scan's single waves are limited.
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 constexpr int kMaxChannels = 1 << 20;
-constexpr int64_t kMaxGroups = ((int64_t)1 << 31) - 1;
+constexpr int64_t kMaxGroups = ((int64_t)1 << 26) - 1;
 // The scan addresses 16 rows by 31-bit byte offsets.
 constexpr int64_t kMaxScanStride = (int64_t)1 << 25;
 
@@ -221,6 +221,7 @@ tg_status tg_selective_scan_backward(const tg_scan_args* a, const tg_scan_grads*
     TG_CHECK(check_scan(a));
     TG_CHECK(check_scan_inputs(a));
     TG_REQUIRE(g && g->dA && (!g->dz.p == !a->z.p), TG_ERR_INVALID_ARGUMENT);
+    TG_REQUIRE(scan_sum_groups(*a) < (int64_t)1 << 24, TG_ERR_UNSUPPORTED);  // of 256 threads
     const size_t e = elem_bytes(a->dtype);
     const int64_t gn = (int64_t)a->G * a->N;
     TG_CHECK(check_scan_rows(g->dy, a->seqs, a->D, e, false));

@@ -50,6 +50,7 @@ hipError_t launch_causal_conv_step(const void* x, int64_t xs, void* state, int64
                                    hipStream_t st);
 
 void scan_sizes(const tg_scan_args& a, size_t* work, size_t* saved, size_t* backward);
+int64_t scan_sum_groups(const tg_scan_args& a);  // workgroups of the backward pass's sums
 hipError_t launch_scan(const tg_scan_args& a, void* ws, void* saved, hipStream_t st);
 hipError_t launch_scan_backward(const tg_scan_args& a, const tg_scan_grads& g, const void* saved,
                                 void* ws, hipStream_t st);

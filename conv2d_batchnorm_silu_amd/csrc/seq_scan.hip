@@ -1269,6 +1269,13 @@ BackwardWs backward_ws(const tg_scan_args& a, const Plan& p) {
 
 }  // namespace
 
+static int64_t sum_row_groups(const tg_scan_args& a) {
+    return ceil_div(a.seqs.rows * a.G * 2 * 4 * states_for(a.N), 64);
+}
+int64_t scan_sum_groups(const tg_scan_args& a) {
+    return sum_row_groups(a) + ceil_div((int64_t)a.D * (a.N + 2), 64);
+}
+
 void scan_sizes(const tg_scan_args& a, size_t* work, size_t* saved, size_t* backward) {
     const Plan f = plan_of(a, true), p = plan_of(a, false);
     const int64_t slots = a.seqs.rows / p.tt + a.seqs.seqs;
@@ -1303,10 +1310,10 @@ hipError_t launch_scan_backward(const tg_scan_args& a, const tg_scan_grads& g, c
 #undef TG_X
     if (e != hipSuccess) return e;
     const int np = 4 * p.ns;
-    const int64_t row_blocks = ceil_div(a.seqs.rows * a.G * 2 * np, 64);
+    const int64_t row_blocks = sum_row_groups(a);
     const ScanSums s{b.part_bc, b.part_a, np, (int)p.slots, (int)row_blocks,
                      rows_of<void>(g.dB), rows_of<void>(g.dC), g.dA, g.dD, g.ddt_bias};
-    const unsigned grid = (unsigned)(row_blocks + ceil_div((int64_t)a.D * (a.N + 2), 64));
+    const unsigned grid = (unsigned)scan_sum_groups(a);
     constexpr int threads = 64 * kPhases;
     if (dtype == TG_F32) scan_sums<float><<<grid, threads, 0, st>>>(f, s);
     else if (dtype == TG_BF16) scan_sums<bf16><<<grid, threads, 0, st>>>(f, s);

@@ -137,9 +137,9 @@ tg_status tg_causal_conv_step(const void *x, int64_t x_stride, void *state, int6
  *   y[t,c] = v[t] * silu(z[t,c])      (v[t] where z is not given)
  * B and C are shared by the D/G channels of a group g = c / (D/G); a row of
  * B or C is [G][N], contiguous. A fp32 [D][N]; D_skip, dt_bias fp32 [D] or
- * NULL; initial, final fp32 [seqs][D][N] or NULL; final may alias initial
- * only if it is the same buffer. Row strides here stay below 2^25 elements
- * (else TG_ERR_UNSUPPORTED). */
+ * NULL; initial, final fp32 [seqs][D][N] or NULL. TG_ERR_UNSUPPORTED for row
+ * strides of 2^25 elements or more, 2^26 or more pairs of a sequence and 16
+ * channels, and in the backward pass for 2^29 or more values of dB. */
 typedef struct {
     tg_seqs seqs;
     int D, N, G;

@@ -191,3 +191,15 @@ def test_symbols_are_declared():
     names = tg.exported_symbols()
     for n in ("tg_layer_norm", "tg_causal_conv_step", "tg_selective_scan_backward"):
         assert n in names
+
+
+def test_scan_limits(lib):
+    """Launches of 2^32 threads or more are refused, not attempted."""
+    n = 1 << 26
+    assert lib.tg_selective_scan(ctypes.byref(_scan(seqs=n, rows=n)), P, 1 << 60, 0, 0, 0) == UNSUP
+    g = S._ScanGrads(_rows(seq=32), 0, _rows(seq=32), _rows(seq=32), _rows(seq=64, row=16),
+                     _rows(seq=64, row=16), _rows(seq=32), P)
+    big = _scan(rows=1 << 29)
+    assert lib.tg_selective_scan_backward(ctypes.byref(big), ctypes.byref(g), P, 1 << 60, P, 1 << 60, 0) == UNSUP
+    far = _scan(x=_rows(seq=1 << 27, row=1 << 25))
+    assert lib.tg_selective_scan(ctypes.byref(far), P, 1 << 60, 0, 0, 0) == UNSUP
