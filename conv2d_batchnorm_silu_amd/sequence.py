@@ -250,7 +250,8 @@ def _norm_forward(x, gamma, beta, eps, residual, train, out, dev):
         total = torch.empty_like(x, memory_format=_DENSE)
         tp = total.data_ptr()
     if train:
-        mean, rstd = torch.empty((2,) + shape[:-1], dtype=_F32, device=x.device)
+        mean = torch.empty(shape[:-1], dtype=_F32, device=x.device)
+        rstd = torch.empty_like(mean)
         mp, qp = mean.data_ptr(), rstd.data_ptr()
     st = _lib().tg_layer_norm(xp, xs, rp, rs, gp, bp, eps, rows, C, dt, y.data_ptr(), tp, mp, qp,
                               _raw_stream(dev))
@@ -305,13 +306,12 @@ def layer_norm_backward(dy, s, gamma, mean, rstd, dsum=None, out=None, stream=No
     _check(lib.tg_layer_norm_backward_workspace(rows, C, dt, ctypes.byref(need)),
            "tg_layer_norm_backward_workspace")
     dx = _new_or(out, s, dev, True)
-    dw = torch.empty((2, C), dtype=_F32, device=s.device)
+    dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
     ws = torch.empty(need.value, dtype=torch.uint8, device=s.device)
     _check(lib.tg_layer_norm_backward(
-        gp, gs, sp, ss, wp, mp, qp, dp, ds, rows, C, dt, dx.data_ptr(), dw.data_ptr(),
-        dw.data_ptr() + 4 * C, ws.data_ptr(), need.value, _raw_stream(dev)),
-        "tg_layer_norm_backward")
-    return dx, dw[0], dw[1]
+        gp, gs, sp, ss, wp, mp, qp, dp, ds, rows, C, dt, dx.data_ptr(), dgamma.data_ptr(),
+        dbeta.data_ptr(), ws.data_ptr(), need.value, _raw_stream(dev)), "tg_layer_norm_backward")
+    return dx, dgamma, dbeta
 
 
 # -------------------------------------------------- short causal convolution
@@ -382,7 +382,7 @@ def causal_conv_backward(dy, x, w, bias=None, act="silu", initial_state=None, of
         with there:
             return causal_conv_backward(dy, x, w, bias, act, initial_state, offsets, dstate)
     args, packed, held, D = _conv_args(x, w, bias, act, initial_state, offsets, dev)
-    a, K = args(_NO_ROWS, 0), held[1] + 1
+    a = args(_NO_ROWS, 0)
     g = _rows(_some(dy, "dy"), "dy", dev, x.shape, x.dtype, packed, D)
     df = _flat(dstate, "dstate", dev, held, x.dtype)
     lib = _lib()
@@ -390,7 +390,7 @@ def causal_conv_backward(dy, x, w, bias=None, act="silu", initial_state=None, of
     _check(lib.tg_causal_conv_backward_workspace(a, ctypes.byref(need)),
            "tg_causal_conv_backward_workspace")
     dx = torch.empty_like(x, memory_format=_DENSE)
-    dw = torch.empty((K + 1, D), dtype=_F32, device=x.device)
+    dw, db = torch.empty_like(w), torch.empty(D, dtype=_F32, device=x.device)
     d0, d0p = None, 0
     if initial_state is not None:
         d0 = torch.empty(held, dtype=x.dtype, device=x.device)
@@ -398,9 +398,9 @@ def causal_conv_backward(dy, x, w, bias=None, act="silu", initial_state=None, of
     ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
     _check(lib.tg_causal_conv_backward(
         a, _Rows(*g), _Rows(*_place(dx, dx.stride(), packed, D)), dw.data_ptr(),
-        dw.data_ptr() + 4 * K * D, df, d0p, ws.data_ptr(), need.value,
+        db.data_ptr(), df, d0p, ws.data_ptr(), need.value,
         _raw_stream(dev)), "tg_causal_conv_backward")
-    return dx, dw[:K], dw[K], d0
+    return dx, dw, db, d0
 
 
 def causal_conv_step(x, state, w, bias=None, act="silu", slots=None, out=None, stream=None):
