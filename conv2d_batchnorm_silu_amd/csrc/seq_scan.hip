@@ -845,11 +845,27 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
             float P[NS], e[NS];
 #pragma unroll
             for (int j = 0; j < NS; ++j) e[j] = 0.0f;
-            for_tokens<NS, TT, false, true, false>(tile, p.cl, p.q, [&](int t, const Token<NS>& k) {
-                const float dv = both.dv[t][p.cl];
+            // Two operations for each state: the reads go two tokens ahead (one
+            // ahead 236 us, two or three 228: 2 x 2048 tokens, 2048 channels, both passes).
+            constexpr int kLead = 2;
+            float dv[kLead + 1], C[kLead + 1][NS];
+            int q = p.q, cl = p.cl;
+            asm volatile("" : "+v"(cl), "+v"(q));
+            const auto read = [&](int t) {
+                dv[t % (kLead + 1)] = both.dv[t][cl];
+                get<NS>(&tile.C[t][q * NS], C[t % (kLead + 1)]);
+            };
 #pragma unroll
-                for (int j = 0; j < NS; ++j) e[j] = __builtin_fmaf(dv, k.C[j], e[j]) * dec[t][j];
-            });
+            for (int t = TT - 1; t >= TT - kLead; --t) read(t);
+#pragma unroll
+            for (int t = TT - 1; t >= 0; --t) {
+                if (t >= kLead) read(t - kLead);
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    e[j] = __builtin_fmaf(dv[t % (kLead + 1)], C[t % (kLead + 1)][j], e[j]) *
+                           dec[t][j];
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
             for (int j = 0; j < NS; ++j) P[j] = __builtin_amdgcn_exp2f(sum * A2[j]);
             float* const ex = exchange + flip * exchange_floats(W, NS);
