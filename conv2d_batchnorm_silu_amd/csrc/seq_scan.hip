@@ -139,6 +139,7 @@ struct alignas(16) BackTile {
     Tile<NS, TT> f;
     float dv[TT][kCh];
     float4 item[TT / 4][64];
+    float dA[2][64][NS];  // a lane's sum so far, and what its additions dropped
 };
 // NS consecutive floats of LDS or memory (NS floats aligned).
 template <int NS>
@@ -754,7 +755,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
     float* const exchange = (float*)((BackTile<NS, TT>*)lds + W);
     const int lane = threadIdx.x & 63;
     // c: a[t+1]*g[t+1] of the next token.
-    float A2[NS], c[NS], dA[NS], lost[NS];
+    float A2[NS], c[NS], dA[NS];
     load_A2<NS, false>(a, p, A2);
     load_state<NS, false>(b.dfinal, a, p, c);
     if (a.PL) {
@@ -762,7 +763,9 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
         fold_parts<NS>(a, p, last, last - p.part(a.PL), -1, c);
     }
 #pragma unroll
-    for (int j = 0; j < NS; ++j) dA[j] = lost[j] = 0.0f;
+    for (int j = 0; j < NS; ++j) dA[j] = 0.0f;
+    put<NS>(both.dA[0][lane], dA);
+    put<NS>(both.dA[1][lane], dA);
     const float skip = a.D_skip ? a.D_skip[p.ch] : 0.0f;
     const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
     float dD = 0.0f, dbias = 0.0f;
@@ -874,7 +877,19 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
             put<NS>(exchange_at<NS>(ex, p.w, 1), e);
             __syncthreads();
             get<NS>(exchange_at<NS>(ex, W, 0), c);
-            for (int m = W - 1; m > p.w; --m) {
+            // Two segments at a time: one by one the reads' latency adds up.
+            int m = W - 1;
+            for (; m > p.w + 1; m -= 2) {
+                float P1[NS], e1[NS];
+                get<NS>(exchange_at<NS>(ex, m, 0), P);
+                get<NS>(exchange_at<NS>(ex, m, 1), e);
+                get<NS>(exchange_at<NS>(ex, m - 1, 0), P1);
+                get<NS>(exchange_at<NS>(ex, m - 1, 1), e1);
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    c[j] = __builtin_fmaf(P1[j], __builtin_fmaf(P[j], c[j], e[j]), e1[j]);
+            }
+            if (m > p.w) {
                 get<NS>(exchange_at<NS>(ex, m, 0), P);
                 get<NS>(exchange_at<NS>(ex, m, 1), e);
 #pragma unroll
@@ -940,12 +955,17 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
         }
         // The sum over all tokens is long: what each addition drops is kept
         // (Kahan), so that it is as exact as a chunk's own sum.
+        float lost[NS];
+        get<NS>(both.dA[0][lane], dA);
+        get<NS>(both.dA[1][lane], lost);
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
             const float add = dAc[j] - lost[j], s = dA[j] + add;
             lost[j] = (s - dA[j]) - add;
             dA[j] = s;
         }
+        put<NS>(both.dA[0][lane], dA);
+        put<NS>(both.dA[1][lane], lost);
         if (SPLIT && p.w == 0)
             put<NS>(exchange_at<NS>(exchange + flip * exchange_floats(W, NS), W, 0), c);
         float dt[kItems], dx[kItems], dz[kItems];
@@ -967,6 +987,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
     }
     dD = quad_sum(dD);
     dbias = quad_sum(dbias);
+    get<NS>(both.dA[0][lane], dA);
     if constexpr (SPLIT) {
         // The waves' sums, one after another.
         __syncthreads();
