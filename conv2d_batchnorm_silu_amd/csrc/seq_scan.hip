@@ -25,7 +25,7 @@
 // workgroups split the tokens in the same way (parts of PL tokens): a first
 // kernel computes the parts' P and last states.
 //
-// Tokens past the end count as d = x = B = C = 0: a = 1, and the state stays.
+// Tokens past the end count as d = 0 (and dL/dv = 0): a = 1, and the state stays.
 #include "seq_device.hpp"
 #include "seq_internal.hpp"
 #include "tg_internal.hpp"
@@ -238,7 +238,9 @@ struct Place {
 
 // A tensor's rows of one sequence. A chunk's rows are read and written through a
 // buffer descriptor that ends with the last token: what lies past it reads
-// as zero and is not written, so the tail of a sequence takes no branch. The host
+// as zero and is not written, so the tail of a sequence takes no branch. (Rows
+// that are one row for all tokens, with a stride of 0, read as that row
+// there: what has to be zero past the end, d and dv, is set so by itself.) The host
 // keeps row strides below 2^25 elements, so that a chunk's offsets fit 31 bits.
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past any chunk
 struct Col {
@@ -813,9 +815,12 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
             }
             if (l + TT > p.hi) {
                 // Past the end the state and its adjoint only pass through, but
-                // their product, which dL/dd holds, is not zero.
-                d = l + t < p.hi ? d : 0.0f;
-                slope = l + t < p.hi ? slope : 0.0f;
+                // their product, which dL/dd holds, is not zero; and rows that are
+                // one row for all tokens do not read as zero there.
+                const bool real = l + t < p.hi;
+                d = real ? d : 0.0f;
+                slope = real ? slope : 0.0f;
+                dv = real ? dv : 0.0f;
             }
             tile.d[t][p.cl] = make_float2(d, d * x);
             both.dv[t][p.cl] = dv;
@@ -1051,9 +1056,12 @@ __global__ __launch_bounds__(64 * waves_for(NS)) void scan_bwd_parts(const ScanA
         for (int i = 0; i < TT / 4; ++i) {
             const int t = p.q + 4 * i;
             float d = step_size(a, rdt[i] + bias);
-            if (l + TT > p.hi) d = l + t < p.hi ? d : 0.0f;
-            const float dy = rdy[i];
-            tile.d[t][p.cl] = make_float2(d, a.z.p ? dy * silu_f32(rz[i]) : dy);
+            float dv = a.z.p ? rdy[i] * silu_f32(rz[i]) : rdy[i];
+            if (l + TT > p.hi) {
+                d = l + t < p.hi ? d : 0.0f;
+                dv = l + t < p.hi ? dv : 0.0f;
+            }
+            tile.d[t][p.cl] = make_float2(d, dv);
         }
         rC.put(tile.C);
         wave_sync();

@@ -1,0 +1,87 @@
+"""The sequence operators on the GPU where a call is easily got wrong: rows
+that are broadcast over tokens. Against the 64-bit references of seq_ref.py,
+with that file's bounds."""
+from __future__ import annotations
+
+import pytest
+
+import conv2d_batchnorm_silu_amd as tg
+import seq_ref as R
+from gpu_cases import note
+from test_sequence_gpu import ScanCase, _cat, up
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+# ---- rows broadcast over the tokens
+
+class Broadcast(ScanCase):
+    """A scan whose tensors in ``names`` are one row for all tokens (row stride 0)."""
+
+    def __init__(self, case, names):
+        super().__init__(case)
+        self.dy = self.r(*self.x.shape, dtype=self.dtype)
+        for name in names.split():
+            t = getattr(self, name)
+            if t is not None:
+                setattr(self, name, t[:1].expand(t.shape))
+
+    def dev(self, t):
+        if t is None or t.stride(0) != 0:
+            return super().dev(t)
+        return t[0].cuda().expand(self.lead + t.shape[1:])
+
+    def bc(self, t):
+        return self.dev(t) if t.stride(0) == 0 else super().bc(t)
+
+
+BROADCAST = [
+    # Tails of a tile: dense, packed, in parts (600 and 300 tokens of one block of channels).
+    ([21, 21], False, 20, 16, 1, "f32", False, True, True, 0), ([21, 21], False, 20, 16, 1, "bf16", True, True, False, 0),
+    ([5, 0, 37, 1], True, 34, 16, 2, "f16", True, True, True, 0), ([600], False, 16, 16, 1, "f32", True, True, True, 0),
+    ([300, 301], True, 16, 5, 1, "f32", False, False, True, 0), ([23], False, 16, 100, 2, "f32", True, True, False, 0),
+]
+
+
+@pytest.mark.parametrize("names", ["dy C", "dy x", "dy B C", "dy x dt B C z"])
+@pytest.mark.parametrize("case", BROADCAST, ids=str)
+def test_scan_rows_broadcast(case, names):
+    note("scan %s, broadcast %s" % (case, names))
+    c = Broadcast(case, names)
+    dstate = c.r(c.S, c.D, c.N) if c.init is not None else None
+    y, state, saved = tg.selective_scan_train(*c.args(), return_state=True, **c.more())
+    got = tg.selective_scan_backward(c.dev(c.dy), *c.args(), saved, dstate=up(dstate), **c.more())
+    fwd = [c.ref(i, R.scan) for i in range(c.S)]
+    R.check("y", y.reshape(c.x.shape), *_cat([r[0] for r in fwd]))
+    R.check("state", state, torch.stack([r[1][0] for r in fwd]), torch.stack([r[1][1] for r in fwd]))
+    refs = [c.ref(i, R.scan_grads, c.dy, dfinal=None if dstate is None else dstate[i].double())
+            for i in range(c.S)]
+    for name in ("dx", "ddt", "dz"):
+        if getattr(got, name) is not None:
+            R.check(name, getattr(got, name).reshape(c.x.shape), *_cat([r[name] for r in refs]))
+    for name in ("dB", "dC"):
+        R.check(name, getattr(got, name).reshape(c.T, c.G, c.N), *_cat([r[name] for r in refs]))
+    for name, key in (("dA", "dA"), ("dD", "dD"), ("ddt_bias", "dbias")):
+        v, e = sum(r[key][0] for r in refs), sum(r[key][1] for r in refs)
+        R.check(name, getattr(got, name), v, e + (c.S + 1) * R.E * sum(r[key][0].abs() for r in refs))
+    if c.init is not None:
+        R.check("dinit", got.dinitial_state, torch.stack([r["dinit"][0] for r in refs]),
+                torch.stack([r["dinit"][1] for r in refs]))
+
+
+def test_scan_rows_broadcast_many_sequences():
+    """Sequences that single waves take whole: the gradients of broadcast rows
+    are those of the same rows written out."""
+    S, L, D, N = 4100, 19, 16, 16
+    r = ScanCase(([1], False, 1, 1, 1, "f32", True, True, False, 0)).r
+    row = [r(1, 1, D).cuda(), r(1, 1, D, scale=0.5).cuda(), r(1, 1, 1, N).cuda(), r(1, 1, 1, N).cuda(), r(1, 1, D).cuda()]
+    wide = [t.expand((S, L) + t.shape[2:]) for t in row]
+    A = -torch.arange(1, N + 1).float().repeat(D, 1).cuda()
+    more = dict(D=r(D).cuda(), dt_bias=r(D, shift=-3.0).cuda())
+
+    def grads(x, dt, B, C, dy):
+        _, saved = tg.selective_scan_train(x, dt, A, B, C, **more)
+        return tg.selective_scan_backward(dy, x, dt, A, B, C, saved, **more)
+    for name, a, b in zip(tg.ScanGradients._fields, grads(*wide), grads(*(t.contiguous() for t in wide))):
+        assert (a is None and b is None) or torch.equal(a, b), name
