@@ -1237,11 +1237,19 @@ size_t parts_bytes(const tg_scan_args& a, const Plan& p) {
     return p.PL ? (size_t)p.slots * 2 * a.D * 4 * p.ns * sizeof(float) : 0;
 }
 
+// Written rows whose stride keeps the tokens past the end out of the one before:
+// with a single row in the batch any stride is accepted, and none is used.
+Rows<void> written_rows(const tg_rows& r, const tg_scan_args& a) {
+    Rows<void> w = rows_of<void>(r);
+    if (a.seqs.rows == 1) w.row = a.D;
+    return w;
+}
+
 ScanArgs args_of(const tg_scan_args& a, const Plan& p, float* saved, void* parts) {
     const int Dg = a.D / a.G;
     return {map_of(a.seqs), a.D, a.N, a.G, Dg, (int)ceil_div(Dg, kCh), a.softplus, p.PL,
             rows_of<const void>(a.x), rows_of<const void>(a.dt), rows_of<const void>(a.B),
-            rows_of<const void>(a.C), rows_of<const void>(a.z), rows_of<void>(a.y), a.A, a.D_skip,
+            rows_of<const void>(a.C), rows_of<const void>(a.z), written_rows(a.y, a), a.A, a.D_skip,
             a.dt_bias, a.initial, a.final, saved, (float*)parts};
 }
 
@@ -1347,7 +1355,7 @@ hipError_t launch_scan_backward(const tg_scan_args& a, const tg_scan_grads& g, c
     char* const base = (char*)ws;
     const ScanArgs f = args_of(a, p, nullptr, base + w.parts);
     const ScanGrads b{rows_of<const void>(g.dy), g.dfinal, (const float*)saved,
-                      rows_of<void>(g.dx), rows_of<void>(g.ddt), rows_of<void>(g.dz), g.dinitial,
+                      written_rows(g.dx, a), written_rows(g.ddt, a), written_rows(g.dz, a), g.dinitial,
                       (float*)(base + w.bc), (float*)base};
     hipError_t e = hipSuccess;
 #define TG_X(T, NS) e = bwd_typed<T, NS>(p, f, b, st)

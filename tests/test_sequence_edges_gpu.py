@@ -1,12 +1,15 @@
 """The sequence operators on the GPU where a call is easily got wrong: rows
-that are broadcast over tokens. Against the 64-bit references of seq_ref.py,
+that are broadcast over tokens, and batches of one row. Against the 64-bit references of seq_ref.py,
 with that file's bounds."""
 from __future__ import annotations
+
+import ctypes
 
 import pytest
 
 import conv2d_batchnorm_silu_amd as tg
 import seq_ref as R
+from conv2d_batchnorm_silu_amd import sequence as S
 from gpu_cases import note
 from test_sequence_gpu import ScanCase, _cat, up
 
@@ -73,10 +76,10 @@ def test_scan_rows_broadcast(case, names):
 def test_scan_rows_broadcast_many_sequences():
     """Sequences that single waves take whole: the gradients of broadcast rows
     are those of the same rows written out."""
-    S, L, D, N = 4100, 19, 16, 16
+    seqs, L, D, N = 4100, 19, 16, 16
     r = ScanCase(([1], False, 1, 1, 1, "f32", True, True, False, 0)).r
     row = [r(1, 1, D).cuda(), r(1, 1, D, scale=0.5).cuda(), r(1, 1, 1, N).cuda(), r(1, 1, 1, N).cuda(), r(1, 1, D).cuda()]
-    wide = [t.expand((S, L) + t.shape[2:]) for t in row]
+    wide = [t.expand((seqs, L) + t.shape[2:]) for t in row]
     A = -torch.arange(1, N + 1).float().repeat(D, 1).cuda()
     more = dict(D=r(D).cuda(), dt_bias=r(D, shift=-3.0).cuda())
 
@@ -85,3 +88,53 @@ def test_scan_rows_broadcast_many_sequences():
         return tg.selective_scan_backward(dy, x, dt, A, B, C, saved, **more)
     for name, a, b in zip(tg.ScanGradients._fields, grads(*wide), grads(*(t.contiguous() for t in wide))):
         assert (a is None and b is None) or torch.equal(a, b), name
+
+
+# ---- batches of one row, through the C entry points
+
+@pytest.mark.parametrize("stride", [0, 3, -5, 1000])
+@pytest.mark.parametrize("packed", [False, True])
+def test_scan_one_row_any_stride(packed, stride):
+    """The stride of a single written row means nothing: what is past the row's
+    end in the tile must not land in it."""
+    note("one row, stride %d" % stride)
+    D, N, dt = 40, 16, torch.float32
+    c = ScanCase(([0, 1] if packed else [1], packed, D, N, 1, "f32", True, True, False, 0))
+    args, more = c.args(), c.more()
+    y, saved = tg.selective_scan_train(*args, **more)
+    dy = c.r(1, D).cuda().reshape(y.shape)
+    want = tg.selective_scan_backward(dy, *args, saved, **more)
+    x, step, A, B, C = args
+    lib, E = S._lib(), ctypes.c_size_t
+    a = S._ScanArgs(S._Seqs(c.S, 1, c.off.data_ptr() if packed else 0), D, N, 1, S._DTYPES[dt], 1)
+    for name, t in (("x", x), ("dt", step), ("z", more["z"])):
+        setattr(a, name, S._Rows(t.data_ptr(), D, D))
+    for name, t in (("B", B), ("C", C)):
+        setattr(a, name, S._Rows(t.data_ptr(), N, N))
+    a.A, a.D_skip, a.dt_bias = A.data_ptr(), more["D"].data_ptr(), more["dt_bias"].data_ptr()
+
+    def written():
+        t = torch.full((3, D), 7.0, device="cuda")
+        return t, S._Rows(t[1].data_ptr(), stride, stride)
+    ys, a.y = written()
+    work, keep, need = E(), E(), E()
+    assert lib.tg_selective_scan_sizes(ctypes.byref(a), *(ctypes.byref(v) for v in (work, keep, need))) == 0
+    ws = torch.empty(max(work.value, need.value, 16), dtype=torch.uint8, device="cuda")
+    kept = torch.empty_like(saved)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.tg_selective_scan(ctypes.byref(a), ws.data_ptr(), ws.numel(), kept.data_ptr(), keep.value, stream) == 0
+    g = S._ScanGrads(S._Rows(dy.data_ptr(), D, D))
+    outs = {}
+    for name in ("dx", "ddt", "dz"):
+        outs[name], rows = written()
+        setattr(g, name, rows)
+    dB, dC = torch.empty(1, N, device="cuda"), torch.empty(1, N, device="cuda")
+    dA = torch.empty(D, N, device="cuda")
+    g.dB, g.dC, g.dA = S._Rows(dB.data_ptr(), N, N), S._Rows(dC.data_ptr(), N, N), dA.data_ptr()
+    assert lib.tg_selective_scan_backward(ctypes.byref(a), ctypes.byref(g), kept.data_ptr(), keep.value, ws.data_ptr(),
+                                          ws.numel(), stream) == 0
+    torch.cuda.synchronize()
+    for name, got, w in [("y", ys, y)] + [(k, outs[k], getattr(want, k)) for k in outs]:
+        assert torch.equal(got[1], w.reshape(D)), name
+        assert bool((got[0] == 7).all()) and bool((got[2] == 7).all()), name
+    assert torch.equal(dB, want.dB.reshape(1, N)) and torch.equal(dC, want.dC.reshape(1, N)) and torch.equal(dA, want.dA)
