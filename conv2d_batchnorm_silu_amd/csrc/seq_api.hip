@@ -8,16 +8,22 @@ using namespace tg;
 namespace {
 
 // Row numbers, and a strip or chunk past them, are ints in the kernels; a
-// launch has fewer than 2^32 threads, so the scan's single waves are limited.
+// launch has fewer than 2^32 threads along x, so the scan's single waves, and the
+// single token's workgroups of 256 threads, are limited.
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 constexpr int kMaxChannels = 1 << 20;
 constexpr int64_t kMaxGroups = ((int64_t)1 << 26) - 1;
+constexpr int64_t kMaxStepGroups = ((int64_t)1 << 24) - 1;
 // The scan addresses 16 rows by 31-bit byte offsets.
 constexpr int64_t kMaxScanStride = (int64_t)1 << 25;
 
 bool dtype_ok(int d) { return d == TG_F16 || d == TG_BF16 || d == TG_F32; }
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-tg_status of(hipError_t e) { return e == hipSuccess ? TG_OK : TG_ERR_HIP; }
+// A launcher finds sizes that no launch holds before it launches anything.
+tg_status of(hipError_t e) {
+    return e == hipSuccess ? TG_OK
+           : e == hipErrorInvalidConfiguration ? TG_ERR_UNSUPPORTED : TG_ERR_HIP;
+}
 
 #define TG_REQUIRE(cond, status) \
     do {                         \
@@ -75,7 +81,10 @@ tg_status check_scan(const tg_scan_args* a) {
     TG_CHECK(check_seqs(a->seqs));
     TG_REQUIRE(a->D >= 1 && a->N >= 1 && a->G >= 1 && a->D % a->G == 0, TG_ERR_INVALID_ARGUMENT);
     TG_REQUIRE(dtype_ok((int)a->dtype) && a->D <= kMaxChannels && a->N <= 128, TG_ERR_UNSUPPORTED);
-    // Workgroups: one for each sequence and (at least one) block of channels.
+    return TG_OK;
+}
+// Workgroups: one for each sequence and (at least one) block of channels.
+tg_status check_scan_groups(const tg_scan_args* a) {
     TG_REQUIRE(a->seqs.seqs * ceil_div(a->D / a->G, 16) * a->G <= kMaxGroups, TG_ERR_UNSUPPORTED);
     return TG_OK;
 }
@@ -198,6 +207,7 @@ tg_status tg_causal_conv_step(const void* x, int64_t x_stride, void* state, int6
 tg_status tg_selective_scan_sizes(const tg_scan_args* a, size_t* workspace_bytes,
                                   size_t* saved_bytes, size_t* backward_bytes) {
     TG_CHECK(check_scan(a));
+    TG_CHECK(check_scan_groups(a));
     scan_sizes(*a, workspace_bytes, saved_bytes, backward_bytes);
     return TG_OK;
 }
@@ -205,6 +215,7 @@ tg_status tg_selective_scan_sizes(const tg_scan_args* a, size_t* workspace_bytes
 tg_status tg_selective_scan(const tg_scan_args* a, void* workspace, size_t workspace_bytes,
                             void* saved, size_t saved_bytes, void* stream) {
     TG_CHECK(check_scan(a));
+    TG_CHECK(check_scan_groups(a));
     TG_CHECK(check_scan_inputs(a));
     TG_CHECK(check_scan_rows(a->y, a->seqs, a->D, elem_bytes(a->dtype), true));
     size_t work = 0, keep = 0;
@@ -219,6 +230,7 @@ tg_status tg_selective_scan_backward(const tg_scan_args* a, const tg_scan_grads*
                                      const void* saved, size_t saved_bytes, void* workspace,
                                      size_t workspace_bytes, void* stream) {
     TG_CHECK(check_scan(a));
+    TG_CHECK(check_scan_groups(a));
     TG_CHECK(check_scan_inputs(a));
     TG_REQUIRE(g && g->dA && (!g->dz.p == !a->z.p), TG_ERR_INVALID_ARGUMENT);
     TG_REQUIRE(scan_sum_groups(*a) < (int64_t)1 << 24, TG_ERR_UNSUPPORTED);  // of 256 threads
@@ -246,6 +258,7 @@ tg_status tg_selective_scan_step(const tg_scan_args* a, float* state, int64_t nu
     if (a->seqs.seqs == 0) return TG_OK;
     TG_REQUIRE(a->seqs.rows == a->seqs.seqs && !a->seqs.offsets, TG_ERR_INVALID_ARGUMENT);
     TG_CHECK(check_scan(a));
+    TG_REQUIRE(a->seqs.seqs * ceil_div(a->D, 64) <= kMaxStepGroups, TG_ERR_UNSUPPORTED);
     // Rows are a step's sequences: only the row strides count.
     tg_scan_args b = *a;
     for (tg_rows* r : {&b.x, &b.dt, &b.B, &b.C, &b.z, &b.y}) r->seq_stride = r->row_stride;

@@ -396,6 +396,14 @@ Block conv_block(int D, int V) {
     return {dim3(bx, kBlock / bx), (unsigned)ceil_div(n, bx)};
 }
 
+// The grid for `pieces` strips or rows; false where a launch does not hold them:
+// fewer than 2^32 threads along x (16 to 256 for each piece, by D).
+bool conv_grid(const Block& bl, int64_t pieces, dim3& grid) {
+    const int64_t x = ceil_div(pieces, bl.block.y);
+    grid = dim3((unsigned)x, bl.cblocks);
+    return x * bl.block.x < (int64_t)1 << 32;
+}
+
 void widest_rows(Widest& w, const tg_causal_conv_args& a, const tg_rows& r) {
     w.ptr(r.p, elem_bytes(a.dtype));
     w.len(r.row_stride);
@@ -431,7 +439,8 @@ hipError_t launch_causal_conv(const tg_causal_conv_args& a, hipStream_t st) {
                     rows_of<void>(a.y), a.w, a.bias, a.initial, a.final};
     const int64_t pieces = strips + (a.final ? a.seqs.seqs : 0);
     if (pieces == 0) return hipSuccess;
-    const dim3 grid((unsigned)ceil_div(pieces, bl.block.y), bl.cblocks);
+    dim3 grid;
+    if (!conv_grid(bl, pieces, grid)) return hipErrorInvalidConfiguration;
 #define TG_X(T, V, K) conv_fwd<T, V, K><<<grid, bl.block, 0, st>>>(f, strips)
     TG_CONV_DISPATCH(TG_X);
 #undef TG_X
@@ -477,7 +486,8 @@ hipError_t launch_causal_conv_backward(const tg_causal_conv_args& a, const tg_ro
                     dinitial, (float*)ws};
     const int64_t pieces = strips + (dinitial ? a.seqs.seqs : 0);
     if (pieces > 0) {
-        const dim3 grid((unsigned)ceil_div(pieces, bl.block.y), bl.cblocks);
+        dim3 grid;
+        if (!conv_grid(bl, pieces, grid)) return hipErrorInvalidConfiguration;
 #define TG_X(T, V, K) conv_bwd<T, V, K><<<grid, bl.block, 0, st>>>(f, strips)
         TG_CONV_DISPATCH(TG_X);
 #undef TG_X
@@ -498,7 +508,8 @@ hipError_t launch_causal_conv_step(const void* x, int64_t xs, void* state, int64
     const int V = vec_for(dtype, wd);
     const Block bl = conv_block(D, V);
     const ConvStep f{x, xs, state, num_slots, slots, w, bias, n, D, silu, y};
-    const dim3 grid((unsigned)ceil_div(n, bl.block.y), bl.cblocks);
+    dim3 grid;
+    if (!conv_grid(bl, n, grid)) return hipErrorInvalidConfiguration;
 #define TG_X(T, V, K) conv_step<T, V, K><<<grid, bl.block, 0, st>>>(f)
     TG_CONV_DISPATCH(TG_X);
 #undef TG_X

@@ -27,6 +27,9 @@
  * alias inputs unless the function says so. Results do not depend on
  * scheduling: the same call gives the same bits.
  *
+ * Limits, for every function: rows, sequences and state slots below 2^30, up to 2^20
+ * channels; more are TG_ERR_UNSUPPORTED, as is what an operator's own text names.
+ *
  * Errors, for every function: TG_ERR_INVALID_ARGUMENT for a NULL required
  * pointer or a size, stride or eps out of its range; TG_ERR_UNSUPPORTED for a
  * dtype other than the three or sizes past the stated limits; TG_ERR_ALIGNMENT
@@ -53,7 +56,7 @@ typedef struct {
 
 typedef struct {
     int64_t seqs;           /* >= 1 */
-    int64_t rows;           /* all sequences together, 0 .. 2^31-1 */
+    int64_t rows;           /* all sequences together, >= 0 */
     const int32_t *offsets; /* device [seqs + 1], or NULL: dense */
 } tg_seqs;
 
@@ -95,7 +98,10 @@ tg_status tg_layer_norm_backward(const void *dy, int64_t dy_stride, const void *
  * sequence's state: initial [seqs][K-1][D], the K-1 rows before the sequence,
  * oldest first; NULL: zeros. final [seqs][K-1][D] (may be NULL) gets the last
  * K-1 rows in the same form; it must not alias initial. w: fp32 [K][D]
- * (taps outside, channels contiguous); bias: fp32 [D] or NULL. */
+ * (taps outside, channels contiguous); bias: fp32 [D] or NULL.
+ * Fewer than 2^23 sequences of fewer than 2^28 rows are always taken, as are fewer
+ * than 2^24 single tokens; beyond that TG_ERR_UNSUPPORTED where one launch does not
+ * hold them. */
 typedef struct {
     tg_seqs seqs;
     int D, K;
@@ -178,7 +184,8 @@ tg_status tg_selective_scan_backward(const tg_scan_args *a, const tg_scan_grads 
 /* One token for each of n sequences: x, dt, z [n][D] and B, C [n][G][N] by
  * row stride (seqs.seqs = seqs.rows = n, offsets NULL; seq_stride is not
  * read), y likewise. state fp32 [num_slots][D][N], updated in place; slots as
- * in tg_causal_conv_step. initial and final are not read. */
+ * in tg_causal_conv_step. initial and final are not read. TG_ERR_UNSUPPORTED
+ * for 2^24 or more pairs of a sequence and 64 channels. */
 tg_status tg_selective_scan_step(const tg_scan_args *a, float *state, int64_t num_slots,
                                  const int32_t *slots, void *stream);
 
