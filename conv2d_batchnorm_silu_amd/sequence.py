@@ -11,7 +11,9 @@ Parameters are fp32. A batch is dense, ``[S, L, C]`` (any batch and row
 strides, so a slice of a wider projection is taken as it is), or packed,
 ``[T, C]`` with ``offsets``, an int32 device tensor of S + 1 row numbers
 (non-decreasing, from 0 to T; sequences may be empty). Outputs are dense new
-tensors unless ``out`` is given.
+tensors unless ``out`` is given. ``out`` shares no memory with an argument,
+but for the ones that a function's text says it may be: that tensor itself,
+with its strides. Any other overlap raises ValueError.
 
 ``stream`` is a ``torch.cuda.Stream`` (default: the current one). New
 outputs and scratch are allocated for that stream; making the inputs ready on
@@ -199,11 +201,66 @@ def _place(t, st, packed, width):
     return t.data_ptr(), st[0] if t.shape[0] > 1 else row * t.shape[1], row
 
 
-def _new_or(out, like, dev, dense):
-    """A new tensor like ``like``, dense, or ``out`` if it fits."""
+def _span(t):
+    """(first byte, bytes in a run, [(bytes apart, how many)] of the runs)."""
+    run, steps = t.element_size(), []
+    for step, n in sorted((st * t.element_size(), n) for st, n in zip(t.stride(), t.shape) if n > 1):
+        if step == run and not steps:
+            run *= n
+        elif step:
+            steps.append((step, n))
+    return t.data_ptr(), run, steps
+
+
+def _overlap(a, b):
+    """Whether two tensors have a byte in common: whether a whole number of
+    each of their strides leads from a run of one into a run of the other. A
+    search that does not end soon (strides that do not nest) counts as yes."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    (pa, wa, sa), (pb, wb, sb) = _span(a), _span(b)
+    reach = {}
+    for step, n in sa:
+        lo, hi = reach.get(step, (0, 0))
+        reach[step] = lo, hi + n - 1
+    for step, n in sb:
+        lo, hi = reach.get(step, (0, 0))
+        reach[step] = lo - (n - 1), hi
+    terms = sorted(reach.items(), reverse=True)
+    rest = [(0, 0)]  # least and most that the terms from here on add up to
+    for step, (lo, hi) in reversed(terms):
+        rest.append((rest[-1][0] + step * lo, rest[-1][1] + step * hi))
+    rest.reverse()
+    left = 10000
+
+    def search(i, lo, hi):  # sum of the terms from i on within lo .. hi
+        nonlocal left
+        left -= 1
+        if hi < rest[i][0] or lo > rest[i][1]:
+            return False
+        if i == len(terms) or left < 0:
+            return True
+        step, (least, most) = terms[i]
+        first = max(least, -((rest[i + 1][1] - lo) // step))
+        last = min(most, (hi - rest[i + 1][0]) // step)
+        return any(search(i + 1, lo - k * step, hi - k * step) for k in range(first, last + 1))
+    return search(0, pb - pa - wa + 1, pb - pa + wb - 1)
+
+
+def _is(a, b):
+    return (a.data_ptr() == b.data_ptr() and a.shape == b.shape
+            and all(n == 1 or x == y for n, x, y in zip(a.shape, a.stride(), b.stride())))
+
+
+def _new_or(out, like, dev, dense, may, apart):
+    """A new tensor like ``like``, dense, or ``out`` if it fits: it may be one of
+    ``may`` and shares memory with none of ``apart`` ({name: argument})."""
     if out is None:
         return torch.empty_like(like, memory_format=_DENSE)
     _refuse(out, "out", dev, like.shape, like.dtype, dense)
+    for name, t in {**may, **apart}.items():
+        if t is not None and not (name in may and _is(out, t)) and _overlap(out, t):
+            raise ValueError("out shares memory with %s" % name)
     return out
 
 
@@ -244,7 +301,10 @@ def _norm_forward(x, gamma, beta, eps, residual, train, out, dev):
     rp, rs = _norm_rows(residual, "residual", dev, shape, dtype)
     gp = _flat(_some(gamma, "gamma"), "gamma", dev, (C,))
     bp = _flat(beta, "beta", dev, (C,))
-    y = _new_or(out, x, dev, True)
+    # Training hands x back as s where there is no residual.
+    own = dict(x=x, residual=residual)
+    y = _new_or(out, x, dev, True, {} if train and residual is None else own,
+                dict(own, gamma=gamma, beta=beta))
     total, tp, mean, rstd, mp, qp = None, 0, None, None, 0, 0
     if residual is not None:
         total = torch.empty_like(x, memory_format=_DENSE)
@@ -262,7 +322,8 @@ def _norm_forward(x, gamma, beta, eps, residual, train, out, dev):
 
 def layer_norm(x, gamma, beta=None, eps=1e-5, residual=None, out=None, stream=None):
     """Layer norm over the last dimension: y, or with ``residual`` (x's shape
-    and type) the pair (y, x + residual), the norm taken of the sum."""
+    and type) the pair (y, x + residual), the norm taken of the sum. ``out``
+    may be x or residual."""
     dev = _device(x, "x")
     there = _elsewhere(dev, stream)
     if there is not None:
@@ -274,7 +335,8 @@ def layer_norm(x, gamma, beta=None, eps=1e-5, residual=None, out=None, stream=No
 
 def layer_norm_train(x, gamma, beta=None, eps=1e-5, residual=None, out=None, stream=None):
     """(y, s, mean, rstd): layer norm and what its backward pass takes. s is
-    the normalised input: x itself, or x + residual."""
+    the normalised input: x itself, or x + residual, and then ``out`` may be x
+    or residual."""
     dev = _device(x, "x")
     there = _elsewhere(dev, stream)
     if there is not None:
@@ -287,7 +349,8 @@ def layer_norm_train(x, gamma, beta=None, eps=1e-5, residual=None, out=None, str
 def layer_norm_backward(dy, s, gamma, mean, rstd, dsum=None, out=None, stream=None):
     """(dx, dgamma, dbeta) from dy and layer_norm_train's s, mean and rstd.
     ``dsum``: a gradient that reaches s past the norm (the residual stream's),
-    added to dx. dx is the gradient of x and of the residual alike."""
+    added to dx. dx is the gradient of x and of the residual alike. ``out``
+    (dx) may be dy, s or dsum."""
     dev = _device(s, "s")
     there = _elsewhere(dev, stream)
     if there is not None:
@@ -305,7 +368,8 @@ def layer_norm_backward(dy, s, gamma, mean, rstd, dsum=None, out=None, stream=No
     need = sz()
     _check(lib.tg_layer_norm_backward_workspace(rows, C, dt, ctypes.byref(need)),
            "tg_layer_norm_backward_workspace")
-    dx = _new_or(out, s, dev, True)
+    dx = _new_or(out, s, dev, True, dict(dy=dy, s=s, dsum=dsum),
+                 dict(gamma=gamma, mean=mean, rstd=rstd))
     dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
     ws = torch.empty(need.value, dtype=torch.uint8, device=s.device)
     _check(lib.tg_layer_norm_backward(
@@ -361,7 +425,8 @@ def causal_conv(x, w, bias=None, act="silu", initial_state=None, offsets=None, r
         with there:
             return causal_conv(x, w, bias, act, initial_state, offsets, return_state, out)
     args, packed, held, D = _conv_args(x, w, bias, act, initial_state, offsets, dev)
-    y = _new_or(out, x, dev, False)
+    y = _new_or(out, x, dev, False, {}, dict(x=x, w=w, bias=bias, initial_state=initial_state,
+                                             offsets=offsets))
     state, final = None, 0
     if return_state:
         state = torch.empty(held, dtype=x.dtype, device=x.device)
@@ -407,7 +472,8 @@ def causal_conv_step(x, state, w, bias=None, act="silu", slots=None, out=None, s
     """One token of each of n sequences: x [n, D] -> y [n, D]; ``state``
     [num_slots, K-1, D] moves on in place. ``slots`` (int32 [n]): each
     sequence's place in ``state`` (default: its number); a slot outside the
-    state marks a row without a sequence (y zero, nothing updated)."""
+    state marks a row without a sequence (y zero, nothing updated). ``out`` may
+    be x."""
     dev = _device(x, "x")
     there = _elsewhere(dev, stream)
     if there is not None:
@@ -421,7 +487,7 @@ def causal_conv_step(x, state, w, bias=None, act="silu", slots=None, out=None, s
     hp = _flat(state, "state", dev, (num, K - 1, D), dtype)
     sp = _flat(slots, "slots", dev, (n,), _I32)
     wp, bp = _flat(w, "w", dev, (K, D)), _flat(bias, "bias", dev, (D,))
-    y = _new_or(out, x, dev, True)
+    y = _new_or(out, x, dev, True, dict(x=x), dict(state=state, slots=slots, w=w, bias=bias))
     st = _lib().tg_causal_conv_step(xp, xs, hp, num, sp, wp, bp, n, D, K, dt, _activation(act),
                                     y.data_ptr(), _raw_stream(dev))
     if st:
@@ -466,7 +532,11 @@ def _scan_forward(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, offset
     packed, seqs = offsets is not None, _batch(x, offsets, dev)
     args, width, N, _ = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, seqs,
                                    packed, dev)
-    y = _new_or(out, x, dev, False)
+    # A token's x, dt and z are read by the thread that writes its y.
+    own = dict(x=x, dt=dt, z=z)
+    y = _new_or(out, x, dev, False, {} if train else own,
+                dict(own, A=A, B=B, C=C, D=D, dt_bias=dt_bias, initial_state=initial_state,
+                     offsets=offsets))
     state, final = None, 0
     if want_state:
         state = torch.empty((seqs[0], width, N), dtype=_F32, device=x.device)
@@ -500,7 +570,8 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=True, 
     x, dt, z: [S, L, channels] or packed [T, channels]; A [channels, N], N <=
     128; B, C [..., G, N], each group shared by channels/G neighbouring channels;
     D, dt_bias [channels]. ``initial_state`` fp32 [S, channels, N] (default
-    zeros). Returns y, or with ``return_state`` (y, state)."""
+    zeros). Returns y, or with ``return_state`` (y, state). ``out`` may be x, dt
+    or z."""
     dev = _device(x, "x")
     there = _elsewhere(dev, stream)
     if there is not None:
@@ -588,7 +659,7 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, sof
                         slots=None, out=None, stream=None):
     """One token of each of n sequences: x, dt, z [n, channels], B, C [n, G, N]
     -> y [n, channels]; ``state`` fp32 [num_slots, channels, N] is updated in
-    place. ``slots`` as in causal_conv_step."""
+    place. ``slots`` as in causal_conv_step. ``out`` may be x, dt or z."""
     dev = _device(x, "x")
     there = _elsewhere(dev, stream)
     if there is not None:
@@ -602,7 +673,8 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, sof
     num = state.shape[0]
     hp = _flat(state, "state", dev, (num, width, N))
     sp = _flat(slots, "slots", dev, (n,), _I32)
-    y = _new_or(out, x, dev, False)
+    y = _new_or(out, x, dev, False, dict(x=x, dt=dt, z=z),
+                dict(A=A, B=B, C=C, D=D, dt_bias=dt_bias, state=state, slots=slots))
     st = _lib().tg_selective_scan_step(args(_place(y, y.stride(), True, width), 0), hp, num, sp,
                                        _raw_stream(dev))
     if st:

@@ -67,8 +67,8 @@ typedef struct {
  * over each of `rows` rows of C >= 1 channels. x, residual: row strides >= C
  * (or 0: one row for all); y, sum: dense [rows][C]. residual and sum are given
  * together or not at all; sum may alias x or residual (same rows, dense), y
- * may alias x. beta, and mean with rstd (fp32 [rows], for the backward pass)
- * may be NULL. rows == 0 does nothing. */
+ * the other of the two (or, without a residual, x). beta, and mean with rstd
+ * (fp32 [rows], for the backward pass) may be NULL. rows == 0 does nothing. */
 tg_status tg_layer_norm(const void *x, int64_t x_stride, const void *residual,
                         int64_t residual_stride, const float *gamma, const float *beta, float eps,
                         int64_t rows, int C, tg_dtype dtype, void *y, void *sum, float *mean,
@@ -80,10 +80,10 @@ tg_status tg_layer_norm(const void *x, int64_t x_stride, const void *residual,
  *   dx = rstd * (g - sum_c g / C - h * sum_c (g*h) / C) (+ dsum)
  *   dgamma = sum over rows of dy * h,   dbeta = sum over rows of dy
  * dsum (may be NULL): a gradient that reaches s past the norm. dx, dense
- * [rows][C], is the gradient of x and of the residual alike; it may alias dsum
- * or dy (dense). dgamma, dbeta: fp32 [C], written (not added to), dbeta may be NULL.
- * rows == 0 writes zeros there. workspace: from the size query, 16-byte
- * aligned. */
+ * [rows][C], is the gradient of x and of the residual alike; it may alias dsum,
+ * dy or s (dense). dgamma, dbeta: fp32 [C], written (not added to), dbeta may
+ * be NULL. rows == 0 writes zeros there. workspace: from the size query,
+ * 16-byte aligned. */
 tg_status tg_layer_norm_backward_workspace(int64_t rows, int C, tg_dtype dtype, size_t *bytes);
 tg_status tg_layer_norm_backward(const void *dy, int64_t dy_stride, const void *s, int64_t s_stride,
                                  const float *gamma, const float *mean, const float *rstd,
@@ -128,7 +128,7 @@ tg_status tg_causal_conv_backward(const tg_causal_conv_args *a, tg_rows dy, tg_r
  * in place. state [num_slots][K-1][D] dense; sequence i keeps its state in
  * slot slots[i] (device int32 [n]; NULL: slot i, then n <= num_slots). Slots
  * below 0 or past the end mark rows without a sequence: y there is zero and
- * no state changes. Two sequences must not share a slot. */
+ * no state changes. Two sequences must not share a slot. y may alias x (dense). */
 tg_status tg_causal_conv_step(const void *x, int64_t x_stride, void *state, int64_t num_slots,
                               const int32_t *slots, const float *w, const float *bias, int64_t n,
                               int D, int K, tg_dtype dtype, tg_activation act, void *y,
@@ -162,7 +162,8 @@ typedef struct {
  * backward_bytes: scratch of tg_selective_scan_backward. Any may be NULL. */
 tg_status tg_selective_scan_sizes(const tg_scan_args *a, size_t *workspace_bytes,
                                   size_t *saved_bytes, size_t *backward_bytes);
-/* saved (fp32, may be NULL): filled for the backward pass. */
+/* saved (fp32, may be NULL): filled for the backward pass. y may be x, dt or z
+ * themselves (same address and strides), which a backward pass then lacks. */
 tg_status tg_selective_scan(const tg_scan_args *a, void *workspace, size_t workspace_bytes,
                             void *saved, size_t saved_bytes, void *stream);
 
@@ -183,9 +184,10 @@ tg_status tg_selective_scan_backward(const tg_scan_args *a, const tg_scan_grads 
 
 /* One token for each of n sequences: x, dt, z [n][D] and B, C [n][G][N] by
  * row stride (seqs.seqs = seqs.rows = n, offsets NULL; seq_stride is not
- * read), y likewise. state fp32 [num_slots][D][N], updated in place; slots as
- * in tg_causal_conv_step. initial and final are not read. TG_ERR_UNSUPPORTED
- * for 2^24 or more pairs of a sequence and 64 channels. */
+ * read), y likewise; it may be x, dt or z themselves. state fp32
+ * [num_slots][D][N], updated in place; slots as in tg_causal_conv_step. initial
+ * and final are not read. TG_ERR_UNSUPPORTED for 2^24 or more pairs of a
+ * sequence and 64 channels. */
 tg_status tg_selective_scan_step(const tg_scan_args *a, float *state, int64_t num_slots,
                                  const int32_t *slots, void *stream);
 

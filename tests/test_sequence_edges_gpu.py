@@ -1,5 +1,6 @@
 """The sequence operators on the GPU where a call is easily got wrong: rows
-that are broadcast over tokens, and batches of one row. Against the 64-bit references of seq_ref.py,
+that are broadcast over tokens, batches of one row, and outputs that share memory
+with arguments. Against the 64-bit references of seq_ref.py,
 with that file's bounds."""
 from __future__ import annotations
 
@@ -138,3 +139,70 @@ def test_scan_one_row_any_stride(packed, stride):
         assert torch.equal(got[1], w.reshape(D)), name
         assert bool((got[0] == 7).all()) and bool((got[2] == 7).all()), name
     assert torch.equal(dB, want.dB.reshape(1, N)) and torch.equal(dC, want.dC.reshape(1, N)) and torch.equal(dA, want.dA)
+
+
+# ---- outputs that share memory with arguments
+
+def _calls():
+    """name -> (call(out, tensors), the tensors that out may be, the others)."""
+    r = ScanCase(([1], False, 1, 1, 1, "f32", True, True, False, 0)).r
+    F16, S_, L, D, N = torch.float16, 2, 300, 64, 16
+    dev = lambda *s, **k: r(*s, **k).cuda()  # noqa: E731
+    A, w = -torch.arange(1, N + 1).float().repeat(D, 1).cuda(), dev(4, D)
+    b = dev(S_, L, 1, N, dtype=F16), dev(S_, L, 1, N, dtype=F16)
+    b1 = dev(S_, 1, N, dtype=F16), dev(S_, 1, N, dtype=F16)
+    rows, one = [dev(S_, L, D, dtype=F16) for _ in range(3)], [dev(S_, D, dtype=F16) for _ in range(3)]
+    g = dev(D)
+    mean, rstd = dev(S_, L), dev(S_, L).abs()
+    cs, ss = dev(S_, 3, D, dtype=F16), dev(S_, D, N)
+    return {
+        "norm": (lambda o, x: tg.layer_norm(x, g, out=o), rows[:1], []),
+        "norm residual": (lambda o, x, s: tg.layer_norm(x, g, residual=s, out=o)[0], rows[:2], []),
+        "norm train": (lambda o, x: tg.layer_norm_train(x, g, out=o)[0], [], rows[:1]),
+        "norm train residual": (lambda o, x, s: tg.layer_norm_train(x, g, residual=s, out=o)[0], rows[:2], []),
+        "norm backward": (lambda o, dy, s, ds: tg.layer_norm_backward(dy, s, g, mean, rstd, ds, out=o)[0], rows, []),
+        "conv": (lambda o, x: tg.causal_conv(x, w, out=o), [], rows[:1]),
+        "conv step": (lambda o, x: tg.causal_conv_step(x, cs.clone(), w, out=o), one[:1], []),
+        "scan": (lambda o, x, dt, z: tg.selective_scan(x, dt, A, *b, z=z, out=o), rows, []),
+        "scan train": (lambda o, x, dt, z: tg.selective_scan_train(x, dt, A, *b, z=z, out=o)[0], [], rows),
+        "scan step": (lambda o, x, dt, z: tg.selective_scan_step(x, dt, A, *b1, ss.clone(), z=z, out=o), one, []),
+    }
+
+
+@pytest.mark.parametrize("name", ["norm", "norm residual", "norm train", "norm train residual", "norm backward", "conv",
+                                  "conv step", "scan", "scan train", "scan step"])
+def test_out_and_arguments(name):
+    """An argument that out may be gives the same bits as a new tensor; any
+    other overlap is refused before a launch and leaves the arguments alone."""
+    call, may, apart = _calls()[name]
+    tensors = may or apart
+    want = call(None, *tensors)
+    assert torch.equal(call(torch.empty_like(want), *tensors), want)
+    for k in range(len(tensors)):
+        copies = [t.clone() for t in tensors]
+        if may:
+            assert torch.equal(call(copies[k], *copies), want), k
+        else:
+            with pytest.raises(ValueError, match="out shares memory"):
+                call(copies[k], *copies)
+            assert torch.equal(copies[k], tensors[k])
+        # One row further on in the same buffer.
+        flat = torch.zeros(want.numel() + want.shape[-1], dtype=want.dtype, device="cuda")
+        copies[k] = flat[:want.numel()].view_as(want).copy_(tensors[k])
+        with pytest.raises(ValueError, match="out shares memory"):
+            call(flat[want.shape[-1]:].view_as(want), *copies)
+        assert torch.equal(copies[k], tensors[k])
+
+
+def test_out_beside_an_argument():
+    """The other half of the projection's rows, and the rows after a chunk's, are free."""
+    r = ScanCase(([1], False, 1, 1, 1, "f32", True, True, False, 0)).r
+    xz, w = r(2, 50, 64, dtype=torch.float16).cuda(), r(4, 32).cuda()
+    want = tg.causal_conv(xz[..., :32], w)
+    assert torch.equal(tg.causal_conv(xz[..., :32], w, out=xz[..., 32:]), want)
+    x = r(2, 50, 32, dtype=torch.float16).cuda()
+    want = tg.causal_conv(x[:, :20], w)
+    assert torch.equal(tg.causal_conv(x[:, :20], w, out=x[:, 30:]), want)
+    state = r(2, 3, 32).cuda()
+    with pytest.raises(ValueError, match="out shares memory with initial_state"):
+        tg.causal_conv(r(2, 3, 32).cuda(), w, initial_state=state, out=state)
