@@ -26,6 +26,8 @@
 // kernel computes the parts' P and last states.
 //
 // Tokens past the end count as d = 0 (and dL/dv = 0): a = 1, and the state stays.
+#include <float.h>
+
 #include "seq_device.hpp"
 #include "seq_internal.hpp"
 #include "tg_internal.hpp"
@@ -358,6 +360,13 @@ __device__ __forceinline__ int state_of(int q, int j) {
     return !ROWS || NS < 4 ? q * NS + j : (j & ~3) * 4 + q * 4 + (j & 3);
 }
 
+// A * log2(e), held within fp32: a rate past it would make NaN of a step of zero, as
+// tokens past the end have, and forgets the state at any other step either way.
+__device__ __forceinline__ float rate2(float A) {
+    const float v = A * kLog2e;
+    return v < -FLT_MAX ? -FLT_MAX : v > FLT_MAX ? FLT_MAX : v;  // NaN stays
+}
+
 // log2(a) = d * A2 of the lane's states, zero past N and for lanes without a
 // channel.
 template <int NS, bool ROWS>
@@ -365,7 +374,7 @@ __device__ __forceinline__ void load_A2(const ScanArgs& a, const Place& p, float
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
         const int n = state_of<NS, ROWS>(p.q, j);
-        A2[j] = p.in && n < a.N ? a.A[(int64_t)p.ch * a.N + n] * kLog2e : 0.0f;
+        A2[j] = p.in && n < a.N ? rate2(a.A[(int64_t)p.ch * a.N + n]) : 0.0f;
     }
 }
 template <int NS, bool ROWS>
@@ -1181,7 +1190,7 @@ __global__ __launch_bounds__(256) void scan_step(const StepArgs b) {
         load_f32<float, VN>(Ap + n, A);
 #pragma unroll
         for (int j = 0; j < VN; ++j) {
-            const float e = __builtin_amdgcn_exp2f(d * (A[j] * kLog2e));
+            const float e = __builtin_amdgcn_exp2f(d * rate2(A[j]));
             h[j] = __builtin_fmaf(e, h[j], d * x * (float)Bp[n + j]);
             v = __builtin_fmaf(h[j], (float)Cp[n + j], v);
         }

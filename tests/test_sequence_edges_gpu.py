@@ -1,6 +1,6 @@
 """The sequence operators on the GPU where a call is easily got wrong: rows
-that are broadcast over tokens, batches of one row, and outputs that share memory
-with arguments. Against the 64-bit references of seq_ref.py,
+that are broadcast over tokens, batches of one row, outputs that share memory
+with arguments, and decays without bounds. Against the 64-bit references of seq_ref.py,
 with that file's bounds."""
 from __future__ import annotations
 
@@ -206,3 +206,72 @@ def test_out_beside_an_argument():
     state = r(2, 3, 32).cuda()
     with pytest.raises(ValueError, match="out shares memory with initial_state"):
         tg.causal_conv(r(2, 3, 32).cuda(), w, initial_state=state, out=state)
+
+
+# ---- decays without bounds
+
+def _check_scan(c, dy=None):
+    """Outputs and final states, and with dy the gradients, against the reference."""
+    y, state, saved = tg.selective_scan_train(*c.args(), return_state=True, **c.more())
+    y2, state2 = tg.selective_scan(*c.args(), return_state=True, **c.more())
+    assert torch.equal(y, y2) and torch.equal(state, state2)
+    refs = [c.ref(i, R.scan) for i in range(c.S)]
+    R.check("y", y.reshape(c.x.shape), *_cat([r[0] for r in refs]))
+    R.check("state", state, torch.stack([r[1][0] for r in refs]), torch.stack([r[1][1] for r in refs]))
+    if dy is None:
+        return
+    got = tg.selective_scan_backward(c.dev(dy), *c.args(), saved, **c.more())
+    refs = [c.ref(i, R.scan_grads, dy) for i in range(c.S)]
+    for name in ("dx", "ddt", "dz"):
+        if getattr(got, name) is not None:
+            R.check(name, getattr(got, name).reshape(c.x.shape), *_cat([r[name] for r in refs]))
+    for name in ("dB", "dC"):
+        R.check(name, getattr(got, name).reshape(c.T, c.G, c.N), *_cat([r[name] for r in refs]))
+    for name, key in (("dA", "dA"), ("dD", "dD"), ("ddt_bias", "dbias")):
+        v, e = sum(r[key][0] for r in refs), sum(r[key][1] for r in refs)
+        R.check(name, getattr(got, name), v, e + (c.S + 1) * R.E * sum(r[key][0].abs() for r in refs))
+    if c.init is not None:
+        R.check("dinit", got.dinitial_state, torch.stack([r["dinit"][0] for r in refs]),
+                torch.stack([r["dinit"][1] for r in refs]))
+
+
+FORGET = [([21, 21], False, 20, 16, 1, "f32", False, True, True, 0), ([5, 0, 37, 1], True, 34, 16, 2, "f16", True, True, True, 0),
+          ([600], False, 16, 16, 1, "f32", True, True, True, 0), ([23], False, 16, 100, 2, "f32", True, True, False, 0)]
+
+
+@pytest.mark.parametrize("case", FORGET, ids=str)
+def test_scan_forgets_at_once(case):
+    """Rates whose product with log2(e) is past fp32: the state is forgotten at
+    every step above zero and kept by a step of zero, as by the tokens past the end."""
+    note("scan %s, rates of -3e38" % (case,))
+    c = ScanCase(case)
+    c.A[0], c.A[3, 1] = -3e38, -3e38
+    _check_scan(c, c.r(*c.x.shape, dtype=c.dtype))
+    c.dt[c.T // 2:c.T // 2 + 2] = -200  # a step that softplus makes zero
+    _check_scan(c)
+    # With a rate of minus infinity the same (seq_ref.py's bounds need finite ones).
+    want = tg.selective_scan(*c.args(), return_state=True, **c.more())
+    c.A[0], c.A[3, 1] = -float("inf"), -float("inf")
+    got = tg.selective_scan(*c.args(), return_state=True, **c.more())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_scan_many_sequences_and_step_forget_at_once():
+    r = ScanCase(([1], False, 1, 1, 1, "f32", True, True, False, 0)).r
+    S_, L, D, N = 4100, 19, 16, 16
+    A = -torch.arange(1, N + 1).float().repeat(D, 1)
+    A[0], A[3, 1] = -3e38, -3e38
+    x, dt, B, C = r(S_, L, D), r(S_, L, D, scale=0.5), r(S_, L, 1, N), r(S_, L, 1, N)
+    init = r(S_, D, N)
+    dt[7, 5] = -200
+    y, state = tg.selective_scan(up(x), up(dt), up(A), up(B), up(C), initial_state=up(init), return_state=True)
+    st = up(init)
+    for t in range(L):
+        yt = tg.selective_scan_step(up(x[:, t]), up(dt[:, t]), up(A), up(B[:, t]), up(C[:, t]), st)
+    for i in (0, 7, S_ - 1):
+        ref = (x[i].double(), dt[i].double(), A.double(), B[i].double(), C[i].double(), None, None, None, True, init[i].double())
+        (v, b), (h, eh), _ = R.scan(*ref)
+        R.check("y", y[i], v, b)
+        R.check("state", state[i], h, eh)
+        R.check("step y", yt[i], v[-1], b[-1])
+        R.check("step state", st[i], h, eh)
