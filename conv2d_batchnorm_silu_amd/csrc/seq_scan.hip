@@ -25,6 +25,12 @@
 // workgroups split the tokens in the same way (parts of PL tokens): a first
 // kernel computes the parts' P and last states.
 //
+// A decay P over a segment may be past fp32 (a rate above zero, a negative step) where
+// the states that it carries are not: a state of zero, above all. Multiplying twice by
+// the root of P, held at fp32's largest, is right for those: P past the square of that
+// makes any state but zero infinite. Calls that may have such decays see a state come out
+// infinite or NaN and go over the segments again by the roots.
+//
 // Tokens past the end count as d = 0 (and dL/dv = 0): a = 1, and the state stays.
 #include <float.h>
 
@@ -57,7 +63,7 @@ struct ScanArgs {
     Rows<void> y;
     const float *A, *D_skip, *dt_bias, *initial;
     float *final, *saved;
-    float* parts;  // [slots of PL tokens][2][D][4*NS]: P and last state
+    float* parts;  // [slots of PL tokens][2][D][4*NS]: P (or its root) and last state
 };
 
 // Value k of a pair over two lanes: the lane whose bit is clear keeps a, the
@@ -344,14 +350,18 @@ struct Shared {
     }
 };
 
-// A wave's states (or their adjoints) after its segment from zero, and the decay over it:
-// LDS [W][2][64][NS] floats, and after them [64][NS]: the true state that the round
-// before left.
+// A wave's states (or their adjoints) after its segment from zero, and the decay over it
+// (or its root): LDS [W][2][64][NS] floats, and after them [64][NS]: the true state that the round
+// before left; then [W][64], the segments' sums of step sizes.
 template <int NS>
 __device__ __forceinline__ float* exchange_at(float* ex, int w, int which) {
     return ex + ((w * 2 + which) * 64 + (threadIdx.x & 63)) * NS;
 }
-constexpr int exchange_floats(int W, int ns) { return (2 * W + 1) * 64 * ns; }
+template <int NS>
+__device__ __forceinline__ float* sum_at(float* ex, int W, int w) {
+    return ex + (2 * W + 1) * 64 * NS + w * 64 + (threadIdx.x & 63);
+}
+constexpr int exchange_floats(int W, int ns) { return (2 * W + 1) * 64 * ns + W * 64; }
 
 // State j of a lane, with lanes by rows: the rows of a 16 x 16 matrix that the
 // lane holds, 4q to 4q+3 (with NS < 4 only NS of them are used).
@@ -396,6 +406,43 @@ __device__ __forceinline__ void store_state(float* st, const ScanArgs& a, const 
         if (n < a.N) st[((int64_t)p.s * a.D + p.ch) * a.N + n] = h[j];
     }
 }
+// The root of a decay 2^L.
+__device__ __forceinline__ float root_decay(float L) {
+    return fminf(__builtin_amdgcn_exp2f(0.5f * L), FLT_MAX);
+}
+// The state (or adjoint) h over a segment of that root which leaves e from zero.
+__device__ __forceinline__ float carried(float root, float h, float e) {
+    return __builtin_fmaf(root, root * h, e);
+}
+// Whether a segment's decay can be more than 1, by whole waves: the same in all waves
+// that hold these channels.
+template <int NS>
+__device__ __forceinline__ bool may_grow(const ScanArgs& a, const float (&A2)[NS]) {
+    float most = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) most = fmaxf(most, A2[j]);
+    return !a.softplus || __ballot(most > 0.0f) != 0;
+}
+// The state h after the segments first, first + step, ... (n of them) of the exchange: if
+// it came out infinite or NaN, as a decay past fp32 makes any state and more decays
+// keep it, again by the roots.
+template <int NS>
+__device__ __forceinline__ void carry_grown(float* ex, int W, int first, int n, int step,
+                                            const float (&A2)[NS], float (&h)[NS]) {
+    float nan = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) nan = __builtin_fmaf(h[j], 0.0f, nan);
+    if (__ballot(nan != 0.0f) == 0) return;
+    get<NS>(exchange_at<NS>(ex, W, 0), h);
+#pragma clang loop unroll(disable)
+    for (int k = 0; k < n; ++k) {
+        float e[NS];
+        const float sum = *sum_at<NS>(ex, W, first + k * step);
+        get<NS>(exchange_at<NS>(ex, first + k * step, 1), e);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) h[j] = carried(root_decay(sum * A2[j]), h[j], e[j]);
+    }
+}
 template <int NS>
 __device__ __forceinline__ float* part_at(const ScanArgs& a, const Place& p, int part, int which) {
     return a.parts + (((p.part0 + part) * 2 + which) * a.D + p.ch) * (4 * NS) + p.q * NS;
@@ -404,7 +451,7 @@ __device__ __forceinline__ float* part_at(const ScanArgs& a, const Place& p, int
 // h through parts first, first + step, ... (n of them), from memory four at a time.
 template <int NS>
 __device__ __forceinline__ void fold_parts(const ScanArgs& a, const Place& p, int first, int n,
-                                           int step, float (&h)[NS]) {
+                                           int step, bool grow, float (&h)[NS]) {
     for (int k = 0; k < n; k += 4) {
         float P[4][NS], e[4][NS];
 #pragma unroll
@@ -417,7 +464,9 @@ __device__ __forceinline__ void fold_parts(const ScanArgs& a, const Place& p, in
         for (int u = 0; u < 4; ++u)
             if (k + u < n)
 #pragma unroll
-                for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(P[u][j], h[j], e[u][j]);
+                for (int j = 0; j < NS; ++j)
+                    h[j] = grow ? carried(P[u][j], h[j], e[u][j])
+                                : __builtin_fmaf(P[u][j], h[j], e[u][j]);
     }
 }
 
@@ -506,8 +555,9 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64)
     float* const exchange = (float*)((Steps<TT>*)lds + W);
     float A2[NS], h[NS];
     load_A2<NS, true>(a, p, A2);
+    const bool grow = SPLIT && may_grow<NS>(a, A2);
     load_state<NS, true>(a.initial, a, p, h);
-    if (a.PL) fold_parts<NS>(a, p, 0, p.part(a.PL), 1, h);
+    if (a.PL) fold_parts<NS>(a, p, 0, p.part(a.PL), 1, grow, h);
     const float skip = a.D_skip ? a.D_skip[p.ch] : 0.0f;
     const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
     constexpr int E = sizeof(T);
@@ -579,6 +629,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64)
             flip ^= 1;
             put<NS>(exchange_at<NS>(ex, p.w, 0), P);
             put<NS>(exchange_at<NS>(ex, p.w, 1), e);
+            *sum_at<NS>(ex, W, p.w) = sum;
             __syncthreads();
             // The other buffer is written next, past this barrier of the next
             // round: nobody still reads it then.
@@ -601,6 +652,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64)
 #pragma unroll
                 for (int j = 0; j < NS; ++j) r[j] = __builtin_fmaf(P[j], r[j], e[j]);
             }
+            if (__builtin_expect(grow, 0)) carry_grown<NS>(ex, W, 0, p.w, 1, A2, r);
             save(l, r);
             // The second run, from the true state. Its products d*x*B are made
             // again: holding them would take as many registers as the decays.
@@ -656,6 +708,28 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64)
     if (p.w == W - 1 && p.hi == p.len) store_state<NS, true>(a.final, a, p, h);
 }
 
+// The decay of one run (its root, if a decay can be more than 1) and its state h over
+// n more, first, first + step, ...; sum: of the run's step sizes.
+template <int NS>
+__device__ __forceinline__ void join_runs(float* ex, int W, int first, int n, int step,
+                                          const float (&A2)[NS], bool grow, float sum,
+                                          float (&P)[NS], float (&h)[NS]) {
+    for (int k = 0; k < n; ++k) {
+        float Q[NS], e[NS];
+        get<NS>(exchange_at<NS>(ex, first + k * step, 0), Q);
+        get<NS>(exchange_at<NS>(ex, first + k * step, 1), e);
+        sum += *sum_at<NS>(ex, W, first + k * step);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            h[j] = grow ? carried(Q[j], h[j], e[j]) : __builtin_fmaf(Q[j], h[j], e[j]);
+            P[j] *= Q[j];
+        }
+    }
+    if (grow)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) P[j] = root_decay(sum * A2[j]);
+}
+
 // The parts' decays and last states from zero, for all parts but a sequence's
 // last. The waves take a part's tokens in W runs side by side.
 template <typename T, int NS, int TT>
@@ -668,6 +742,7 @@ __global__ __launch_bounds__(64 * waves_for(NS)) void scan_parts(const ScanArgs 
     float* const ex = (float*)((Steps<TT>*)lds + W);
     float A2[NS], h[NS], sum = 0.0f;
     load_A2<NS, true>(a, p, A2);
+    const bool grow = may_grow<NS>(a, A2);
 #pragma unroll
     for (int j = 0; j < NS; ++j) h[j] = 0.0f;
     const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
@@ -711,18 +786,14 @@ __global__ __launch_bounds__(64 * waves_for(NS)) void scan_parts(const ScanArgs 
     }
     float P[NS];
 #pragma unroll
-    for (int j = 0; j < NS; ++j) P[j] = __builtin_amdgcn_exp2f(sum * A2[j]);
+    for (int j = 0; j < NS; ++j)
+        P[j] = grow ? root_decay(sum * A2[j]) : __builtin_amdgcn_exp2f(sum * A2[j]);
     put<NS>(exchange_at<NS>(ex, p.w, 0), P);
     put<NS>(exchange_at<NS>(ex, p.w, 1), h);
+    *sum_at<NS>(ex, W, p.w) = sum;
     __syncthreads();
     if (p.w != 0) return;
-    for (int k = 1; k < W; ++k) {
-        float Q[NS], e[NS];
-        get<NS>(exchange_at<NS>(ex, k, 0), Q);
-        get<NS>(exchange_at<NS>(ex, k, 1), e);
-#pragma unroll
-        for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(Q[j], h[j], e[j]), P[j] *= Q[j];
-    }
+    join_runs<NS>(ex, W, 1, W - 1, 1, A2, grow, sum, P, h);
     if (!p.in) return;
     put<NS>(part_at<NS>(a, p, p.part(a.PL), 0), P);
     put<NS>(part_at<NS>(a, p, p.part(a.PL), 1), h);
@@ -750,6 +821,10 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
                                                                             const ScanGrads b) {
     // dB and dC: values of a token after its own levels, and tokens of a group.
     constexpr int kItems = TT / 4, kHeld = NS >> levels_of(NS), GT = NS < 16 ? 16 / NS : 1;
+    // Segments by their decays' roots at once, or by their decays: going over them
+    // again costs registers, the roots operations (2 x 2048 tokens, 2048 channels, both
+    // passes: 16 states 225 us and 2 more by roots, 24 states 464 and 418 by roots).
+    constexpr bool kRoots = NS > 4;
     extern __shared__ float4 lds[];
     const int W = SPLIT ? blockDim.x >> 6 : 1;
     const Place p(a, false);
@@ -768,10 +843,11 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
     // c: a[t+1]*g[t+1] of the next token.
     float A2[NS], c[NS], dA[NS];
     load_A2<NS, false>(a, p, A2);
+    const bool grow = SPLIT && may_grow<NS>(a, A2);
     load_state<NS, false>(b.dfinal, a, p, c);
     if (a.PL) {
         const int last = p.len > 0 ? (p.len - 1) / a.PL : 0;
-        fold_parts<NS>(a, p, last, last - p.part(a.PL), -1, c);
+        fold_parts<NS>(a, p, last, last - p.part(a.PL), -1, grow, c);
     }
 #pragma unroll
     for (int j = 0; j < NS; ++j) dA[j] = 0.0f;
@@ -884,12 +960,17 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int j = 0; j < NS; ++j) P[j] = __builtin_amdgcn_exp2f(sum * A2[j]);
+            for (int j = 0; j < NS; ++j)
+                P[j] = kRoots ? root_decay(sum * A2[j]) : __builtin_amdgcn_exp2f(sum * A2[j]);
             float* const ex = exchange + flip * exchange_floats(W, NS);
             flip ^= 1;
             put<NS>(exchange_at<NS>(ex, p.w, 0), P);
             put<NS>(exchange_at<NS>(ex, p.w, 1), e);
+            if (!kRoots) *sum_at<NS>(ex, W, p.w) = sum;
             __syncthreads();
+            const auto over = [](float v, float x, float y) {
+                return kRoots ? carried(v, x, y) : __builtin_fmaf(v, x, y);
+            };
             get<NS>(exchange_at<NS>(ex, W, 0), c);
             // Two segments at a time: one by one the reads' latency adds up.
             int m = W - 1;
@@ -901,14 +982,16 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
                 get<NS>(exchange_at<NS>(ex, m - 1, 1), e1);
 #pragma unroll
                 for (int j = 0; j < NS; ++j)
-                    c[j] = __builtin_fmaf(P1[j], __builtin_fmaf(P[j], c[j], e[j]), e1[j]);
+                    c[j] = over(P1[j], over(P[j], c[j], e[j]), e1[j]);
             }
             if (m > p.w) {
                 get<NS>(exchange_at<NS>(ex, m, 0), P);
                 get<NS>(exchange_at<NS>(ex, m, 1), e);
 #pragma unroll
-                for (int j = 0; j < NS; ++j) c[j] = __builtin_fmaf(P[j], c[j], e[j]);
+                for (int j = 0; j < NS; ++j) c[j] = over(P[j], c[j], e[j]);
             }
+            if (!kRoots && __builtin_expect(grow, 0))
+                carry_grown<NS>(ex, W, W - 1, W - 1 - p.w, -1, A2, c);
         }
         float dAc[NS];
 #pragma unroll
@@ -1043,6 +1126,7 @@ __global__ __launch_bounds__(64 * waves_for(NS)) void scan_bwd_parts(const ScanA
     float* const ex = (float*)((Tile<NS, TT>*)lds + W);
     float A2[NS], c[NS], sum = 0.0f;
     load_A2<NS, false>(a, p, A2);
+    const bool grow = may_grow<NS>(a, A2);
 #pragma unroll
     for (int j = 0; j < NS; ++j) c[j] = 0.0f;
     const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
@@ -1085,18 +1169,14 @@ __global__ __launch_bounds__(64 * waves_for(NS)) void scan_bwd_parts(const ScanA
     }
     float P[NS];
 #pragma unroll
-    for (int j = 0; j < NS; ++j) P[j] = __builtin_amdgcn_exp2f(sum * A2[j]);
+    for (int j = 0; j < NS; ++j)
+        P[j] = grow ? root_decay(sum * A2[j]) : __builtin_amdgcn_exp2f(sum * A2[j]);
     put<NS>(exchange_at<NS>(ex, p.w, 0), P);
     put<NS>(exchange_at<NS>(ex, p.w, 1), c);
+    *sum_at<NS>(ex, W, p.w) = sum;
     __syncthreads();
     if (p.w != W - 1) return;
-    for (int k = W - 2; k >= 0; --k) {
-        float Q[NS], e[NS];
-        get<NS>(exchange_at<NS>(ex, k, 0), Q);
-        get<NS>(exchange_at<NS>(ex, k, 1), e);
-#pragma unroll
-        for (int j = 0; j < NS; ++j) c[j] = __builtin_fmaf(Q[j], c[j], e[j]), P[j] *= Q[j];
-    }
+    join_runs<NS>(ex, W, W - 2, W - 1, -1, A2, grow, sum, P, c);
     if (!p.in) return;
     put<NS>(part_at<NS>(a, p, p.part(a.PL), 0), P);
     put<NS>(part_at<NS>(a, p, p.part(a.PL), 1), c);

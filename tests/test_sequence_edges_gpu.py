@@ -210,7 +210,18 @@ def test_out_beside_an_argument():
 
 # ---- decays without bounds
 
-def _check_scan(c, dy=None):
+def _flipped(c, i, dy, dstate, n):
+    """The reference's bound on dx of the first n channels with -dt, -A and -B, which give
+    the same products: it counts a step d as d, not |d|, so of the two the larger
+    is the bound wherever the sign."""
+    lo, hi = c.b[i], c.b[i + 1]
+    cut = lambda t: None if t is None else t[lo:hi, :n].double()  # noqa: E731
+    bc = lambda t: t[lo:hi, :1].double()  # noqa: E731
+    return R.scan_grads(cut(dy), cut(c.x), -cut(c.dt), -c.A[:n].double(), -bc(c.B), bc(c.C), c.skip[:n].double(),
+                        cut(c.z), -c.bias[:n].double(), False, c.init[i, :n].double(), dfinal=dstate[i, :n].double())["dx"][1]
+
+
+def _check_scan(c, dy=None, dstate=None, below=0):
     """Outputs and final states, and with dy the gradients, against the reference."""
     y, state, saved = tg.selective_scan_train(*c.args(), return_state=True, **c.more())
     y2, state2 = tg.selective_scan(*c.args(), return_state=True, **c.more())
@@ -220,8 +231,12 @@ def _check_scan(c, dy=None):
     R.check("state", state, torch.stack([r[1][0] for r in refs]), torch.stack([r[1][1] for r in refs]))
     if dy is None:
         return
-    got = tg.selective_scan_backward(c.dev(dy), *c.args(), saved, **c.more())
-    refs = [c.ref(i, R.scan_grads, dy) for i in range(c.S)]
+    got = tg.selective_scan_backward(c.dev(dy), *c.args(), saved, dstate=up(dstate), **c.more())
+    refs = [c.ref(i, R.scan_grads, dy, dfinal=None if dstate is None else dstate[i].double())
+            for i in range(c.S)]
+    for i in range(c.S if below else 0):
+        bound = refs[i]["dx"][1]
+        bound[:, :below] = torch.maximum(bound[:, :below], _flipped(c, i, dy, dstate, below))
     for name in ("dx", "ddt", "dz"):
         if getattr(got, name) is not None:
             R.check(name, getattr(got, name).reshape(c.x.shape), *_cat([r[name] for r in refs]))
@@ -275,3 +290,49 @@ def test_scan_many_sequences_and_step_forget_at_once():
         R.check("state", state[i], h, eh)
         R.check("step y", yt[i], v[-1], b[-1])
         R.check("step state", st[i], h, eh)
+
+
+GROW = [
+    # the scan; the growing tokens of each sequence, and log2 of a step's growth
+    (([30], False, 16, 16, 1, "f32", False, False, True, 0), 8, 18, 18.75),
+    (([30, 30], False, 40, 16, 2, "bf16", True, False, True, 0), 9, 19, 18.75),
+    (([2, 30, 0, 25], True, 20, 5, 1, "f32", True, False, True, 0), 8, 18, 18.75),
+    (([30], False, 16, 16, 1, "f32", True, True, True, 0), 8, 18, 18.75),
+    (([20], False, 16, 100, 1, "f32", False, False, True, 0), 8, 11, 60.0),
+    (([600], False, 16, 16, 1, "f32", True, False, True, 0), 100, 190, 2.1),
+    (([600], False, 16, 4, 1, "f32", True, True, True, 0), 300, 390, 2.1),
+    (([40, 900, 1], True, 18, 24, 1, "f32", False, False, True, 0), 380, 470, 2.1),
+]
+
+
+@pytest.mark.parametrize("case,lo,hi,rate", GROW, ids=str)
+def test_scan_grows_past_fp32_on_the_way(case, lo, hi, rate):
+    """Channels 0 to 3 grow (positive rates, or negative steps) by 2^180 or more in
+    all: past fp32 over a segment of the split, while their states stay within it,
+    2^-100 becoming 2^80, and zero staying zero. The adjoints likewise, backwards."""
+    note("scan %s grows by 2^%g a step from %d to %d" % (case, rate, lo, hi))
+    c = ScanCase(case)
+    step = rate * 0.6931471805599453
+    inside = torch.zeros(c.T, dtype=torch.bool)
+    for b, e in zip(c.b, c.b[1:]):
+        inside[b + lo:max(b + lo, min(b + hi, e))] = True
+    grow = torch.where(inside, 1.0, 0.0)[:, None]
+    c.bias[:4] = 0
+    if c.soft:  # a rate above zero; steps of 1 and, elsewhere, of almost nothing
+        c.A[:4] = step
+        c.dt[:, :4] = (grow * 0.5413248546 - (1 - grow) * 40).to(c.dtype)
+    else:  # steps below zero
+        c.A[:4] = -1.0
+        c.dt[:, :4] = (grow * -step + (1 - grow) * 0.001).to(c.dtype)
+    c.x[:, :4] = 0
+    c.init[:, :4] = 2.0 ** -100
+    c.init[:, 0] = c.init[:, 2] = 0
+    dy = c.r(*c.x.shape, dtype=c.dtype)
+    dy[:, :4] = 0
+    dstate = c.r(c.S, c.D, c.N)
+    dstate[:, :4] = 2.0 ** -100
+    dstate[:, 0] = dstate[:, 3] = 0
+    y, state = tg.selective_scan(*c.args(), return_state=True, **c.more())
+    assert not state[:, 0].any() and not state[:, 2].any()
+    assert float(state[:, 1].max()) > 2.0 ** 75
+    _check_scan(c, dy, dstate, below=0 if c.soft else 4)
