@@ -28,8 +28,10 @@
 // A decay P over a segment may be past fp32 (a rate above zero, a negative step) where
 // the states that it carries are not: a state of zero, above all. Multiplying twice by
 // the root of P, held at fp32's largest, is right for those: P past the square of that
-// makes any state but zero infinite. Calls that may have such decays see a state come out
-// infinite or NaN and go over the segments again by the roots.
+// makes any state but zero infinite. The backward pass takes the roots always. The forward
+// pass, where the second multiplication counts for more (prompts 208 us for 192), takes P, and
+// where such decays may be sees a state come out infinite or NaN and goes over the
+// segments again by the roots.
 //
 // Tokens past the end count as d = 0 (and dL/dv = 0): a = 1, and the state stays.
 #include <float.h>
@@ -45,14 +47,17 @@ constexpr int kCh = 16;  // channels of a wave
 constexpr float kLn2 = 0.69314718055994531f;
 
 // Tokens that a wave takes at a time. The backward pass holds TT tokens'
-// decays and states (for NS = 4 two waves on a SIMD with 16 tokens; 8 tokens
-// and three waves took 5% longer, with the joins twice as often). The forward
-// pass holds decays only: 8 tokens leave room for four waves on a SIMD, which
-// took 203 us where two waves of 16 tokens took 241 (4 x 4096 tokens, 2048 channels, bf16).
+// decays and states: for NS = 4 two waves on a SIMD with 16 tokens. With 8 its kernel took
+// as long on three waves (163 us against 167, 2 x 2048 tokens, 2048 channels), the
+// training step 5% more, saving twice the states. The split kernels go to scratch even so:
+// 6 registers for NS = 4, 16 for 8, over 100 for 32. The forward pass holds decays only,
+// without scratch: 8 tokens leave room for four waves on a SIMD, which took
+// 203 us where two waves of 16 tokens took 241 (4 x 4096 tokens, 2048 channels, bf16).
 constexpr int chunk_for(int ns) { return ns <= 4 ? 16 : 64 / ns < 4 ? 4 : 64 / ns; }
 constexpr int fwd_chunk_for(int ns) { return ns <= 4 ? 8 : chunk_for(ns); }
-// Waves of a workgroup side by side: what they exchange (2*NS values for
-// each lane, in two buffers) stays within 64 KB of LDS.
+// Waves of a workgroup side by side: what they exchange (2*NS values for each lane, in
+// two buffers) takes 12 to 38 KiB of LDS for NS up to 4 and 72 to 81 above, 148 with the
+// backward pass's tiles at most (NS = 8), of a compute unit's 160.
 constexpr int waves_for(int ns) { return ns <= 8 ? 8 : 64 / ns; }
 
 struct ScanArgs {
@@ -423,12 +428,11 @@ __device__ __forceinline__ bool may_grow(const ScanArgs& a, const float (&A2)[NS
     for (int j = 0; j < NS; ++j) most = fmaxf(most, A2[j]);
     return !a.softplus || __ballot(most > 0.0f) != 0;
 }
-// The state h after the segments first, first + step, ... (n of them) of the exchange: if
-// it came out infinite or NaN, as a decay past fp32 makes any state and more decays
-// keep it, again by the roots.
+// The state h after the exchange's first n segments: if it came out infinite or NaN, as
+// a decay past fp32 makes any state and more decays keep it, again by the roots.
 template <int NS>
-__device__ __forceinline__ void carry_grown(float* ex, int W, int first, int n, int step,
-                                            const float (&A2)[NS], float (&h)[NS]) {
+__device__ __forceinline__ void carry_grown(float* ex, int W, int n, const float (&A2)[NS],
+                                            float (&h)[NS]) {
     float nan = 0.0f;
 #pragma unroll
     for (int j = 0; j < NS; ++j) nan = __builtin_fmaf(h[j], 0.0f, nan);
@@ -437,8 +441,8 @@ __device__ __forceinline__ void carry_grown(float* ex, int W, int first, int n, 
 #pragma clang loop unroll(disable)
     for (int k = 0; k < n; ++k) {
         float e[NS];
-        const float sum = *sum_at<NS>(ex, W, first + k * step);
-        get<NS>(exchange_at<NS>(ex, first + k * step, 1), e);
+        const float sum = *sum_at<NS>(ex, W, k);
+        get<NS>(exchange_at<NS>(ex, k, 1), e);
 #pragma unroll
         for (int j = 0; j < NS; ++j) h[j] = carried(root_decay(sum * A2[j]), h[j], e[j]);
     }
@@ -652,7 +656,7 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64)
 #pragma unroll
                 for (int j = 0; j < NS; ++j) r[j] = __builtin_fmaf(P[j], r[j], e[j]);
             }
-            if (__builtin_expect(grow, 0)) carry_grown<NS>(ex, W, 0, p.w, 1, A2, r);
+            if (__builtin_expect(grow, 0)) carry_grown<NS>(ex, W, p.w, A2, r);
             save(l, r);
             // The second run, from the true state. Its products d*x*B are made
             // again: holding them would take as many registers as the decays.
@@ -821,10 +825,6 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
                                                                             const ScanGrads b) {
     // dB and dC: values of a token after its own levels, and tokens of a group.
     constexpr int kItems = TT / 4, kHeld = NS >> levels_of(NS), GT = NS < 16 ? 16 / NS : 1;
-    // Segments by their decays' roots at once, or by their decays: going over them
-    // again costs registers, the roots operations (2 x 2048 tokens, 2048 channels, both
-    // passes: 16 states 225 us and 2 more by roots, 24 states 464 and 418 by roots).
-    constexpr bool kRoots = NS > 4;
     extern __shared__ float4 lds[];
     const int W = SPLIT ? blockDim.x >> 6 : 1;
     const Place p(a, false);
@@ -843,11 +843,10 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
     // c: a[t+1]*g[t+1] of the next token.
     float A2[NS], c[NS], dA[NS];
     load_A2<NS, false>(a, p, A2);
-    const bool grow = SPLIT && may_grow<NS>(a, A2);
     load_state<NS, false>(b.dfinal, a, p, c);
     if (a.PL) {
         const int last = p.len > 0 ? (p.len - 1) / a.PL : 0;
-        fold_parts<NS>(a, p, last, last - p.part(a.PL), -1, grow, c);
+        fold_parts<NS>(a, p, last, last - p.part(a.PL), -1, true, c);
     }
 #pragma unroll
     for (int j = 0; j < NS; ++j) dA[j] = 0.0f;
@@ -960,17 +959,12 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int j = 0; j < NS; ++j)
-                P[j] = kRoots ? root_decay(sum * A2[j]) : __builtin_amdgcn_exp2f(sum * A2[j]);
+            for (int j = 0; j < NS; ++j) P[j] = root_decay(sum * A2[j]);
             float* const ex = exchange + flip * exchange_floats(W, NS);
             flip ^= 1;
             put<NS>(exchange_at<NS>(ex, p.w, 0), P);
             put<NS>(exchange_at<NS>(ex, p.w, 1), e);
-            if (!kRoots) *sum_at<NS>(ex, W, p.w) = sum;
             __syncthreads();
-            const auto over = [](float v, float x, float y) {
-                return kRoots ? carried(v, x, y) : __builtin_fmaf(v, x, y);
-            };
             get<NS>(exchange_at<NS>(ex, W, 0), c);
             // Two segments at a time: one by one the reads' latency adds up.
             int m = W - 1;
@@ -982,16 +976,14 @@ __global__ __launch_bounds__(SPLIT ? 64 * waves_for(NS) : 64) void scan_bwd(cons
                 get<NS>(exchange_at<NS>(ex, m - 1, 1), e1);
 #pragma unroll
                 for (int j = 0; j < NS; ++j)
-                    c[j] = over(P1[j], over(P[j], c[j], e[j]), e1[j]);
+                    c[j] = carried(P1[j], carried(P[j], c[j], e[j]), e1[j]);
             }
             if (m > p.w) {
                 get<NS>(exchange_at<NS>(ex, m, 0), P);
                 get<NS>(exchange_at<NS>(ex, m, 1), e);
 #pragma unroll
-                for (int j = 0; j < NS; ++j) c[j] = over(P[j], c[j], e[j]);
+                for (int j = 0; j < NS; ++j) c[j] = carried(P[j], c[j], e[j]);
             }
-            if (!kRoots && __builtin_expect(grow, 0))
-                carry_grown<NS>(ex, W, W - 1, W - 1 - p.w, -1, A2, c);
         }
         float dAc[NS];
 #pragma unroll
@@ -1126,7 +1118,6 @@ __global__ __launch_bounds__(64 * waves_for(NS)) void scan_bwd_parts(const ScanA
     float* const ex = (float*)((Tile<NS, TT>*)lds + W);
     float A2[NS], c[NS], sum = 0.0f;
     load_A2<NS, false>(a, p, A2);
-    const bool grow = may_grow<NS>(a, A2);
 #pragma unroll
     for (int j = 0; j < NS; ++j) c[j] = 0.0f;
     const float bias = a.dt_bias ? a.dt_bias[p.ch] : 0.0f;
@@ -1169,14 +1160,13 @@ __global__ __launch_bounds__(64 * waves_for(NS)) void scan_bwd_parts(const ScanA
     }
     float P[NS];
 #pragma unroll
-    for (int j = 0; j < NS; ++j)
-        P[j] = grow ? root_decay(sum * A2[j]) : __builtin_amdgcn_exp2f(sum * A2[j]);
+    for (int j = 0; j < NS; ++j) P[j] = root_decay(sum * A2[j]);
     put<NS>(exchange_at<NS>(ex, p.w, 0), P);
     put<NS>(exchange_at<NS>(ex, p.w, 1), c);
     *sum_at<NS>(ex, W, p.w) = sum;
     __syncthreads();
     if (p.w != W - 1) return;
-    join_runs<NS>(ex, W, W - 2, W - 1, -1, A2, grow, sum, P, c);
+    join_runs<NS>(ex, W, W - 2, W - 1, -1, A2, true, sum, P, c);
     if (!p.in) return;
     put<NS>(part_at<NS>(a, p, p.part(a.PL), 0), P);
     put<NS>(part_at<NS>(a, p, p.part(a.PL), 1), c);
@@ -1308,7 +1298,11 @@ Plan plan_of(const tg_scan_args& a, bool forward) {
     // Fewer than four waves for each compute unit: parts of the sequences, so
     // many that there are sixteen, and not shorter than two rounds of a workgroup.
     // The parts' own pass costs two thirds of the scan and a launch: 9 packed
-    // sequences with 1728 waves take 24 to 33 us whole and 33 to 37 in parts.
+    // sequences with 1728 waves take 24 to 33 us whole and 33 to 37 in parts. The rule
+    // counts sequences, not their tokens, and does badly by one that is long: 16384
+    // tokens take 396 us with 1920 channels, in parts, and 465 with 2048, whole (4 x
+    // 4096: 194); 12000 packed with 15 of 10 each, 4096 channels, by single waves, 2026 us
+    // (16 of 759: 261).
     if (p.waves > 1 && groups * p.waves < 1024) {
         const int64_t round = (int64_t)p.waves * p.tt;
         int64_t pl = a.seqs.rows * p.nb * p.waves / 4096 / round * round;
