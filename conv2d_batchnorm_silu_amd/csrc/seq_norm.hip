@@ -8,8 +8,8 @@
 // strides and the pointers allows. The statistics are two sums over the
 // held values, the mean first and then the squared distances from it: the
 // one-pass form (sum of squares minus square of the sum) cancels when the
-// mean is large against the spread. Sums are fp32, over at most 64 values in a
-// thread and a tree over the threads.
+// mean is large against the spread. Sums are fp32, over at most 16 values in a
+// thread (C / 1024 where a row is too long to be held) and a tree over the threads.
 //
 // A workgroup walks over rows with gamma and beta in registers: reading them
 // for every row would be four bytes each next to two of x. Rows too long for

@@ -142,8 +142,8 @@ tg_status tg_causal_conv_step(const void *x, int64_t x_stride, void *state, int6
  *   v[t]   = sum_n C[t,g,n] * h[t,n] + D[c] * x[t,c]
  *   y[t,c] = v[t] * silu(z[t,c])      (v[t] where z is not given)
  * A step d of 0 keeps the state for any A, -inf included. Decays exp(d*A) above 1
- * are taken as they are; a channel's state that is infinite or NaN makes its y
- * infinite or NaN from there on.
+ * are taken as they are, those below 2^-126 as 0; a channel's state that is infinite
+ * or NaN makes its y infinite or NaN from there on.
  * B and C are shared by the D/G channels of a group g = c / (D/G); a row of
  * B or C is [G][N], contiguous. A fp32 [D][N]; D_skip, dt_bias fp32 [D] or
  * NULL; initial, final fp32 [seqs][D][N] or NULL. TG_ERR_UNSUPPORTED for row
