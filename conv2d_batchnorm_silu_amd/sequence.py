@@ -252,15 +252,27 @@ def _is(a, b):
             and all(n == 1 or x == y for n, x, y in zip(a.shape, a.stride(), b.stride())))
 
 
-def _new_or(out, like, dev, dense, may, apart):
-    """A new tensor like ``like``, dense, or ``out`` if it fits: it may be one of
-    ``may`` and shares memory with none of ``apart`` ({name: argument})."""
-    if out is None:
-        return torch.empty_like(like, memory_format=_DENSE)
+def _new(like):
+    return torch.empty_like(like, memory_format=_DENSE)
+
+
+def _given(out, like, dev, dense, may, apart):
+    """``out`` if it fits ``like``: it may be one of ``may`` and shares memory with
+    none of ``apart`` ({name: argument})."""
     _refuse(out, "out", dev, like.shape, like.dtype, dense)
-    for name, t in {**may, **apart}.items():
-        if t is not None and not (name in may and _is(out, t)) and _overlap(out, t):
-            raise ValueError("out shares memory with %s" % name)
+    held = out.untyped_storage()
+    lo = held.data_ptr()
+    hi = lo + held.nbytes()
+    for names in (may, apart):
+        for name, t in names.items():
+            if t is None:
+                continue
+            held = t.untyped_storage()
+            p = held.data_ptr()
+            # Strides are looked at only within one allocation.
+            if (p < hi and lo < p + held.nbytes() and not (name in may and _is(out, t))
+                    and _overlap(out, t)):
+                raise ValueError("out shares memory with %s" % name)
     return out
 
 
@@ -302,9 +314,9 @@ def _norm_forward(x, gamma, beta, eps, residual, train, out, dev):
     gp = _flat(_some(gamma, "gamma"), "gamma", dev, (C,))
     bp = _flat(beta, "beta", dev, (C,))
     # Training hands x back as s where there is no residual.
-    own = dict(x=x, residual=residual)
-    y = _new_or(out, x, dev, True, {} if train and residual is None else own,
-                dict(own, gamma=gamma, beta=beta))
+    y = _new(x) if out is None else _given(
+        out, x, dev, True, {} if train and residual is None else dict(x=x, residual=residual),
+        dict(x=x, residual=residual, gamma=gamma, beta=beta))
     total, tp, mean, rstd, mp, qp = None, 0, None, None, 0, 0
     if residual is not None:
         total = torch.empty_like(x, memory_format=_DENSE)
@@ -368,8 +380,8 @@ def layer_norm_backward(dy, s, gamma, mean, rstd, dsum=None, out=None, stream=No
     need = sz()
     _check(lib.tg_layer_norm_backward_workspace(rows, C, dt, ctypes.byref(need)),
            "tg_layer_norm_backward_workspace")
-    dx = _new_or(out, s, dev, True, dict(dy=dy, s=s, dsum=dsum),
-                 dict(gamma=gamma, mean=mean, rstd=rstd))
+    dx = _new(s) if out is None else _given(out, s, dev, True, dict(dy=dy, s=s, dsum=dsum),
+                                            dict(gamma=gamma, mean=mean, rstd=rstd))
     dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
     ws = torch.empty(need.value, dtype=torch.uint8, device=s.device)
     _check(lib.tg_layer_norm_backward(
@@ -425,8 +437,9 @@ def causal_conv(x, w, bias=None, act="silu", initial_state=None, offsets=None, r
         with there:
             return causal_conv(x, w, bias, act, initial_state, offsets, return_state, out)
     args, packed, held, D = _conv_args(x, w, bias, act, initial_state, offsets, dev)
-    y = _new_or(out, x, dev, False, {}, dict(x=x, w=w, bias=bias, initial_state=initial_state,
-                                             offsets=offsets))
+    y = _new(x) if out is None else _given(
+        out, x, dev, False, {}, dict(x=x, w=w, bias=bias, initial_state=initial_state,
+                                     offsets=offsets))
     state, final = None, 0
     if return_state:
         state = torch.empty(held, dtype=x.dtype, device=x.device)
@@ -487,7 +500,8 @@ def causal_conv_step(x, state, w, bias=None, act="silu", slots=None, out=None, s
     hp = _flat(state, "state", dev, (num, K - 1, D), dtype)
     sp = _flat(slots, "slots", dev, (n,), _I32)
     wp, bp = _flat(w, "w", dev, (K, D)), _flat(bias, "bias", dev, (D,))
-    y = _new_or(out, x, dev, True, dict(x=x), dict(state=state, slots=slots, w=w, bias=bias))
+    y = _new(x) if out is None else _given(out, x, dev, True, dict(x=x),
+                                           dict(state=state, slots=slots, w=w, bias=bias))
     st = _lib().tg_causal_conv_step(xp, xs, hp, num, sp, wp, bp, n, D, K, dt, _activation(act),
                                     y.data_ptr(), _raw_stream(dev))
     if st:
@@ -533,10 +547,10 @@ def _scan_forward(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, offset
     args, width, N, _ = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, seqs,
                                    packed, dev)
     # A token's x, dt and z are read by the thread that writes its y.
-    own = dict(x=x, dt=dt, z=z)
-    y = _new_or(out, x, dev, False, {} if train else own,
-                dict(own, A=A, B=B, C=C, D=D, dt_bias=dt_bias, initial_state=initial_state,
-                     offsets=offsets))
+    y = _new(x) if out is None else _given(
+        out, x, dev, False, {} if train else dict(x=x, dt=dt, z=z),
+        dict(x=x, dt=dt, z=z, A=A, B=B, C=C, D=D, dt_bias=dt_bias, initial_state=initial_state,
+             offsets=offsets))
     state, final = None, 0
     if want_state:
         state = torch.empty((seqs[0], width, N), dtype=_F32, device=x.device)
@@ -673,8 +687,9 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, sof
     num = state.shape[0]
     hp = _flat(state, "state", dev, (num, width, N))
     sp = _flat(slots, "slots", dev, (n,), _I32)
-    y = _new_or(out, x, dev, False, dict(x=x, dt=dt, z=z),
-                dict(A=A, B=B, C=C, D=D, dt_bias=dt_bias, state=state, slots=slots))
+    y = _new(x) if out is None else _given(
+        out, x, dev, False, dict(x=x, dt=dt, z=z),
+        dict(A=A, B=B, C=C, D=D, dt_bias=dt_bias, state=state, slots=slots))
     st = _lib().tg_selective_scan_step(args(_place(y, y.stride(), True, width), 0), hp, num, sp,
                                        _raw_stream(dev))
     if st:
