@@ -20,6 +20,8 @@ _SEQUENCE_NAMES = {
     "layer_norm", "layer_norm_train", "layer_norm_backward", "causal_conv",
     "causal_conv_backward", "causal_conv_step", "selective_scan", "selective_scan_train",
     "selective_scan_backward", "selective_scan_step", "ScanGradients",
+    "gated_delta_rule", "gated_delta_rule_train", "gated_delta_rule_backward",
+    "gated_delta_rule_step", "DeltaGradients",
 }
 
 

@@ -101,6 +101,35 @@ tg_status check_scan_inputs(const tg_scan_args* a) {
     return TG_OK;
 }
 
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;  // of 256 threads
+
+tg_status check_delta(const tg_delta_args* a) {
+    TG_REQUIRE(a, TG_ERR_INVALID_ARGUMENT);
+    TG_CHECK(check_seqs(a->seqs));
+    TG_REQUIRE(a->HK >= 1 && a->HV >= 1 && a->HV % a->HK == 0 && a->K >= 1 && a->V >= 1,
+               TG_ERR_INVALID_ARGUMENT);
+    TG_REQUIRE(dtype_ok((int)a->dtype) && a->K <= 256 && (int64_t)a->HV * a->V <= kMaxChannels &&
+                   (int64_t)a->HK * a->K <= kMaxChannels, TG_ERR_UNSUPPORTED);
+    return TG_OK;
+}
+tg_status check_delta_groups(const tg_delta_args* a) {
+    TG_REQUIRE(delta_groups(*a) <= kMaxBlocks, TG_ERR_UNSUPPORTED);
+    return TG_OK;
+}
+tg_status check_delta_inputs(const tg_delta_args* a) {
+    const size_t e = elem_bytes(a->dtype);
+    const int64_t kw = (int64_t)a->HK * a->K, vw = (int64_t)a->HV * a->V;
+    TG_REQUIRE(a->A, TG_ERR_INVALID_ARGUMENT);
+    TG_REQUIRE(aligned(a->A, 4) && aligned(a->dt_bias, 4) && aligned(a->initial, 4) &&
+                   aligned(a->final, 4), TG_ERR_ALIGNMENT);
+    TG_CHECK(check_rows(a->q, a->seqs, kw, e, false));
+    TG_CHECK(check_rows(a->k, a->seqs, kw, e, false));
+    TG_CHECK(check_rows(a->v, a->seqs, vw, e, false));
+    TG_CHECK(check_rows(a->dt, a->seqs, a->HV, e, false));
+    TG_CHECK(check_rows(a->beta, a->seqs, a->HV, e, false));
+    return TG_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -269,6 +298,72 @@ tg_status tg_selective_scan_step(const tg_scan_args* a, float* state, int64_t nu
     TG_REQUIRE(num_slots < kMaxRows, TG_ERR_UNSUPPORTED);
     TG_REQUIRE(aligned(state, 4) && aligned(slots, 4), TG_ERR_ALIGNMENT);
     return of(launch_scan_step(b, state, num_slots, slots, (hipStream_t)stream));
+}
+
+tg_status tg_gated_delta_rule_sizes(const tg_delta_args* a, size_t* workspace_bytes,
+                                    size_t* saved_bytes, size_t* backward_bytes) {
+    TG_CHECK(check_delta(a));
+    TG_CHECK(check_delta_groups(a));
+    delta_sizes(*a, workspace_bytes, saved_bytes, backward_bytes);
+    return TG_OK;
+}
+
+tg_status tg_gated_delta_rule(const tg_delta_args* a, void* workspace, size_t workspace_bytes,
+                              void* saved, size_t saved_bytes, void* stream) {
+    TG_CHECK(check_delta(a));
+    TG_CHECK(check_delta_groups(a));
+    TG_CHECK(check_delta_inputs(a));
+    TG_CHECK(check_rows(a->y, a->seqs, (int64_t)a->HV * a->V, elem_bytes(a->dtype), true));
+    size_t work = 0, keep = 0;
+    delta_sizes(*a, &work, &keep, nullptr);
+    TG_REQUIRE(aligned(workspace, 16) && aligned(saved, 16), TG_ERR_ALIGNMENT);
+    TG_REQUIRE(work == 0 || (workspace && workspace_bytes >= work), TG_ERR_WORKSPACE);
+    TG_REQUIRE(!saved || saved_bytes >= keep, TG_ERR_WORKSPACE);
+    return of(launch_delta(*a, workspace, saved, (hipStream_t)stream));
+}
+
+tg_status tg_gated_delta_rule_backward(const tg_delta_args* a, const tg_delta_grads* g,
+                                       const void* saved, size_t saved_bytes, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    TG_CHECK(check_delta(a));
+    TG_CHECK(check_delta_groups(a));
+    TG_CHECK(check_delta_inputs(a));
+    TG_REQUIRE(g && g->dA, TG_ERR_INVALID_ARGUMENT);
+    const size_t e = elem_bytes(a->dtype);
+    const int64_t kw = (int64_t)a->HK * a->K, vw = (int64_t)a->HV * a->V;
+    TG_CHECK(check_rows(g->dy, a->seqs, vw, e, false));
+    TG_CHECK(check_rows(g->dq, a->seqs, kw, e, true));
+    TG_CHECK(check_rows(g->dk, a->seqs, kw, e, true));
+    TG_CHECK(check_rows(g->dv, a->seqs, vw, e, true));
+    TG_CHECK(check_rows(g->ddt, a->seqs, a->HV, e, true));
+    TG_CHECK(check_rows(g->dbeta, a->seqs, a->HV, e, true));
+    TG_REQUIRE(aligned(g->dA, 4) && aligned(g->ddt_bias, 4) && aligned(g->dfinal, 4) &&
+                   aligned(g->dinitial, 4) && aligned(saved, 16) && aligned(workspace, 16),
+               TG_ERR_ALIGNMENT);
+    size_t keep = 0, need = 0;
+    delta_sizes(*a, nullptr, &keep, &need);
+    TG_REQUIRE((keep == 0 || (saved && saved_bytes >= keep)) &&
+                   (need == 0 || (workspace && workspace_bytes >= need)), TG_ERR_WORKSPACE);
+    return of(launch_delta_backward(*a, *g, saved, workspace, (hipStream_t)stream));
+}
+
+tg_status tg_gated_delta_rule_step(const tg_delta_args* a, float* state, int64_t num_slots,
+                                   const int32_t* slots, void* stream) {
+    TG_REQUIRE(a && a->seqs.seqs >= 0 && num_slots >= 0, TG_ERR_INVALID_ARGUMENT);
+    if (a->seqs.seqs == 0) return TG_OK;
+    TG_REQUIRE(a->seqs.rows == a->seqs.seqs && !a->seqs.offsets, TG_ERR_INVALID_ARGUMENT);
+    TG_CHECK(check_delta(a));
+    // Slices of 32 columns at the least.
+    TG_REQUIRE(a->seqs.seqs * a->HV * ceil_div(a->V, 32) <= kMaxBlocks, TG_ERR_UNSUPPORTED);
+    tg_delta_args b = *a;
+    for (tg_rows* r : {&b.q, &b.k, &b.v, &b.dt, &b.beta, &b.y}) r->seq_stride = r->row_stride;
+    TG_CHECK(check_delta_inputs(&b));
+    TG_CHECK(check_rows(b.y, b.seqs, (int64_t)b.HV * b.V, elem_bytes(b.dtype), true));
+    TG_REQUIRE((slots || a->seqs.seqs <= num_slots) && (state || num_slots == 0),
+               TG_ERR_INVALID_ARGUMENT);
+    TG_REQUIRE(num_slots < kMaxRows, TG_ERR_UNSUPPORTED);
+    TG_REQUIRE(aligned(state, 4) && aligned(slots, 4), TG_ERR_ALIGNMENT);
+    return of(launch_delta_step(b, state, num_slots, slots, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -57,6 +57,14 @@ hipError_t launch_scan_backward(const tg_scan_args& a, const tg_scan_grads& g, c
 hipError_t launch_scan_step(const tg_scan_args& a, float* state, int64_t num_slots,
                             const int32_t* slots, hipStream_t st);
 
+void delta_sizes(const tg_delta_args& a, size_t* work, size_t* saved, size_t* backward);
+int64_t delta_groups(const tg_delta_args& a);  // workgroups of its largest launch
+hipError_t launch_delta(const tg_delta_args& a, void* ws, void* saved, hipStream_t st);
+hipError_t launch_delta_backward(const tg_delta_args& a, const tg_delta_grads& g,
+                                 const void* saved, void* ws, hipStream_t st);
+hipError_t launch_delta_step(const tg_delta_args& a, float* state, int64_t num_slots,
+                             const int32_t* slots, hipStream_t st);
+
 // out[m] = sum over p < P of part[p*M + m], in a fixed order (seq_norm.hip).
 // Columns from `split` on go to out2; either may be NULL (dropped).
 hipError_t launch_column_sums(const float* part, int P, int64_t M, float* out, int64_t split,

@@ -63,14 +63,30 @@ class _ScanGrads(ctypes.Structure):
                 ("dinitial", vp)]
 
 
+class _DeltaArgs(ctypes.Structure):
+    _fields_ = [("seqs", _Seqs), ("HK", i32), ("HV", i32), ("K", i32), ("V", i32), ("dtype", i32),
+                ("softplus", i32), ("sigmoid", i32), ("normalize", i32), ("scale", ctypes.c_float),
+                ("q", _Rows), ("k", _Rows), ("v", _Rows), ("dt", _Rows), ("beta", _Rows),
+                ("y", _Rows), ("A", vp), ("dt_bias", vp), ("initial", vp), ("final", vp)]
+
+
+class _DeltaGrads(ctypes.Structure):
+    _fields_ = [("dy", _Rows), ("dfinal", vp), ("dq", _Rows), ("dk", _Rows), ("dv", _Rows),
+                ("ddt", _Rows), ("dbeta", _Rows), ("dA", vp), ("ddt_bias", vp), ("dinitial", vp)]
+
+
 # The same layouts as flat numbers: filling a ctypes structure field by field
 # takes several microseconds, which a single token's call would mostly consist of.
 _CONV = struct.Struct("3q4i10q")
 _SCAN = struct.Struct("3q5i4x23q")
+_DELTA = struct.Struct("3q8if4x22q")
 assert _CONV.size == ctypes.sizeof(_ConvArgs) and _SCAN.size == ctypes.sizeof(_ScanArgs)
+assert _DELTA.size == ctypes.sizeof(_DeltaArgs)
 
 ScanGradients = collections.namedtuple(
     "ScanGradients", "dx ddt dA dB dC dD dz ddt_bias dinitial_state")
+DeltaGradients = collections.namedtuple(
+    "DeltaGradients", "dq dk dv ddt dA dbeta ddt_bias dinitial_state")
 
 _loaded = None
 
@@ -96,6 +112,11 @@ def _lib():
     lib.tg_selective_scan.argtypes = [scan, vp, sz, vp, sz, vp]
     lib.tg_selective_scan_backward.argtypes = [scan, grads, vp, sz, vp, sz, vp]
     lib.tg_selective_scan_step.argtypes = [scan, vp, i64, vp, vp]
+    delta = vp
+    lib.tg_gated_delta_rule_sizes.argtypes = [delta, psz, psz, psz]
+    lib.tg_gated_delta_rule.argtypes = [delta, vp, sz, vp, sz, vp]
+    lib.tg_gated_delta_rule_backward.argtypes = [delta, ctypes.POINTER(_DeltaGrads), vp, sz, vp, sz, vp]
+    lib.tg_gated_delta_rule_step.argtypes = [delta, vp, i64, vp, vp]
     _loaded = lib
     return lib
 
@@ -694,4 +715,221 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, sof
                                        _raw_stream(dev))
     if st:
         _check(st, "tg_selective_scan_step")
+    return y
+
+
+# -------------------------------------------------------- gated delta rule
+
+def _heads(t, name, lead):
+    """(heads, width) of a tensor of rows of heads, one head after another."""
+    if t.dim() != len(lead) + 2 or t.shape[:-2] != lead:
+        raise ValueError("%s must be %s + [heads, width], got %s"
+                         % (name, tuple(lead), tuple(t.shape)))
+    H, W = t.shape[-2:]
+    if H < 1 or W < 1:
+        raise ValueError("%s must hold a head of one column at the least, got %s"
+                         % (name, tuple(t.shape)))
+    if H > 1 and t.stride(-2) != W:
+        raise ValueError("%s: the heads of a row must lie one after another" % name)
+    return H, W
+
+
+def _delta_batch(v, offsets, dev):
+    """As _batch, for rows of heads."""
+    if v.dim() != (4 if offsets is None else 3):
+        raise ValueError("v must be [S, L, heads, V], or [T, heads, V] with offsets; got %s"
+                         % (tuple(v.shape),))
+    return _batch(v.select(-2, 0) if v.shape[-2] else v.flatten(-2), offsets, dev)
+
+
+def _delta_args(q, k, v, dt, A, beta, dt_bias, softplus, sigmoid, normalize, scale, initial_state,
+                seqs, packed, dev):
+    """A function of (y's rows, address of the final states) that gives the
+    call's arguments; value heads, V; the states' shape."""
+    d, dtype, lead = _dtype(v, "v"), v.dtype, v.shape[:-2]
+    HV, V = _heads(v, "v", lead)
+    HK, K = _heads(_some(k, "k"), "k", lead)
+    if HV % HK:
+        raise ValueError("the %d heads of k must divide the %d of v" % (HK, HV))
+    held = (seqs[0], HV, K, V)
+    if q is not None and q.dim() == len(lead) + 2:
+        _heads(q, "q", lead)
+    gates = lead + (HV,)
+    if scale is None:
+        scale = K ** -0.5
+    head = (*seqs, HK, HV, K, V, d, 1 if softplus else 0, 1 if sigmoid else 0,
+            1 if normalize else 0, scale,
+            *_rows(_some(q, "q"), "q", dev, k.shape, dtype, packed, HK * K),
+            *_rows(k, "k", dev, k.shape, dtype, packed, HK * K),
+            *_rows(v, "v", dev, v.shape, dtype, packed, HV * V),
+            *_rows(_some(dt, "dt"), "dt", dev, gates, dtype, packed, HV),
+            *_rows(_some(beta, "beta"), "beta", dev, gates, dtype, packed, HV))
+    tail = (_flat(_some(A, "A"), "A", dev, (HV,)), _flat(dt_bias, "dt_bias", dev, (HV,)),
+            _flat(initial_state, "initial_state", dev, held))
+    return (lambda y, final: _DELTA.pack(*head, *y, *tail, final)), HV, V, held
+
+
+def _delta_forward(q, k, v, dt, A, beta, dt_bias, softplus, sigmoid, normalize, scale,
+                   initial_state, offsets, want_state, train, out, dev):
+    packed, seqs = offsets is not None, _delta_batch(v, offsets, dev)
+    args, HV, V, held = _delta_args(q, k, v, dt, A, beta, dt_bias, softplus, sigmoid, normalize,
+                                    scale, initial_state, seqs, packed, dev)
+    # A workgroup reads its columns of v for 64 tokens before it writes their y.
+    y = _new(v) if out is None else _given(
+        out, v, dev, False, {} if train else dict(v=v),
+        dict(q=q, k=k, v=v, dt=dt, A=A, beta=beta, dt_bias=dt_bias, initial_state=initial_state,
+             offsets=offsets))
+    if out is not None:
+        _heads(y, "out", v.shape[:-2])
+    state, final = None, 0
+    if want_state:
+        state = torch.empty(held, dtype=_F32, device=v.device)
+        final = state.data_ptr()
+    a = args(_place(y, y.stride(), packed, HV * V), final)
+    lib = _lib()
+    work, keep = sz(), sz()
+    _check(lib.tg_gated_delta_rule_sizes(a, ctypes.byref(work), ctypes.byref(keep), None),
+           "tg_gated_delta_rule_sizes")
+    saved, kp = None, 0
+    if train:
+        saved = torch.empty(keep.value // 4, dtype=_F32, device=v.device)
+        kp = saved.data_ptr()
+    ws = torch.empty(work.value, dtype=torch.uint8, device=v.device)
+    _check(lib.tg_gated_delta_rule(a, ws.data_ptr(), work.value, kp, keep.value if train else 0,
+                                   _raw_stream(dev)), "tg_gated_delta_rule")
+    return y, state, saved
+
+
+def gated_delta_rule(q, k, v, dt, A, beta, dt_bias=None, softplus=True, sigmoid=True,
+                     normalize=True, scale=None, initial_state=None, offsets=None,
+                     return_state=False, out=None, stream=None):
+    """The gated delta rule over each sequence's tokens, a K x V matrix S for
+    each value head:
+
+        d = softplus(dt + dt_bias)            (d = dt + dt_bias if not softplus)
+        b = sigmoid(beta)                     (b = beta if not sigmoid)
+        q, k = q / sqrt(sum q^2 + 1e-6), k / sqrt(sum k^2 + 1e-6)  (if normalize)
+        S = exp(d * A) * S
+        S = S + b * k (v - k S)
+        y = scale * q S                       (scale: default K ** -0.5)
+
+    q, k: [S, L, key heads, K] or packed [T, key heads, K], K <= 256; v [...,
+    value heads, V], each key head shared by value heads / key heads neighbouring
+    ones; dt, beta [..., value heads]; A, dt_bias [value heads]. The heads of a
+    row lie one after another. ``initial_state`` fp32 [S, value heads, K, V]
+    (default zeros). Returns y, or with ``return_state`` (y, state). ``out`` may
+    be v.
+
+    With 16-bit tensors the states, which are fp32, are computed to 17 bits. Decays
+    above 1 (A > 0) are taken as they are while the product over any 64 tokens in a
+    row stays within fp32."""
+    dev = _device(v, "v")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return gated_delta_rule(q, k, v, dt, A, beta, dt_bias, softplus, sigmoid, normalize,
+                                    scale, initial_state, offsets, return_state, out)
+    y, state, _ = _delta_forward(q, k, v, dt, A, beta, dt_bias, softplus, sigmoid, normalize, scale,
+                                 initial_state, offsets, return_state, False, out, dev)
+    return (y, state) if return_state else y
+
+
+def gated_delta_rule_train(q, k, v, dt, A, beta, dt_bias=None, softplus=True, sigmoid=True,
+                           normalize=True, scale=None, initial_state=None, offsets=None,
+                           return_state=False, out=None, stream=None):
+    """gated_delta_rule for training: (y, saved) or (y, state, saved); ``saved``
+    holds the states and corrections that gated_delta_rule_backward starts from."""
+    dev = _device(v, "v")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return gated_delta_rule_train(q, k, v, dt, A, beta, dt_bias, softplus, sigmoid,
+                                          normalize, scale, initial_state, offsets, return_state,
+                                          out)
+    y, state, saved = _delta_forward(q, k, v, dt, A, beta, dt_bias, softplus, sigmoid, normalize,
+                                     scale, initial_state, offsets, return_state, True, out, dev)
+    return (y, state, saved) if return_state else (y, saved)
+
+
+def gated_delta_rule_backward(dy, q, k, v, dt, A, beta, saved, dt_bias=None, softplus=True,
+                              sigmoid=True, normalize=True, scale=None, initial_state=None,
+                              offsets=None, dstate=None, stream=None):
+    """DeltaGradients (dq, dk, dv, ddt, dA, dbeta, ddt_bias, dinitial_state) of
+    gated_delta_rule_train's y with the same arguments and its ``saved``; entries
+    are None for arguments that were not given. ``dstate`` fp32 [S, value heads,
+    K, V]: the gradient of the returned state."""
+    dev = _device(v, "v")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return gated_delta_rule_backward(dy, q, k, v, dt, A, beta, saved, dt_bias, softplus,
+                                             sigmoid, normalize, scale, initial_state, offsets,
+                                             dstate)
+    packed, seqs = offsets is not None, _delta_batch(v, offsets, dev)
+    args, HV, V, held = _delta_args(q, k, v, dt, A, beta, dt_bias, softplus, sigmoid, normalize,
+                                    scale, initial_state, seqs, packed, dev)
+    a = args(_NO_ROWS, 0)
+    if _some(dy, "dy").shape == v.shape:
+        _heads(dy, "dy", v.shape[:-2])
+    g = _DeltaGrads(_rows(dy, "dy", dev, v.shape, v.dtype, packed, HV * V),
+                    _flat(dstate, "dstate", dev, held))
+    lib = _lib()
+    keep, need = sz(), sz()
+    _check(lib.tg_gated_delta_rule_sizes(a, None, ctypes.byref(keep), ctypes.byref(need)),
+           "tg_gated_delta_rule_sizes")
+    sp = _flat(_some(saved, "saved"), "saved", dev, (keep.value // 4,))
+
+    def rows_like(t):
+        o = torch.empty_like(t, memory_format=_DENSE)
+        return o, _place(o, o.stride(), packed, o.shape[-1] * (o.shape[-2] if t.dim() == v.dim() else 1))
+
+    dq, g.dq = rows_like(q)
+    dk, g.dk = rows_like(k)
+    dv, g.dv = rows_like(v)
+    ddt, g.ddt = rows_like(dt)
+    dbeta, g.dbeta = rows_like(beta)
+    dA = torch.empty_like(A)
+    g.dA = dA.data_ptr()
+    db = d0 = None
+    if dt_bias is not None:
+        db = torch.empty_like(dt_bias)
+        g.ddt_bias = db.data_ptr()
+    if initial_state is not None:
+        d0 = torch.empty_like(initial_state)
+        g.dinitial = d0.data_ptr()
+    ws = torch.empty(need.value, dtype=torch.uint8, device=v.device)
+    _check(lib.tg_gated_delta_rule_backward(a, ctypes.byref(g), sp, keep.value, ws.data_ptr(),
+                                            need.value, _raw_stream(dev)),
+           "tg_gated_delta_rule_backward")
+    return DeltaGradients(dq, dk, dv, ddt, dA, dbeta, db, d0)
+
+
+def gated_delta_rule_step(q, k, v, dt, A, beta, state, dt_bias=None, softplus=True, sigmoid=True,
+                          normalize=True, scale=None, slots=None, out=None, stream=None):
+    """One token of each of n sequences: q, k [n, key heads, K], v [n, value
+    heads, V], dt, beta [n, value heads] -> y like v; ``state`` fp32 [num_slots,
+    value heads, K, V] is updated in place. ``slots`` as in causal_conv_step."""
+    dev = _device(v, "v")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return gated_delta_rule_step(q, k, v, dt, A, beta, state, dt_bias, softplus, sigmoid,
+                                         normalize, scale, slots, out)
+    if v.dim() != 3:
+        raise ValueError("v must be [n, heads, V], got %s" % (tuple(v.shape),))
+    n = v.shape[0]
+    args, HV, V, held = _delta_args(q, k, v, dt, A, beta, dt_bias, softplus, sigmoid, normalize,
+                                    scale, None, (n, n, 0), True, dev)
+    num = _some(state, "state").shape[0]
+    hp = _flat(state, "state", dev, (num,) + held[1:])
+    sp = _flat(slots, "slots", dev, (n,), _I32)
+    y = _new(v) if out is None else _given(
+        out, v, dev, False, {}, dict(q=q, k=k, v=v, dt=dt, A=A, beta=beta, dt_bias=dt_bias,
+                                     state=state, slots=slots))
+    if out is not None:
+        _heads(y, "out", v.shape[:-2])
+    st = _lib().tg_gated_delta_rule_step(args(_place(y, y.stride(), True, HV * V), 0), hp, num, sp,
+                                         _raw_stream(dev))
+    if st:
+        _check(st, "tg_gated_delta_rule_step")
     return y

@@ -194,6 +194,67 @@ tg_status tg_selective_scan_backward(const tg_scan_args *a, const tg_scan_grads 
 tg_status tg_selective_scan_step(const tg_scan_args *a, float *state, int64_t num_slots,
                                  const int32_t *slots, void *stream);
 
+/* ---- Gated delta rule --------------------------------------------------
+ * For each sequence and value head h, with a K x V matrix S, the initial state
+ * (or zeros) before the first token, and hk = h / (HV/HK) its key head:
+ *   d  = dt[t,h] + dt_bias[h], through softplus if softplus;  b = beta[t,h],
+ *        through the logistic function if sigmoid
+ *   q, k = q[t,hk], k[t,hk], divided by sqrt(sum of squares + 1e-6) if normalize
+ *   S  = exp(d * A[h]) * S;   u = b * (v[t,h] - k S);   S = S + k u^T
+ *   y[t,h] = scale * q S
+ * q and k rows [HK][K], v and y rows [HV][V], dt and beta rows [HV], each
+ * contiguous; K 1 .. 256. A fp32 [HV]; dt_bias fp32 [HV] or NULL; initial, final
+ * fp32 [seqs][HV][K][V] or NULL.
+ * A step d of 0 keeps the state for any A, -inf included; decays below 2^-126 are
+ * taken as 0. Decays above 1 are taken as they are while their product over any 64
+ * tokens in a row is within fp32. With 16-bit tensors, states
+ * and what lies between enter the products with 17 bits (off by 2^-18), those that
+ * only reach bf16 results with 8; with fp32 tensors all keep 24. A NaN or infinite value of a token may reach all tokens from its
+ * sequence's 64 (counted from its first; 32 for fp16 and fp32 with K > 128) on.
+ * TG_ERR_UNSUPPORTED for K > 256 and for 2^24 or more pairs of a value head and 64
+ * (32) tokens, or of a sequence, a value head and 16 columns. */
+typedef struct {
+    tg_seqs seqs;
+    int HK, HV, K, V;
+    tg_dtype dtype;
+    int softplus, sigmoid, normalize;
+    float scale;
+    tg_rows q, k, v, dt, beta, y;
+    const float *A, *dt_bias;
+    const float *initial;
+    float *final;
+} tg_delta_args;
+
+/* As tg_selective_scan_sizes. */
+tg_status tg_gated_delta_rule_sizes(const tg_delta_args *a, size_t *workspace_bytes,
+                                    size_t *saved_bytes, size_t *backward_bytes);
+/* saved (fp32, may be NULL): filled for the backward pass with the state before
+ * each 64 (32) tokens and their corrections. y may be v itself (same address and
+ * strides), which a backward pass then lacks. */
+tg_status tg_gated_delta_rule(const tg_delta_args *a, void *workspace, size_t workspace_bytes,
+                              void *saved, size_t saved_bytes, void *stream);
+
+/* Gradients, all written: dq, dk, dv, ddt, dbeta as rows like q, k, v, dt, beta;
+ * dA, ddt_bias fp32 [HV] (ddt_bias may be NULL); dinitial fp32
+ * [seqs][HV][K][V] or NULL. dfinal (or NULL): the gradient of the final states.
+ * a: the forward call's arguments (y, final are not read; initial only enters
+ * through saved). */
+typedef struct {
+    tg_rows dy;
+    const float *dfinal;
+    tg_rows dq, dk, dv, ddt, dbeta;
+    float *dA, *ddt_bias, *dinitial;
+} tg_delta_grads;
+tg_status tg_gated_delta_rule_backward(const tg_delta_args *a, const tg_delta_grads *g,
+                                       const void *saved, size_t saved_bytes, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+/* One token for each of n sequences, rows by row stride as in
+ * tg_selective_scan_step; state fp32 [num_slots][HV][K][V], updated in place; slots as in
+ * tg_causal_conv_step. */
+tg_status tg_gated_delta_rule_step(const tg_delta_args *a, float *state, int64_t num_slots,
+                                   const int32_t *slots, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
