@@ -21,7 +21,8 @@ _SEQUENCE_NAMES = {
     "causal_conv_backward", "causal_conv_step", "selective_scan", "selective_scan_train",
     "selective_scan_backward", "selective_scan_step", "ScanGradients",
     "gated_delta_rule", "gated_delta_rule_train", "gated_delta_rule_backward",
-    "gated_delta_rule_step", "DeltaGradients",
+    "gated_delta_rule_step", "DeltaGradients", "group_norm", "group_norm_train",
+    "group_norm_backward", "GroupNormGradients",
 }
 
 

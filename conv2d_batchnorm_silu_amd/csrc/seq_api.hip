@@ -130,6 +130,30 @@ tg_status check_delta_inputs(const tg_delta_args* a) {
     return TG_OK;
 }
 
+bool row_stride_ok(int64_t st, int64_t C, int64_t rows) { return st == 0 || st >= C || rows == 1; }
+
+tg_status check_group_norm(const tg_group_norm_args* a) {
+    TG_REQUIRE(a && a->N >= 0 && a->L >= 1 && a->C >= 1 && a->G >= 1 && a->C % a->G == 0 &&
+                   a->eps >= 0.0f, TG_ERR_INVALID_ARGUMENT);
+    TG_REQUIRE(dtype_ok((int)a->dtype) && a->C <= kMaxChannels && a->G <= 4096 &&
+                   a->L < kMaxRows && a->N < kMaxRows && a->N * a->L < kMaxRows,
+               TG_ERR_UNSUPPORTED);
+    TG_REQUIRE((int)a->act == TG_ACT_SILU || (int)a->act == TG_ACT_NONE, TG_ERR_UNSUPPORTED);
+    TG_REQUIRE(group_norm_groups(*a) <= kMaxBlocks, TG_ERR_UNSUPPORTED);
+    return TG_OK;
+}
+tg_status check_group_norm_inputs(const tg_group_norm_args* a) {
+    const size_t e = elem_bytes(a->dtype);
+    const int64_t rows = a->N * a->L;
+    TG_REQUIRE(a->gamma && !a->mean == !a->rstd, TG_ERR_INVALID_ARGUMENT);
+    TG_REQUIRE(rows == 0 || (a->x && row_stride_ok(a->x_stride, a->C, rows) &&
+                             (!a->z || row_stride_ok(a->z_stride, a->C, rows))),
+               TG_ERR_INVALID_ARGUMENT);
+    TG_REQUIRE(aligned(a->x, e) && aligned(a->z, e) && aligned(a->gamma, 4) && aligned(a->beta, 4) &&
+                   aligned(a->mean, 4) && aligned(a->rstd, 4), TG_ERR_ALIGNMENT);
+    return TG_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -364,6 +388,44 @@ tg_status tg_gated_delta_rule_step(const tg_delta_args* a, float* state, int64_t
     TG_REQUIRE(num_slots < kMaxRows, TG_ERR_UNSUPPORTED);
     TG_REQUIRE(aligned(state, 4) && aligned(slots, 4), TG_ERR_ALIGNMENT);
     return of(launch_delta_step(b, state, num_slots, slots, (hipStream_t)stream));
+}
+
+tg_status tg_group_norm_sizes(const tg_group_norm_args* a, size_t* workspace_bytes,
+                              size_t* backward_bytes) {
+    TG_CHECK(check_group_norm(a));
+    group_norm_sizes(*a, workspace_bytes, backward_bytes);
+    return TG_OK;
+}
+
+tg_status tg_group_norm(const tg_group_norm_args* a, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+    TG_CHECK(check_group_norm(a));
+    TG_CHECK(check_group_norm_inputs(a));
+    if (a->N == 0) return TG_OK;
+    TG_REQUIRE(a->y, TG_ERR_INVALID_ARGUMENT);
+    TG_REQUIRE(aligned(a->y, elem_bytes(a->dtype)) && aligned(workspace, 16), TG_ERR_ALIGNMENT);
+    size_t work = 0;
+    group_norm_sizes(*a, &work, nullptr);
+    TG_REQUIRE(work == 0 || (workspace && workspace_bytes >= work), TG_ERR_WORKSPACE);
+    return of(launch_group_norm(*a, workspace, (hipStream_t)stream));
+}
+
+tg_status tg_group_norm_backward(const tg_group_norm_args* a, const tg_group_norm_grads* g,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+    TG_CHECK(check_group_norm(a));
+    TG_CHECK(check_group_norm_inputs(a));
+    TG_REQUIRE(g && g->dgamma && (!g->dz == !a->z), TG_ERR_INVALID_ARGUMENT);
+    const size_t e = elem_bytes(a->dtype);
+    if (a->N > 0) {
+        TG_REQUIRE(g->dy && g->dx && a->mean && row_stride_ok(g->dy_stride, a->C, a->N * a->L),
+                   TG_ERR_INVALID_ARGUMENT);
+        size_t need = 0;
+        group_norm_sizes(*a, nullptr, &need);
+        TG_REQUIRE(workspace && workspace_bytes >= need, TG_ERR_WORKSPACE);
+    }
+    TG_REQUIRE(aligned(g->dy, e) && aligned(g->dx, e) && aligned(g->dz, e) && aligned(g->dgamma, 4) &&
+                   aligned(g->dbeta, 4) && aligned(workspace, 16), TG_ERR_ALIGNMENT);
+    return of(launch_group_norm_backward(*a, *g, workspace, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -65,6 +65,12 @@ hipError_t launch_delta_backward(const tg_delta_args& a, const tg_delta_grads& g
 hipError_t launch_delta_step(const tg_delta_args& a, float* state, int64_t num_slots,
                              const int32_t* slots, hipStream_t st);
 
+void group_norm_sizes(const tg_group_norm_args& a, size_t* work, size_t* backward);
+int64_t group_norm_groups(const tg_group_norm_args& a);  // workgroups of its largest launch
+hipError_t launch_group_norm(const tg_group_norm_args& a, void* ws, hipStream_t st);
+hipError_t launch_group_norm_backward(const tg_group_norm_args& a, const tg_group_norm_grads& g,
+                                      void* ws, hipStream_t st);
+
 // out[m] = sum over p < P of part[p*M + m], in a fixed order (seq_norm.hip).
 // Columns from `split` on go to out2; either may be NULL (dropped).
 hipError_t launch_column_sums(const float* part, int P, int64_t M, float* out, int64_t split,

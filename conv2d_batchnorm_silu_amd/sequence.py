@@ -75,18 +75,31 @@ class _DeltaGrads(ctypes.Structure):
                 ("ddt", _Rows), ("dbeta", _Rows), ("dA", vp), ("ddt_bias", vp), ("dinitial", vp)]
 
 
+class _GroupNormArgs(ctypes.Structure):
+    _fields_ = [("N", i64), ("L", i64), ("C", i32), ("G", i32), ("dtype", i32), ("act", i32),
+                ("eps", ctypes.c_float), ("x", vp), ("x_stride", i64), ("z", vp), ("z_stride", i64),
+                ("gamma", vp), ("beta", vp), ("y", vp), ("mean", vp), ("rstd", vp)]
+
+
+class _GroupNormGrads(ctypes.Structure):
+    _fields_ = [("dy", vp), ("dy_stride", i64), ("dx", vp), ("dz", vp), ("dgamma", vp),
+                ("dbeta", vp)]
+
+
 # The same layouts as flat numbers: filling a ctypes structure field by field
 # takes several microseconds, which a single token's call would mostly consist of.
 _CONV = struct.Struct("3q4i10q")
 _SCAN = struct.Struct("3q5i4x23q")
 _DELTA = struct.Struct("3q8if4x22q")
+_GROUP = struct.Struct("2q4if4x9q")
 assert _CONV.size == ctypes.sizeof(_ConvArgs) and _SCAN.size == ctypes.sizeof(_ScanArgs)
-assert _DELTA.size == ctypes.sizeof(_DeltaArgs)
+assert _DELTA.size == ctypes.sizeof(_DeltaArgs) and _GROUP.size == ctypes.sizeof(_GroupNormArgs)
 
 ScanGradients = collections.namedtuple(
     "ScanGradients", "dx ddt dA dB dC dD dz ddt_bias dinitial_state")
 DeltaGradients = collections.namedtuple(
     "DeltaGradients", "dq dk dv ddt dA dbeta ddt_bias dinitial_state")
+GroupNormGradients = collections.namedtuple("GroupNormGradients", "dx dgamma dbeta dz")
 
 _loaded = None
 
@@ -112,7 +125,10 @@ def _lib():
     lib.tg_selective_scan.argtypes = [scan, vp, sz, vp, sz, vp]
     lib.tg_selective_scan_backward.argtypes = [scan, grads, vp, sz, vp, sz, vp]
     lib.tg_selective_scan_step.argtypes = [scan, vp, i64, vp, vp]
-    delta = vp
+    delta = group = vp
+    lib.tg_group_norm_sizes.argtypes = [group, psz, psz]
+    lib.tg_group_norm.argtypes = [group, vp, sz, vp]
+    lib.tg_group_norm_backward.argtypes = [group, ctypes.POINTER(_GroupNormGrads), vp, sz, vp]
     lib.tg_gated_delta_rule_sizes.argtypes = [delta, psz, psz, psz]
     lib.tg_gated_delta_rule.argtypes = [delta, vp, sz, vp, sz, vp]
     lib.tg_gated_delta_rule_backward.argtypes = [delta, ctypes.POINTER(_DeltaGrads), vp, sz, vp, sz, vp]
@@ -409,6 +425,107 @@ def layer_norm_backward(dy, s, gamma, mean, rstd, dsum=None, out=None, stream=No
         gp, gs, sp, ss, wp, mp, qp, dp, ds, rows, C, dt, dx.data_ptr(), dgamma.data_ptr(),
         dbeta.data_ptr(), ws.data_ptr(), need.value, _raw_stream(dev)), "tg_layer_norm_backward")
     return dx, dgamma, dbeta
+
+
+# -------------------------------------------------------------- group norm
+
+def _group_args(x, groups, gamma, beta, eps, act, z, dev):
+    """A function of (y's, mean's and rstd's addresses) that gives the call's
+    arguments; the statistics' shape."""
+    dt = _dtype(x, "x")
+    if x.dim() < 2 or x.shape[-1] < 1:
+        raise ValueError("x must be [N, ..., C] with C >= 1, got %s" % (tuple(x.shape),))
+    shape, N, C, dtype = x.shape, x.shape[0], x.shape[-1], x.dtype
+    if groups < 1 or C % groups:
+        raise ValueError("the %d groups must divide the %d channels" % (groups, C))
+    L = 1
+    for n in shape[1:-1]:
+        L *= n
+    if L < 1:
+        raise ValueError("x must hold a row for each of its N, got %s" % (tuple(shape),))
+    xp, xs = _norm_rows(x, "x", dev, shape, dtype)
+    zp, zs = _norm_rows(z, "z", dev, shape, dtype)
+    head = (N, L, C, groups, dt, _activation(act), eps, xp, xs, zp, zs,
+            _flat(_some(gamma, "gamma"), "gamma", dev, (C,)), _flat(beta, "beta", dev, (C,)))
+    return (lambda y, mean, rstd: _GROUP.pack(*head, y, mean, rstd)), (N, groups)
+
+
+def _group_forward(x, groups, gamma, beta, eps, act, z, train, out, dev):
+    args, stats = _group_args(x, groups, gamma, beta, eps, act, z, dev)
+    # The backward pass takes x and z again.
+    y = _new(x) if out is None else _given(
+        out, x, dev, True, {} if train else dict(x=x, z=z), dict(x=x, z=z, gamma=gamma, beta=beta))
+    mean = rstd = None
+    mp = rp = 0
+    if train:
+        mean = torch.empty(stats, dtype=_F32, device=x.device)
+        rstd = torch.empty_like(mean)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    a = args(y.data_ptr(), mp, rp)
+    lib = _lib()
+    work = sz()
+    _check(lib.tg_group_norm_sizes(a, ctypes.byref(work), None), "tg_group_norm_sizes")
+    ws, wp = None, 0
+    if work.value:
+        ws = torch.empty(work.value, dtype=torch.uint8, device=x.device)
+        wp = ws.data_ptr()
+    _check(lib.tg_group_norm(a, wp, work.value, _raw_stream(dev)), "tg_group_norm")
+    return y, mean, rstd
+
+
+def group_norm(x, groups, gamma, beta=None, eps=1e-5, act="silu", z=None, out=None, stream=None):
+    """Group norm of x [N, ..., C], channels last, then ``act`` ("silu" or
+    "none") and the gate: y = act(h * gamma + beta) * silu(z), where h is x less its
+    mean, divided by its standard deviation, over each n and each of ``groups``
+    groups of neighbouring channels. Maps are [N, H, W, C]; with x [N, C] the groups
+    are the heads of single tokens. gamma, beta [C]; z like x. ``out`` may be x or z."""
+    dev = _device(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return group_norm(x, groups, gamma, beta, eps, act, z, out)
+    return _group_forward(x, groups, gamma, beta, eps, act, z, False, out, dev)[0]
+
+
+def group_norm_train(x, groups, gamma, beta=None, eps=1e-5, act="silu", z=None, out=None,
+                     stream=None):
+    """(y, mean, rstd): group norm and what its backward pass takes, [N, groups]."""
+    dev = _device(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return group_norm_train(x, groups, gamma, beta, eps, act, z, out)
+    return _group_forward(x, groups, gamma, beta, eps, act, z, True, out, dev)
+
+
+def group_norm_backward(dy, x, groups, gamma, mean, rstd, beta=None, act="silu", z=None, out=None,
+                        stream=None):
+    """GroupNormGradients (dx, dgamma, dbeta, dz) of group_norm_train's y with the
+    same arguments and its mean and rstd; dz is None without z. ``out`` (dx) may be
+    x or dy."""
+    dev = _device(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return group_norm_backward(dy, x, groups, gamma, mean, rstd, beta, act, z, out)
+    args, stats = _group_args(x, groups, gamma, beta, 0.0, act, z, dev)
+    a = args(0, _flat(_some(mean, "mean"), "mean", dev, stats),
+             _flat(_some(rstd, "rstd"), "rstd", dev, stats))
+    gp, gs = _norm_rows(_some(dy, "dy"), "dy", dev, x.shape, x.dtype)
+    lib = _lib()
+    need = sz()
+    _check(lib.tg_group_norm_sizes(a, None, ctypes.byref(need)), "tg_group_norm_sizes")
+    dx = _new(x) if out is None else _given(out, x, dev, True, dict(x=x, dy=dy),
+                                            dict(x=x, dy=dy, z=z, gamma=gamma, beta=beta, mean=mean,
+                                                 rstd=rstd))
+    dz = None if z is None else _new(x)
+    dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
+    ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+    g = _GroupNormGrads(gp, gs, dx.data_ptr(), 0 if dz is None else dz.data_ptr(),
+                        dgamma.data_ptr(), dbeta.data_ptr())
+    _check(lib.tg_group_norm_backward(a, ctypes.byref(g), ws.data_ptr(), need.value,
+                                      _raw_stream(dev)), "tg_group_norm_backward")
+    return GroupNormGradients(dx, dgamma, dbeta, dz)
 
 
 # -------------------------------------------------- short causal convolution

@@ -255,6 +255,52 @@ tg_status tg_gated_delta_rule_backward(const tg_delta_args *a, const tg_delta_gr
 tg_status tg_gated_delta_rule_step(const tg_delta_args *a, float *state, int64_t num_slots,
                                    const int32_t *slots, void *stream);
 
+/* ---- Group norm --------------------------------------------------------
+ * Over each n and group g of C/G neighbouring channels of x [N][L][C], L rows (the
+ * pixels of a map; 1: the heads of a token) for each n:
+ *   mean = sum x / (L*C/G), rstd = 1 / sqrt(sum (x - mean)^2 / (L*C/G) + eps)
+ *   v = (x - mean) * rstd * gamma[c] + beta[c]
+ *   y = act(v) * silu(z)         (act(v) where z is not given)
+ * with act SiLU or none (TG_ACT_SILU, TG_ACT_NONE). Rows of x and z are a row
+ * stride >= C apart (or 0: one row for all); y is dense and may be x or z
+ * themselves (dense). beta, and mean with rstd (fp32 [N][G], for the backward
+ * pass) may be NULL. N == 0 does nothing; L >= 1. TG_ERR_UNSUPPORTED for more than
+ * 4096 groups, or L or N*L of 2^30 or more, or N past 2^24 where a group has more than
+ * 256 channels or L is not 1. */
+typedef struct {
+    int64_t N, L;
+    int C, G;
+    tg_dtype dtype;
+    tg_activation act;
+    float eps;
+    const void *x;
+    int64_t x_stride;
+    const void *z;
+    int64_t z_stride;
+    const float *gamma, *beta;
+    void *y;
+    float *mean, *rstd;
+} tg_group_norm_args;
+
+/* Scratch of tg_group_norm (may be 0) and of its backward pass; either may be NULL. */
+tg_status tg_group_norm_sizes(const tg_group_norm_args *a, size_t *workspace_bytes,
+                              size_t *backward_bytes);
+tg_status tg_group_norm(const tg_group_norm_args *a, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* Gradients. a: the forward call's arguments (y is not read), with its mean and
+ * rstd, which are required. dy by row stride; dx, dz dense (dz NULL iff z is): dx may
+ * be x or dy, dz may be z or the other of dx's two (dense). dgamma, dbeta fp32 [C],
+ * written; dbeta may be NULL. N == 0 writes zeros there. */
+typedef struct {
+    const void *dy;
+    int64_t dy_stride;
+    void *dx, *dz;
+    float *dgamma, *dbeta;
+} tg_group_norm_grads;
+tg_status tg_group_norm_backward(const tg_group_norm_args *a, const tg_group_norm_grads *g,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
