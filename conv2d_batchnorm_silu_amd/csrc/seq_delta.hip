@@ -101,7 +101,9 @@ __device__ __forceinline__ void invert(float* m) {
 template <typename T, int KP>
 struct PrepShape {
     static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 16, ML = C + 4;
-    static constexpr int lds = kScales * C * 4 + C * 8 + 2 * C * ML * 4 + 2 * NI * C * LD * 2;
+    // The matrices take the place of q and k.
+    static constexpr int square = 2 * C * ML * 4, rows = 2 * NI * C * LD * 2;
+    static constexpr int lds = kScales * C * 4 + C * 8 + (square > rows ? square : rows);
 };
 
 // One workgroup for a chunk and value head. NM: parts of X; BACK: the transposed matrices.
@@ -115,7 +117,7 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
     double* G = (double*)(scal + kScales * C);
     float* mat = (float*)(G + C);
     float* pm = mat + C * ML;
-    const Planes<NI> kp{(bf16*)(pm + C * ML), LD, C * LD}, qp{kp.p + NI * C * LD, LD, C * LD};
+    const Planes<NI> kp{(bf16*)mat, LD, C * LD}, qp{kp.p + NI * C * LD, LD, C * LD};
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g = l >> 4, col = l & 15;
     const int slot = blockIdx.x / a.HV, h = blockIdx.x % a.HV, hk = h / (a.HV / a.HK);
     const int s = a.map.owner(slot, C), start = a.map.start(s);
@@ -125,10 +127,11 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
 
     // With the chunk's last tokens all rows are written: those past the sequence's
     // end are zero, with a decay of 1.
-    stage(kp, row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, a.k.row, C, KP, n, a.K,
-          a.wide_qk);
-    stage(qp, row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, a.q.row, C, KP, n, a.K,
-          a.wide_qk);
+    Tile<T, C, KP, 256> kt, qt;
+    kt.fetch(tid, row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, a.k.row, n, a.K,
+             a.wide_qk);
+    qt.fetch(tid, row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, a.q.row, n, a.K,
+             a.wide_qk);
     if (w == 0) {
         DeltaGate t = {0.0f, 0.0f, 0.0f, 0.0f};
         if (l < n)
@@ -140,6 +143,8 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
             scal[kBeta * C + l] = t.b;
         }
     }
+    kt.put(tid, kp);
+    qt.put(tid, qp);
     __syncthreads();
 
     // k k^T and q k^T, a wave for each 16 rows (and product, where there are only 32).
@@ -228,32 +233,67 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
 
 template <typename T, int KP, int NM>
 struct FwdShape {
-    static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 16;
+    static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 16, VL = kMaxColumns * 16 + 8;
     static constexpr int prep = prep_bytes(C, NM + NI);
-    static int lds(int waves) {
-        return prep + 2 * NI * C * LD * 2 + C * (waves * 16 + 8) * (int)sizeof(T);
-    }
+    static constexpr int stage = prep + 2 * NI * C * LD * 2 + C * VL * (int)sizeof(T);
+    static constexpr int stages = 2 * stage <= 160 * 1024 ? 2 : 1, lds = stages * stage;
+    static_assert(lds <= 160 * 1024, "more LDS than a compute unit has");
 };
 
 template <typename T, int KP, int NM>
-__global__ __launch_bounds__(256) void delta_forward(const DeltaArgs a) {
+__global__ __launch_bounds__((kMaxColumns + delta_loaders(KP)) * 64) void delta_forward(const DeltaArgs a) {
     using Sh = FwdShape<T, KP, NM>;
-    constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, NT = C / 16, KT = KP / 16, NK = KP / 32;
+    constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, VL = Sh::VL, NT = C / 16, KT = KP / 16, NK = KP / 32;
+    constexpr int kLoaders = delta_loaders(KP);
     extern __shared__ float4 lds[];
-    const float* scal = (const float*)lds;
-    const bf16* fx = (const bf16*)(scal + kScales * C);
-    const bf16* fp = fx + frag_count(C) * 512 * NM;
-    const Planes<NI> kp{(bf16*)((char*)lds + Sh::prep), LD, C * LD}, qp{kp.p + NI * C * LD, LD, C * LD};
-    T* vl = (T*)(qp.p + NI * C * LD);
-    const int waves = blockDim.x >> 6, w = threadIdx.x >> 6, l = threadIdx.x & 63, g = l >> 4;
-    const int col = l & 15, VL = waves * 16 + 8;
+    const int waves = (int)(blockDim.x >> 6) - kLoaders, w = (threadIdx.x >> 6) - kLoaders;
+    const int l = threadIdx.x & 63, g = l >> 4, col = l & 15;
     const HeadSlice at = head_slice((a.V + waves * 16 - 1) / (waves * 16));
     if (at.pair >= a.map.seqs * a.HV) return;
     const int s = at.pair / a.HV, h = at.pair % a.HV, hk = h / (a.HV / a.HK);
     const int start = a.map.start(s), len = a.map.end(s) - start, slot0 = a.map.slot0(s, C);
-    const int v0 = at.slice * waves * 16, v = v0 + w * 16 + col, vy = v0 + w * 16 + 4 * g;
-    const int64_t KV = (int64_t)a.K * a.V, held = ((int64_t)s * a.HV + h) * KV;
+    const int chunks = (len + C - 1) / C, v0 = at.slice * waves * 16;
+    // A stage: the prepared matrices, k, q, the slice of v.
+    const auto planes_k = [&](int c) {
+        return Planes<NI>{(bf16*)((char*)lds + (c % Sh::stages) * Sh::stage + Sh::prep), LD, C * LD};
+    };
+    const auto planes_q = [&](int c) {
+        const Planes<NI> k = planes_k(c);
+        return Planes<NI>{k.p + NI * C * LD, LD, C * LD};
+    };
 
+    if (w < 0) {
+        ChunkLoad<T, KP, C, Sh::prep> load;
+        const auto fetch = [&](int c) {
+            load.fetch(a, a.v, a.wide_v, s, start, c * C, imin(C, len - c * C), hk, h, v0,
+                       (int64_t)(slot0 + c) * a.HV + h);
+        };
+        const auto put = [&](int c) {
+            const Planes<NI> q = planes_q(c);
+            load.put(lds + (c % Sh::stages) * (Sh::stage / 16), planes_k(c), q);
+            T* vl = (T*)(q.p + NI * C * LD);
+#pragma unroll
+            for (int i = 0; i < load.v.COUNT; ++i) {
+                const int o = i * kLoaders * 64 + threadIdx.x;
+                if (o < load.v.total)
+                    *(typename VecOf<T, 8>::type*)(vl + o / (kMaxColumns * 2) * VL +
+                                                   o % (kMaxColumns * 2) * 8) = load.v.e[i].r;
+            }
+        };
+        if (chunks > 0) fetch(0);
+        for (int c = 0; c < chunks; ++c) {
+            // Chunk c - 1 is being worked on; with one stage, it has to be over.
+            if (Sh::stages == 1 && c > 0) __syncthreads();
+            put(c);
+            if (c + 1 < chunks) fetch(c + 1);
+            __syncthreads();
+        }
+        if (Sh::stages == 1 && chunks > 0) __syncthreads();
+        return;
+    }
+
+    const int v = v0 + w * 16 + col, vy = v0 + w * 16 + 4 * g;
+    const int64_t KV = (int64_t)a.K * a.V, held = ((int64_t)s * a.HV + h) * KV;
     float4_t S[KT];
 #pragma unroll
     for (int t = 0; t < KT; ++t)
@@ -262,27 +302,15 @@ __global__ __launch_bounds__(256) void delta_forward(const DeltaArgs a) {
             const int k = t * 16 + 4 * g + r;
             S[t][r] = a.initial && k < a.K && v < a.V ? a.initial[held + (int64_t)k * a.V + v] : 0.0f;
         }
-    for (int c = 0; c * C < len; ++c) {
+    for (int c = 0; c < chunks; ++c) {
+        __syncthreads();  // chunk c has been brought
         const int lo = c * C, n = imin(C, len - lo);
         const int64_t chunk = (int64_t)(slot0 + c) * a.HV + h;
-        __syncthreads();
-        stage(kp, row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, a.k.row, C, KP, n,
-              a.K, a.wide_qk);
-        stage(qp, row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, a.q.row, C, KP, n,
-              a.K, a.wide_qk);
-        {
-            const float4* src = (const float4*)(a.prep + chunk * Sh::prep);
-            for (int i = threadIdx.x; i < Sh::prep / 16; i += blockDim.x) lds[i] = src[i];
-            const T* vs = row_of<const T>(a.v, a.map, s, start, lo) + (int64_t)h * a.V + v0;
-            for (int i = threadIdx.x; i < C * waves * 2; i += blockDim.x) {
-                const int r = i / (waves * 2), x = (i - r * waves * 2) * 8;
-                float f[8];
-                load8(vs + r * a.v.row + x, r < n ? a.V - v0 - x : 0, a.wide_v, f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) vl[r * VL + x + j] = (T)f[j];
-            }
-        }
-        __syncthreads();
+        const float* scal = (const float*)(lds + (c % Sh::stages) * (Sh::stage / 16));
+        const bf16* fx = (const bf16*)(scal + kScales * C);
+        const bf16* fp = fx + frag_count(C) * 512 * NM;
+        const Planes<NI> kp = planes_k(c), qp = planes_q(c);
+        const T* vl = (const T*)(qp.p + NI * C * LD);
 
         Frag<NM> sf[NK];
 #pragma unroll
@@ -313,9 +341,9 @@ __global__ __launch_bounds__(256) void delta_forward(const DeltaArgs a) {
         }
         if (a.saved) {
             float* keep = a.saved + chunk * (KV + (int64_t)C * a.V);
+            if (v < a.V)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (v < a.V) {
+                for (int r = 0; r < 4; ++r) {
 #pragma unroll
                     for (int t = 0; t < KT; ++t) {
                         const int k = t * 16 + 4 * g + r;
@@ -326,21 +354,34 @@ __global__ __launch_bounds__(256) void delta_forward(const DeltaArgs a) {
                         keep[KV + (int64_t)(mt * 16 + 4 * g + r) * a.V + v] = e[mt][r];
                 }
         }
-        // What the corrections add to y and to the state.
+        // What the corrections add to the state and to y.
+        const float total = scal[kDecay * C + C - 1];
+        {
+            Frag<NM> wf[C / 32];
+#pragma unroll
+            for (int t = 0; t < C / 32; ++t) {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[j] = e[2 * t + (j >> 2)][j & 3] * scal[kWrite * C + t * 32 + frag_at(g, j)];
+                wf[t] = frag_of<NM>(x);
+            }
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[t][r] *= total;
+#pragma unroll
+                for (int u = 0; u < C / 32; ++u) mma<NM>(S[t], kp.cols(u * 32, t * 16), wf[u]);
+            }
+        }
         Frag<NI> uf[C / 32];
-        Frag<NM> wf[C / 32];
 #pragma unroll
         for (int t = 0; t < C / 32; ++t) {
-            float u[8], x[8];
+            float u[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int i = t * 32 + frag_at(g, j);
-                const float f = e[2 * t + (j >> 2)][j & 3];
-                u[j] = f * scal[kBeta * C + i];
-                x[j] = f * scal[kWrite * C + i];
-            }
+            for (int j = 0; j < 8; ++j)
+                u[j] = e[2 * t + (j >> 2)][j & 3] * scal[kBeta * C + t * 32 + frag_at(g, j)];
             uf[t] = frag_of<NI>(u);
-            wf[t] = frag_of<NM>(x);
         }
         // y transposed, so that a lane holds four neighbouring columns of a token.
 #pragma unroll
@@ -368,14 +409,7 @@ __global__ __launch_bounds__(256) void delta_forward(const DeltaArgs a) {
                 }
             }
         }
-        const float total = scal[kDecay * C + C - 1];
-#pragma unroll
-        for (int t = 0; t < KT; ++t) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[t][r] *= total;
-#pragma unroll
-            for (int u = 0; u < C / 32; ++u) mma<NM>(S[t], kp.cols(u * 32, t * 16), wf[u]);
-        }
+        if (Sh::stages == 1) __syncthreads();
     }
     if (a.final && v < a.V)
 #pragma unroll
@@ -507,22 +541,23 @@ hipError_t step_typed(const DeltaStep& p, bool v4, unsigned n, hipStream_t st) {
 }
 
 template <typename T, int KP, int NM>
-hipError_t forward_at(const DeltaArgs& a, int waves, int64_t slots, hipStream_t st) {
+hipError_t forward_at(const DeltaArgs& a, int64_t slots, hipStream_t st) {
+    const int waves = delta_waves(a.V);
     hipError_t e = launch_delta_prep<T, NM, false>(a, KP, slots, st);
     if (e != hipSuccess) return e;
-    const int lds = FwdShape<T, KP, NM>::lds(waves);
+    constexpr int lds = FwdShape<T, KP, NM>::lds;
     e = ensure_dynamic_lds((const void*)delta_forward<T, KP, NM>, lds);
     if (e != hipSuccess) return e;
     const int64_t grid = head_slice_grid((int64_t)a.map.seqs * a.HV, (int)ceil_div(a.V, waves * 16));
-    delta_forward<T, KP, NM><<<(unsigned)grid, waves * 64, lds, st>>>(a);
+    delta_forward<T, KP, NM><<<(unsigned)grid, (waves + delta_loaders(KP)) * 64, lds, st>>>(a);
     return hipGetLastError();
 }
 template <typename T, int NM>
-hipError_t forward_typed(const DeltaArgs& a, int waves, int64_t slots, hipStream_t st) {
+hipError_t forward_typed(const DeltaArgs& a, int64_t slots, hipStream_t st) {
     switch (delta_padded(a.K)) {
-        case 64: return forward_at<T, 64, NM>(a, waves, slots, st);
-        case 128: return forward_at<T, 128, NM>(a, waves, slots, st);
-        default: return forward_at<T, 256, NM>(a, waves, slots, st);
+        case 64: return forward_at<T, 64, NM>(a, slots, st);
+        case 128: return forward_at<T, 128, NM>(a, slots, st);
+        default: return forward_at<T, 256, NM>(a, slots, st);
     }
 }
 
@@ -572,14 +607,6 @@ DeltaArgs delta_args(const tg_delta_args& a) {
     return b;
 }
 
-// As many workgroups as there are compute units before wider ones.
-int delta_waves(const tg_delta_args& a) {
-    const int64_t pairs = a.seqs.seqs * a.HV;
-    for (int waves = 4; waves > 1; waves /= 2)
-        if (a.V > (waves / 2) * 16 && pairs * ceil_div(a.V, waves * 16) >= 192) return waves;
-    return a.V > 16 ? 2 : 1;
-}
-
 void delta_sizes(const tg_delta_args& a, size_t* work, size_t* saved, size_t* backward) {
     const int in = delta_in(a.dtype), C = delta_chunk_of(a);
     const int64_t chunks = delta_slots(a.seqs, C) * a.HV;
@@ -593,7 +620,7 @@ void delta_sizes(const tg_delta_args& a, size_t* work, size_t* saved, size_t* ba
 
 int64_t delta_groups(const tg_delta_args& a) {
     const int64_t chunks = delta_slots(a.seqs, delta_chunk_of(a)) * a.HV;
-    const int64_t serial = head_slice_grid(a.seqs.seqs * a.HV, (int)ceil_div(a.V, delta_waves(a) * 16));
+    const int64_t serial = head_slice_grid(a.seqs.seqs * a.HV, (int)ceil_div(a.V, delta_waves(a.V) * 16));
     return chunks > serial ? chunks : serial;
 }
 
@@ -602,13 +629,12 @@ hipError_t launch_delta(const tg_delta_args& a, void* ws, void* saved, hipStream
     b.prep = (char*)ws;
     b.saved = (float*)saved;
     const int64_t slots = delta_slots(a.seqs, delta_chunk_of(a));
-    const int waves = delta_waves(a);
-    if (a.dtype == TG_F32) return forward_typed<float, kTrain>(b, waves, slots, st);
+    if (a.dtype == TG_F32) return forward_typed<float, kTrain>(b, slots, st);
     if (a.dtype == TG_BF16)
-        return saved ? forward_typed<bf16, kTrain>(b, waves, slots, st)
-                     : forward_typed<bf16, kMid<bf16>>(b, waves, slots, st);
-    return saved ? forward_typed<f16, kTrain>(b, waves, slots, st)
-                 : forward_typed<f16, kMid<f16>>(b, waves, slots, st);
+        return saved ? forward_typed<bf16, kTrain>(b, slots, st)
+                     : forward_typed<bf16, kMid<bf16>>(b, slots, st);
+    return saved ? forward_typed<f16, kTrain>(b, slots, st)
+                 : forward_typed<f16, kMid<f16>>(b, slots, st);
 }
 
 hipError_t launch_delta_step(const tg_delta_args& a, float* state, int64_t num_slots,

@@ -40,9 +40,9 @@ template <typename T>
 inline constexpr int kMid = sizeof(T) == 4 ? 3 : 2;  // parts of an intermediate in a prompt
 constexpr int kTrain = 3;                            // and in training
 
-// Tokens of a chunk: 64, or 32 where 64 rows of the parts of q and k (padded to KP)
-// would leave no room in LDS.
-constexpr int delta_chunk(int in, int KP) { return in * KP <= 256 ? 64 : 32; }
+// Tokens of a chunk: 64, or 32 where two chunks' parts of q and k (padded to KP) and
+// the matrices made from them would not fit LDS together.
+constexpr int delta_chunk(int in, int KP) { return in == 1 && KP <= 128 ? 64 : 32; }
 
 template <int N>
 struct Frag {
@@ -141,51 +141,66 @@ struct Planes {
     }
 };
 
-// Up to eight elements from p on (n <= 0: none, zeros); wide: all eight are there
-// and lie on 16 bytes where n > 0.
+// Eight elements of a row on their way through registers.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool wide, float (&v)[8]) {
-    if (wide) {
-        if (n > 0) {
-            if constexpr (sizeof(T) == 4) {
-                float a[4], b[4];
-                load_f32<T, 4>(p, a);
-                load_f32<T, 4>(p + 4, b);
+struct Eight {
+    typename VecOf<T, 8>::type r;
+    // Up to n from p on (n <= 0: none), zeros behind; wide: all eight are there and
+    // lie on 16 bytes where n > 0.
+    __device__ __forceinline__ void load(const T* p, int n, bool wide) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
-            } else {
-                load_f32<T, 8>(p, v);
-            }
-            return;
+        for (int j = 0; j < 8; ++j) r[j] = (T)0.0f;
+        if (wide) {
+            if (n > 0) r = *(const typename VecOf<T, 8>::type*)p;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) r[j] = p[j];
         }
-        n = 0;
     }
+    template <int N>
+    __device__ __forceinline__ void put(const Planes<N>& d, int row, int c) const {
+        float x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? (float)p[j] : 0.0f;
-}
+        for (int j = 0; j < 8; ++j) x[j] = (float)r[j];
+        const Frag<N> f = frag_of<N>(x);
+#pragma unroll
+        for (int q = 0; q < N; ++q) *(bf16x8_t*)(d.p + q * d.plane + row * d.ld + c) = f.p[q];
+    }
+};
 
-// R rows of W columns (a multiple of 8) of T from src (rows `stride` apart) into
-// planes; zeros past n rows and m columns.
-template <typename T, int N>
-__device__ __forceinline__ void stage(const Planes<N>& d, const T* src, int64_t stride, int R,
-                                      int W, int n, int m, bool wide) {
-    const int per = W / 8;
-    for (int i = threadIdx.x; i < R * per; i += blockDim.x) {
-        const int r = i / per, c = (i - r * per) * 8;
-        float v[8];
-        load8(src + r * stride + c, r < n ? m - c : 0, wide, v);
+// R rows of W columns of T from src (rows `stride` apart) as eights, by `THREADS`
+// threads: fetch() starts the loads, put() writes them as parts; zeros past n
+// rows and m columns. More than one batch in flight where COUNT is more than one.
+template <typename T, int R, int W, int THREADS>
+struct Tile {
+    static constexpr int total = R * W / 8, COUNT = (total + THREADS - 1) / THREADS;
+    Eight<T> e[COUNT];
+    __device__ __forceinline__ void fetch(int tid, const T* src, int64_t stride, int n, int m,
+                                          bool wide) {
 #pragma unroll
-        for (int q = 0; q < N; ++q) {
-            bf16x8_t o;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                bf16 p[N];
-                split<N>(v[j], p);
-                o[j] = p[q];
-            }
-            *(bf16x8_t*)(d.p + q * d.plane + r * d.ld + c) = o;
+        for (int i = 0; i < COUNT; ++i) {
+            const int at = i * THREADS + tid, r = at / (W / 8), c = at % (W / 8) * 8;
+            const bool in = total % THREADS == 0 || at < total;
+            e[i].load(src + r * stride + c, in && r < n ? m - c : 0, wide);
         }
     }
+    template <int N>
+    __device__ __forceinline__ void put(int tid, const Planes<N>& d) const {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            const int at = i * THREADS + tid;
+            if (total % THREADS == 0 || at < total) e[i].put(d, at / (W / 8), at % (W / 8) * 8);
+        }
+    }
+};
+// The same in one go.
+template <typename T, int R, int W, int THREADS, int N>
+__device__ __forceinline__ void stage(const Planes<N>& d, const T* src, int64_t stride, int n, int m,
+                                      bool wide) {
+    Tile<T, R, W, THREADS> t;
+    t.fetch(threadIdx.x, src, stride, n, m, wide);
+    t.put(threadIdx.x, d);
 }
 
 // What a chunk's tokens scale by (rows of `scal`, C floats each); G the decays'
@@ -288,6 +303,56 @@ __device__ __forceinline__ float decay_between(double hi, double lo) {
     return __builtin_amdgcn_exp2f((float)(hi - lo));
 }
 
+// The serial kernels: a workgroup has up to two waves that compute, 16 columns each,
+// and loaders before them that bring the next chunk's rows and matrices to LDS
+// (through registers: rows of any stride, split into parts once for all columns)
+// while the first work on this one's; the loads of the one after that are then on
+// their way. With one set of buffers (stages == 1, where two do not fit) loads still
+// are a chunk ahead, but their writing waits for the computation.
+constexpr int kMaxColumns = 2;
+// Four loading waves; two where a computing wave needs more than 256 registers, half of
+// its SIMD's.
+constexpr int delta_loaders(int KP) { return KP == 256 ? 2 : 4; }
+
+// One chunk on its way: q, k, the prepared matrices (PREP bytes) and rows of 16
+// or 32 columns of a V-wide tensor.
+template <typename T, int KP, int C, int PREP>
+struct ChunkLoad {
+    static constexpr int kLoadThreads = delta_loaders(KP) * 64;
+    static constexpr int NP = (PREP / 16 + kLoadThreads - 1) / kLoadThreads;
+    Tile<T, C, KP, kLoadThreads> q, k;
+    float4 p[NP];
+    Tile<T, C, kMaxColumns * 16, kLoadThreads> v;
+    __device__ __forceinline__ void fetch(const DeltaArgs& a, const Rows<const void>& vr, bool wide_v,
+                                          int s, int start, int lo, int n, int hk, int h, int v0,
+                                          int64_t chunk) {
+        const int tid = threadIdx.x % kLoadThreads;
+        k.fetch(tid, row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, a.k.row, n, a.K,
+                a.wide_qk);
+        q.fetch(tid, row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, a.q.row, n, a.K,
+                a.wide_qk);
+        const float4* src = (const float4*)(a.prep + chunk * PREP);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int at = i * kLoadThreads + tid;
+            if (PREP / 16 % kLoadThreads == 0 || at < PREP / 16) p[i] = src[at];
+        }
+        v.fetch(tid, row_of<const T>(vr, a.map, s, start, lo) + (int64_t)h * a.V + v0, vr.row, n,
+                a.V - v0, wide_v);
+    }
+    template <int N>
+    __device__ __forceinline__ void put(float4* prep, const Planes<N>& kp, const Planes<N>& qp) const {
+        const int tid = threadIdx.x % kLoadThreads;
+        k.put(tid, kp);
+        q.put(tid, qp);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int at = i * kLoadThreads + tid;
+            if (PREP / 16 % kLoadThreads == 0 || at < PREP / 16) prep[at] = p[i];
+        }
+    }
+};
+
 // One fragment of the prepared matrices, N parts, from LDS.
 template <int N>
 __device__ __forceinline__ Frag<N> prepared(const bf16* f, int index) {
@@ -306,7 +371,7 @@ extern template hipError_t launch_delta_prep<f16, kTrain, true>(const DeltaArgs&
 extern template hipError_t launch_delta_prep<bf16, kTrain, true>(const DeltaArgs&, int, int64_t, hipStream_t);
 
 DeltaArgs delta_args(const tg_delta_args& a);
-// Waves (of 16 columns) of a serial kernel's workgroups.
-int delta_waves(const tg_delta_args& a);
+// Waves that compute (16 columns each) in a serial kernel's workgroups.
+inline int delta_waves(int V) { return V > 16 ? 2 : 1; }
 
 }  // namespace tg

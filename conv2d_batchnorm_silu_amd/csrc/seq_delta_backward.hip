@@ -23,33 +23,52 @@ namespace {
 
 template <typename T, int KP>
 struct BackShape {
-    static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 16;
+    static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 16, WL = kMaxColumns * 16 + 16;
     static constexpr int prep = prep_bytes(C, 2 * kTrain);
-    static int lds(int waves) {
-        return prep + 2 * NI * C * LD * 2 + NI * C * (waves * 16 + 16) * 2;
-    }
+    static constexpr int stage = prep + 2 * NI * C * LD * 2 + NI * C * WL * 2;
+    static constexpr int stages = 2 * stage <= 160 * 1024 ? 2 : 1, lds = stages * stage;
+    static_assert(lds <= 160 * 1024, "more LDS than a compute unit has");
 };
 
 // The states' gradients, from the last chunk to the first: 16 columns in a wave.
 template <typename T, int KP>
-__global__ __launch_bounds__(256) void delta_backward(const DeltaArgs a) {
+__global__ __launch_bounds__((kMaxColumns + delta_loaders(KP)) * 64) void delta_backward(const DeltaArgs a) {
     using Sh = BackShape<T, KP>;
-    constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, NT = C / 16, KT = KP / 16, NK = KP / 32;
+    constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, WL = Sh::WL, NT = C / 16, KT = KP / 16, NK = KP / 32;
+    constexpr int kLoaders = delta_loaders(KP);
     extern __shared__ float4 lds[];
-    const float* scal = (const float*)lds;
-    const bf16* fx = (const bf16*)(scal + kScales * C);
-    const bf16* fp = fx + frag_count(C) * 512 * kTrain;
-    const int waves = blockDim.x >> 6, w = threadIdx.x >> 6, l = threadIdx.x & 63, g = l >> 4;
-    const int col = l & 15, WL = waves * 16 + 16;
-    const Planes<NI> kp{(bf16*)((char*)lds + Sh::prep), LD, C * LD}, qp{kp.p + NI * C * LD, LD, C * LD};
-    const Planes<NI> wp{qp.p + NI * C * LD, WL, C * WL};
+    const int waves = (int)(blockDim.x >> 6) - kLoaders, w = (threadIdx.x >> 6) - kLoaders;
+    const int l = threadIdx.x & 63, g = l >> 4, col = l & 15;
     const HeadSlice at = head_slice((a.V + waves * 16 - 1) / (waves * 16));
     if (at.pair >= a.map.seqs * a.HV) return;
     const int s = at.pair / a.HV, h = at.pair % a.HV, hk = h / (a.HV / a.HK);
     const int start = a.map.start(s), len = a.map.end(s) - start, slot0 = a.map.slot0(s, C);
-    const int v0 = at.slice * waves * 16, v = v0 + w * 16 + col;
-    const int64_t KV = (int64_t)a.K * a.V, held = ((int64_t)s * a.HV + h) * KV;
+    const int chunks = (len + C - 1) / C, v0 = at.slice * waves * 16, v = v0 + w * 16 + col;
+    // A stage: the prepared matrices, k, q, the slice of dy.
+    const auto planes = [&](int c, int which) {
+        bf16* k = (bf16*)((char*)lds + (c % Sh::stages) * Sh::stage + Sh::prep);
+        return Planes<NI>{k + which * NI * C * LD, which < 2 ? LD : WL, which < 2 ? C * LD : C * WL};
+    };
 
+    if (w < 0) {
+        ChunkLoad<T, KP, C, Sh::prep> load;
+        const auto fetch = [&](int c) {
+            load.fetch(a, a.dy, a.wide_dy, s, start, c * C, imin(C, len - c * C), hk, h, v0,
+                       (int64_t)(slot0 + c) * a.HV + h);
+        };
+        if (chunks > 0) fetch(chunks - 1);
+        for (int c = chunks - 1; c >= 0; --c) {
+            if (Sh::stages == 1 && c < chunks - 1) __syncthreads();
+            load.put(lds + (c % Sh::stages) * (Sh::stage / 16), planes(c, 0), planes(c, 1));
+            load.v.put(threadIdx.x, planes(c, 2));
+            if (c > 0) fetch(c - 1);
+            __syncthreads();
+        }
+        if (Sh::stages == 1 && chunks > 0) __syncthreads();
+        return;
+    }
+
+    const int64_t KV = (int64_t)a.K * a.V, held = ((int64_t)s * a.HV + h) * KV;
     float4_t S[KT];  // dS
 #pragma unroll
     for (int t = 0; t < KT; ++t)
@@ -58,19 +77,14 @@ __global__ __launch_bounds__(256) void delta_backward(const DeltaArgs a) {
             const int k = t * 16 + 4 * g + r;
             S[t][r] = a.dfinal && k < a.K && v < a.V ? a.dfinal[held + (int64_t)k * a.V + v] : 0.0f;
         }
-    for (int c = (len + C - 1) / C - 1; c >= 0; --c) {
+    for (int c = chunks - 1; c >= 0; --c) {
+        __syncthreads();  // chunk c has been brought
         const int lo = c * C, n = imin(C, len - lo);
         const int64_t chunk = (int64_t)(slot0 + c) * a.HV + h;
-        __syncthreads();
-        stage(kp, row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, a.k.row, C, KP, n,
-              a.K, a.wide_qk);
-        stage(qp, row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, a.q.row, C, KP, n,
-              a.K, a.wide_qk);
-        stage(wp, row_of<const T>(a.dy, a.map, s, start, lo) + (int64_t)h * a.V + v0, a.dy.row, C,
-              waves * 16, n, a.V - v0, a.wide_dy);
-        const float4* src = (const float4*)(a.prep + chunk * Sh::prep);
-        for (int i = threadIdx.x; i < Sh::prep / 16; i += blockDim.x) lds[i] = src[i];
-        __syncthreads();
+        const float* scal = (const float*)(lds + (c % Sh::stages) * (Sh::stage / 16));
+        const bf16* fx = (const bf16*)(scal + kScales * C);
+        const bf16* fp = fx + frag_count(C) * 512 * kTrain;
+        const Planes<NI> kp = planes(c, 0), qp = planes(c, 1), wp = planes(c, 2);
 
         float* keep = a.back + chunk * (KV + (int64_t)C * a.V);
         if (v < a.V)
@@ -148,6 +162,7 @@ __global__ __launch_bounds__(256) void delta_backward(const DeltaArgs a) {
                 mma<kTrain>(S[t], kp.cols(u * 32, t * 16), kr[u]);
             }
         }
+        if (Sh::stages == 1) __syncthreads();
     }
     if (a.dinitial && v < a.V)
 #pragma unroll
@@ -215,10 +230,10 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
         for (int i = tid; i < rep; i += kThreads) sums[hk * rep + i] = sums[a.HV + hk * rep + i] = 0.0f;
         return;
     }
-    stage(kp, row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, a.k.row, C, KP, n, a.K,
-          a.wide_qk);
-    stage(qp, row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, a.q.row, C, KP, n, a.K,
-          a.wide_qk);
+    stage<T, C, KP, kThreads>(kp, row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K,
+                              a.k.row, n, a.K, a.wide_qk);
+    stage<T, C, KP, kThreads>(qp, row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K,
+                              a.q.row, n, a.K, a.wide_qk);
 
     float4_t dq[NB][WT] = {}, dk[NB][WT] = {};
     for (int h = hk * rep; h < (hk + 1) * rep; ++h) {
@@ -254,24 +269,24 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
             float4_t qs[WT] = {}, rs[WT] = {}, es[WT] = {};
             for (int vb = 0; vb < a.V; vb += VB) {
                 __syncthreads();
-                stage(wp, dy + vb, a.dy.row, C, VB, n, a.V - vb, a.wide_dy);
-                stage(ep, E + vb, a.V, C, VB, C, a.V - vb, a.wide_s);
-                stage(rp, R + vb, a.V, C, VB, C, a.V - vb, a.wide_s);
-                for (int i = tid; i < KB * (VB / 8); i += kThreads) {
-                    const int r = i / (VB / 8), c = (i % (VB / 8)) * 8;
-                    const int m = kb + r < a.K ? a.V - vb - c : 0;
-                    float x[8], y[8];
-                    load8(S0 + (int64_t)(kb + r) * a.V + vb + c, m, a.wide_s, x);
-                    load8(dS + (int64_t)(kb + r) * a.V + vb + c, m, a.wide_s, y);
-                    const Frag<kTrain> xs = frag_of<kTrain>(x), ys = frag_of<kTrain>(y);
+                Tile<T, C, VB, kThreads> tw;
+                Tile<float, C, VB, kThreads> te, tr;
+                Tile<float, KB, VB, kThreads> ts, td;
+                tw.fetch(tid, dy + vb, a.dy.row, n, a.V - vb, a.wide_dy);
+                te.fetch(tid, E + vb, a.V, C, a.V - vb, a.wide_s);
+                tr.fetch(tid, R + vb, a.V, C, a.V - vb, a.wide_s);
+                ts.fetch(tid, S0 + (int64_t)kb * a.V + vb, a.V, a.K - kb, a.V - vb, a.wide_s);
+                td.fetch(tid, dS + (int64_t)kb * a.V + vb, a.V, a.K - kb, a.V - vb, a.wide_s);
+                tw.put(tid, wp);
+                te.put(tid, ep);
+                tr.put(tid, rp);
+                ts.put(tid, sp);
+                td.put(tid, dp);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) whole = __builtin_fmaf(x[j], y[j], whole);
+                for (int i = 0; i < ts.COUNT; ++i)
 #pragma unroll
-                    for (int q = 0; q < kTrain; ++q) {
-                        *(bf16x8_t*)(sp.p + q * sp.plane + r * VL + c) = xs.p[q];
-                        *(bf16x8_t*)(dp.p + q * dp.plane + r * VL + c) = ys.p[q];
-                    }
-                }
+                    for (int j = 0; j < 8; ++j)
+                        whole = __builtin_fmaf(ts.e[i].r[j], td.e[i].r[j], whole);
                 __syncthreads();
                 const Frag<NI> wf = wp.rows(row0, 0);
                 const Frag<kTrain> rf = rp.rows(row0, 0), ef = ep.rows(row0, 0);
@@ -476,14 +491,15 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
 }
 
 template <typename T, int KP>
-hipError_t backward_at(const DeltaArgs& a, int waves, int64_t slots, hipStream_t st) {
+hipError_t backward_at(const DeltaArgs& a, int64_t slots, hipStream_t st) {
+    const int waves = delta_waves(a.V);
     hipError_t e = launch_delta_prep<T, kTrain, true>(a, KP, slots, st);
     if (e != hipSuccess) return e;
-    const int lds = BackShape<T, KP>::lds(waves);
+    constexpr int lds = BackShape<T, KP>::lds;
     e = ensure_dynamic_lds((const void*)delta_backward<T, KP>, lds);
     if (e != hipSuccess) return e;
     const int64_t grid = head_slice_grid((int64_t)a.map.seqs * a.HV, (int)ceil_div(a.V, waves * 16));
-    delta_backward<T, KP><<<(unsigned)grid, waves * 64, lds, st>>>(a);
+    delta_backward<T, KP><<<(unsigned)grid, (waves + delta_loaders(KP)) * 64, lds, st>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess || slots == 0) return e;
     constexpr int bytes = GradShape<T, KP>::lds;
@@ -494,11 +510,11 @@ hipError_t backward_at(const DeltaArgs& a, int waves, int64_t slots, hipStream_t
     return hipGetLastError();
 }
 template <typename T>
-hipError_t backward_typed(const DeltaArgs& a, int waves, int64_t slots, hipStream_t st) {
+hipError_t backward_typed(const DeltaArgs& a, int64_t slots, hipStream_t st) {
     switch (delta_padded(a.K)) {
-        case 64: return backward_at<T, 64>(a, waves, slots, st);
-        case 128: return backward_at<T, 128>(a, waves, slots, st);
-        default: return backward_at<T, 256>(a, waves, slots, st);
+        case 64: return backward_at<T, 64>(a, slots, st);
+        case 128: return backward_at<T, 128>(a, slots, st);
+        default: return backward_at<T, 256>(a, slots, st);
     }
 }
 
@@ -524,10 +540,9 @@ hipError_t launch_delta_backward(const tg_delta_args& a, const tg_delta_grads& g
     if (!a.seqs.offsets) dy.len(gr.dy.seq_stride);
     s.len(a.V), s.ptr(saved, 4), s.ptr(b.back, 4);
     b.wide_dy = dy.width(8) == 8, b.wide_s = s.width(8) == 8;
-    const int waves = delta_waves(a);
-    hipError_t err = a.dtype == TG_F32   ? backward_typed<float>(b, waves, slots, st)
-                     : a.dtype == TG_BF16 ? backward_typed<bf16>(b, waves, slots, st)
-                                          : backward_typed<f16>(b, waves, slots, st);
+    hipError_t err = a.dtype == TG_F32   ? backward_typed<float>(b, slots, st)
+                     : a.dtype == TG_BF16 ? backward_typed<bf16>(b, slots, st)
+                                          : backward_typed<f16>(b, slots, st);
     if (err != hipSuccess) return err;
     return launch_column_sums(b.part, (int)slots, 2 * (int64_t)a.HV, gr.dA, a.HV, gr.ddt_bias, st);
 }
