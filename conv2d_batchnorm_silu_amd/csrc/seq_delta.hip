@@ -64,7 +64,7 @@ __device__ __forceinline__ void invert(float* m) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) d[i * LD + c] = x[i];
     }
-    __syncthreads();
+    lds_barrier();
     if (w < C / 32) {
         float* b = m + w * 32 * (LD + 1) + 16 * LD;  // the block below the first diagonal one
         float4_t t = {0, 0, 0, 0}, u = {0, 0, 0, 0};
@@ -72,7 +72,7 @@ __device__ __forceinline__ void invert(float* m) {
         mm16(u, b + 16, LD, t);
         put16(b, LD, u, -1.0f);
     }
-    __syncthreads();
+    lds_barrier();
     if constexpr (C == 64) {
         float4_t u[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
         float* b = m + 32 * LD;
@@ -89,25 +89,25 @@ __device__ __forceinline__ void invert(float* m) {
             mm16(u[1], b + 16 * LD + 32, LD, t[0]);
             mm16(u[1], b + 16 * LD + 48, LD, t[1]);
         }
-        __syncthreads();
+        lds_barrier();
         if (w < 2) {
             put16(b + w * 16, LD, u[0], -1.0f);
             put16(b + 16 * LD + w * 16, LD, u[1], -1.0f);
         }
-        __syncthreads();
+        lds_barrier();
     }
 }
 
 template <typename T, int KP>
 struct PrepShape {
-    static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 16, ML = C + 4;
+    static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 8, ML = C + 4;
     // The matrices take the place of q and k.
     static constexpr int square = 2 * C * ML * 4, rows = 2 * NI * C * LD * 2;
     static constexpr int lds = kScales * C * 4 + C * 8 + (square > rows ? square : rows);
 };
 
 // One workgroup for a chunk and value head. NM: parts of X; BACK: the transposed matrices.
-template <typename T, int KP, int NM, bool BACK>
+template <typename T, int KP, int NM, bool BACK, bool WIDE>
 __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
     using Sh = PrepShape<T, KP>;
     constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, ML = Sh::ML, NT = C / 16;
@@ -124,14 +124,15 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
     int lo, hi;
     if (!SeqMap::piece(slot, a.map.slot0(s, C), a.map.end(s) - start, C, lo, hi)) return;
     const int n = hi - lo;
+    if (n <= 0) return;
 
     // With the chunk's last tokens all rows are written: those past the sequence's
     // end are zero, with a decay of 1.
-    Tile<T, C, KP, 256> kt, qt;
-    kt.fetch(tid, row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, a.k.row, n, a.K,
-             a.wide_qk);
-    qt.fetch(tid, row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, a.q.row, n, a.K,
-             a.wide_qk);
+    Tile<T, C, KP, 256, WIDE> kt, qt;
+    kt.shape(a.k.row, a.K);
+    qt.shape(a.q.row, a.K);
+    kt.fetch(row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, n);
+    qt.fetch(row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, n);
     if (w == 0) {
         DeltaGate t = {0.0f, 0.0f, 0.0f, 0.0f};
         if (l < n)
@@ -143,9 +144,9 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
             scal[kBeta * C + l] = t.b;
         }
     }
-    kt.put(tid, kp);
-    qt.put(tid, qp);
-    __syncthreads();
+    kt.put(kp);
+    qt.put(qp);
+    lds_barrier();
 
     // k k^T and q k^T, a wave for each 16 rows (and product, where there are only 32).
     const int tile = C == 64 ? w : w & 1;
@@ -173,7 +174,7 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
                     scal[kUnitK * C + i] = a.normalize ? rsqrtf(kk[jt][r] + kUnitEps) : 1.0f;
                 if (qk_here) scal[kUnitQ * C + i] = a.normalize ? rsqrtf(qq[r] + kUnitEps) : 1.0f;
             }
-    __syncthreads();
+    lds_barrier();
     char* out = a.prep + (int64_t)blockIdx.x * prep_bytes(C, NM + PP);
     if (tid < C) {
         const float e = __builtin_amdgcn_exp2f((float)G[tid]), t = decay_between(G[C - 1], G[tid]);
@@ -202,7 +203,7 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
                 pm[i * ML + j] = j <= i ? D * qk[jt][r] * scal[kUnitQ * C + i] * rk * a.scale : 0.0f;
         }
     }
-    __syncthreads();
+    lds_barrier();
     invert<C, ML>(mat);
 
     // As fragments, in the order in which the serial kernel reads them.
@@ -229,196 +230,6 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
 #pragma unroll
             for (int q = 0; q < PP; ++q) *(bf16x8_t*)(fp + (f * PP + q) * 512 + l * 8) = pf.p[q];
         }
-}
-
-template <typename T, int KP, int NM>
-struct FwdShape {
-    static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 16, VL = kMaxColumns * 16 + 8;
-    static constexpr int prep = prep_bytes(C, NM + NI);
-    static constexpr int stage = prep + 2 * NI * C * LD * 2 + C * VL * (int)sizeof(T);
-    static constexpr int stages = 2 * stage <= 160 * 1024 ? 2 : 1, lds = stages * stage;
-    static_assert(lds <= 160 * 1024, "more LDS than a compute unit has");
-};
-
-template <typename T, int KP, int NM>
-__global__ __launch_bounds__((kMaxColumns + delta_loaders(KP)) * 64) void delta_forward(const DeltaArgs a) {
-    using Sh = FwdShape<T, KP, NM>;
-    constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, VL = Sh::VL, NT = C / 16, KT = KP / 16, NK = KP / 32;
-    constexpr int kLoaders = delta_loaders(KP);
-    extern __shared__ float4 lds[];
-    const int waves = (int)(blockDim.x >> 6) - kLoaders, w = (threadIdx.x >> 6) - kLoaders;
-    const int l = threadIdx.x & 63, g = l >> 4, col = l & 15;
-    const HeadSlice at = head_slice((a.V + waves * 16 - 1) / (waves * 16));
-    if (at.pair >= a.map.seqs * a.HV) return;
-    const int s = at.pair / a.HV, h = at.pair % a.HV, hk = h / (a.HV / a.HK);
-    const int start = a.map.start(s), len = a.map.end(s) - start, slot0 = a.map.slot0(s, C);
-    const int chunks = (len + C - 1) / C, v0 = at.slice * waves * 16;
-    // A stage: the prepared matrices, k, q, the slice of v.
-    const auto planes_k = [&](int c) {
-        return Planes<NI>{(bf16*)((char*)lds + (c % Sh::stages) * Sh::stage + Sh::prep), LD, C * LD};
-    };
-    const auto planes_q = [&](int c) {
-        const Planes<NI> k = planes_k(c);
-        return Planes<NI>{k.p + NI * C * LD, LD, C * LD};
-    };
-
-    if (w < 0) {
-        ChunkLoad<T, KP, C, Sh::prep> load;
-        const auto fetch = [&](int c) {
-            load.fetch(a, a.v, a.wide_v, s, start, c * C, imin(C, len - c * C), hk, h, v0,
-                       (int64_t)(slot0 + c) * a.HV + h);
-        };
-        const auto put = [&](int c) {
-            const Planes<NI> q = planes_q(c);
-            load.put(lds + (c % Sh::stages) * (Sh::stage / 16), planes_k(c), q);
-            T* vl = (T*)(q.p + NI * C * LD);
-#pragma unroll
-            for (int i = 0; i < load.v.COUNT; ++i) {
-                const int o = i * kLoaders * 64 + threadIdx.x;
-                if (o < load.v.total)
-                    *(typename VecOf<T, 8>::type*)(vl + o / (kMaxColumns * 2) * VL +
-                                                   o % (kMaxColumns * 2) * 8) = load.v.e[i].r;
-            }
-        };
-        if (chunks > 0) fetch(0);
-        for (int c = 0; c < chunks; ++c) {
-            // Chunk c - 1 is being worked on; with one stage, it has to be over.
-            if (Sh::stages == 1 && c > 0) __syncthreads();
-            put(c);
-            if (c + 1 < chunks) fetch(c + 1);
-            __syncthreads();
-        }
-        if (Sh::stages == 1 && chunks > 0) __syncthreads();
-        return;
-    }
-
-    const int v = v0 + w * 16 + col, vy = v0 + w * 16 + 4 * g;
-    const int64_t KV = (int64_t)a.K * a.V, held = ((int64_t)s * a.HV + h) * KV;
-    float4_t S[KT];
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int k = t * 16 + 4 * g + r;
-            S[t][r] = a.initial && k < a.K && v < a.V ? a.initial[held + (int64_t)k * a.V + v] : 0.0f;
-        }
-    for (int c = 0; c < chunks; ++c) {
-        __syncthreads();  // chunk c has been brought
-        const int lo = c * C, n = imin(C, len - lo);
-        const int64_t chunk = (int64_t)(slot0 + c) * a.HV + h;
-        const float* scal = (const float*)(lds + (c % Sh::stages) * (Sh::stage / 16));
-        const bf16* fx = (const bf16*)(scal + kScales * C);
-        const bf16* fp = fx + frag_count(C) * 512 * NM;
-        const Planes<NI> kp = planes_k(c), qp = planes_q(c);
-        const T* vl = (const T*)(qp.p + NI * C * LD);
-
-        Frag<NM> sf[NK];
-#pragma unroll
-        for (int t = 0; t < NK; ++t) sf[t] = frag_of<NM>(S[2 * t], S[2 * t + 1]);
-        // v - e^G k S0, and through X.
-        float4_t e[NT];
-#pragma unroll
-        for (int mt = 0; mt < NT; ++mt) {
-            float4_t x = {0, 0, 0, 0};
-#pragma unroll
-            for (int t = 0; t < NK; ++t) mma<NM>(x, kp.rows(mt * 16, t * 32), sf[t]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = mt * 16 + 4 * g + r;
-                e[mt][r] = __builtin_fmaf(-scal[kReadK * C + i], x[r], (float)vl[i * VL + w * 16 + col]);
-            }
-        }
-        Frag<NM> rf[C / 32];
-#pragma unroll
-        for (int t = 0; t < C / 32; ++t) rf[t] = frag_of<NM>(e[2 * t], e[2 * t + 1]);
-#pragma unroll
-        for (int mt = 0; mt < NT; ++mt) {
-            e[mt] = float4_t{0, 0, 0, 0};
-#pragma unroll
-            for (int t = 0; t < C / 32; ++t)
-                if (frag_used(C, mt, t, false))
-                    mma<NM>(e[mt], prepared<NM>(fx, frag_index(C, mt, t, false)), rf[t]);
-        }
-        if (a.saved) {
-            float* keep = a.saved + chunk * (KV + (int64_t)C * a.V);
-            if (v < a.V)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-#pragma unroll
-                    for (int t = 0; t < KT; ++t) {
-                        const int k = t * 16 + 4 * g + r;
-                        if (k < a.K) keep[(int64_t)k * a.V + v] = S[t][r];
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < NT; ++mt)
-                        keep[KV + (int64_t)(mt * 16 + 4 * g + r) * a.V + v] = e[mt][r];
-                }
-        }
-        // What the corrections add to the state and to y.
-        const float total = scal[kDecay * C + C - 1];
-        {
-            Frag<NM> wf[C / 32];
-#pragma unroll
-            for (int t = 0; t < C / 32; ++t) {
-                float x[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] = e[2 * t + (j >> 2)][j & 3] * scal[kWrite * C + t * 32 + frag_at(g, j)];
-                wf[t] = frag_of<NM>(x);
-            }
-#pragma unroll
-            for (int t = 0; t < KT; ++t) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[t][r] *= total;
-#pragma unroll
-                for (int u = 0; u < C / 32; ++u) mma<NM>(S[t], kp.cols(u * 32, t * 16), wf[u]);
-            }
-        }
-        Frag<NI> uf[C / 32];
-#pragma unroll
-        for (int t = 0; t < C / 32; ++t) {
-            float u[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                u[j] = e[2 * t + (j >> 2)][j & 3] * scal[kBeta * C + t * 32 + frag_at(g, j)];
-            uf[t] = frag_of<NI>(u);
-        }
-        // y transposed, so that a lane holds four neighbouring columns of a token.
-#pragma unroll
-        for (int mt = 0; mt < NT; ++mt) {
-            float4_t y = {0, 0, 0, 0};
-#pragma unroll
-            for (int t = 0; t < NK; ++t) mma<NI>(y, sf[t], qp.rows(mt * 16, t * 32));
-            const int i = mt * 16 + col;
-            const float f = scal[kReadQ * C + i];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] *= f;
-#pragma unroll
-            for (int t = 0; t < C / 32; ++t)
-                if (frag_used(C, mt, t, false))
-                    mma<NI>(y, uf[t], prepared<NI>(fp, frag_index(C, mt, t, false)));
-            if (i < n) {
-                T* yp = row_of<T>(a.y, a.map, s, start, lo + i) + (int64_t)h * a.V + vy;
-                float o[4] = {y[0], y[1], y[2], y[3]};
-                if (a.wide_y) {
-                    if (vy < a.V) store_f32<T, 4>(yp, o);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (vy + r < a.V) yp[r] = (T)o[r];
-                }
-            }
-        }
-        if (Sh::stages == 1) __syncthreads();
-    }
-    if (a.final && v < a.V)
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int k = t * 16 + 4 * g + r;
-                if (k < a.K) a.final[held + (int64_t)k * a.V + v] = S[t][r];
-            }
 }
 
 // ---- single tokens
@@ -540,25 +351,18 @@ hipError_t step_typed(const DeltaStep& p, bool v4, unsigned n, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <typename T, int KP, int NM>
-hipError_t forward_at(const DeltaArgs& a, int64_t slots, hipStream_t st) {
-    const int waves = delta_waves(a.V);
-    hipError_t e = launch_delta_prep<T, NM, false>(a, KP, slots, st);
-    if (e != hipSuccess) return e;
-    constexpr int lds = FwdShape<T, KP, NM>::lds;
-    e = ensure_dynamic_lds((const void*)delta_forward<T, KP, NM>, lds);
-    if (e != hipSuccess) return e;
-    const int64_t grid = head_slice_grid((int64_t)a.map.seqs * a.HV, (int)ceil_div(a.V, waves * 16));
-    delta_forward<T, KP, NM><<<(unsigned)grid, (waves + delta_loaders(KP)) * 64, lds, st>>>(a);
-    return hipGetLastError();
-}
 template <typename T, int NM>
 hipError_t forward_typed(const DeltaArgs& a, int64_t slots, hipStream_t st) {
-    switch (delta_padded(a.K)) {
-        case 64: return forward_at<T, 64, NM>(a, slots, st);
-        case 128: return forward_at<T, 128, NM>(a, slots, st);
-        default: return forward_at<T, 256, NM>(a, slots, st);
-    }
+    const int KP = delta_padded(a.K);
+    const hipError_t e = launch_delta_prep<T, NM, false>(a, KP, slots, st);
+    return e == hipSuccess ? launch_delta_forward<T, NM>(a, KP, st) : e;
+}
+template <typename T>
+hipError_t backward_typed(const DeltaArgs& a, int64_t slots, hipStream_t st) {
+    const int KP = delta_padded(a.K);
+    hipError_t e = launch_delta_prep<T, kTrain, true>(a, KP, slots, st);
+    if (e == hipSuccess) e = launch_delta_states<T>(a, KP, st);
+    return e == hipSuccess ? launch_delta_grads<T>(a, KP, slots, st) : e;
 }
 
 }  // namespace
@@ -570,9 +374,11 @@ hipError_t launch_delta_prep(const DeltaArgs& a, int KP, int64_t slots, hipStrea
 #define TG_X(KP_)                                                                               \
     do {                                                                                        \
         constexpr int bytes = PrepShape<T, KP_>::lds;                                           \
-        const hipError_t e = ensure_dynamic_lds((const void*)delta_prep<T, KP_, NM, BACK>, bytes);  \
+        const auto kernel = a.wide_qk ? delta_prep<T, KP_, NM, BACK, true>                      \
+                                      : delta_prep<T, KP_, NM, BACK, false>;                    \
+        const hipError_t e = ensure_dynamic_lds((const void*)kernel, bytes);                    \
         if (e != hipSuccess) return e;                                                          \
-        delta_prep<T, KP_, NM, BACK><<<grid, 256, bytes, st>>>(a);                                  \
+        kernel<<<grid, 256, bytes, st>>>(a);                                                    \
     } while (0)
     if (KP == 64) TG_X(64);
     else if (KP == 128) TG_X(128);
@@ -580,9 +386,6 @@ hipError_t launch_delta_prep(const DeltaArgs& a, int KP, int64_t slots, hipStrea
 #undef TG_X
     return hipGetLastError();
 }
-template hipError_t launch_delta_prep<float, kTrain, true>(const DeltaArgs&, int, int64_t, hipStream_t);
-template hipError_t launch_delta_prep<f16, kTrain, true>(const DeltaArgs&, int, int64_t, hipStream_t);
-template hipError_t launch_delta_prep<bf16, kTrain, true>(const DeltaArgs&, int, int64_t, hipStream_t);
 
 DeltaArgs delta_args(const tg_delta_args& a) {
     DeltaArgs b{};
@@ -620,7 +423,7 @@ void delta_sizes(const tg_delta_args& a, size_t* work, size_t* saved, size_t* ba
 
 int64_t delta_groups(const tg_delta_args& a) {
     const int64_t chunks = delta_slots(a.seqs, delta_chunk_of(a)) * a.HV;
-    const int64_t serial = head_slice_grid(a.seqs.seqs * a.HV, (int)ceil_div(a.V, delta_waves(a.V) * 16));
+    const int64_t serial = head_slice_grid(a.seqs.seqs * a.HV, (int)ceil_div(a.V, slice_of(delta_in(a.dtype), delta_padded(a.K))));
     return chunks > serial ? chunks : serial;
 }
 
@@ -635,6 +438,33 @@ hipError_t launch_delta(const tg_delta_args& a, void* ws, void* saved, hipStream
                      : forward_typed<bf16, kMid<bf16>>(b, slots, st);
     return saved ? forward_typed<f16, kTrain>(b, slots, st)
                  : forward_typed<f16, kMid<f16>>(b, slots, st);
+}
+
+hipError_t launch_delta_backward(const tg_delta_args& a, const tg_delta_grads& gr,
+                                 const void* saved, void* ws, hipStream_t st) {
+    DeltaArgs b = delta_args(a);
+    const int C = delta_chunk_of(a);
+    const int64_t slots = delta_slots(a.seqs, C), chunks = slots * a.HV;
+    const size_t states = (size_t)chunks * ((size_t)a.K * a.V + (size_t)C * a.V) * 4;
+    b.saved = (float*)saved;
+    b.prep = (char*)ws;
+    b.back = (float*)(b.prep + up256((size_t)chunks * prep_bytes(C, 2 * kTrain)));
+    b.part = (float*)((char*)b.back + up256(states));
+    b.dy = rows_of<const void>(gr.dy);
+    b.dq = rows_of<void>(gr.dq), b.dk = rows_of<void>(gr.dk), b.dv = rows_of<void>(gr.dv);
+    b.ddt = rows_of<void>(gr.ddt), b.dbeta = rows_of<void>(gr.dbeta);
+    b.dfinal = gr.dfinal, b.dinitial = gr.dinitial;
+    const size_t e = elem_bytes(a.dtype);
+    Widest dy, s;
+    dy.len(a.V), dy.len(gr.dy.row_stride), dy.ptr(gr.dy.p, e);
+    if (!a.seqs.offsets) dy.len(gr.dy.seq_stride);
+    s.len(a.V), s.ptr(saved, 4), s.ptr(b.back, 4);
+    b.wide_dy = dy.width(8) == 8, b.wide_s = s.width(8) == 8;
+    hipError_t err = a.dtype == TG_F32   ? backward_typed<float>(b, slots, st)
+                     : a.dtype == TG_BF16 ? backward_typed<bf16>(b, slots, st)
+                                          : backward_typed<f16>(b, slots, st);
+    if (err != hipSuccess) return err;
+    return launch_column_sums(b.part, (int)slots, 2 * (int64_t)a.HV, gr.dA, a.HV, gr.ddt_bias, st);
 }
 
 hipError_t launch_delta_step(const tg_delta_args& a, float* state, int64_t num_slots,

@@ -90,6 +90,40 @@ __device__ __forceinline__ void mma(float4_t& c, const Frag<NA>& a, const Frag<N
                 c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], c, 0, 0, 0);
 }
 
+// c[m] += a[m] b, or a b[m], where m is used, the same products: independent
+// accumulators in turn, as one has to wait for its last product.
+template <int N, int M, int NA, int NB, typename Used>
+__device__ __forceinline__ void mma_rows(float4_t (&c)[M], const Frag<NA> (&a)[M], const Frag<NB>& b,
+                                         Used used) {
+#pragma unroll
+    for (int s = N - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i)
+            if (i < NA && s - i < NB)
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                    if (used(m))
+                        c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[m].p[i], b.p[s - i], c[m], 0,
+                                                                       0, 0);
+}
+template <int N, int M, int NA, int NB, typename Used>
+__device__ __forceinline__ void mma_cols(float4_t (&c)[M], const Frag<NA>& a, const Frag<NB> (&b)[M],
+                                         Used used) {
+#pragma unroll
+    for (int s = N - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i)
+            if (i < NA && s - i < NB)
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                    if (used(m))
+                        c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b[m].p[s - i], c[m], 0,
+                                                                       0, 0);
+}
+struct All {
+    __device__ __forceinline__ constexpr bool operator()(int) const { return true; }
+};
+
 // A matrix in LDS, in N planes of parts: row r of a plane at r * ld elements.
 template <int N>
 struct Planes {
@@ -141,67 +175,102 @@ struct Planes {
     }
 };
 
-// Eight elements of a row on their way through registers.
-template <typename T>
-struct Eight {
-    typename VecOf<T, 8>::type r;
-    // Up to n from p on (n <= 0: none), zeros behind; wide: all eight are there and
-    // lie on 16 bytes where n > 0.
-    __device__ __forceinline__ void load(const T* p, int n, bool wide) {
+// R rows of W columns of T on their way through the registers of THREADS threads,
+// eight elements in each: fetch() starts the loads, put() writes them as parts, with
+// zeros past n >= 0 rows and m >= 1 columns. WIDE: m and all addresses are multiples of
+// eight elements (of 16 bytes for fp32). What lies outside is loaded from the last
+// row and column inside and dropped in put(): a load under a condition, into
+// registers that would have to be zeroed before, would wait for all loads on
+// their way. A thread's offsets are 32-bit and found once, its addresses are a
+// uniform pointer and an offset.
+template <typename T, int R, int W, int THREADS, bool WIDE>
+struct Tile {
+    typedef typename VecOf<T, 8>::type eight;
+    static constexpr int total = R * W / 8, COUNT = (total + THREADS - 1) / THREADS;
+    eight e[COUNT];
+    uint32_t off[COUNT];
+    uint32_t stride;
+    int n, m;
+    __device__ __forceinline__ static int tid() { return threadIdx.x % THREADS; }
+    __device__ __forceinline__ static int row(int i) { return (i * THREADS + tid()) / (W / 8); }
+    __device__ __forceinline__ static int column(int i) { return (i * THREADS + tid()) % (W / 8) * 8; }
+    __device__ __forceinline__ static bool inside(int i) {
+        return total % THREADS == 0 || i * THREADS + tid() < total;
+    }
+    __device__ __forceinline__ void shape(int64_t row_stride, int cols) {
+        stride = (uint32_t)row_stride;
+        m = cols;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = (T)0.0f;
-        if (wide) {
-            if (n > 0) r = *(const typename VecOf<T, 8>::type*)p;
+        for (int i = 0; i < COUNT; ++i)
+            off[i] = (uint32_t)imin(row(i), R - 1) * stride +
+                     (uint32_t)(WIDE ? imin(column(i), m - 8) : imin(column(i), m - 1));
+    }
+    __device__ __forceinline__ void fetch(const T* src, int rows) {
+        n = imin(rows, R);
+        if (WIDE && n == R) {
+#pragma unroll
+            for (int i = 0; i < COUNT; ++i) e[i] = *(const eight*)(src + off[i]);
+            return;
+        }
+        const int last = n > 0 ? n - 1 : 0;
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            const int r = imin(row(i), R - 1);
+            const T* p = src + (off[i] - (uint32_t)(r - imin(r, last)) * stride);
+            if constexpr (WIDE) {
+                e[i] = *(const eight*)p;
+            } else {
+                const int left = m - 1 - imin(column(i), m - 1);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) e[i][j] = p[imin(j, left)];
+            }
+        }
+    }
+    __device__ __forceinline__ eight value(int i) const {
+        if (WIDE && n == R && m == W) return e[i];
+        const int r = row(i), c = column(i);
+        eight o;
+        if constexpr (WIDE) {
+            const bool ok = r < n && c < m;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = ok ? e[i][j] : (T)0.0f;
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) r[j] = p[j];
+            for (int j = 0; j < 8; ++j) o[j] = r < n && c + j < m ? e[i][j] : (T)0.0f;
         }
+        return o;
     }
     template <int N>
-    __device__ __forceinline__ void put(const Planes<N>& d, int row, int c) const {
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = (float)r[j];
-        const Frag<N> f = frag_of<N>(x);
-#pragma unroll
-        for (int q = 0; q < N; ++q) *(bf16x8_t*)(d.p + q * d.plane + row * d.ld + c) = f.p[q];
+    __device__ __forceinline__ void put(const Planes<N>& d) const {
+        if (WIDE && n == R && m == W) put_values<N, true>(d);
+        else put_values<N, false>(d);
     }
-};
-
-// R rows of W columns of T from src (rows `stride` apart) as eights, by `THREADS`
-// threads: fetch() starts the loads, put() writes them as parts; zeros past n
-// rows and m columns. More than one batch in flight where COUNT is more than one.
-template <typename T, int R, int W, int THREADS>
-struct Tile {
-    static constexpr int total = R * W / 8, COUNT = (total + THREADS - 1) / THREADS;
-    Eight<T> e[COUNT];
-    __device__ __forceinline__ void fetch(int tid, const T* src, int64_t stride, int n, int m,
-                                          bool wide) {
+    template <int N, bool FULL>
+    __device__ __forceinline__ void put_values(const Planes<N>& d) const {
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
-            const int at = i * THREADS + tid, r = at / (W / 8), c = at % (W / 8) * 8;
-            const bool in = total % THREADS == 0 || at < total;
-            e[i].load(src + r * stride + c, in && r < n ? m - c : 0, wide);
+            if (!inside(i)) continue;
+            const eight v = FULL ? e[i] : value(i);
+            bf16* at = d.p + row(i) * d.ld + column(i);
+            if constexpr (sizeof(T) == 2 && N == 1) {
+                *(eight*)at = v;
+            } else {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = (float)v[j];
+                const Frag<N> f = frag_of<N>(x);
+#pragma unroll
+                for (int q = 0; q < N; ++q) *(bf16x8_t*)(at + q * d.plane) = f.p[q];
+            }
         }
     }
-    template <int N>
-    __device__ __forceinline__ void put(int tid, const Planes<N>& d) const {
+    // As they are, into rows of ld elements.
+    __device__ __forceinline__ void put_raw(T* d, int ld) const {
 #pragma unroll
-        for (int i = 0; i < COUNT; ++i) {
-            const int at = i * THREADS + tid;
-            if (total % THREADS == 0 || at < total) e[i].put(d, at / (W / 8), at % (W / 8) * 8);
-        }
+        for (int i = 0; i < COUNT; ++i)
+            if (inside(i)) *(eight*)(d + row(i) * ld + column(i)) = value(i);
     }
 };
-// The same in one go.
-template <typename T, int R, int W, int THREADS, int N>
-__device__ __forceinline__ void stage(const Planes<N>& d, const T* src, int64_t stride, int n, int m,
-                                      bool wide) {
-    Tile<T, R, W, THREADS> t;
-    t.fetch(threadIdx.x, src, stride, n, m, wide);
-    t.put(threadIdx.x, d);
-}
 
 // What a chunk's tokens scale by (rows of `scal`, C floats each); G the decays'
 // logarithms added up from the chunk's first token, rk and rq the inverse lengths.
@@ -303,75 +372,86 @@ __device__ __forceinline__ float decay_between(double hi, double lo) {
     return __builtin_amdgcn_exp2f((float)(hi - lo));
 }
 
-// The serial kernels: a workgroup has up to two waves that compute, 16 columns each,
-// and loaders before them that bring the next chunk's rows and matrices to LDS
-// (through registers: rows of any stride, split into parts once for all columns)
-// while the first work on this one's; the loads of the one after that are then on
-// their way. With one set of buffers (stages == 1, where two do not fit) loads still
-// are a chunk ahead, but their writing waits for the computation.
-constexpr int kMaxColumns = 2;
-// Four loading waves; two where a computing wave needs more than 256 registers, half of
-// its SIMD's.
-constexpr int delta_loaders(int KP) { return KP == 256 ? 2 : 4; }
+// The serial kernels. A workgroup has 32 columns of V (16 where more do not fit LDS) and
+// for each 16 of them two waves that carry S, and two that help. Wave (ct, hf) of the
+// first has the 16 columns of ct, the half hf of S's K rows (in its accumulators)
+// and the half hf of a chunk's tokens. What a product sums over all K rows is formed
+// as two halves for all tokens and joined through LDS; what a token has found is given
+// to the other half as fragments. So a chunk takes three barriers more than with
+// a wave for 16 whole columns, but half the instructions one after another, and each
+// SIMD has such a wave.
+//
+// The helpers bring rows of q, k and v to LDS through registers (rows of any stride,
+// split into parts once for all columns), a chunk ahead and the loads another
+// chunk ahead, and form what the recurrence does not wait for. A wave loads the
+// prepared fragments of its own tokens to registers as soon as it has used the last
+// chunk's. 4 x 4096 tokens of 16 heads, bf16: a wave for 16 whole columns and four that
+// load 215 us, four waves that share S and everything else 206, with helpers FWD_US.
+constexpr int slice_of(int in, int KP) { return in * KP > 512 ? 16 : 32; }
 
-// One chunk on its way: q, k, the prepared matrices (PREP bytes) and rows of 16
-// or 32 columns of a V-wide tensor.
-template <typename T, int KP, int C, int PREP>
-struct ChunkLoad {
-    static constexpr int kLoadThreads = delta_loaders(KP) * 64;
-    static constexpr int NP = (PREP / 16 + kLoadThreads - 1) / kLoadThreads;
-    Tile<T, C, KP, kLoadThreads> q, k;
-    float4 p[NP];
-    Tile<T, C, kMaxColumns * 16, kLoadThreads> v;
-    __device__ __forceinline__ void fetch(const DeltaArgs& a, const Rows<const void>& vr, bool wide_v,
-                                          int s, int start, int lo, int n, int hk, int h, int v0,
-                                          int64_t chunk) {
-        const int tid = threadIdx.x % kLoadThreads;
-        k.fetch(tid, row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, a.k.row, n, a.K,
-                a.wide_qk);
-        q.fetch(tid, row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, a.q.row, n, a.K,
-                a.wide_qk);
-        const float4* src = (const float4*)(a.prep + chunk * PREP);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int at = i * kLoadThreads + tid;
-            if (PREP / 16 % kLoadThreads == 0 || at < PREP / 16) p[i] = src[at];
-        }
-        v.fetch(tid, row_of<const T>(vr, a.map, s, start, lo) + (int64_t)h * a.V + v0, vr.row, n,
-                a.V - v0, wide_v);
+// A barrier for what lies in LDS: __syncthreads would also wait for the loads and
+// stores of global memory that are on their way (258 us in place of what it takes now).
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Half fragments (the four rows that a lane has of a tile of 16) of N parts in LDS.
+template <int N>
+struct HalfFrags {
+    bf16* p;
+    __device__ __forceinline__ bf16x4_t* at(int tile, int n) const {
+        return (bf16x4_t*)(p + ((tile * N + n) * 64 + (threadIdx.x & 63)) * 4);
     }
-    template <int N>
-    __device__ __forceinline__ void put(float4* prep, const Planes<N>& kp, const Planes<N>& qp) const {
-        const int tid = threadIdx.x % kLoadThreads;
-        k.put(tid, kp);
-        q.put(tid, qp);
+    __device__ __forceinline__ void put(int tile, const float4_t& v) const {
+        bf16x4_t o[N];
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int at = i * kLoadThreads + tid;
-            if (PREP / 16 % kLoadThreads == 0 || at < PREP / 16) prep[at] = p[i];
+        for (int j = 0; j < 4; ++j) {
+            bf16 q[N];
+            split<N>(v[j], q);
+#pragma unroll
+            for (int n = 0; n < N; ++n) o[n][j] = q[n];
         }
+#pragma unroll
+        for (int n = 0; n < N; ++n) *at(tile, n) = o[n];
+    }
+    // Of tiles 2t and 2t + 1.
+    __device__ __forceinline__ Frag<N> frag(int t) const {
+        Frag<N> f;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            f.p[n] = __builtin_shufflevector(*at(2 * t, n), *at(2 * t + 1, n), 0, 1, 2, 3, 4, 5, 6, 7);
+        return f;
     }
 };
+__device__ __forceinline__ float4_t* sum_at(float* p, int tile) {
+    return (float4_t*)(p + (tile * 64 + (threadIdx.x & 63)) * 4);
+}
 
-// One fragment of the prepared matrices, N parts, from LDS.
+// One fragment of the prepared matrices, N parts, from the workspace.
 template <int N>
-__device__ __forceinline__ Frag<N> prepared(const bf16* f, int index) {
-    Frag<N> o;
+__device__ __forceinline__ void prepared(Frag<N>& o, const bf16* f, int index) {
 #pragma unroll
     for (int q = 0; q < N; ++q)
         o.p[q] = *(const bf16x8_t*)(f + (index * N + q) * 512 + (threadIdx.x & 63) * 8);
-    return o;
 }
 
-// NM: parts of X; BACK: the transposed matrices.
+// A scale of the four rows that a lane has of tile mt.
+__device__ __forceinline__ float4_t scales(const float* scal, int C, DeltaScale which, int mt) {
+    return *(const float4_t*)(scal + which * C + mt * 16 + 4 * ((threadIdx.x & 63) >> 4));
+}
+
+// The kernels' launches; NM: parts of X; BACK: the transposed matrices.
 template <typename T, int NM, bool BACK>
 hipError_t launch_delta_prep(const DeltaArgs& a, int KP, int64_t slots, hipStream_t st);
-extern template hipError_t launch_delta_prep<float, kTrain, true>(const DeltaArgs&, int, int64_t, hipStream_t);
-extern template hipError_t launch_delta_prep<f16, kTrain, true>(const DeltaArgs&, int, int64_t, hipStream_t);
-extern template hipError_t launch_delta_prep<bf16, kTrain, true>(const DeltaArgs&, int, int64_t, hipStream_t);
+template <typename T, int NM>
+hipError_t launch_delta_forward(const DeltaArgs& a, int KP, hipStream_t st);
+template <typename T>
+hipError_t launch_delta_states(const DeltaArgs& a, int KP, hipStream_t st);
+template <typename T>
+hipError_t launch_delta_grads(const DeltaArgs& a, int KP, int64_t slots, hipStream_t st);
 
 DeltaArgs delta_args(const tg_delta_args& a);
-// Waves that compute (16 columns each) in a serial kernel's workgroups.
-inline int delta_waves(int V) { return V > 16 ? 2 : 1; }
 
 }  // namespace tg
