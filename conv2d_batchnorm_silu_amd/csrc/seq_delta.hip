@@ -413,7 +413,7 @@ DeltaArgs delta_args(const tg_delta_args& a) {
 void delta_sizes(const tg_delta_args& a, size_t* work, size_t* saved, size_t* backward) {
     const int in = delta_in(a.dtype), C = delta_chunk_of(a);
     const int64_t chunks = delta_slots(a.seqs, C) * a.HV;
-    const size_t states = (size_t)chunks * ((size_t)a.K * a.V + (size_t)C * a.V) * 4;
+    const size_t states = (size_t)(chunks * kept_floats(a.V, delta_padded(a.K), C)) * 4;
     if (work) *work = (size_t)chunks * prep_bytes(C, kTrain + in);
     if (saved) *saved = states;
     if (backward)
@@ -445,7 +445,7 @@ hipError_t launch_delta_backward(const tg_delta_args& a, const tg_delta_grads& g
     DeltaArgs b = delta_args(a);
     const int C = delta_chunk_of(a);
     const int64_t slots = delta_slots(a.seqs, C), chunks = slots * a.HV;
-    const size_t states = (size_t)chunks * ((size_t)a.K * a.V + (size_t)C * a.V) * 4;
+    const size_t states = (size_t)(chunks * kept_floats(a.V, delta_padded(a.K), C)) * 4;
     b.saved = (float*)saved;
     b.prep = (char*)ws;
     b.back = (float*)(b.prep + up256((size_t)chunks * prep_bytes(C, 2 * kTrain)));
@@ -455,11 +455,10 @@ hipError_t launch_delta_backward(const tg_delta_args& a, const tg_delta_grads& g
     b.ddt = rows_of<void>(gr.ddt), b.dbeta = rows_of<void>(gr.dbeta);
     b.dfinal = gr.dfinal, b.dinitial = gr.dinitial;
     const size_t e = elem_bytes(a.dtype);
-    Widest dy, s;
+    Widest dy;
     dy.len(a.V), dy.len(gr.dy.row_stride), dy.ptr(gr.dy.p, e);
     if (!a.seqs.offsets) dy.len(gr.dy.seq_stride);
-    s.len(a.V), s.ptr(saved, 4), s.ptr(b.back, 4);
-    b.wide_dy = dy.width(8) == 8, b.wide_s = s.width(8) == 8;
+    b.wide_dy = dy.width(8) == 8;
     hipError_t err = a.dtype == TG_F32   ? backward_typed<float>(b, slots, st)
                      : a.dtype == TG_BF16 ? backward_typed<bf16>(b, slots, st)
                                           : backward_typed<f16>(b, slots, st);

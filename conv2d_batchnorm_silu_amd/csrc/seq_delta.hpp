@@ -300,6 +300,19 @@ constexpr bool frag_used(int C, int mt, int kt, bool upper) {
 }
 constexpr int prep_bytes(int C, int parts) { return kScales * C * 4 + frag_count(C) * 1024 * parts; }
 
+// What the passes keep for a chunk (`saved`: the state before it and its corrections;
+// `back`: the gradient of the state after it and of v): for each 16 columns of V the
+// accumulators of KP/16 and C/16 tiles as they are, four floats of a lane after the
+// other, so that a wave writes a kilobyte at a time (rows of V took 54 of 178 us of the
+// backward walk). In floats:
+inline __host__ __device__ int64_t kept_floats(int V, int KP, int C) {
+    return (int64_t)((V + 15) / 16) * (KP / 16 + C / 16) * 256;
+}
+// Tile `tile` (S's first) of 16 columns vt.
+__device__ __forceinline__ float4_t* kept_at(float* chunk, int KP, int C, int vt, int tile) {
+    return (float4_t*)(chunk + ((int64_t)vt * (KP / 16 + C / 16) + tile) * 256) + (threadIdx.x & 63);
+}
+
 struct DeltaArgs {
     SeqMap map;
     int HK, HV, K, V;
@@ -309,9 +322,9 @@ struct DeltaArgs {
     Rows<void> y;
     const float *A, *dt_bias, *initial;
     float* final;
-    bool wide_qk, wide_v, wide_y, wide_s;  // 16-byte rows of q and k, of v, of y (4 values), of saved states
+    bool wide_qk, wide_v, wide_y;  // rows of 16 bytes of q and k, of v, of 4 values of y
     char* prep;    // [slots][HV] of prep_bytes
-    float* saved;  // [slots][HV] of K*V + C*V, or null
+    float* saved;  // [slots][HV] of kept_floats(), or null
     // The backward pass.
     Rows<const void> dy;
     Rows<void> dq, dk, dv, ddt, dbeta;

@@ -23,38 +23,36 @@ namespace {
 
 template <typename T, int KP>
 struct BackShape {
-    static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 8, WL = 32 + 8, NT = C / 16;
+    static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 8, NT = C / 16;
+    static constexpr int slice = slice_of(NI, KP), cols = slice / 16, WL = slice + 8;
     static constexpr int rows = NI * C * LD * 2;
     static constexpr int stage = kScales * C * 4 + 2 * rows + NI * C * WL * 2;
-    // For 16 columns: sums of halves; b dU, R for dS.
-    static constexpr int sums = NT * 1024, share = sums + NT * 512 * 2 * kTrain;
-    static constexpr int stages = 2 * stage + 2 * share <= 160 * 1024 ? 2 : 1;
-    static constexpr int lds = stages * stage + 2 * share;
+    // For 16 columns: sums of halves and P^T w; b dU, R for dS; q's part of dS.
+    static constexpr int sums = NT * 1024, share = 2 * sums + NT * 512 * 2 * kTrain + KP / 16 * 1024;
+    static constexpr int stages = 2 * stage + cols * share <= 160 * 1024 ? 2 : 1;
+    static constexpr int lds = stages * stage + cols * share, carriers = cols * 2, threads = carriers * 128;
     static_assert(lds <= 160 * 1024, "more LDS than a compute unit has");
 };
 
 // The states' gradients, from the last chunk to the first, divided among the waves
-// like the forward pass.
-template <typename T, int KP, bool WIDE>
-__global__ __launch_bounds__(256, 1) void delta_backward(const DeltaArgs a) {
+// like the forward pass; the helpers form P^T w and q's part of dS0.
+template <typename T, int KP, bool WIDE, bool WIDE_V>
+__global__ __launch_bounds__(512, 1) void delta_backward(const DeltaArgs a) {
     using Sh = BackShape<T, KP>;
     constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, WL = Sh::WL, NT = Sh::NT, HT = NT / 2;
     constexpr int KH = KP / 2, KT = KH / 16, NK = KH / 32, CT = C / 32;
     extern __shared__ float4 lds[];
-    const int tid = threadIdx.x, w = tid >> 6, ct = w & 1, hf = w >> 1, l = tid & 63, g = l >> 4;
-    const int col = l & 15;
-    const HeadSlice at = head_slice((a.V + 32 - 1) / 32);
+    const int w = (threadIdx.x >> 6) % Sh::carriers, l = threadIdx.x & 63, g = l >> 4, col = l & 15;
+    const int ct = w % Sh::cols, hf = w / Sh::cols;
+    const bool helper = threadIdx.x >= Sh::carriers * 64;
+    const HeadSlice at = head_slice((a.V + Sh::slice - 1) / Sh::slice);
     if (at.pair >= a.map.seqs * a.HV) return;
     const int s = at.pair / a.HV, h = at.pair % a.HV, hk = h / (a.HV / a.HK);
     const int start = a.map.start(s), len = a.map.end(s) - start, slot0 = a.map.slot0(s, C);
-    const int chunks = (len + C - 1) / C, v0 = at.slice * 32;
-    const int v = v0 + ct * 16 + col, k0 = hf * KH;
-    const int64_t KV = (int64_t)a.K * a.V, held = ((int64_t)s * a.HV + h) * KV;
+    const int chunks = (len + C - 1) / C, v0 = at.slice * Sh::slice, k0 = hf * KH;
     char* share = (char*)lds + Sh::stages * Sh::stage + ct * Sh::share;
-    float* xsum = (float*)share;
-    const HalfFrags<kTrain> rx{(bf16*)(share + Sh::sums)}, wx{rx.p + NT * kTrain * 256};
-
-    const auto tile_at = [&](int i) { return i < HT ? (1 - hf) * HT + i : hf * HT + i - HT; };
+    float *xsum = (float*)share, *usum = (float*)(share + Sh::sums), *qsum = (float*)(share + 2 * Sh::sums);
+    const HalfFrags<kTrain> rx{(bf16*)(share + 2 * Sh::sums + KP / 16 * 1024)}, wx{rx.p + NT * kTrain * 256};
 
     // A stage: scales, k, q, the slice of dy.
     const auto stage = [&](int c) { return (char*)lds + (c % Sh::stages) * Sh::stage; };
@@ -65,49 +63,121 @@ __global__ __launch_bounds__(256, 1) void delta_backward(const DeltaArgs a) {
     const auto record = [&](int c) {
         return a.prep + ((int64_t)(slot0 + c) * a.HV + h) * prep_bytes(C, 2 * kTrain);
     };
-    Tile<T, C, KP, 256, WIDE> kt, qt;
-    Tile<T, C, 32, 256, WIDE> vt;
-    kt.shape(a.k.row, a.K);
-    qt.shape(a.q.row, a.K);
-    vt.shape(a.dy.row, imin(32, a.V - v0));
-    float4 st;
-    const auto fetch = [&](int c) {
-        c = c < 0 ? 0 : c;
-        const int lo = c * C, n = imin(C, len - lo);
-        kt.fetch(row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, n);
-        qt.fetch(row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, n);
-        vt.fetch(row_of<const T>(a.dy, a.map, s, start, lo) + (int64_t)h * a.V + v0, n);
-        st = ((const float4*)record(c))[tid % (kScales * C / 4)];
-    };
-    const auto put = [&](int c) {
-        if (c < 0) return;
-        if (tid < kScales * C / 4) ((float4*)stage(c))[tid] = st;
-        kt.put(planes(c, 0));
-        qt.put(planes(c, 1));
-        vt.put(planes(c, 2));
-    };
-    // The wave's rows of X^T and P^T: blocks of 32 columns from theirs on.
-    Frag<kTrain> xf[HT][CT], pf[HT][CT];
+    // Tiles hf * HT + i of X^T and P^T, blocks of 32 columns from theirs on.
+    Frag<kTrain> prep[HT][CT];
     const auto used = [&](int t) { return t == CT - 1 || hf == 0; };
-    const auto fetch_prepared = [&](Frag<kTrain> (&o)[HT][CT], int c, int which) {
-        const bf16* f =
-            (const bf16*)(record(c < 0 ? 0 : c) + kScales * C * 4) + which * frag_count(C) * 512 * kTrain;
+    const auto fetch_prepared = [&](int c, int which) {
+        const bf16* f = (const bf16*)(record(c < 0 ? 0 : c) + kScales * C * 4) +
+                        which * frag_count(C) * 512 * kTrain;
 #pragma unroll
         for (int i = 0; i < HT; ++i)
 #pragma unroll
             for (int t = 0; t < CT; ++t)
-                prepared(o[i][t], f, used(t) ? frag_index(C, hf * HT + i, t, true) : 0);
+                prepared(prep[i][t], f, used(t) ? frag_index(C, hf * HT + i, t, true) : 0);
     };
 
-    if (chunks > 0) {
-        fetch(chunks - 1);
-        fetch_prepared(xf, chunks - 1, 0);
-        fetch_prepared(pf, chunks - 1, 1);
+    if (helper) {
+        Tile<T, C, KP, Sh::carriers * 64, WIDE> kt, qt;
+        Tile<T, C, Sh::slice, Sh::carriers * 64, WIDE_V> vt;
+        kt.shape(a.k.row, a.K);
+        qt.shape(a.q.row, a.K);
+        vt.shape(a.dy.row, imin(Sh::slice, a.V - v0));
+        constexpr int SC = kScales * C / 4, SN = (SC + Sh::carriers * 64 - 1) / (Sh::carriers * 64);
+        float4 st[SN];
+        const auto fetch = [&](int c) {
+            c = c < 0 ? 0 : c;
+            const int lo = c * C, n = imin(C, len - lo);
+            kt.fetch(row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, n);
+            qt.fetch(row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, n);
+            vt.fetch(row_of<const T>(a.dy, a.map, s, start, lo) + (int64_t)h * a.V + v0, n);
+#pragma unroll
+            for (int i = 0; i < SN; ++i)
+                st[i] = ((const float4*)record(c))[(i * Sh::carriers * 64 + kt.tid()) % SC];
+        };
+        const auto put = [&](int c) {
+            if (c < 0) return;
+#pragma unroll
+            for (int i = 0; i < SN; ++i)
+                ((float4*)stage(c))[(i * Sh::carriers * 64 + kt.tid()) % SC] = st[i];
+            kt.put(planes(c, 0));
+            qt.put(planes(c, 1));
+            vt.put(planes(c, 2));
+        };
+        if (chunks > 0) {
+            fetch(chunks - 1);
+            fetch_prepared(chunks - 1, 1);
+            put(chunks - 1);
+            fetch(chunks - 2);
+        }
+        for (int c = chunks - 1; c >= 0; --c) {
+            lds_barrier();  // chunk c is there
+            const float* scal = (const float*)stage(c);
+            const Planes<NI> qp = planes(c, 1), wp = planes(c, 2);
+            Frag<NI> wf[CT];
+#pragma unroll
+            for (int t = 0; t < CT; ++t) wf[t] = wp.cols(t * 32, ct * 16);
+            float4_t u[HT] = {};  // P^T w
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+                if (used(t)) {
+                    Frag<kTrain> f[HT];
+#pragma unroll
+                    for (int i = 0; i < HT; ++i) f[i] = prep[i][t];
+                    mma_rows<kTrain>(u, f, wf[t], All());
+                }
+#pragma unroll
+            for (int i = 0; i < HT; ++i) *sum_at(usum, hf * HT + i) = u[i];
+            if (Sh::stages == 2) {
+                put(c - 1);
+                fetch(c - 2);
+            }
+            lds_barrier();
+            fetch_prepared(c - 1, 1);
+            // Half of the tiles on each side of a barrier that the others come to soon.
+            Frag<kTrain> qw[CT];
+#pragma unroll
+            for (int b = 0; b < CT; ++b) {
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    y[j] = 0.0f;
+#pragma unroll
+                    for (int q = NI - 1; q >= 0; --q) y[j] += (float)wf[b].p[q][j];
+                }
+                qw[b] =
+                    frag_of<kTrain>(float4_t{y[0], y[1], y[2], y[3]} * scales(scal, C, kReadQ, 2 * b),
+                                    float4_t{y[4], y[5], y[6], y[7]} * scales(scal, C, kReadQ, 2 * b + 1));
+            }
+            const auto tiles = [&](int first) {
+                float4_t D[KT / 2] = {};
+#pragma unroll
+                for (int b = 0; b < CT; ++b) {
+                    Frag<NI> f[KT / 2];
+#pragma unroll
+                    for (int t = 0; t < KT / 2; ++t) f[t] = qp.cols(b * 32, k0 + (first + t) * 16);
+                    mma_rows<kTrain>(D, f, qw[b], All());
+                }
+#pragma unroll
+                for (int t = 0; t < KT / 2; ++t) *sum_at(qsum, hf * KT + first + t) = D[t];
+            };
+            tiles(0);
+            lds_barrier();
+            tiles(KT / 2);
+            lds_barrier();
+            if (Sh::stages == 1) {
+                lds_barrier();  // chunk c has been read
+                put(c - 1);
+                fetch(c - 2);
+            }
+        }
+        return;
     }
-    // Where the wave's rows of dS and R are in `back`, its columns of dv.
-    const uint32_t at_s = (uint32_t)(k0 + 4 * g) * a.V + v, at_r = (uint32_t)(hf * HT * 16 + 4 * g) * a.V + v;
-    const uint32_t at_v = (uint32_t)(hf * HT * 16 + 4 * g) * (uint32_t)a.dv.row + ct * 16 + col;
-    const bool whole_k = a.K == KP;
+
+    __builtin_amdgcn_s_setprio(2);  // the helpers have time
+    const int v = v0 + ct * 16 + col;
+    const int64_t KV = (int64_t)a.K * a.V, held = ((int64_t)s * a.HV + h) * KV;
+    const auto tile_at = [&](int i) { return i < HT ? (1 - hf) * HT + i : hf * HT + i - HT; };
+    if (chunks > 0) fetch_prepared(chunks - 1, 0);
     float4_t S[KT];  // dS
 #pragma unroll
     for (int t = 0; t < KT; ++t)
@@ -116,24 +186,15 @@ __global__ __launch_bounds__(256, 1) void delta_backward(const DeltaArgs a) {
             const int k = k0 + t * 16 + 4 * g + r;
             S[t][r] = a.dfinal && k < a.K && v < a.V ? a.dfinal[held + (int64_t)k * a.V + v] : 0.0f;
         }
-    if (chunks > 0) {
-        put(chunks - 1);
-        fetch(chunks - 2);
-    }
     for (int c = chunks - 1; c >= 0; --c) {
         lds_barrier();  // chunk c is there
-        const int lo = c * C, n = imin(C, len - lo);
         const float* scal = (const float*)stage(c);
-        const Planes<NI> kp = planes(c, 0), qp = planes(c, 1), wp = planes(c, 2);
-        T* dvb = row_of<T>(a.dv, a.map, s, start, lo) + (int64_t)h * a.V + v0;
-        float* keep = a.back + ((int64_t)(slot0 + c) * a.HV + h) * (KV + (int64_t)C * a.V);
-        if (v < a.V)
+        const Planes<NI> kp = planes(c, 0);
+        float* keep = a.back + ((int64_t)(slot0 + c) * a.HV + h) * kept_floats(a.V, KP, C);
+        const int vt = v0 / 16 + ct;
+        if (vt * 16 < a.V)
 #pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (whole_k || k0 + t * 16 + 4 * g + r < a.K)
-                        (keep + (t * 16 + r) * a.V)[at_s] = S[t][r];
+            for (int t = 0; t < KT; ++t) *kept_at(keep, KP, C, vt, hf * KT + t) = S[t];
         // k dS over this half's rows: the other half's tokens, then its own.
         float4_t x[NT] = {};
 #pragma unroll
@@ -145,31 +206,14 @@ __global__ __launch_bounds__(256, 1) void delta_backward(const DeltaArgs a) {
             mma_rows<kTrain>(x, f, sf, All());
         }
 #pragma unroll
-        for (int i = 0; i < HT; ++i)  // to the other half: its tokens' sums
-            *sum_at(xsum, tile_at(i)) = x[i];
-        Frag<NI> wf[CT];
-#pragma unroll
-        for (int t = 0; t < CT; ++t) wf[t] = wp.cols(t * 32, ct * 16);
-        float4_t u[HT] = {}, R[HT] = {};  // P^T w
-#pragma unroll
-        for (int t = 0; t < CT; ++t)
-            if (used(t)) {
-                Frag<kTrain> f[HT];
-#pragma unroll
-                for (int i = 0; i < HT; ++i) f[i] = pf[i][t];
-                mma_rows<kTrain>(u, f, wf[t], All());
-            }
-        fetch_prepared(pf, c - 1, 1);
-        if (Sh::stages == 2) {
-            put(c - 1);
-            fetch(c - 2);
-        }
+        for (int i = 0; i < HT; ++i) *sum_at(xsum, tile_at(i)) = x[i];
         lds_barrier();
+        float4_t R[HT] = {};
 #pragma unroll
         for (int i = 0; i < HT; ++i) {
             const int mt = hf * HT + i;
             const float4_t z = x[HT + i] + *sum_at(xsum, mt);
-            rx.put(mt, (u[i] + z * scales(scal, C, kTailK, mt)) * scales(scal, C, kBeta, mt));
+            rx.put(mt, (*sum_at(usum, mt) + z * scales(scal, C, kTailK, mt)) * scales(scal, C, kBeta, mt));
         }
         lds_barrier();
 #pragma unroll
@@ -178,44 +222,17 @@ __global__ __launch_bounds__(256, 1) void delta_backward(const DeltaArgs a) {
                 const Frag<kTrain> bf = rx.frag(t);
                 Frag<kTrain> f[HT];
 #pragma unroll
-                for (int i = 0; i < HT; ++i) f[i] = xf[i][t];
+                for (int i = 0; i < HT; ++i) f[i] = prep[i][t];
                 mma_rows<kTrain>(R, f, bf, All());
             }
-        fetch_prepared(xf, c - 1, 0);
+        fetch_prepared(c - 1, 0);
 #pragma unroll
-        for (int i = 0; i < HT; ++i) {
-            const int mt = hf * HT + i;
-            wx.put(mt, -R[i] * scales(scal, C, kReadK, mt));
-            if (v < a.V)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    (keep + KV + (i * 16 + r) * a.V)[at_r] = R[i][r];
-                    if (n == C || mt * 16 + 4 * g + r < n)
-                        (dvb + (int64_t)(i * 16 + r) * a.dv.row)[at_v] = (T)R[i][r];
-                }
-        }
+        for (int i = 0; i < HT; ++i)
+            wx.put(hf * HT + i, -R[i] * scales(scal, C, kReadK, hf * HT + i));
         const float total = scal[kDecay * C + C - 1];
-#pragma unroll
-        for (int t = 0; t < KT; ++t) S[t] *= total;
-        // q's part of dS0 needs no other wave.
-#pragma unroll
-        for (int b = 0; b < CT; ++b) {
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                y[j] = 0.0f;
-#pragma unroll
-                for (int q = NI - 1; q >= 0; --q) y[j] += (float)wf[b].p[q][j];
-            }
-            const Frag<kTrain> qw =
-                frag_of<kTrain>(float4_t{y[0], y[1], y[2], y[3]} * scales(scal, C, kReadQ, 2 * b),
-                                float4_t{y[4], y[5], y[6], y[7]} * scales(scal, C, kReadQ, 2 * b + 1));
-            Frag<NI> f[KT];
-#pragma unroll
-            for (int t = 0; t < KT; ++t) f[t] = qp.cols(b * 32, k0 + t * 16);
-            mma_rows<kTrain>(S, f, qw, All());
-        }
         lds_barrier();
+#pragma unroll
+        for (int t = 0; t < KT; ++t) S[t] = S[t] * total + *sum_at(qsum, hf * KT + t);
 #pragma unroll
         for (int b = 0; b < CT; ++b) {
             const Frag<kTrain> kr = wx.frag(b);
@@ -224,11 +241,10 @@ __global__ __launch_bounds__(256, 1) void delta_backward(const DeltaArgs a) {
             for (int t = 0; t < KT; ++t) f[t] = kp.cols(b * 32, k0 + t * 16);
             mma_rows<kTrain>(S, f, kr, All());
         }
-        if (Sh::stages == 1) {
-            lds_barrier();
-            put(c - 1);
-            fetch(c - 2);
-        }
+        if (vt * 16 < a.V)
+#pragma unroll
+            for (int i = 0; i < HT; ++i) *kept_at(keep, KP, C, vt, KP / 16 + hf * HT + i) = R[i];
+        if (Sh::stages == 1) lds_barrier();
     }
     if (a.dinitial && v < a.V)
 #pragma unroll
@@ -242,12 +258,14 @@ __global__ __launch_bounds__(256, 1) void delta_backward(const DeltaArgs a) {
 
 template <typename T, int KP>
 hipError_t states_at(const DeltaArgs& a, hipStream_t st) {
-    constexpr int lds = BackShape<T, KP>::lds;
-    const auto kernel = a.wide_qk && a.wide_dy ? delta_backward<T, KP, true> : delta_backward<T, KP, false>;
-    const hipError_t e = ensure_dynamic_lds((const void*)kernel, lds);
+    using Sh = BackShape<T, KP>;
+    const auto kernel = !a.wide_qk   ? delta_backward<T, KP, false, false>
+                        : a.wide_dy ? delta_backward<T, KP, true, true>
+                                    : delta_backward<T, KP, true, false>;
+    const hipError_t e = ensure_dynamic_lds((const void*)kernel, Sh::lds);
     if (e != hipSuccess) return e;
-    const int64_t grid = head_slice_grid((int64_t)a.map.seqs * a.HV, (int)ceil_div(a.V, 32));
-    kernel<<<(unsigned)grid, 256, lds, st>>>(a);
+    const int64_t grid = head_slice_grid((int64_t)a.map.seqs * a.HV, (int)ceil_div(a.V, Sh::slice));
+    kernel<<<(unsigned)grid, Sh::threads, Sh::lds, st>>>(a);
     return hipGetLastError();
 }
 

@@ -40,7 +40,7 @@ struct FwdShape {
     static_assert(lds <= 160 * 1024, "more LDS than a compute unit has");
 };
 
-template <typename T, int KP, int NM, bool WIDE>
+template <typename T, int KP, int NM, bool WIDE, bool WIDE_V>
 __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
     using Sh = FwdShape<T, KP, NM>;
     constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, VL = Sh::VL, NT = Sh::NT, HT = NT / 2;
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
         const int vy = v0 + ct * 16 + 4 * g;
         const uint32_t at_y = (uint32_t)(hf * HT * 16 + col) * (uint32_t)a.y.row + ct * 16 + 4 * g;
         Tile<T, C, KP, Sh::carriers * 64, WIDE> kt, qt;
-        Tile<T, C, Sh::slice, Sh::carriers * 64, WIDE> vt;
+        Tile<T, C, Sh::slice, Sh::carriers * 64, WIDE_V> vt;
         kt.shape(a.k.row, a.K);
         qt.shape(a.q.row, a.K);
         vt.shape(a.v.row, imin(Sh::slice, a.V - v0));
@@ -127,18 +127,23 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
             const Planes<NI> qp = planes(c, 1);
             lds_barrier();  // so is S0 for y
             // y transposed, so that a lane holds four neighbouring columns of a token.
+            // Half of it on each side of a barrier that the others come to soon.
             float4_t ys[HT] = {};
+            const auto blocks = [&](int first) {
 #pragma unroll
-            for (int t = 0; t < KP / 32; ++t) {
-                Frag<NI> sf, f[HT];
-                prepared(sf, sx, t);
+                for (int t = 0; t < KP / 64; ++t) {
+                    Frag<NI> sf, f[HT];
+                    prepared(sf, sx, first + t);
 #pragma unroll
-                for (int i = 0; i < HT; ++i) f[i] = qp.rows((hf * HT + i) * 16, t * 32);
-                mma_cols<NI>(ys, sf, f, All());
-            }
+                    for (int i = 0; i < HT; ++i) f[i] = qp.rows((hf * HT + i) * 16, (first + t) * 32);
+                    mma_cols<NI>(ys, sf, f, All());
+                }
+            };
+            blocks(0);
+            lds_barrier();
+            blocks(KP / 64);
 #pragma unroll
             for (int i = 0; i < HT; ++i) ys[i] *= scal[kReadQ * C + (hf * HT + i) * 16 + col];
-            lds_barrier();
             lds_barrier();  // the corrections are there
 #pragma unroll
             for (int t = 0; t < CT; ++t)
@@ -187,9 +192,6 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
                 prepared(xf[i][t], f, used(t) ? frag_index(C, hf * HT + i, t, false) : 0);
     };
     if (chunks > 0) fetch_x(0);
-    // Where the wave's rows of S and E are in `saved`.
-    const uint32_t at_s = (uint32_t)(k0 + 4 * g) * a.V + v, at_e = (uint32_t)(hf * HT * 16 + 4 * g) * a.V + v;
-    const bool whole_k = a.K == KP;
     float4_t S[KT];
 #pragma unroll
     for (int t = 0; t < KT; ++t)
@@ -247,17 +249,14 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
         }
         lds_barrier();
         if (a.saved) {
-            float* keep = a.saved + ((int64_t)(slot0 + c) * a.HV + h) * (KV + (int64_t)C * a.V);
-            if (v < a.V)
+            float* keep = a.saved + ((int64_t)(slot0 + c) * a.HV + h) * kept_floats(a.V, KP, C);
+            const int vt = v0 / 16 + ct;
+            if (vt * 16 < a.V) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
+                for (int t = 0; t < KT; ++t) *kept_at(keep, KP, C, vt, hf * KT + t) = S[t];
 #pragma unroll
-                    for (int t = 0; t < KT; ++t)
-                        if (whole_k || k0 + t * 16 + 4 * g + r < a.K)
-                            (keep + (t * 16 + r) * a.V)[at_s] = S[t][r];
-#pragma unroll
-                    for (int i = 0; i < HT; ++i) (keep + KV + (i * 16 + r) * a.V)[at_e] = e[i][r];
-                }
+                for (int i = 0; i < HT; ++i) *kept_at(keep, KP, C, vt, KP / 16 + hf * HT + i) = e[i];
+            }
         }
         const float total = scal[kDecay * C + C - 1];
 #pragma unroll
@@ -285,8 +284,9 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
 template <typename T, int KP, int NM>
 hipError_t forward_at(const DeltaArgs& a, hipStream_t st) {
     using Sh = FwdShape<T, KP, NM>;
-    const auto kernel = a.wide_qk && a.wide_v ? delta_forward<T, KP, NM, true>
-                                              : delta_forward<T, KP, NM, false>;
+    const auto kernel = !a.wide_qk  ? delta_forward<T, KP, NM, false, false>
+                        : a.wide_v ? delta_forward<T, KP, NM, true, true>
+                                   : delta_forward<T, KP, NM, true, false>;
     const hipError_t e = ensure_dynamic_lds((const void*)kernel, Sh::lds);
     if (e != hipSuccess) return e;
     const int64_t grid = head_slice_grid((int64_t)a.map.seqs * a.HV, (int)ceil_div(a.V, Sh::slice));

@@ -17,8 +17,9 @@ struct GradShape {
     static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 8, NT = C / 16;
     static constexpr int waves = KP == 256 ? 8 : 4;  // 256 registers for each, with all of dq and dk
     static constexpr int parts = waves / NT, KB = NI == 1 && KP == 128 ? 128 : 64, KW = KB / parts, NB = KP / KB;
-    static constexpr int VB = 32, VL = VB + 8, ML = C + 8;
-    static constexpr int wide = (NI + 2 * kTrain) * C * VL * 2 + 2 * kTrain * KB * VL * 2;  // a block of V
+    static constexpr int VB = 32, VL = VB + 8, ML = C + 8, CL = C + 8, KL = KB + 8;
+    // A block of V: dy as rows of tokens; E, R, S0 and dS as rows of V.
+    static constexpr int wide = NI * C * VL * 2 + 2 * kTrain * VB * (CL + KL) * 2;
     static constexpr int square = 2 * NI * C * ML * 2;                                  // C x C
     static constexpr int scratch = wide > square ? wide : square;
     static constexpr int floats = 8 * C + NT * C + 2 * parts * C + 2 * waves * 16 + 16;
@@ -30,7 +31,7 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
     using Sh = GradShape<T, KP>;
     constexpr int kThreads = 64 * Sh::waves;
     constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, NT = Sh::NT, NB = Sh::NB, KB = Sh::KB;
-    constexpr int KW = Sh::KW, WT = KW / 16, VB = Sh::VB, VL = Sh::VL, ML = Sh::ML;
+    constexpr int KW = Sh::KW, WT = KW / 16, VB = Sh::VB, VL = Sh::VL, ML = Sh::ML, CL = Sh::CL, KL = Sh::KL;
     extern __shared__ float4 lds[];
     double* G = (double*)lds;
     float* gb = (float*)(G + C);     // b
@@ -48,8 +49,8 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
     const Planes<NI> qp{kp.p + NI * C * LD, LD, C * LD};
     bf16* scratch = qp.p + NI * C * LD;
     const Planes<NI> wp{scratch, VL, C * VL};
-    const Planes<kTrain> ep{wp.p + NI * C * VL, VL, C * VL}, rp{ep.p + kTrain * C * VL, VL, C * VL};
-    const Planes<kTrain> sp{rp.p + kTrain * C * VL, VL, KB * VL}, dp{sp.p + kTrain * KB * VL, VL, KB * VL};
+    const Planes<kTrain> ep{wp.p + NI * C * VL, CL, VB * CL}, rp{ep.p + kTrain * VB * CL, CL, VB * CL};
+    const Planes<kTrain> sp{rp.p + kTrain * VB * CL, KL, VB * KL}, dp{sp.p + kTrain * VB * KL, KL, VB * KL};
     const Planes<NI> bm{scratch, ML, C * ML}, mm{bm.p + NI * C * ML, ML, C * ML};
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g = l >> 4, col = l & 15;
     const int tile = w % NT, part = w / NT, row0 = tile * 16;
@@ -75,9 +76,9 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
 
     float4_t dq[NB][WT] = {}, dk[NB][WT] = {};
     for (int h = hk * rep; h < (hk + 1) * rep; ++h) {
-        const int64_t KV = (int64_t)a.K * a.V;
-        const int64_t chunk = (int64_t)slot * a.HV + h, size = KV + (int64_t)C * a.V;
-        const float *S0 = a.saved + chunk * size, *E = S0 + KV, *dS = a.back + chunk * size, *R = dS + KV;
+        const int64_t chunk = (int64_t)slot * a.HV + h, size = kept_floats(a.V, KP, C);
+        float *S0 = a.saved + chunk * size, *dS = a.back + chunk * size;
+        T* dv = row_of<T>(a.dv, a.map, s, start, lo) + (int64_t)h * a.V;
         const T* dy = row_of<const T>(a.dy, a.map, s, start, lo) + (int64_t)h * a.V;
         lds_barrier();
         if (w == 0) {
@@ -108,46 +109,85 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
             for (int vb = 0; vb < a.V; vb += VB) {
                 lds_barrier();
                 Tile<T, C, VB, kThreads, WIDE> tw;
-                Tile<float, C, VB, kThreads, WIDE> te, tr;
-                Tile<float, KB, VB, kThreads, WIDE> ts, td;
-                const int m = imin(VB, a.V - vb);
-                tw.shape(a.dy.row, m);
-                te.shape(a.V, m), tr.shape(a.V, m), ts.shape(a.V, m), td.shape(a.V, m);
-                const int64_t block = (int64_t)imin(kb, a.K - 1) * a.V + vb;
+                tw.shape(a.dy.row, imin(VB, a.V - vb));
                 tw.fetch(dy + vb, n);
-                te.fetch(E + vb, C);
-                tr.fetch(R + vb, C);
-                ts.fetch(S0 + block, a.K - kb);
-                td.fetch(dS + block, a.K - kb);
+                // Tiles of a wave's lanes: each lane four rows of one column of V.
+                constexpr int EN = NT * 2 * 64 / kThreads, SN = KB / 16 * 2 * 64 / kThreads;
+                constexpr int EC = EN ? EN : 1, SC = SN ? SN : 1;
+                float4_t er[EC], rr[EC], sr[SC], dr[SC];
+                const auto of = [&](float* kept, int i, int tiles, int first) {
+                    const int q = (i * kThreads + tid) >> 6, vt = vb / 16 + q / tiles;
+                    const float4_t* at =
+                        kept_at(kept, KP, C, imin(vt, (a.V - 1) / 16), first + q % tiles);
+                    return vt * 16 < a.V ? *at : float4_t{0, 0, 0, 0};
+                };
+                const auto there = [&](int i, int tiles) { return i * kThreads + tid < tiles * 128; };
+#pragma unroll
+                for (int i = 0; i < EC; ++i)
+                    if (EN || there(i, NT)) {
+                        er[i] = of(S0, i, NT, KP / 16);
+                        rr[i] = of(dS, i, NT, KP / 16);
+                    }
+#pragma unroll
+                for (int i = 0; i < SC; ++i)
+                    if (SN || there(i, KB / 16)) {
+                        sr[i] = of(S0, i, KB / 16, kb / 16);
+                        dr[i] = of(dS, i, KB / 16, kb / 16);
+                    }
                 tw.put(wp);
-                te.put(ep);
-                tr.put(rp);
-                ts.put(sp);
-                td.put(dp);
+                const auto give = [&](const Planes<kTrain>& d, const float4_t& x, int i, int tiles) {
+                    const int q = (i * kThreads + tid) >> 6;
+                    bf16* at = d.p + (q / tiles * 16 + col) * d.ld + q % tiles * 16 + 4 * g;
+                    bf16x4_t o[kTrain];
 #pragma unroll
-                for (int i = 0; i < ts.COUNT; ++i)
-                    if (ts.inside(i)) {
-                        const auto x = ts.value(i), y = td.value(i);
+                    for (int j = 0; j < 4; ++j) {
+                        bf16 b[kTrain];
+                        split<kTrain>(x[j], b);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) whole = __builtin_fmaf(x[j], y[j], whole);
+                        for (int m = 0; m < kTrain; ++m) o[m][j] = b[m];
+                    }
+#pragma unroll
+                    for (int m = 0; m < kTrain; ++m) *(bf16x4_t*)(at + m * d.plane) = o[m];
+                };
+#pragma unroll
+                for (int i = 0; i < EC; ++i)
+                    if (EN || there(i, NT)) {
+                        give(ep, er[i], i, NT);
+                        give(rp, rr[i], i, NT);
+                        if (nb == 0) {  // R is the gradient of v
+                            const int q = (i * kThreads + tid) >> 6, v = vb + q / NT * 16 + col;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const int t = q % NT * 16 + 4 * g + r;
+                                if (t < n && v < a.V) dv[t * a.dv.row + v] = (T)rr[i][r];
+                            }
+                        }
+                    }
+#pragma unroll
+                for (int i = 0; i < SC; ++i)
+                    if (SN || there(i, KB / 16)) {
+                        give(sp, sr[i], i, KB / 16);
+                        give(dp, dr[i], i, KB / 16);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) whole = __builtin_fmaf(sr[i][j], dr[i][j], whole);
                     }
                 lds_barrier();
                 const Frag<NI> wf = wp.rows(row0, 0);
-                const Frag<kTrain> rf = rp.rows(row0, 0), ef = ep.rows(row0, 0);
+                const Frag<kTrain> rf = rp.cols(0, row0), ef = ep.cols(0, row0);
                 if (nb == 0)
 #pragma unroll
                     for (int jt = 0; jt < NT; ++jt)
                         if (jt <= tile) {
-                            const Frag<kTrain> o = ep.rows(jt * 16, 0);
+                            const Frag<kTrain> o = ep.cols(0, jt * 16);
                             mma<kTrain>(F[jt], wf, o);
                             mma<kTrain>(H[jt], rf, o);
                         }
 #pragma unroll
                 for (int t = 0; t < WT; ++t) {
-                    const Frag<kTrain> x = sp.rows(part * KW + t * 16, 0);
+                    const Frag<kTrain> x = sp.cols(0, part * KW + t * 16);
                     mma<kTrain>(qs[t], wf, x);
                     mma<kTrain>(rs[t], rf, x);
-                    mma<kTrain>(es[t], ef, dp.rows(part * KW + t * 16, 0));
+                    mma<kTrain>(es[t], ef, dp.cols(0, part * KW + t * 16));
                 }
             }
             // Rows' factors, and the rows' products with q and k.
@@ -338,7 +378,7 @@ template <typename T, int KP>
 hipError_t grads_at(const DeltaArgs& a, int64_t slots, hipStream_t st) {
     using Sh = GradShape<T, KP>;
     static_assert(Sh::lds <= 160 * 1024, "more LDS than a compute unit has");
-    const auto kernel = a.wide_qk && a.wide_dy && a.wide_s ? delta_grads<T, KP, true>
+    const auto kernel = a.wide_qk && a.wide_dy ? delta_grads<T, KP, true>
                                                            : delta_grads<T, KP, false>;
     const hipError_t e = ensure_dynamic_lds((const void*)kernel, Sh::lds);
     if (e != hipSuccess) return e;
