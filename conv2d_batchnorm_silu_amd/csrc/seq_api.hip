@@ -14,7 +14,8 @@ constexpr int64_t kMaxRows = (int64_t)1 << 30;
 constexpr int kMaxChannels = 1 << 20;
 constexpr int64_t kMaxGroups = ((int64_t)1 << 26) - 1;
 constexpr int64_t kMaxStepGroups = ((int64_t)1 << 24) - 1;
-// The scan addresses 16 rows by 31-bit byte offsets.
+// The scan addresses 16 rows by 31-bit byte offsets, the delta rule 64 by 32-bit element
+// offsets.
 constexpr int64_t kMaxScanStride = (int64_t)1 << 25;
 
 bool dtype_ok(int d) { return d == TG_F16 || d == TG_BF16 || d == TG_F32; }
@@ -122,11 +123,11 @@ tg_status check_delta_inputs(const tg_delta_args* a) {
     TG_REQUIRE(a->A, TG_ERR_INVALID_ARGUMENT);
     TG_REQUIRE(aligned(a->A, 4) && aligned(a->dt_bias, 4) && aligned(a->initial, 4) &&
                    aligned(a->final, 4), TG_ERR_ALIGNMENT);
-    TG_CHECK(check_rows(a->q, a->seqs, kw, e, false));
-    TG_CHECK(check_rows(a->k, a->seqs, kw, e, false));
-    TG_CHECK(check_rows(a->v, a->seqs, vw, e, false));
-    TG_CHECK(check_rows(a->dt, a->seqs, a->HV, e, false));
-    TG_CHECK(check_rows(a->beta, a->seqs, a->HV, e, false));
+    TG_CHECK(check_scan_rows(a->q, a->seqs, kw, e, false));
+    TG_CHECK(check_scan_rows(a->k, a->seqs, kw, e, false));
+    TG_CHECK(check_scan_rows(a->v, a->seqs, vw, e, false));
+    TG_CHECK(check_scan_rows(a->dt, a->seqs, a->HV, e, false));
+    TG_CHECK(check_scan_rows(a->beta, a->seqs, a->HV, e, false));
     return TG_OK;
 }
 
@@ -337,7 +338,7 @@ tg_status tg_gated_delta_rule(const tg_delta_args* a, void* workspace, size_t wo
     TG_CHECK(check_delta(a));
     TG_CHECK(check_delta_groups(a));
     TG_CHECK(check_delta_inputs(a));
-    TG_CHECK(check_rows(a->y, a->seqs, (int64_t)a->HV * a->V, elem_bytes(a->dtype), true));
+    TG_CHECK(check_scan_rows(a->y, a->seqs, (int64_t)a->HV * a->V, elem_bytes(a->dtype), true));
     size_t work = 0, keep = 0;
     delta_sizes(*a, &work, &keep, nullptr);
     TG_REQUIRE(aligned(workspace, 16) && aligned(saved, 16), TG_ERR_ALIGNMENT);
@@ -355,12 +356,12 @@ tg_status tg_gated_delta_rule_backward(const tg_delta_args* a, const tg_delta_gr
     TG_REQUIRE(g && g->dA, TG_ERR_INVALID_ARGUMENT);
     const size_t e = elem_bytes(a->dtype);
     const int64_t kw = (int64_t)a->HK * a->K, vw = (int64_t)a->HV * a->V;
-    TG_CHECK(check_rows(g->dy, a->seqs, vw, e, false));
-    TG_CHECK(check_rows(g->dq, a->seqs, kw, e, true));
-    TG_CHECK(check_rows(g->dk, a->seqs, kw, e, true));
-    TG_CHECK(check_rows(g->dv, a->seqs, vw, e, true));
-    TG_CHECK(check_rows(g->ddt, a->seqs, a->HV, e, true));
-    TG_CHECK(check_rows(g->dbeta, a->seqs, a->HV, e, true));
+    TG_CHECK(check_scan_rows(g->dy, a->seqs, vw, e, false));
+    TG_CHECK(check_scan_rows(g->dq, a->seqs, kw, e, true));
+    TG_CHECK(check_scan_rows(g->dk, a->seqs, kw, e, true));
+    TG_CHECK(check_scan_rows(g->dv, a->seqs, vw, e, true));
+    TG_CHECK(check_scan_rows(g->ddt, a->seqs, a->HV, e, true));
+    TG_CHECK(check_scan_rows(g->dbeta, a->seqs, a->HV, e, true));
     TG_REQUIRE(aligned(g->dA, 4) && aligned(g->ddt_bias, 4) && aligned(g->dfinal, 4) &&
                    aligned(g->dinitial, 4) && aligned(saved, 16) && aligned(workspace, 16),
                TG_ERR_ALIGNMENT);
@@ -382,7 +383,7 @@ tg_status tg_gated_delta_rule_step(const tg_delta_args* a, float* state, int64_t
     tg_delta_args b = *a;
     for (tg_rows* r : {&b.q, &b.k, &b.v, &b.dt, &b.beta, &b.y}) r->seq_stride = r->row_stride;
     TG_CHECK(check_delta_inputs(&b));
-    TG_CHECK(check_rows(b.y, b.seqs, (int64_t)b.HV * b.V, elem_bytes(b.dtype), true));
+    TG_CHECK(check_scan_rows(b.y, b.seqs, (int64_t)b.HV * b.V, elem_bytes(b.dtype), true));
     TG_REQUIRE((slots || a->seqs.seqs <= num_slots) && (state || num_slots == 0),
                TG_ERR_INVALID_ARGUMENT);
     TG_REQUIRE(num_slots < kMaxRows, TG_ERR_UNSUPPORTED);

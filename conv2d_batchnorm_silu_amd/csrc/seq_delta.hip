@@ -421,9 +421,12 @@ void delta_sizes(const tg_delta_args& a, size_t* work, size_t* saved, size_t* ba
                     (size_t)chunks * 2 * sizeof(float);
 }
 
+// In workgroups of 256 threads.
 int64_t delta_groups(const tg_delta_args& a) {
-    const int64_t chunks = delta_slots(a.seqs, delta_chunk_of(a)) * a.HV;
-    const int64_t serial = head_slice_grid(a.seqs.seqs * a.HV, (int)ceil_div(a.V, slice_of(delta_in(a.dtype), delta_padded(a.K))));
+    const int KP = delta_padded(a.K);
+    const int64_t chunks = delta_slots(a.seqs, delta_chunk_of(a)) * a.HV * (KP == 256 ? 2 : 1);
+    const int64_t serial =
+        2 * head_slice_grid(a.seqs.seqs * a.HV, (int)ceil_div(a.V, slice_of(delta_in(a.dtype), KP)));
     return chunks > serial ? chunks : serial;
 }
 

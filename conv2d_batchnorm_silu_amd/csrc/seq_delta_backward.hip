@@ -11,6 +11,7 @@
 //          M = b D H, strictly lower
 //     db[j] = Z[j] + sum_i T[i,j],        T = (D scale q k^T) F + (D k k^T) H
 //     dG[i] = sum_j T[i,j] b[j] - b[i] db[i] + e^G[i] (scale q[i].(w S0^T)[i] - k[i].(R S0^T)[i])
+//             (without T[i,i] in either sum)
 //     dG[C-1] += e^(G[C-1]) <dS, S0> + sum_j b[j] Z[j]
 // and a token's decay logarithm gets the sum of dG from it to the chunk's end:
 // the pairs of tokens on either side of it, nothing that cancels but T's own

@@ -22,7 +22,7 @@ struct GradShape {
     static constexpr int wide = NI * C * VL * 2 + 2 * kTrain * VB * (CL + KL) * 2;
     static constexpr int square = 2 * NI * C * ML * 2;                                  // C x C
     static constexpr int scratch = wide > square ? wide : square;
-    static constexpr int floats = 8 * C + NT * C + 2 * parts * C + 2 * waves * 16 + 16;
+    static constexpr int floats = 9 * C + NT * C + 2 * parts * C + 2 * waves * 16 + 16;
     static constexpr int lds = C * 8 + floats * 4 + 2 * NI * C * LD * 2 + scratch;
 };
 
@@ -41,7 +41,8 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
     float* gd = gs + C;              // step sizes
     float* rk = gd + C;
     float* rq = rk + C;
-    float* colsum = rq + C;          // [NT][C]: column sums of T by row tile
+    float* own = rq + C;             // T's diagonal
+    float* colsum = own + C;         // [NT][C]: column sums of T by row tile
     float* dots = colsum + NT * C;   // [2][parts][C]: rows' sums by part: the S0 terms and T, Z
     float* inner = dots + 2 * Sh::parts * C;   // [2][waves][16]: dq.q and dk.k of a tile's rows
     float* red = inner + 2 * Sh::waves * 16;   // <dS, S0> by wave
@@ -237,8 +238,14 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
                     f = F[jt][r] * D * a.scale * rq[i];
                     m = j < i ? -H[jt][r] * D * rk[i] : 0.0f;
                     const float t = f * qk[jt][r] + m * kk[jt][r];
-                    sum += t;
-                    rowt[r] = __builtin_fmaf(t, b, rowt[r]);
+                    // A token's own term has no decay: its place in the row's and the
+                    // column's sum would cancel, but for its rounding.
+                    if (j < i) {
+                        sum += t;
+                        rowt[r] = __builtin_fmaf(t, b, rowt[r]);
+                    } else if (part == 0) {
+                        own[i] = t;
+                    }
                 }
                 if (part == 0) {
                     bm.put(i, j, f * b);
@@ -268,10 +275,11 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
 #pragma unroll
                 for (int p = 0; p < Sh::parts; ++p)
                     u += dots[p * C + l], z += dots[(Sh::parts + p) * C + l];
-                db = z;
+                float after = z;
 #pragma unroll
-                for (int t = 0; t < NT; ++t) db += colsum[t * C + l];
-                dg = u - gb[l] * db;
+                for (int t = 0; t < NT; ++t) after += colsum[t * C + l];
+                db = after + own[l];
+                dg = u - gb[l] * after;
                 bz = gb[l] * z;
             }
             bz = wave_sum(bz);

@@ -210,9 +210,10 @@ tg_status tg_selective_scan_step(const tg_scan_args *a, float *state, int64_t nu
  * tokens in a row is within fp32. With 16-bit tensors, states
  * and what lies between enter the products with 17 bits (off by 2^-18), those that
  * only reach bf16 results with 8; with fp32 tensors all keep 24. A NaN or infinite value of a token may reach all tokens from its
- * sequence's 64 (counted from its first; 32 for fp16 and fp32 with K > 128) on.
- * TG_ERR_UNSUPPORTED for K > 256 and for 2^24 or more pairs of a value head and 64
- * (32) tokens, or of a sequence, a value head and 16 columns. */
+ * sequence's 64 (counted from its first; 32 for fp16, fp32 and K > 128) on.
+ * TG_ERR_UNSUPPORTED for K > 256, row strides of 2^25 elements or more, 2^23 or more
+ * pairs of a value head and 64 (32) tokens, and 2^22 or more of a sequence, a value
+ * head and 16 columns. */
 typedef struct {
     tg_seqs seqs;
     int HK, HV, K, V;
