@@ -351,17 +351,38 @@ hipError_t step_typed(const DeltaStep& p, bool v4, unsigned n, hipStream_t st) {
     return hipGetLastError();
 }
 
+// The maps of all segments, the states between them, and the walk from those.
+template <typename Walk>
+hipError_t in_segments(const DeltaArgs& a, const float* first, bool reverse, float* states, int KP,
+                       int slice, hipStream_t st, Walk walk) {
+    DeltaArgs b = a;
+    b.through = true;
+    hipError_t e = walk(b);
+    if (e == hipSuccess) e = launch_delta_join(a, first, reverse, states, KP, slice, st);
+    if (e != hipSuccess) return e;
+    b.through = false;
+    (reverse ? b.dfinal : b.initial) = states;
+    return walk(b);
+}
+
 template <typename T, int NM>
-hipError_t forward_typed(const DeltaArgs& a, int64_t slots, hipStream_t st) {
+hipError_t forward_typed(const DeltaArgs& a, int64_t slots, float* states, hipStream_t st) {
     const int KP = delta_padded(a.K);
     const hipError_t e = launch_delta_prep<T, NM, false>(a, KP, slots, st);
-    return e == hipSuccess ? launch_delta_forward<T, NM>(a, KP, st) : e;
+    if (e != hipSuccess || !a.segment) return e == hipSuccess ? launch_delta_forward<T, NM>(a, KP, st) : e;
+    return in_segments(a, a.initial, false, states, KP, slice_of(kIn<T>, KP), st, [&](const DeltaArgs& b) {
+        return launch_delta_forward<T, NM>(b, KP, st);
+    });
 }
 template <typename T>
-hipError_t backward_typed(const DeltaArgs& a, int64_t slots, hipStream_t st) {
+hipError_t backward_typed(const DeltaArgs& a, int64_t slots, float* states, hipStream_t st) {
     const int KP = delta_padded(a.K);
     hipError_t e = launch_delta_prep<T, kTrain, true>(a, KP, slots, st);
-    if (e == hipSuccess) e = launch_delta_states<T>(a, KP, st);
+    if (e != hipSuccess) return e;
+    if (a.segment)
+        e = in_segments(a, a.dfinal, true, states, KP, slice_of(kIn<T>, KP), st,
+                        [&](const DeltaArgs& b) { return launch_delta_states<T>(b, KP, st); });
+    else e = launch_delta_states<T>(a, KP, st);
     return e == hipSuccess ? launch_delta_grads<T>(a, KP, slots, st) : e;
 }
 
@@ -410,49 +431,81 @@ DeltaArgs delta_args(const tg_delta_args& a) {
     return b;
 }
 
-void delta_sizes(const tg_delta_args& a, size_t* work, size_t* saved, size_t* backward) {
-    const int in = delta_in(a.dtype), C = delta_chunk_of(a);
-    const int64_t chunks = delta_slots(a.seqs, C) * a.HV;
-    const size_t states = (size_t)(chunks * kept_floats(a.V, delta_padded(a.K), C)) * 4;
-    if (work) *work = (size_t)chunks * prep_bytes(C, kTrain + in);
-    if (saved) *saved = states;
-    if (backward)
-        *backward = up256((size_t)chunks * prep_bytes(C, 2 * kTrain)) + up256(states) +
-                    (size_t)chunks * 2 * sizeof(float);
+namespace {
+
+// What a pass keeps for the segments: their maps and the states between them.
+struct SegmentRoom {
+    int segment;
+    int64_t units;
+    size_t maps, states;
+    explicit SegmentRoom(const tg_delta_args& a) {
+        const int in = delta_in(a.dtype), KP = delta_padded(a.K);
+        segment = delta_segment(a);
+        units = segment ? delta_slots(a.seqs, segment) : a.seqs.seqs;
+        maps = segment ? up256((size_t)(units * a.HV * KP * map_columns(a.V, KP, slice_of(in, KP))) * 4) : 0;
+        states = segment ? up256((size_t)(units * a.HV * a.K * a.V) * 4) : 0;
+    }
+};
+size_t kept_bytes(const tg_delta_args& a) {
+    const int C = delta_chunk_of(a);
+    return (size_t)(delta_slots(a.seqs, C) * a.HV * kept_floats(a.V, delta_padded(a.K), C)) * 4;
 }
+size_t prep_room(const tg_delta_args& a, int parts) {
+    const int C = delta_chunk_of(a);
+    return up256((size_t)(delta_slots(a.seqs, C) * a.HV) * prep_bytes(C, parts));
+}
+
+}  // namespace
 
 // In workgroups of 256 threads.
 int64_t delta_groups(const tg_delta_args& a) {
-    const int KP = delta_padded(a.K);
+    const int KP = delta_padded(a.K), slice = slice_of(delta_in(a.dtype), KP);
     const int64_t chunks = delta_slots(a.seqs, delta_chunk_of(a)) * a.HV * (KP == 256 ? 2 : 1);
-    const int64_t serial =
-        2 * head_slice_grid(a.seqs.seqs * a.HV, (int)ceil_div(a.V, slice_of(delta_in(a.dtype), KP)));
+    const SegmentRoom room(a);
+    const int slices = (int)ceil_div(a.V, slice) + (room.segment ? KP / slice : 0);
+    const int64_t serial = 2 * head_slice_grid(room.units * a.HV, slices);
     return chunks > serial ? chunks : serial;
+}
+
+void delta_sizes(const tg_delta_args& a, size_t* work, size_t* saved, size_t* backward) {
+    const SegmentRoom room(a);
+    const size_t kept = kept_bytes(a), between = room.maps + room.states;
+    if (work) *work = prep_room(a, kTrain + delta_in(a.dtype)) + between;
+    if (saved) *saved = kept;
+    if (backward)
+        *backward = prep_room(a, 2 * kTrain) + up256(kept) + between +
+                    (size_t)(delta_slots(a.seqs, delta_chunk_of(a)) * a.HV) * 2 * sizeof(float);
 }
 
 hipError_t launch_delta(const tg_delta_args& a, void* ws, void* saved, hipStream_t st) {
     DeltaArgs b = delta_args(a);
+    const SegmentRoom room(a);
     b.prep = (char*)ws;
     b.saved = (float*)saved;
+    b.segment = room.segment, b.units = (int)room.units;
+    b.maps = (float*)(b.prep + prep_room(a, kTrain + delta_in(a.dtype)));
+    float* states = (float*)((char*)b.maps + room.maps);
     const int64_t slots = delta_slots(a.seqs, delta_chunk_of(a));
-    if (a.dtype == TG_F32) return forward_typed<float, kTrain>(b, slots, st);
+    if (a.dtype == TG_F32) return forward_typed<float, kTrain>(b, slots, states, st);
     if (a.dtype == TG_BF16)
-        return saved ? forward_typed<bf16, kTrain>(b, slots, st)
-                     : forward_typed<bf16, kMid<bf16>>(b, slots, st);
-    return saved ? forward_typed<f16, kTrain>(b, slots, st)
-                 : forward_typed<f16, kMid<f16>>(b, slots, st);
+        return saved ? forward_typed<bf16, kTrain>(b, slots, states, st)
+                     : forward_typed<bf16, kMid<bf16>>(b, slots, states, st);
+    return saved ? forward_typed<f16, kTrain>(b, slots, states, st)
+                 : forward_typed<f16, kMid<f16>>(b, slots, states, st);
 }
 
 hipError_t launch_delta_backward(const tg_delta_args& a, const tg_delta_grads& gr,
                                  const void* saved, void* ws, hipStream_t st) {
     DeltaArgs b = delta_args(a);
-    const int C = delta_chunk_of(a);
-    const int64_t slots = delta_slots(a.seqs, C), chunks = slots * a.HV;
-    const size_t states = (size_t)(chunks * kept_floats(a.V, delta_padded(a.K), C)) * 4;
+    const int64_t slots = delta_slots(a.seqs, delta_chunk_of(a));
+    const SegmentRoom room(a);
+    b.segment = room.segment, b.units = (int)room.units;
     b.saved = (float*)saved;
     b.prep = (char*)ws;
-    b.back = (float*)(b.prep + up256((size_t)chunks * prep_bytes(C, 2 * kTrain)));
-    b.part = (float*)((char*)b.back + up256(states));
+    b.back = (float*)(b.prep + prep_room(a, 2 * kTrain));
+    b.maps = (float*)((char*)b.back + up256(kept_bytes(a)));
+    float* states = (float*)((char*)b.maps + room.maps);
+    b.part = (float*)((char*)states + room.states);
     b.dy = rows_of<const void>(gr.dy);
     b.dq = rows_of<void>(gr.dq), b.dk = rows_of<void>(gr.dk), b.dv = rows_of<void>(gr.dv);
     b.ddt = rows_of<void>(gr.ddt), b.dbeta = rows_of<void>(gr.dbeta);
@@ -462,9 +515,9 @@ hipError_t launch_delta_backward(const tg_delta_args& a, const tg_delta_grads& g
     dy.len(a.V), dy.len(gr.dy.row_stride), dy.ptr(gr.dy.p, e);
     if (!a.seqs.offsets) dy.len(gr.dy.seq_stride);
     b.wide_dy = dy.width(8) == 8;
-    hipError_t err = a.dtype == TG_F32   ? backward_typed<float>(b, slots, st)
-                     : a.dtype == TG_BF16 ? backward_typed<bf16>(b, slots, st)
-                                          : backward_typed<f16>(b, slots, st);
+    hipError_t err = a.dtype == TG_F32   ? backward_typed<float>(b, slots, states, st)
+                     : a.dtype == TG_BF16 ? backward_typed<bf16>(b, slots, states, st)
+                                          : backward_typed<f16>(b, slots, states, st);
     if (err != hipSuccess) return err;
     return launch_column_sums(b.part, (int)slots, 2 * (int64_t)a.HV, gr.dA, a.HV, gr.ddt_bias, st);
 }

@@ -323,6 +323,12 @@ struct DeltaArgs {
     const float *A, *dt_bias, *initial;
     float* final;
     bool wide_qk, wide_v, wide_y;  // rows of 16 bytes of q and k, of v, of 4 values of y
+    // Long sequences in segments (0: whole sequences) of whole chunks, a workgroup for
+    // each: see seq_delta_segments.hip.
+    int segment;
+    int units;      // sequences, or the segments of all
+    bool through;   // what a segment makes of a state is wanted, not y
+    float* maps;    // [units][HV][KP][map_columns()]
     char* prep;    // [slots][HV] of prep_bytes
     float* saved;  // [slots][HV] of kept_floats(), or null
     // The backward pass.
@@ -341,6 +347,24 @@ inline int delta_padded(int K) { return K <= 64 ? 64 : K <= 128 ? 128 : 256; }
 inline int delta_in(tg_dtype d) { return d == TG_BF16 ? 1 : d == TG_F16 ? 2 : 3; }
 inline int delta_chunk_of(const tg_delta_args& a) {
     return delta_chunk(delta_in(a.dtype), delta_padded(a.K));
+}
+
+// The segment (or sequence) that a workgroup of the serial kernels has: sequence s,
+// rows lo .. hi-1 of its len.
+struct Segment {
+    int s, start, len, lo, hi;
+    __device__ __forceinline__ bool find(const DeltaArgs& a, int unit) {
+        s = a.segment ? a.map.owner(unit, a.segment) : unit;
+        start = a.map.start(s);
+        len = a.map.end(s) - start;
+        lo = 0;
+        hi = len;
+        return !a.segment || SeqMap::piece(unit, a.map.slot0(s, a.segment), len, a.segment, lo, hi);
+    }
+};
+// Columns of a segment's map of states: those of V, rounded up to a slice, and KP.
+inline __host__ __device__ int map_columns(int V, int KP, int slice) {
+    return (V + slice - 1) / slice * slice + KP;
 }
 
 // The chunk of (sequence, slice of the columns) that a workgroup of the serial
@@ -462,6 +486,10 @@ template <typename T, int NM>
 hipError_t launch_delta_forward(const DeltaArgs& a, int KP, hipStream_t st);
 template <typename T>
 hipError_t launch_delta_states(const DeltaArgs& a, int KP, hipStream_t st);
+// The states before (reverse: their gradients after) each segment from those before the
+// first (after the last): [units][HV][K][V].
+hipError_t launch_delta_join(const DeltaArgs& a, const float* first, bool reverse, float* states, int KP,
+                             int slice, hipStream_t st);
 template <typename T>
 hipError_t launch_delta_grads(const DeltaArgs& a, int KP, int64_t slots, hipStream_t st);
 

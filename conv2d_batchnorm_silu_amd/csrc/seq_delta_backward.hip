@@ -38,7 +38,7 @@ struct BackShape {
 // The states' gradients, from the last chunk to the first, divided among the waves
 // like the forward pass; the helpers form P^T w and q's part of dS0.
 template <typename T, int KP, bool WIDE, bool WIDE_V>
-__global__ __launch_bounds__(512, 1) void delta_backward(const DeltaArgs a) {
+__global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_backward(const DeltaArgs a) {
     using Sh = BackShape<T, KP>;
     constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, WL = Sh::WL, NT = Sh::NT, HT = NT / 2;
     constexpr int KH = KP / 2, KT = KH / 16, NK = KH / 32, CT = C / 32;
@@ -46,11 +46,18 @@ __global__ __launch_bounds__(512, 1) void delta_backward(const DeltaArgs a) {
     const int w = (threadIdx.x >> 6) % Sh::carriers, l = threadIdx.x & 63, g = l >> 4, col = l & 15;
     const int ct = w % Sh::cols, hf = w / Sh::cols;
     const bool helper = threadIdx.x >= Sh::carriers * 64;
-    const HeadSlice at = head_slice((a.V + Sh::slice - 1) / Sh::slice);
-    if (at.pair >= a.map.seqs * a.HV) return;
-    const int s = at.pair / a.HV, h = at.pair % a.HV, hk = h / (a.HV / a.HK);
-    const int start = a.map.start(s), len = a.map.end(s) - start, slot0 = a.map.slot0(s, C);
-    const int chunks = (len + C - 1) / C, v0 = at.slice * Sh::slice, k0 = hf * KH;
+    const int slices = (a.V + Sh::slice - 1) / Sh::slice;
+    const HeadSlice at = head_slice(a.through ? slices + KP / Sh::slice : slices);
+    if (at.pair >= a.units * a.HV) return;
+    const int unit = at.pair / a.HV, h = at.pair % a.HV, hk = h / (a.HV / a.HK);
+    Segment seg;
+    if (!seg.find(a, unit)) return;
+    if (a.through && seg.lo == 0) return;  // nobody goes on from there
+    const int s = seg.s, start = seg.start, first = seg.lo, len = seg.hi - seg.lo;
+    const int slot0 = a.map.slot0(s, C) + first / C, chunks = (len + C - 1) / C;
+    // The slices behind V's start from columns of the identity, with no dy.
+    const bool unity = at.slice >= slices;
+    const int v0 = unity ? 0 : at.slice * Sh::slice, k0 = hf * KH;
     char* share = (char*)lds + Sh::stages * Sh::stage + ct * Sh::share;
     float *xsum = (float*)share, *usum = (float*)(share + Sh::sums), *qsum = (float*)(share + 2 * Sh::sums);
     const HalfFrags<kTrain> rx{(bf16*)(share + 2 * Sh::sums + KP / 16 * 1024)}, wx{rx.p + NT * kTrain * 256};
@@ -88,9 +95,10 @@ __global__ __launch_bounds__(512, 1) void delta_backward(const DeltaArgs a) {
         const auto fetch = [&](int c) {
             c = c < 0 ? 0 : c;
             const int lo = c * C, n = imin(C, len - lo);
-            kt.fetch(row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, n);
-            qt.fetch(row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, n);
-            vt.fetch(row_of<const T>(a.dy, a.map, s, start, lo) + (int64_t)h * a.V + v0, n);
+            kt.fetch(row_of<const T>(a.k, a.map, s, start, first + lo) + (int64_t)hk * a.K, n);
+            qt.fetch(row_of<const T>(a.q, a.map, s, start, first + lo) + (int64_t)hk * a.K, n);
+            vt.fetch(row_of<const T>(a.dy, a.map, s, start, first + lo) + (int64_t)h * a.V + v0,
+                     unity ? 0 : n);
 #pragma unroll
             for (int i = 0; i < SN; ++i)
                 st[i] = ((const float4*)record(c))[(i * Sh::carriers * 64 + kt.tid()) % SC];
@@ -176,7 +184,8 @@ __global__ __launch_bounds__(512, 1) void delta_backward(const DeltaArgs a) {
 
     __builtin_amdgcn_s_setprio(2);  // the helpers have time
     const int v = v0 + ct * 16 + col;
-    const int64_t KV = (int64_t)a.K * a.V, held = ((int64_t)s * a.HV + h) * KV;
+    const int64_t KV = (int64_t)a.K * a.V;
+    const float* after = a.dfinal ? a.dfinal + ((int64_t)(a.segment ? unit : s) * a.HV + h) * KV : nullptr;
     const auto tile_at = [&](int i) { return i < HT ? (1 - hf) * HT + i : hf * HT + i - HT; };
     if (chunks > 0) fetch_prepared(chunks - 1, 0);
     float4_t S[KT];  // dS
@@ -185,7 +194,8 @@ __global__ __launch_bounds__(512, 1) void delta_backward(const DeltaArgs a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int k = k0 + t * 16 + 4 * g + r;
-            S[t][r] = a.dfinal && k < a.K && v < a.V ? a.dfinal[held + (int64_t)k * a.V + v] : 0.0f;
+            if (a.through) S[t][r] = unity && k == (at.slice - slices) * Sh::slice + v && k < a.K ? 1.0f : 0.0f;
+            else S[t][r] = after && k < a.K && v < a.V ? after[(int64_t)k * a.V + v] : 0.0f;
         }
     for (int c = chunks - 1; c >= 0; --c) {
         lds_barrier();  // chunk c is there
@@ -193,7 +203,7 @@ __global__ __launch_bounds__(512, 1) void delta_backward(const DeltaArgs a) {
         const Planes<NI> kp = planes(c, 0);
         float* keep = a.back + ((int64_t)(slot0 + c) * a.HV + h) * kept_floats(a.V, KP, C);
         const int vt = v0 / 16 + ct;
-        if (vt * 16 < a.V)
+        if (vt * 16 < a.V && !a.through)
 #pragma unroll
             for (int t = 0; t < KT; ++t) *kept_at(keep, KP, C, vt, hf * KT + t) = S[t];
         // k dS over this half's rows: the other half's tokens, then its own.
@@ -242,19 +252,28 @@ __global__ __launch_bounds__(512, 1) void delta_backward(const DeltaArgs a) {
             for (int t = 0; t < KT; ++t) f[t] = kp.cols(b * 32, k0 + t * 16);
             mma_rows<kTrain>(S, f, kr, All());
         }
-        if (vt * 16 < a.V)
+        if (vt * 16 < a.V && !a.through)
 #pragma unroll
             for (int i = 0; i < HT; ++i) *kept_at(keep, KP, C, vt, KP / 16 + hf * HT + i) = R[i];
         if (Sh::stages == 1) lds_barrier();
     }
-    if (a.dinitial && v < a.V)
+    if (a.through) {
+        const int columns = map_columns(a.V, KP, Sh::slice);
+        float* out = a.maps + ((int64_t)unit * a.HV + h) * KP * columns + at.slice * Sh::slice + ct * 16 + col;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) out[(int64_t)(k0 + t * 16 + 4 * g + r) * columns] = S[t][r];
+    } else if (a.dinitial && seg.lo == 0 && v < a.V) {
+        float* out = a.dinitial + ((int64_t)s * a.HV + h) * KV;
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int k = k0 + t * 16 + 4 * g + r;
-                if (k < a.K) a.dinitial[held + (int64_t)k * a.V + v] = S[t][r];
+                if (k < a.K) out[(int64_t)k * a.V + v] = S[t][r];
             }
+    }
 }
 
 template <typename T, int KP>
@@ -265,7 +284,8 @@ hipError_t states_at(const DeltaArgs& a, hipStream_t st) {
                                     : delta_backward<T, KP, true, false>;
     const hipError_t e = ensure_dynamic_lds((const void*)kernel, Sh::lds);
     if (e != hipSuccess) return e;
-    const int64_t grid = head_slice_grid((int64_t)a.map.seqs * a.HV, (int)ceil_div(a.V, Sh::slice));
+    const int slices = (int)ceil_div(a.V, Sh::slice) + (a.through ? KP / Sh::slice : 0);
+    const int64_t grid = head_slice_grid((int64_t)a.units * a.HV, slices);
     kernel<<<(unsigned)grid, Sh::threads, Sh::lds, st>>>(a);
     return hipGetLastError();
 }

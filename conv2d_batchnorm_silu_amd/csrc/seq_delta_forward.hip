@@ -41,7 +41,7 @@ struct FwdShape {
 };
 
 template <typename T, int KP, int NM, bool WIDE, bool WIDE_V>
-__global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
+__global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(const DeltaArgs a) {
     using Sh = FwdShape<T, KP, NM>;
     constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, VL = Sh::VL, NT = Sh::NT, HT = NT / 2;
     constexpr int KH = KP / 2, KT = KH / 16, NK = KH / 32, CT = C / 32;
@@ -49,11 +49,18 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
     const int w = (threadIdx.x >> 6) % Sh::carriers, l = threadIdx.x & 63, g = l >> 4, col = l & 15;
     const int ct = w % Sh::cols, hf = w / Sh::cols;
     const bool helper = threadIdx.x >= Sh::carriers * 64;
-    const HeadSlice at = head_slice((a.V + Sh::slice - 1) / Sh::slice);
-    if (at.pair >= a.map.seqs * a.HV) return;
-    const int s = at.pair / a.HV, h = at.pair % a.HV, hk = h / (a.HV / a.HK);
-    const int start = a.map.start(s), len = a.map.end(s) - start, slot0 = a.map.slot0(s, C);
-    const int chunks = (len + C - 1) / C, v0 = at.slice * Sh::slice;
+    const int slices = (a.V + Sh::slice - 1) / Sh::slice;
+    const HeadSlice at = head_slice(a.through ? slices + KP / Sh::slice : slices);
+    if (at.pair >= a.units * a.HV) return;
+    const int unit = at.pair / a.HV, h = at.pair % a.HV, hk = h / (a.HV / a.HK);
+    Segment seg;
+    if (!seg.find(a, unit)) return;
+    if (a.through && seg.hi == seg.len) return;  // nobody goes on from there
+    const int s = seg.s, start = seg.start, first = seg.lo, len = seg.hi - seg.lo;
+    const int slot0 = a.map.slot0(s, C) + first / C, chunks = (len + C - 1) / C;
+    // The slices behind V's start from columns of the identity, with no v.
+    const bool unity = at.slice >= slices;
+    const int v0 = unity ? 0 : at.slice * Sh::slice;
     char* share = (char*)lds + Sh::stages * Sh::stage + ct * Sh::share;
     float* xsum = (float*)share;
     const HalfFrags<NM> rx{(bf16*)(share + Sh::sums)}, wx{rx.p + NT * NM * 256};
@@ -85,9 +92,10 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
         const auto fetch = [&](int c) {
             c = imin(c, chunks - 1);
             const int lo = c * C, n = imin(C, len - lo);
-            kt.fetch(row_of<const T>(a.k, a.map, s, start, lo) + (int64_t)hk * a.K, n);
-            qt.fetch(row_of<const T>(a.q, a.map, s, start, lo) + (int64_t)hk * a.K, n);
-            vt.fetch(row_of<const T>(a.v, a.map, s, start, lo) + (int64_t)h * a.V + v0, n);
+            kt.fetch(row_of<const T>(a.k, a.map, s, start, first + lo) + (int64_t)hk * a.K, n);
+            qt.fetch(row_of<const T>(a.q, a.map, s, start, first + lo) + (int64_t)hk * a.K, n);
+            vt.fetch(row_of<const T>(a.v, a.map, s, start, first + lo) + (int64_t)h * a.V + v0,
+                     unity ? 0 : n);
 #pragma unroll
             for (int i = 0; i < SN; ++i)
                 st[i] = ((const float4*)record(c))[(i * Sh::carriers * 64 + kt.tid()) % SC];
@@ -139,12 +147,20 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
                     mma_cols<NI>(ys, sf, f, All());
                 }
             };
-            blocks(0);
+            if (!a.through) blocks(0);
             lds_barrier();
-            blocks(KP / 64);
+            if (!a.through) blocks(KP / 64);
 #pragma unroll
             for (int i = 0; i < HT; ++i) ys[i] *= scal[kReadQ * C + (hf * HT + i) * 16 + col];
             lds_barrier();  // the corrections are there
+            if (a.through) {
+                if (Sh::stages == 1) {
+                    lds_barrier();
+                    put(c + 1);
+                    fetch(c + 2);
+                }
+                continue;
+            }
 #pragma unroll
             for (int t = 0; t < CT; ++t)
                 if (used(t)) {
@@ -155,7 +171,7 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
                     mma_cols<NI>(ys, uf, f, All());
                 }
             fetch_p(c + 1);
-            T* yb = row_of<T>(a.y, a.map, s, start, lo) + (int64_t)h * a.V + v0;
+            T* yb = row_of<T>(a.y, a.map, s, start, first + lo) + (int64_t)h * a.V + v0;
 #pragma unroll
             for (int t = 0; t < HT; ++t)
                 if (n == C || (hf * HT + t) * 16 + col < n) {
@@ -180,7 +196,8 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
 
     __builtin_amdgcn_s_setprio(2);  // the helpers have time
     const int v = v0 + ct * 16 + col, k0 = hf * KH;
-    const int64_t KV = (int64_t)a.K * a.V, held = ((int64_t)s * a.HV + h) * KV;
+    const int64_t KV = (int64_t)a.K * a.V;
+    const float* before = a.initial ? a.initial + ((int64_t)(a.segment ? unit : s) * a.HV + h) * KV : nullptr;
     const auto tile_at = [&](int i) { return i < HT ? (1 - hf) * HT + i : hf * HT + i - HT; };
     Frag<NM> xf[HT][CT];
     const auto fetch_x = [&](int c) {
@@ -198,7 +215,8 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int k = k0 + t * 16 + 4 * g + r;
-            S[t][r] = a.initial && k < a.K && v < a.V ? a.initial[held + (int64_t)k * a.V + v] : 0.0f;
+            if (a.through) S[t][r] = unity && k == (at.slice - slices) * Sh::slice + v && k < a.K ? 1.0f : 0.0f;
+            else S[t][r] = before && k < a.K && v < a.V ? before[(int64_t)k * a.V + v] : 0.0f;
         }
     for (int c = 0; c < chunks; ++c) {
         lds_barrier();  // chunk c is there
@@ -248,7 +266,7 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
             ux.put(mt, e[i] * scales(scal, C, kBeta, mt));
         }
         lds_barrier();
-        if (a.saved) {
+        if (a.saved && !a.through) {
             float* keep = a.saved + ((int64_t)(slot0 + c) * a.HV + h) * kept_floats(a.V, KP, C);
             const int vt = v0 / 16 + ct;
             if (vt * 16 < a.V) {
@@ -271,14 +289,23 @@ __global__ __launch_bounds__(512, 1) void delta_forward(const DeltaArgs a) {
         }
         if (Sh::stages == 1) lds_barrier();
     }
-    if (a.final && v < a.V)
+    if (a.through) {
+        const int columns = map_columns(a.V, KP, Sh::slice);
+        float* out = a.maps + ((int64_t)unit * a.HV + h) * KP * columns + at.slice * Sh::slice + ct * 16 + col;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) out[(int64_t)(k0 + t * 16 + 4 * g + r) * columns] = S[t][r];
+    } else if (a.final && seg.hi == seg.len && v < a.V) {
+        float* out = a.final + ((int64_t)s * a.HV + h) * KV;
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int k = k0 + t * 16 + 4 * g + r;
-                if (k < a.K) a.final[held + (int64_t)k * a.V + v] = S[t][r];
+                if (k < a.K) out[(int64_t)k * a.V + v] = S[t][r];
             }
+    }
 }
 
 template <typename T, int KP, int NM>
@@ -289,7 +316,8 @@ hipError_t forward_at(const DeltaArgs& a, hipStream_t st) {
                                    : delta_forward<T, KP, NM, true, false>;
     const hipError_t e = ensure_dynamic_lds((const void*)kernel, Sh::lds);
     if (e != hipSuccess) return e;
-    const int64_t grid = head_slice_grid((int64_t)a.map.seqs * a.HV, (int)ceil_div(a.V, Sh::slice));
+    const int slices = (int)ceil_div(a.V, Sh::slice) + (a.through ? KP / Sh::slice : 0);
+    const int64_t grid = head_slice_grid((int64_t)a.units * a.HV, slices);
     kernel<<<(unsigned)grid, Sh::threads, Sh::lds, st>>>(a);
     return hipGetLastError();
 }

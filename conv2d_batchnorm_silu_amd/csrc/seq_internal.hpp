@@ -59,6 +59,7 @@ hipError_t launch_scan_step(const tg_scan_args& a, float* state, int64_t num_slo
 
 void delta_sizes(const tg_delta_args& a, size_t* work, size_t* saved, size_t* backward);
 int64_t delta_groups(const tg_delta_args& a);  // workgroups of its largest launch
+int delta_segment(const tg_delta_args& a);  // tokens of a segment, or 0
 hipError_t launch_delta(const tg_delta_args& a, void* ws, void* saved, hipStream_t st);
 hipError_t launch_delta_backward(const tg_delta_args& a, const tg_delta_grads& g,
                                  const void* saved, void* ws, hipStream_t st);

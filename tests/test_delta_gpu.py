@@ -150,6 +150,37 @@ def test_backward(case):
     assert all(a is b or torch.equal(a, b) for a, b in zip(got, again))
 
 
+# Few long sequences, which are walked in segments.
+LONG = [
+    ([1500], False, 1, 1, 32, 16, "f32", True, False, 0), ([1000, 30, 0, 500], True, 1, 2, 64, 40, "bf16", True, False, 3),
+    ([1100], False, 1, 2, 100, 33, "f16", False, False, 0), ([700, 700], False, 1, 1, 130, 20, "bf16", True, True, 0),
+    ([1300], False, 1, 1, 256, 17, "f32", True, False, 0), ([1, 1400, 1], True, 1, 1, 16, 70, "f16", True, False, 0),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_long_forward(case):
+    test_forward(case)
+
+
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_long_backward(case):
+    test_backward(case)
+
+
+def test_long_wrong_offsets_stay_inside():
+    c = Case(([2000], True, 1, 1, 16, 16, "f32", False, False, 0))
+    guard = torch.full((6000, 1, 16), 7.0, device="cuda")
+    for wrong in ([5, 900, 4000], [0, 1990, 20], [-7, 3, 9000], [1700, 10, 0]):
+        off = torch.tensor(wrong, dtype=torch.int32, device="cuda")
+        more = dict(c.more(), offsets=off)
+        tg.gated_delta_rule(*c.args(), out=guard[2000:4000], **more)
+        _, saved = tg.gated_delta_rule_train(*c.args(), **more)
+        tg.gated_delta_rule_backward(c.dev(c.dy), *c.args(), saved, **more)
+    torch.cuda.synchronize()
+    assert bool((guard[:2000] == 7).all()) and bool((guard[4000:] == 7).all())
+
+
 STEPS = [(1, 1, 1, 1, 1, "f32", 0), (3, 2, 4, 20, 13, "bf16", 5), (5, 2, 2, 64, 64, "f16", 0), (2, 1, 2, 128, 128, "bf16", 16),
          (4, 1, 1, 256, 40, "f32", 4), (3, 1, 3, 130, 33, "f16", 0), (2, 4, 8, 96, 132, "f32", 0), (9, 1, 1, 8, 260, "bf16", 0)]
 
