@@ -111,7 +111,7 @@ template <typename T, int KP, int NM, bool BACK, bool WIDE>
 __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
     using Sh = PrepShape<T, KP>;
     constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, ML = Sh::ML, NT = C / 16;
-    constexpr int PP = BACK ? NM : NI;  // parts of P
+    constexpr int PP = BACK ? kParts : kOut<T>;  // parts of P
     extern __shared__ float4 lds[];
     float* scal = (float*)lds;
     double* G = (double*)(scal + kScales * C);
@@ -159,10 +159,10 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
         for (int jt = 0; jt < NT; ++jt) {
             if (jt > tile) continue;
             const Frag<NI> bf = kp.rows(jt * 16, k0);
-            if (kk_here) mma<kTrain>(kk[jt], kf, bf);
-            if (qk_here) mma<kTrain>(qk[jt], qf, bf);
+            if (kk_here) mma<kParts>(kk[jt], kf, bf);
+            if (qk_here) mma<kParts>(qk[jt], qf, bf);
         }
-        if (qk_here) mma<kTrain>(qq, qf, qf);
+        if (qk_here) mma<kParts>(qq, qf, qf);
     }
 #pragma unroll
     for (int jt = 0; jt < NT; ++jt)
@@ -377,7 +377,7 @@ hipError_t forward_typed(const DeltaArgs& a, int64_t slots, float* states, hipSt
 template <typename T>
 hipError_t backward_typed(const DeltaArgs& a, int64_t slots, float* states, hipStream_t st) {
     const int KP = delta_padded(a.K);
-    hipError_t e = launch_delta_prep<T, kTrain, true>(a, KP, slots, st);
+    hipError_t e = launch_delta_prep<T, kParts, true>(a, KP, slots, st);
     if (e != hipSuccess) return e;
     if (a.segment)
         e = in_segments(a, a.dfinal, true, states, KP, slice_of(kIn<T>, KP), st,
@@ -470,10 +470,10 @@ int64_t delta_groups(const tg_delta_args& a) {
 void delta_sizes(const tg_delta_args& a, size_t* work, size_t* saved, size_t* backward) {
     const SegmentRoom room(a);
     const size_t kept = kept_bytes(a), between = room.maps + room.states;
-    if (work) *work = prep_room(a, kTrain + delta_in(a.dtype)) + between;
+    if (work) *work = prep_room(a, kParts + delta_out(a.dtype)) + between;
     if (saved) *saved = kept;
     if (backward)
-        *backward = prep_room(a, 2 * kTrain) + up256(kept) + between +
+        *backward = prep_room(a, 2 * kParts) + up256(kept) + between +
                     (size_t)(delta_slots(a.seqs, delta_chunk_of(a)) * a.HV) * 2 * sizeof(float);
 }
 
@@ -483,14 +483,14 @@ hipError_t launch_delta(const tg_delta_args& a, void* ws, void* saved, hipStream
     b.prep = (char*)ws;
     b.saved = (float*)saved;
     b.segment = room.segment, b.units = (int)room.units;
-    b.maps = (float*)(b.prep + prep_room(a, kTrain + delta_in(a.dtype)));
+    b.maps = (float*)(b.prep + prep_room(a, kParts + delta_out(a.dtype)));
     float* states = (float*)((char*)b.maps + room.maps);
     const int64_t slots = delta_slots(a.seqs, delta_chunk_of(a));
-    if (a.dtype == TG_F32) return forward_typed<float, kTrain>(b, slots, states, st);
+    if (a.dtype == TG_F32) return forward_typed<float, kParts>(b, slots, states, st);
     if (a.dtype == TG_BF16)
-        return saved ? forward_typed<bf16, kTrain>(b, slots, states, st)
+        return saved ? forward_typed<bf16, kParts>(b, slots, states, st)
                      : forward_typed<bf16, kMid<bf16>>(b, slots, states, st);
-    return saved ? forward_typed<f16, kTrain>(b, slots, states, st)
+    return saved ? forward_typed<f16, kParts>(b, slots, states, st)
                  : forward_typed<f16, kMid<f16>>(b, slots, states, st);
 }
 
@@ -502,7 +502,7 @@ hipError_t launch_delta_backward(const tg_delta_args& a, const tg_delta_grads& g
     b.segment = room.segment, b.units = (int)room.units;
     b.saved = (float*)saved;
     b.prep = (char*)ws;
-    b.back = (float*)(b.prep + prep_room(a, 2 * kTrain));
+    b.back = (float*)(b.prep + prep_room(a, 2 * kParts));
     b.maps = (float*)((char*)b.back + up256(kept_bytes(a)));
     float* states = (float*)((char*)b.maps + room.maps);
     b.part = (float*)((char*)states + room.states);

@@ -4,15 +4,18 @@
 //
 // Every product goes through v_mfma_f32_16x16x32_bf16. A bf16 input is its own first
 // part, an fp16 input two parts (exactly), an fp32 input three (24 bits). What lies
-// between is split into two parts for prompts of 16-bit tensors (off by at most
-// 2^-18; the product of two low parts, as small, is dropped), so that states,
-// which are fp32, keep 17 bits at two or three matrix instructions a product; fp16
-// instructions would take one, but have 11 bits and not the range of states. In
-// training, and for fp32, it is three parts: the gradients of A and dt_bias are
-// fp32 sums over all tokens that cancel (17 bits left them off by up to 6e-5).
-// Six instructions a product are fewer than the fp32 matrix instructions' sixteen.
-// Products that only reach an output of the tensors' type take as many parts as an
-// input has.
+// between is split into three, so that states and the gradients of parameters, which
+// are fp32, are as exact as fp32 products would leave them: at three to six
+// instructions a product, fewer than the fp32 matrix instructions' sixteen, and with
+// fp32's range, which fp16 parts would not have.
+//
+// Prompts of 16-bit tensors that keep nothing for training take two parts (kMid: 17
+// bits, 2^-18 of the value): the states, off by 2 to 6e-6 of their norm, go on to
+// tokens that are rounded to 8 or 11 bits, and 4 x 4096 tokens of 16 heads take 164 us
+// in place of 208. In training it left dA and ddt_bias, sums over all tokens that
+// cancel, off by up to 6e-5. Products that only reach y take two parts of 16-bit tensors
+// (a single one left bf16 outputs off by 1.6 times their rounding), those that only
+// reach the gradients of q and k as many as an input has.
 //
 // Fragments. Lane l of a wave holds row (of the left operand) or column (of the
 // right) l % 16 and, with g = l / 16, the eight inner indices 4g .. 4g+3 and
@@ -37,8 +40,10 @@ inline constexpr int kIn = sizeof(T) == 4 ? 3 : 2;  // parts of an input
 template <>
 inline constexpr int kIn<bf16> = 1;
 template <typename T>
-inline constexpr int kMid = sizeof(T) == 4 ? 3 : 2;  // parts of an intermediate in a prompt
-constexpr int kTrain = 3;                            // and in training
+inline constexpr int kOut = kIn<T> > 2 ? 3 : 2;  // of what only reaches y
+constexpr int kParts = 3;                        // of what lies between
+template <typename T>
+inline constexpr int kMid = kIn<T> > 2 ? 3 : 2;  // and of it in prompts
 
 // Tokens of a chunk: 64, or 32 where two chunks' parts of q and k (padded to KP) and
 // the matrices made from them would not fit LDS together.
@@ -344,6 +349,7 @@ inline int64_t delta_slots(const tg_seqs& s, int C) {
     return s.offsets ? s.rows / C + s.seqs : s.seqs * ceil_div(s.rows / s.seqs, C);
 }
 inline int delta_padded(int K) { return K <= 64 ? 64 : K <= 128 ? 128 : 256; }
+inline int delta_out(tg_dtype d) { return d == TG_F32 ? 3 : 2; }
 inline int delta_in(tg_dtype d) { return d == TG_BF16 ? 1 : d == TG_F16 ? 2 : 3; }
 inline int delta_chunk_of(const tg_delta_args& a) {
     return delta_chunk(delta_in(a.dtype), delta_padded(a.K));
@@ -479,7 +485,7 @@ __device__ __forceinline__ float4_t scales(const float* scal, int C, DeltaScale 
     return *(const float4_t*)(scal + which * C + mt * 16 + 4 * ((threadIdx.x & 63) >> 4));
 }
 
-// The kernels' launches; NM: parts of X; BACK: the transposed matrices.
+// The kernels' launches; NM: parts of what lies between; BACK: the transposed matrices.
 template <typename T, int NM, bool BACK>
 hipError_t launch_delta_prep(const DeltaArgs& a, int KP, int64_t slots, hipStream_t st);
 template <typename T, int NM>

@@ -29,7 +29,7 @@ struct BackShape {
     static constexpr int rows = NI * C * LD * 2;
     static constexpr int stage = kScales * C * 4 + 2 * rows + NI * C * WL * 2;
     // For 16 columns: sums of halves and P^T w; b dU, R for dS; q's part of dS.
-    static constexpr int sums = NT * 1024, share = 2 * sums + NT * 512 * 2 * kTrain + KP / 16 * 1024;
+    static constexpr int sums = NT * 1024, share = 2 * sums + NT * 512 * 2 * kParts + KP / 16 * 1024;
     static constexpr int stages = 2 * stage + cols * share <= 160 * 1024 ? 2 : 1;
     static constexpr int lds = stages * stage + cols * share, carriers = cols * 2, threads = carriers * 128;
     static_assert(lds <= 160 * 1024, "more LDS than a compute unit has");
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_backward(c
     const int v0 = unity ? 0 : at.slice * Sh::slice, k0 = hf * KH;
     char* share = (char*)lds + Sh::stages * Sh::stage + ct * Sh::share;
     float *xsum = (float*)share, *usum = (float*)(share + Sh::sums), *qsum = (float*)(share + 2 * Sh::sums);
-    const HalfFrags<kTrain> rx{(bf16*)(share + 2 * Sh::sums + KP / 16 * 1024)}, wx{rx.p + NT * kTrain * 256};
+    const HalfFrags<kParts> rx{(bf16*)(share + 2 * Sh::sums + KP / 16 * 1024)}, wx{rx.p + NT * kParts * 256};
 
     // A stage: scales, k, q, the slice of dy.
     const auto stage = [&](int c) { return (char*)lds + (c % Sh::stages) * Sh::stage; };
@@ -69,14 +69,14 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_backward(c
                           which < 2 ? C * LD : C * WL};
     };
     const auto record = [&](int c) {
-        return a.prep + ((int64_t)(slot0 + c) * a.HV + h) * prep_bytes(C, 2 * kTrain);
+        return a.prep + ((int64_t)(slot0 + c) * a.HV + h) * prep_bytes(C, 2 * kParts);
     };
     // Tiles hf * HT + i of X^T and P^T, blocks of 32 columns from theirs on.
-    Frag<kTrain> prep[HT][CT];
+    Frag<kParts> prep[HT][CT];
     const auto used = [&](int t) { return t == CT - 1 || hf == 0; };
     const auto fetch_prepared = [&](int c, int which) {
         const bf16* f = (const bf16*)(record(c < 0 ? 0 : c) + kScales * C * 4) +
-                        which * frag_count(C) * 512 * kTrain;
+                        which * frag_count(C) * 512 * kParts;
 #pragma unroll
         for (int i = 0; i < HT; ++i)
 #pragma unroll
@@ -129,10 +129,10 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_backward(c
 #pragma unroll
             for (int t = 0; t < CT; ++t)
                 if (used(t)) {
-                    Frag<kTrain> f[HT];
+                    Frag<kParts> f[HT];
 #pragma unroll
                     for (int i = 0; i < HT; ++i) f[i] = prep[i][t];
-                    mma_rows<kTrain>(u, f, wf[t], All());
+                    mma_rows<kParts>(u, f, wf[t], All());
                 }
 #pragma unroll
             for (int i = 0; i < HT; ++i) *sum_at(usum, hf * HT + i) = u[i];
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_backward(c
             lds_barrier();
             fetch_prepared(c - 1, 1);
             // Half of the tiles on each side of a barrier that the others come to soon.
-            Frag<kTrain> qw[CT];
+            Frag<kParts> qw[CT];
 #pragma unroll
             for (int b = 0; b < CT; ++b) {
                 float y[8];
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_backward(c
                     for (int q = NI - 1; q >= 0; --q) y[j] += (float)wf[b].p[q][j];
                 }
                 qw[b] =
-                    frag_of<kTrain>(float4_t{y[0], y[1], y[2], y[3]} * scales(scal, C, kReadQ, 2 * b),
+                    frag_of<kParts>(float4_t{y[0], y[1], y[2], y[3]} * scales(scal, C, kReadQ, 2 * b),
                                     float4_t{y[4], y[5], y[6], y[7]} * scales(scal, C, kReadQ, 2 * b + 1));
             }
             const auto tiles = [&](int first) {
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_backward(c
                     Frag<NI> f[KT / 2];
 #pragma unroll
                     for (int t = 0; t < KT / 2; ++t) f[t] = qp.cols(b * 32, k0 + (first + t) * 16);
-                    mma_rows<kTrain>(D, f, qw[b], All());
+                    mma_rows<kParts>(D, f, qw[b], All());
                 }
 #pragma unroll
                 for (int t = 0; t < KT / 2; ++t) *sum_at(qsum, hf * KT + first + t) = D[t];
@@ -210,11 +210,11 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_backward(c
         float4_t x[NT] = {};
 #pragma unroll
         for (int t = 0; t < NK; ++t) {
-            const Frag<kTrain> sf = frag_of<kTrain>(S[2 * t], S[2 * t + 1]);
+            const Frag<kParts> sf = frag_of<kParts>(S[2 * t], S[2 * t + 1]);
             Frag<NI> f[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i) f[i] = kp.rows(tile_at(i) * 16, k0 + t * 32);
-            mma_rows<kTrain>(x, f, sf, All());
+            mma_rows<kParts>(x, f, sf, All());
         }
 #pragma unroll
         for (int i = 0; i < HT; ++i) *sum_at(xsum, tile_at(i)) = x[i];
@@ -230,11 +230,11 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_backward(c
 #pragma unroll
         for (int t = 0; t < CT; ++t)
             if (used(t)) {
-                const Frag<kTrain> bf = rx.frag(t);
-                Frag<kTrain> f[HT];
+                const Frag<kParts> bf = rx.frag(t);
+                Frag<kParts> f[HT];
 #pragma unroll
                 for (int i = 0; i < HT; ++i) f[i] = prep[i][t];
-                mma_rows<kTrain>(R, f, bf, All());
+                mma_rows<kParts>(R, f, bf, All());
             }
         fetch_prepared(c - 1, 0);
 #pragma unroll
@@ -246,11 +246,11 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_backward(c
         for (int t = 0; t < KT; ++t) S[t] = S[t] * total + *sum_at(qsum, hf * KT + t);
 #pragma unroll
         for (int b = 0; b < CT; ++b) {
-            const Frag<kTrain> kr = wx.frag(b);
+            const Frag<kParts> kr = wx.frag(b);
             Frag<NI> f[KT];
 #pragma unroll
             for (int t = 0; t < KT; ++t) f[t] = kp.cols(b * 32, k0 + t * 16);
-            mma_rows<kTrain>(S, f, kr, All());
+            mma_rows<kParts>(S, f, kr, All());
         }
         if (vt * 16 < a.V && !a.through)
 #pragma unroll

@@ -29,12 +29,12 @@ __device__ __forceinline__ float4_t values4(const T* p, int ld, int row0, int co
 
 template <typename T, int KP, int NM>
 struct FwdShape {
-    static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 8, NT = C / 16;
+    static constexpr int NI = kIn<T>, NO = kOut<T>, C = delta_chunk(NI, KP), LD = KP + 8, NT = C / 16;
     static constexpr int slice = slice_of(NI, KP), cols = slice / 16, VL = slice + 8;
     static constexpr int rows = NI * C * LD * 2;
     static constexpr int stage = kScales * C * 4 + 2 * rows + C * VL * (int)sizeof(T);
     // For 16 columns: sums of halves; right sides, corrections for S and for y; S for y.
-    static constexpr int sums = NT * 1024, share = sums + NT * 512 * (2 * NM + NI) + KP / 32 * NI * 1024;
+    static constexpr int sums = NT * 1024, share = sums + NT * 512 * (2 * NM + NO) + KP / 32 * NO * 1024;
     static constexpr int stages = 2 * stage + cols * share <= 160 * 1024 ? 2 : 1;
     static constexpr int lds = stages * stage + cols * share, carriers = cols * 2, threads = carriers * 128;
     static_assert(lds <= 160 * 1024, "more LDS than a compute unit has");
@@ -43,8 +43,10 @@ struct FwdShape {
 template <typename T, int KP, int NM, bool WIDE, bool WIDE_V>
 __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(const DeltaArgs a) {
     using Sh = FwdShape<T, KP, NM>;
-    constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, VL = Sh::VL, NT = Sh::NT, HT = NT / 2;
+    constexpr int NI = Sh::NI, NO = Sh::NO, C = Sh::C, LD = Sh::LD, VL = Sh::VL, NT = Sh::NT, HT = NT / 2;
     constexpr int KH = KP / 2, KT = KH / 16, NK = KH / 32, CT = C / 32;
+    // Products with k: for fp16 in two parts with that of both second parts (k's is exact).
+    constexpr int NS = NI == 2 && NM == 2 ? 3 : NM;
     extern __shared__ float4 lds[];
     const int w = (threadIdx.x >> 6) % Sh::carriers, l = threadIdx.x & 63, g = l >> 4, col = l & 15;
     const int ct = w % Sh::cols, hf = w / Sh::cols;
@@ -64,8 +66,8 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
     char* share = (char*)lds + Sh::stages * Sh::stage + ct * Sh::share;
     float* xsum = (float*)share;
     const HalfFrags<NM> rx{(bf16*)(share + Sh::sums)}, wx{rx.p + NT * NM * 256};
-    const HalfFrags<NI> ux{wx.p + NT * NM * 256};
-    bf16* sx = ux.p + NT * NI * 256;  // S's fragments, NI parts
+    const HalfFrags<NO> ux{wx.p + NT * NM * 256};
+    bf16* sx = ux.p + NT * NO * 256;  // S's fragments, NO parts
 
     // A stage: scales, k, q, the slice of v.
     const auto stage = [&](int c) { return (char*)lds + (c % Sh::stages) * Sh::stage; };
@@ -73,7 +75,7 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
         return Planes<NI>{(bf16*)(stage(c) + kScales * C * 4 + which * Sh::rows), LD, C * LD};
     };
     const auto record = [&](int c) {
-        return a.prep + ((int64_t)(slot0 + c) * a.HV + h) * prep_bytes(C, NM + NI);
+        return a.prep + ((int64_t)(slot0 + c) * a.HV + h) * prep_bytes(C, NM + NO);
     };
     // Tiles hf * HT + i of X and P, blocks of 32 columns up to theirs.
     const auto used = [&](int t) { return t == 0 || hf != 0; };
@@ -88,7 +90,7 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
         vt.shape(a.v.row, imin(Sh::slice, a.V - v0));
         constexpr int SC = kScales * C / 4, SN = (SC + Sh::carriers * 64 - 1) / (Sh::carriers * 64);
         float4 st[SN];
-        Frag<NI> pf[HT][CT];
+        Frag<NO> pf[HT][CT];
         const auto fetch = [&](int c) {
             c = imin(c, chunks - 1);
             const int lo = c * C, n = imin(C, len - lo);
@@ -140,11 +142,12 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
             const auto blocks = [&](int first) {
 #pragma unroll
                 for (int t = 0; t < KP / 64; ++t) {
-                    Frag<NI> sf, f[HT];
+                    Frag<NO> sf;
+                    Frag<NI> f[HT];
                     prepared(sf, sx, first + t);
 #pragma unroll
                     for (int i = 0; i < HT; ++i) f[i] = qp.rows((hf * HT + i) * 16, (first + t) * 32);
-                    mma_cols<NI>(ys, sf, f, All());
+                    mma_cols<NO>(ys, sf, f, All());
                 }
             };
             if (!a.through) blocks(0);
@@ -164,11 +167,11 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
 #pragma unroll
             for (int t = 0; t < CT; ++t)
                 if (used(t)) {
-                    const Frag<NI> uf = ux.frag(t);
-                    Frag<NI> f[HT];
+                    const Frag<NO> uf = ux.frag(t);
+                    Frag<NO> f[HT];
 #pragma unroll
                     for (int i = 0; i < HT; ++i) f[i] = pf[i][t];
-                    mma_cols<NI>(ys, uf, f, All());
+                    mma_cols<NO>(ys, uf, f, All());
                 }
             fetch_p(c + 1);
             T* yb = row_of<T>(a.y, a.map, s, start, first + lo) + (int64_t)h * a.V + v0;
@@ -229,12 +232,12 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
         for (int t = 0; t < NK; ++t) {
             const Frag<NM> sf = frag_of<NM>(S[2 * t], S[2 * t + 1]);
 #pragma unroll
-            for (int q = 0; q < NI; ++q)
-                *(bf16x8_t*)(sx + ((hf * NK + t) * NI + q) * 512 + l * 8) = sf.p[q];
+            for (int q = 0; q < NO; ++q)
+                *(bf16x8_t*)(sx + ((hf * NK + t) * NO + q) * 512 + l * 8) = sf.p[q];
             Frag<NI> f[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i) f[i] = kp.rows(tile_at(i) * 16, k0 + t * 32);
-            mma_rows<NM>(x, f, sf, All());
+            mma_rows<NS>(x, f, sf, All());
         }
 #pragma unroll
         for (int i = 0; i < HT; ++i) *sum_at(xsum, tile_at(i)) = x[i];
@@ -285,7 +288,7 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
             Frag<NI> f[KT];
 #pragma unroll
             for (int t = 0; t < KT; ++t) f[t] = kp.cols(u * 32, k0 + t * 16);
-            mma_rows<NM>(S, f, wf, All());
+            mma_rows<NS>(S, f, wf, All());
         }
         if (Sh::stages == 1) lds_barrier();
     }
@@ -330,10 +333,10 @@ hipError_t launch_delta_forward(const DeltaArgs& a, int KP, hipStream_t st) {
     if (KP == 128) return forward_at<T, 128, NM>(a, st);
     return forward_at<T, 256, NM>(a, st);
 }
-template hipError_t launch_delta_forward<float, 3>(const DeltaArgs&, int, hipStream_t);
-template hipError_t launch_delta_forward<bf16, 3>(const DeltaArgs&, int, hipStream_t);
-template hipError_t launch_delta_forward<bf16, 2>(const DeltaArgs&, int, hipStream_t);
-template hipError_t launch_delta_forward<f16, 3>(const DeltaArgs&, int, hipStream_t);
-template hipError_t launch_delta_forward<f16, 2>(const DeltaArgs&, int, hipStream_t);
+template hipError_t launch_delta_forward<float, kParts>(const DeltaArgs&, int, hipStream_t);
+template hipError_t launch_delta_forward<bf16, kParts>(const DeltaArgs&, int, hipStream_t);
+template hipError_t launch_delta_forward<bf16, kMid<bf16>>(const DeltaArgs&, int, hipStream_t);
+template hipError_t launch_delta_forward<f16, kParts>(const DeltaArgs&, int, hipStream_t);
+template hipError_t launch_delta_forward<f16, kMid<f16>>(const DeltaArgs&, int, hipStream_t);
 
 }  // namespace tg

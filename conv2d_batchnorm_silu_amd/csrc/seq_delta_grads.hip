@@ -19,7 +19,7 @@ struct GradShape {
     static constexpr int parts = waves / NT, KB = NI == 1 && KP == 128 ? 128 : 64, KW = KB / parts, NB = KP / KB;
     static constexpr int VB = 32, VL = VB + 8, ML = C + 8, CL = C + 8, KL = KB + 8;
     // A block of V: dy as rows of tokens; E, R, S0 and dS as rows of V.
-    static constexpr int wide = NI * C * VL * 2 + 2 * kTrain * VB * (CL + KL) * 2;
+    static constexpr int wide = NI * C * VL * 2 + 2 * kParts * VB * (CL + KL) * 2;
     static constexpr int square = 2 * NI * C * ML * 2;                                  // C x C
     static constexpr int scratch = wide > square ? wide : square;
     static constexpr int floats = 9 * C + NT * C + 2 * parts * C + 2 * waves * 16 + 16;
@@ -50,8 +50,8 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
     const Planes<NI> qp{kp.p + NI * C * LD, LD, C * LD};
     bf16* scratch = qp.p + NI * C * LD;
     const Planes<NI> wp{scratch, VL, C * VL};
-    const Planes<kTrain> ep{wp.p + NI * C * VL, CL, VB * CL}, rp{ep.p + kTrain * VB * CL, CL, VB * CL};
-    const Planes<kTrain> sp{rp.p + kTrain * VB * CL, KL, VB * KL}, dp{sp.p + kTrain * VB * KL, KL, VB * KL};
+    const Planes<kParts> ep{wp.p + NI * C * VL, CL, VB * CL}, rp{ep.p + kParts * VB * CL, CL, VB * CL};
+    const Planes<kParts> sp{rp.p + kParts * VB * CL, KL, VB * KL}, dp{sp.p + kParts * VB * KL, KL, VB * KL};
     const Planes<NI> bm{scratch, ML, C * ML}, mm{bm.p + NI * C * ML, ML, C * ML};
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g = l >> 4, col = l & 15;
     const int tile = w % NT, part = w / NT, row0 = tile * 16;
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
                 gd[l] = t.d;
                 ge[l] = __builtin_amdgcn_exp2f((float)p);
                 gt[l] = decay_between(last, p);
-                const float* sc = (const float*)(a.prep + chunk * prep_bytes(C, 2 * kTrain));
+                const float* sc = (const float*)(a.prep + chunk * prep_bytes(C, 2 * kParts));
                 rk[l] = sc[kUnitK * C + l];
                 rq[l] = sc[kUnitQ * C + l];
             }
@@ -136,19 +136,19 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
                         dr[i] = of(dS, i, KB / 16, kb / 16);
                     }
                 tw.put(wp);
-                const auto give = [&](const Planes<kTrain>& d, const float4_t& x, int i, int tiles) {
+                const auto give = [&](const Planes<kParts>& d, const float4_t& x, int i, int tiles) {
                     const int q = (i * kThreads + tid) >> 6;
                     bf16* at = d.p + (q / tiles * 16 + col) * d.ld + q % tiles * 16 + 4 * g;
-                    bf16x4_t o[kTrain];
+                    bf16x4_t o[kParts];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        bf16 b[kTrain];
-                        split<kTrain>(x[j], b);
+                        bf16 b[kParts];
+                        split<kParts>(x[j], b);
 #pragma unroll
-                        for (int m = 0; m < kTrain; ++m) o[m][j] = b[m];
+                        for (int m = 0; m < kParts; ++m) o[m][j] = b[m];
                     }
 #pragma unroll
-                    for (int m = 0; m < kTrain; ++m) *(bf16x4_t*)(at + m * d.plane) = o[m];
+                    for (int m = 0; m < kParts; ++m) *(bf16x4_t*)(at + m * d.plane) = o[m];
                 };
 #pragma unroll
                 for (int i = 0; i < EC; ++i)
@@ -174,21 +174,21 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
                     }
                 lds_barrier();
                 const Frag<NI> wf = wp.rows(row0, 0);
-                const Frag<kTrain> rf = rp.cols(0, row0), ef = ep.cols(0, row0);
+                const Frag<kParts> rf = rp.cols(0, row0), ef = ep.cols(0, row0);
                 if (nb == 0)
 #pragma unroll
                     for (int jt = 0; jt < NT; ++jt)
                         if (jt <= tile) {
-                            const Frag<kTrain> o = ep.cols(0, jt * 16);
-                            mma<kTrain>(F[jt], wf, o);
-                            mma<kTrain>(H[jt], rf, o);
+                            const Frag<kParts> o = ep.cols(0, jt * 16);
+                            mma<kParts>(F[jt], wf, o);
+                            mma<kParts>(H[jt], rf, o);
                         }
 #pragma unroll
                 for (int t = 0; t < WT; ++t) {
-                    const Frag<kTrain> x = sp.cols(0, part * KW + t * 16);
-                    mma<kTrain>(qs[t], wf, x);
-                    mma<kTrain>(rs[t], rf, x);
-                    mma<kTrain>(es[t], ef, dp.cols(0, part * KW + t * 16));
+                    const Frag<kParts> x = sp.cols(0, part * KW + t * 16);
+                    mma<kParts>(qs[t], wf, x);
+                    mma<kParts>(rs[t], rf, x);
+                    mma<kParts>(es[t], ef, dp.cols(0, part * KW + t * 16));
                 }
             }
             // Rows' factors, and the rows' products with q and k.
@@ -218,8 +218,8 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
             for (int jt = 0; jt < NT; ++jt)
                 if (jt <= tile) {
                     const Frag<NI> o = kp.rows(jt * 16, k0);
-                    mma<kTrain>(kk[jt], kf, o);
-                    mma<kTrain>(qk[jt], qf, o);
+                    mma<kParts>(kk[jt], kf, o);
+                    mma<kParts>(qk[jt], qf, o);
                 }
         }
         lds_barrier();  // the last block of V has been read

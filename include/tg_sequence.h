@@ -207,10 +207,10 @@ tg_status tg_selective_scan_step(const tg_scan_args *a, float *state, int64_t nu
  * fp32 [seqs][HV][K][V] or NULL.
  * A step d of 0 keeps the state for any A, -inf included; decays below 2^-126 are
  * taken as 0. Decays above 1 are taken as they are while their product over any 64
- * tokens in a row is within fp32. With 16-bit tensors, states
- * and what lies between enter the products with 17 bits (off by 2^-18), those that
- * only reach bf16 results with 8; with fp32 tensors all keep 24. A NaN or infinite value of a token may reach all tokens from its
- * sequence's 64 (counted from its first; 32 for fp16, fp32 and K > 128) on.
+ * tokens in a row is within fp32. States and what lies between enter the products with
+ * 24 bits; with 16-bit tensors and no `saved` with 17, as does what only reaches y. A NaN or infinite value of a
+ * token may reach the up to 63 tokens before it that share its 64 (counted from its
+ * sequence's first; 32 for fp16, fp32 and K > 128), and all after it, of its head.
  * TG_ERR_UNSUPPORTED for K > 256, row strides of 2^25 elements or more, 2^23 or more
  * pairs of a value head and 64 (32) tokens, and 2^22 or more of a sequence, a value
  * head and 16 columns. */

@@ -8,11 +8,12 @@ taken from the inputs. On the way from one chunk's state to the next lie fewer t
 STEPS = 32 roundings (the parts of S, v - k S, the factors of rows, the parts of the
 right side, X by substitution in 16 steps and two block products, the corrections'
 factors and parts, the sums in the matrix instructions), each of u relative: 2^-18
-where operands are two bf16 parts (prompts of 16-bit tensors), 2^-24 else. So a
-state after n chunks is off by n * STEPS * KAPPA * u of its norm and of what was
+where operands are two bf16 parts (prompts of 16-bit tensors), 2^-24 else. So a state after n chunks is off by n * STEPS * KAPPA * u of its norm and of what was
 added to it, and the gradients, which go through both walks, by twice that with
-KAPPA^2. bf16 outputs are products of first parts alone, three operands of 2^-9; every
-output adds half a step of its type. A single element is held to 8 times that of the
+KAPPA^2. y of 16-bit tensors is made of products of two parts, three operands of 2^-17
+(a part's rounding and the dropped product of two second parts); the pairs' part of
+dq and dk of as many parts as an input has, 2^-9 for bf16. Every output adds half a
+step of its type. A single element is held to 8 times that of the
 root mean square (or of itself where it is larger): four standard deviations of a
 sum of many roundings, twice. Sums over all tokens (dA, ddt_bias) cancel: they are
 held against the sum of the magnitudes."""
@@ -102,16 +103,13 @@ def near(name, got, want, rel, dtype, size=None):
     assert worst <= 8 * rel + 2 * half, "%s: an element off by %.3g, allowed %.3g" % (name, worst, 8 * rel + 2 * half)
 
 
-def allowed(dtype, kap, chunks, gradient=False, train=False, first_parts=False):
-    """Relative error of an output, without its own rounding."""
-    u = E if train or dtype is torch.float32 else 2.0 ** -18
-    rel = chunks * STEPS * kap * u
-    if gradient:
-        rel = 2 * chunks * STEPS * kap * kap * u
-    if first_parts and dtype is torch.bfloat16:
-        rel += 3 * 2.0 ** -9
-    elif first_parts and dtype is torch.float16:
-        rel += 3 * 2.0 ** -18
+def allowed(dtype, kap, chunks, gradient=False, only=None, prompt=False):
+    """Relative error of an output, without its own rounding; ``only``: "y" or "qk",
+    what is made of fewer parts; ``prompt``: without training."""
+    u = 2.0 ** -18 if prompt and dtype is not torch.float32 else E
+    rel = 2 * chunks * STEPS * kap * kap * u if gradient else chunks * STEPS * kap * u
+    if only and dtype is not torch.float32:
+        rel += 3 * (2.0 ** -9 if only == "qk" and dtype is torch.bfloat16 else 2.0 ** -17)
     return rel
 
 

@@ -100,11 +100,11 @@ def test_forward(case):
     _, _, _, y, state, _, kap, chunks = c.want()
     got, s = tg.gated_delta_rule(*c.args(), return_state=True, **c.more())
     shape = c.dev(c.v, 0).shape
-    D.near("y", got, y.reshape(shape), D.allowed(c.dtype, kap, chunks, first_parts=True), c.dtype)
-    D.near("state", s, state, D.allowed(c.dtype, kap, chunks), F32)
+    D.near("y", got, y.reshape(shape), D.allowed(c.dtype, kap, chunks, only="y", prompt=True), c.dtype)
+    D.near("state", s, state, D.allowed(c.dtype, kap, chunks, prompt=True), F32)
     t, s2, saved = tg.gated_delta_rule_train(*c.args(), return_state=True, **c.more())
-    D.near("y", t, y.reshape(shape), D.allowed(c.dtype, kap, chunks, train=True, first_parts=True), c.dtype)
-    D.near("state", s2, state, D.allowed(c.dtype, kap, chunks, train=True), F32)
+    D.near("y", t, y.reshape(shape), D.allowed(c.dtype, kap, chunks, only="y"), c.dtype)
+    D.near("state", s2, state, D.allowed(c.dtype, kap, chunks), F32)
     again, s3 = tg.gated_delta_rule(*c.args(), return_state=True, **c.more())
     assert torch.equal(got, again) and torch.equal(s, s3)
 
@@ -125,8 +125,8 @@ def test_backward(case):
     _, saved = tg.gated_delta_rule_train(*c.args(), **c.more())
     more = c.more()
     got = tg.gated_delta_rule_backward(c.dev(c.dy), *c.args(), saved, dstate=up(c.dstate), **more)
-    rel = D.allowed(c.dtype, kap, chunks, gradient=True, train=True)
-    part = D.allowed(c.dtype, kap, chunks, gradient=True, train=True, first_parts=True)
+    rel = D.allowed(c.dtype, kap, chunks, gradient=True)
+    part = D.allowed(c.dtype, kap, chunks, gradient=True, only="qk")
     shaped = lambda w, t: w.reshape(c.dev(t, 0).shape)  # noqa: E731
     for name, at, t, u in (("dq", 0, c.q, units[0]), ("dk", 1, c.k, units[1])):
         size = None if c.plain else shaped(D.unit_size(x[at].detach(), u), t)
@@ -257,13 +257,13 @@ def test_no_decay_identical_keys_and_zero_keys():
         c.A = torch.zeros(1)
         _, _, _, y, state, _, kap, chunks = c.want()
         got, s = tg.gated_delta_rule(*c.args(), return_state=True, **c.more())
-        D.near("y", got, y.reshape(got.shape), D.allowed(c.dtype, kap, chunks, first_parts=True), c.dtype)
-        D.near("state", s, state, D.allowed(c.dtype, kap, chunks), F32)
+        D.near("y", got, y.reshape(got.shape), D.allowed(c.dtype, kap, chunks, only="y", prompt=True), c.dtype)
+        D.near("state", s, state, D.allowed(c.dtype, kap, chunks, prompt=True), F32)
         c.k = torch.zeros_like(c.k)
         _, _, _, y, state, _, _, _ = c.want()
         got, s = tg.gated_delta_rule(*c.args(), return_state=True, **c.more())
-        D.near("y", got, y.reshape(got.shape), D.allowed(c.dtype, 1.0, chunks, first_parts=True), c.dtype)
-        D.near("state", s, state, D.allowed(c.dtype, 1.0, chunks), F32)
+        D.near("y", got, y.reshape(got.shape), D.allowed(c.dtype, 1.0, chunks, only="y", prompt=True), c.dtype)
+        D.near("state", s, state, D.allowed(c.dtype, 1.0, chunks, prompt=True), F32)
 
 
 def test_decays_at_both_ends():
