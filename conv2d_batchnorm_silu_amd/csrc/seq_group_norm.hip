@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kBlockRows = 32;  // rows with one x0
 constexpr int kThreads = 256;
+constexpr int kAhead = 4;  // rows on their way in a thread
 
 struct GroupArgs {
     const void *x, *z, *dy;
@@ -199,10 +200,18 @@ __device__ __forceinline__ void join_chunks(const GroupArgs& a, int64_t n, float
         const int g = g0 + threadIdx.x / P;
         Moments m = {0.0f, 0.0f, 0.0f};
         if (g < a.G)
-            for (int c = lane; c < a.chunks; c += P) {
-                const float* s = a.stats + ((n * a.chunks + c) * a.G + g) * 2;
-                const int64_t left = a.L - (int64_t)c * a.rows;
-                join(m, Moments{per * (float)(left < a.rows ? left : a.rows), s[0], s[1]});
+            for (int c0 = lane; c0 < a.chunks; c0 += 4 * P) {
+                float2 s[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    s[u] = ((const float2*)a.stats)[(n * a.chunks + imin(c0 + u * P, a.chunks - 1)) * a.G + g];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int c = c0 + u * P;
+                    const int64_t left = a.L - (int64_t)c * a.rows;
+                    if (c < a.chunks)
+                        join(m, Moments{per * (float)(left < a.rows ? left : a.rows), s[u].x, s[u].y});
+                }
             }
         for (int d = 1; d < P; d *= 2)
             join(m, Moments{__shfl_xor(m.n, d), __shfl_xor(m.mean, d), __shfl_xor(m.m2, d)});
@@ -218,6 +227,28 @@ template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void map_apply(const GroupArgs a) {
     extern __shared__ float stat[];
     const Place<V> p(a);
+    const int64_t row0 = p.n * a.L + p.first;
+    Vec<T, V> x[kAhead], z[kAhead];
+    const auto fetch = [&](int v, int r) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (r + u * p.TY < p.rows) {
+                const int64_t row = row0 + r + u * p.TY;
+                x[u].load((const T*)a.x + row * a.xs + v * V);
+                if (a.z) z[u].load((const T*)a.z + row * a.zs + v * V);
+            }
+    };
+    float gamma[V], beta[V];
+    const auto weights = [&](int v) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            gamma[e] = a.gamma[v * V + e];
+            beta[e] = a.beta ? a.beta[v * V + e] : 0.0f;
+        }
+    };
+    // The first rows and weights are on their way while the statistics are joined.
+    fetch(p.tx, p.ty);
+    weights(p.tx);
     join_chunks(a, p.n, stat);
     if (p.chunk == 0 && a.mean)
         for (int g = threadIdx.x; g < a.G; g += kThreads) {
@@ -226,43 +257,38 @@ __global__ __launch_bounds__(kThreads) void map_apply(const GroupArgs a) {
         }
     if (p.ty >= p.TY) return;
     const int Cg = a.C / a.G;
-    const int64_t row0 = p.n * a.L + p.first;
     for (int v = p.tx; v < a.C / V; v += p.TX) {
-        const int c = v * V, g = c / Cg;
-        const float mean = stat[2 * g], rstd = stat[2 * g + 1];
-        float ga[V], be[V];
+        const int c = v * V;
+        float mean[V], ga[V], be[V];
+        int g = c / Cg, left = (g + 1) * Cg - c;  // the group, and its channels from c + e on
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            ga[e] = a.gamma[c + e] * rstd;
-            be[e] = a.beta ? a.beta[c + e] : 0.0f;
+        for (int e = 0; e < V; ++e, --left) {
+            if (left == 0) ++g, left = Cg;
+            mean[e] = stat[2 * g];
+            ga[e] = gamma[e] * stat[2 * g + 1];
+            be[e] = beta[e];
         }
-        const auto one = [&](int r, const Vec<T, V>& xr, const Vec<T, V>& zr) {
-            float x[V], z[V], o[V];
-            xr.values(x);
-            if (a.z) zr.values(z);
+        if (v + p.TX < a.C / V) weights(v + p.TX);
+        for (int r = p.ty; r < p.rows; r += kAhead * p.TY) {
+            float o[kAhead][V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                o[e] = activation(a.silu, __builtin_fmaf(x[e] - mean, ga[e], be[e]));
-                if (a.z) o[e] *= silu_f32(z[e]);
+            for (int u = 0; u < kAhead; ++u) {
+                float xv[V], zv[V];
+                x[u].values(xv);
+                if (a.z) z[u].values(zv);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    o[u][e] = activation(a.silu, __builtin_fmaf(xv[e] - mean[e], ga[e], be[e]));
+                    if (a.z) o[u][e] *= silu_f32(zv[e]);
+                }
             }
-            store_f32<T, V>((T*)a.y + (row0 + r) * a.C + c, o);
-        };
-        int r = p.ty;
-        for (; r + 3 * p.TY < p.rows; r += 4 * p.TY) {
-            Vec<T, V> x[4], z[4];
+            // The next ones, of this column or the thread's next.
+            if (r + kAhead * p.TY < p.rows) fetch(v, r + kAhead * p.TY);
+            else if (v + p.TX < a.C / V) fetch(v + p.TX, p.ty);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                x[u].load((const T*)a.x + (row0 + r + u * p.TY) * a.xs + c);
-                if (a.z) z[u].load((const T*)a.z + (row0 + r + u * p.TY) * a.zs + c);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) one(r + u * p.TY, x[u], z[u]);
-        }
-        for (; r < p.rows; r += p.TY) {
-            Vec<T, V> x, z;
-            x.load((const T*)a.x + (row0 + r) * a.xs + c);
-            if (a.z) z.load((const T*)a.z + (row0 + r) * a.zs + c);
-            one(r, x, z);
+            for (int u = 0; u < kAhead; ++u)
+                if (r + u * p.TY < p.rows)
+                    store_f32<T, V>((T*)a.y + (row0 + r + u * p.TY) * a.C + c, o[u]);
         }
     }
 }
@@ -272,11 +298,12 @@ template <int V>
 struct Slopes {
     float dv[V], h[V], dz[V];
     __device__ __forceinline__ void make(const GroupArgs& a, const float (&x)[V], const float (&z)[V],
-                                         const float (&dy)[V], float mean, float rstd,
-                                         const float (&ga)[V], const float (&be)[V]) {
+                                         const float (&dy)[V], const float (&mean)[V],
+                                         const float (&rstd)[V], const float (&ga)[V],
+                                         const float (&be)[V]) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            h[e] = (x[e] - mean) * rstd;
+            h[e] = (x[e] - mean[e]) * rstd[e];
             float act, slope, d = dy[e];
             activation_grad(a.silu, __builtin_fmaf(h[e], ga[e], be[e]), act, slope);
             if (a.z) {
@@ -300,11 +327,14 @@ __global__ __launch_bounds__(kThreads) void map_sums(const GroupArgs a) {
         const int v = base + p.tx;
         float s[V] = {}, q[V] = {};
         if (p.ty < p.TY && v < a.C / V) {
-            const int c = v * V, g = c / Cg;
-            const float mean = a.mean[p.n * a.G + g], rstd = a.rstd[p.n * a.G + g];
-            float ga[V], be[V];
+            const int c = v * V;
+            float ga[V], be[V], mean[V], rstd[V];
+            int g = c / Cg, left = (g + 1) * Cg - c;
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
+            for (int e = 0; e < V; ++e, --left) {
+                if (left == 0) ++g, left = Cg;
+                mean[e] = a.mean[p.n * a.G + g];
+                rstd[e] = a.rstd[p.n * a.G + g];
                 ga[e] = a.gamma[c + e];
                 be[e] = a.beta ? a.beta[c + e] : 0.0f;
             }
@@ -380,6 +410,34 @@ __global__ __launch_bounds__(kThreads) void map_grads(const GroupArgs a) {
     extern __shared__ float stat[];  // [G][2]: the groups' means of g and of g h
     const Place<V> p(a);
     const int Cg = a.C / a.G;
+    const int64_t row0 = p.n * a.L + p.first;
+    Vec<T, V> x[2], z[2], d[2];
+    const auto fetch = [&](int v, int r) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (r + u * p.TY < p.rows) {
+                const int64_t row = row0 + r + u * p.TY;
+                x[u].load((const T*)a.x + row * a.xs + v * V);
+                d[u].load((const T*)a.dy + row * a.ds + v * V);
+                if (a.z) z[u].load((const T*)a.z + row * a.zs + v * V);
+            }
+    };
+    float mean[V], rstd[V], ga[V], be[V];
+    const auto weights = [&](int v) {
+        const int c = v * V;
+        int g = c / Cg, left = (g + 1) * Cg - c;  // the group, and its channels from c + e on
+#pragma unroll
+        for (int e = 0; e < V; ++e, --left) {
+            if (left == 0) ++g, left = Cg;
+            mean[e] = a.mean[p.n * a.G + g];
+            rstd[e] = a.rstd[p.n * a.G + g];
+            ga[e] = a.gamma[c + e];
+            be[e] = a.beta ? a.beta[c + e] : 0.0f;
+        }
+    };
+    // On their way while the sums are joined.
+    fetch(p.tx, p.ty);
+    weights(p.tx);
     {
         const float inv = 1.0f / ((float)Cg * (float)a.L);
         const int P = lanes_of_group(a.G), lane = threadIdx.x % P;
@@ -387,10 +445,14 @@ __global__ __launch_bounds__(kThreads) void map_grads(const GroupArgs a) {
             const int g = g0 + threadIdx.x / P;
             float s = 0.0f, q = 0.0f;
             if (g < a.G)
-                for (int c = lane; c < a.chunks; c += P) {
-                    const float* at = a.stats + ((p.n * a.chunks + c) * a.G + g) * 2;
-                    s += at[0];
-                    q += at[1];
+                for (int c0 = lane; c0 < a.chunks; c0 += 4 * P) {
+                    float2 t[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        t[u] = ((const float2*)a.stats)[(p.n * a.chunks + imin(c0 + u * P, a.chunks - 1)) * a.G + g];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (c0 + u * P < a.chunks) s += t[u].x, q += t[u].y;
                 }
             for (int d = 1; d < P; d *= 2) s += __shfl_xor(s, d), q += __shfl_xor(q, d);
             if (g < a.G && lane == 0) stat[2 * g] = s * inv, stat[2 * g + 1] = q * inv;
@@ -398,47 +460,41 @@ __global__ __launch_bounds__(kThreads) void map_grads(const GroupArgs a) {
         __syncthreads();
     }
     if (p.ty >= p.TY) return;
-    const int64_t row0 = p.n * a.L + p.first;
     for (int v = p.tx; v < a.C / V; v += p.TX) {
-        const int c = v * V, g = c / Cg;
-        const float mean = a.mean[p.n * a.G + g], rstd = a.rstd[p.n * a.G + g];
-        const float m1 = stat[2 * g], m2 = stat[2 * g + 1];
-        float ga[V], be[V];
+        const int c = v * V;
+        if (v != p.tx) weights(v);
+        float m1[V], m2[V];
+        int g = c / Cg, left = (g + 1) * Cg - c;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            ga[e] = a.gamma[c + e];
-            be[e] = a.beta ? a.beta[c + e] : 0.0f;
+        for (int e = 0; e < V; ++e, --left) {
+            if (left == 0) ++g, left = Cg;
+            m1[e] = stat[2 * g];
+            m2[e] = stat[2 * g + 1];
         }
-        const auto fetch = [&](int r, Vec<T, V>& x, Vec<T, V>& z, Vec<T, V>& d) {
-            x.load((const T*)a.x + (row0 + r) * a.xs + c);
-            d.load((const T*)a.dy + (row0 + r) * a.ds + c);
-            if (a.z) z.load((const T*)a.z + (row0 + r) * a.zs + c);
-        };
-        const auto one = [&](int r, const Vec<T, V>& xr, const Vec<T, V>& zr, const Vec<T, V>& dr) {
-            float x[V], z[V], dy[V], o[V];
-            xr.values(x);
-            dr.values(dy);
-            if (a.z) zr.values(z);
-            Slopes<V> t;
-            t.make(a, x, z, dy, mean, rstd, ga, be);
+        for (int r = p.ty; r < p.rows; r += 2 * p.TY) {
+            Slopes<V> t[2];
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                o[e] = rstd * (__builtin_fmaf(t.dv[e], ga[e], -m1) - t.h[e] * m2);
-            store_f32<T, V>((T*)a.y + (row0 + r) * a.C + c, o);
-            if (a.z) store_f32<T, V>((T*)a.dz + (row0 + r) * a.C + c, t.dz);
-        };
-        int r = p.ty;
-        for (; r + p.TY < p.rows; r += 2 * p.TY) {
-            Vec<T, V> x[2], z[2], d[2];
-            fetch(r, x[0], z[0], d[0]);
-            fetch(r + p.TY, x[1], z[1], d[1]);
-            one(r, x[0], z[0], d[0]);
-            one(r + p.TY, x[1], z[1], d[1]);
-        }
-        if (r < p.rows) {
-            Vec<T, V> x, z, d;
-            fetch(r, x, z, d);
-            one(r, x, z, d);
+            for (int u = 0; u < 2; ++u) {
+                float xv[V], zv[V], dv[V];
+                x[u].values(xv);
+                d[u].values(dv);
+                if (a.z) z[u].values(zv);
+                t[u].make(a, xv, zv, dv, mean, rstd, ga, be);
+            }
+            // The next ones, of this column or the thread's next.
+            if (r + 2 * p.TY < p.rows) fetch(v, r + 2 * p.TY);
+            else if (v + p.TX < a.C / V) fetch(v + p.TX, p.ty);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (r + u * p.TY < p.rows) {
+                    const int64_t at = (row0 + r + u * p.TY) * a.C + c;
+                    float o[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        o[e] = rstd[e] * (__builtin_fmaf(t[u].dv[e], ga[e], -m1[e]) - t[u].h[e] * m2[e]);
+                    store_f32<T, V>((T*)a.y + at, o);
+                    if (a.z) store_f32<T, V>((T*)a.dz + at, t[u].dz);
+                }
         }
     }
 }
@@ -545,7 +601,10 @@ __global__ __launch_bounds__(kThreads) void heads(const GroupArgs a) {
             float s = 0.0f, q = 0.0f;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                t[j].make(a, x[j], z[j], dy[j], mean0, rstd0, ga[j], be[j]);
+                float m[V], q_[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) m[e] = mean0, q_[e] = rstd0;
+                t[j].make(a, x[j], z[j], dy[j], m, q_, ga[j], be[j]);
                 const bool ok = (j * P + lane) * V < D;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
@@ -622,12 +681,14 @@ GroupPlan group_plan(const tg_group_norm_args& a, bool back) {
         p.units = a.N < most ? a.N : most;
         return p;
     }
-    // About 2048 workgroups, none of less than 8 KB of x (16-bit) if there are enough
-    // rows; at most 256 chunks to join.
-    const int64_t most_rows = ceil_div(a.L, 256);
-    int64_t rows = ceil_div(a.L * a.N, 2048), least = ceil_div(4096, a.C);
+    // About 1024 workgroups, none of less than 2048 elements if there are enough rows, in
+    // whole rounds of their threads (16-byte vectors); at most 256 chunks to join.
+    const int64_t cols = ceil_div(a.C, 16 / (int64_t)elem_bytes(a.dtype));
+    const int64_t round = kThreads / (cols < kThreads ? cols : kThreads), most = ceil_div(a.L, 256);
+    int64_t rows = ceil_div(a.L * a.N, 1024), least = ceil_div(2048, a.C);
     if (rows < least) rows = least;
-    if (rows < most_rows) rows = most_rows;
+    if (rows < most) rows = most;
+    rows = ceil_div(rows, round) * round;
     if (rows > a.L) rows = a.L;
     p.rows = (int)rows;
     p.chunks = (int)ceil_div(a.L, rows);
@@ -665,48 +726,60 @@ hipError_t heads_typed(const GroupArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
+// V: of what lies in one group (heads, statistics); W: of a row.
 template <typename T, int V>
-hipError_t forward_typed(const GroupArgs& a, const GroupPlan& p, hipStream_t st) {
-    if (p.heads) return heads_typed<T, V, false>(a, st);
-    const unsigned grid = (unsigned)(a.N * a.chunks);
-    map_stats<T, V><<<grid, kThreads, 0, st>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    map_apply<T, V><<<grid, kThreads, 2 * a.G * sizeof(float), st>>>(a);
+hipError_t stats_typed(const GroupArgs& a, const GroupPlan& p, bool back, hipStream_t st) {
+    if (p.heads) return back ? heads_typed<T, V, true>(a, st) : heads_typed<T, V, false>(a, st);
+    if (!back) map_stats<T, V><<<(unsigned)(a.N * a.chunks), kThreads, 0, st>>>(a);
     return hipGetLastError();
 }
-template <typename T, int V>
-hipError_t backward_typed(const GroupArgs& a, const GroupPlan& p, hipStream_t st) {
-    if (p.heads) return heads_typed<T, V, true>(a, st);
+template <typename T, int W>
+hipError_t sweeps_typed(const GroupArgs& a, bool back, hipStream_t st) {
     const unsigned grid = (unsigned)(a.N * a.chunks);
-    map_sums<T, V><<<grid, kThreads, 0, st>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    map_grads<T, V><<<grid, kThreads, 2 * a.G * sizeof(float), st>>>(a);
-    return hipGetLastError();
-}
-template <typename T>
-hipError_t group_typed(int V, const GroupArgs& a, const GroupPlan& p, bool back, hipStream_t st) {
-    switch (V) {
-        case 8:
-            if constexpr (sizeof(T) == 2)
-                return back ? backward_typed<T, 8>(a, p, st) : forward_typed<T, 8>(a, p, st);
-        case 4: return back ? backward_typed<T, 4>(a, p, st) : forward_typed<T, 4>(a, p, st);
-        case 2: return back ? backward_typed<T, 2>(a, p, st) : forward_typed<T, 2>(a, p, st);
-        default: return back ? backward_typed<T, 1>(a, p, st) : forward_typed<T, 1>(a, p, st);
+    if (back) {
+        map_sums<T, W><<<grid, kThreads, 0, st>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        map_grads<T, W><<<grid, kThreads, 2 * a.G * sizeof(float), st>>>(a);
+    } else {
+        map_apply<T, W><<<grid, kThreads, 2 * a.G * sizeof(float), st>>>(a);
     }
+    return hipGetLastError();
 }
+#define TG_WIDTHS(N, X)                     \
+    do {                                    \
+        if constexpr (sizeof(T) == 2)       \
+            if (N == 8) X(8);               \
+        if (N == 4) X(4);                   \
+        if (N == 2) X(2);                   \
+        if (N == 1) X(1);                   \
+    } while (0)
+template <typename T>
+hipError_t group_typed(int V, int W, const GroupArgs& a, const GroupPlan& p, bool back, hipStream_t st) {
+    hipError_t e = hipErrorInvalidConfiguration;
+#define TG_X(N) e = stats_typed<T, N>(a, p, back, st)
+    TG_WIDTHS(V, TG_X);
+#undef TG_X
+    if (e != hipSuccess || p.heads) return e;
+#define TG_X(N) e = sweeps_typed<T, N>(a, back, st)
+    TG_WIDTHS(W, TG_X);
+#undef TG_X
+    return e;
+}
+#undef TG_WIDTHS
 hipError_t group_run(tg_dtype dt, const GroupArgs& a, const GroupPlan& p, bool back, hipStream_t st) {
     const size_t e = elem_bytes(dt);
     Widest w;
-    w.len(a.C / a.G), w.len(a.xs), w.ptr(a.x, e), w.ptr(a.y, e);
+    w.len(a.C), w.len(a.xs), w.ptr(a.x, e), w.ptr(a.y, e);
     if (a.z) w.len(a.zs), w.ptr(a.z, e);
     if (back) w.len(a.ds), w.ptr(a.dy, e);
     if (back && a.z) w.ptr(a.dz, e);
+    const int W = w.width((int)(16 / e));
+    w.len(a.C / a.G);
     const int V = w.width((int)(16 / e));
-    if (dt == TG_F32) return group_typed<float>(V, a, p, back, st);
-    if (dt == TG_BF16) return group_typed<bf16>(V, a, p, back, st);
-    return group_typed<f16>(V, a, p, back, st);
+    if (dt == TG_F32) return group_typed<float>(V, W, a, p, back, st);
+    if (dt == TG_BF16) return group_typed<bf16>(V, W, a, p, back, st);
+    return group_typed<f16>(V, W, a, p, back, st);
 }
 
 }  // namespace
