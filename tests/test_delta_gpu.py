@@ -442,3 +442,47 @@ def test_many_sequences():
         cut = [t[lo:lo + 5] for t in (q, k, v, dt)]
         ys, ss = tg.gated_delta_rule(*cut, A, beta[lo:lo + 5], return_state=True)
         assert torch.equal(y[lo:lo + 5], ys) and torch.equal(state[lo:lo + 5], ss)
+
+
+def test_no_tokens():
+    """Dense batches of no token, and no sequence to step: states pass through."""
+    z = lambda *s: torch.zeros(*s, device="cuda", dtype=F16)  # noqa: E731
+    A, init = torch.ones(2, device="cuda"), torch.randn(3, 2, 8, 4, device="cuda")
+    args = (z(3, 0, 1, 8), z(3, 0, 1, 8), z(3, 0, 2, 4), z(3, 0, 2), A, z(3, 0, 2))
+    y, state = tg.gated_delta_rule(*args, initial_state=init, return_state=True)
+    assert y.shape == (3, 0, 2, 4) and torch.equal(state, init)
+    y, saved = tg.gated_delta_rule_train(*args, initial_state=init)
+    d = tg.gated_delta_rule_backward(y, *args, saved, initial_state=init, dstate=init * 2)
+    assert torch.equal(d.dinitial_state, init * 2) and not d.dA.any()
+    step = tg.gated_delta_rule_step(*[t if t.dim() == 1 else t[0] for t in args], init.clone())
+    assert step.shape == (0, 2, 4)
+
+
+def test_state_gradient_without_an_initial_state():
+    c = Case(([70, 33], True, 1, 2, 24, 16, "f32", True, False, 0))
+    c.initial = None
+    x, bias, _, y, state, _, kap, chunks = c.want(True)
+    want = torch.autograd.grad((y * c.dy.double()).sum() + (state * c.dstate.double()).sum(), x[2])
+    _, saved = tg.gated_delta_rule_train(*c.args(), **c.more())
+    got = tg.gated_delta_rule_backward(c.dev(c.dy), *c.args(), saved, dstate=up(c.dstate), **c.more())
+    D.near("dv", got.dv, want[0], D.allowed(F32, kap, chunks, gradient=True), F32)
+
+
+def test_two_streams_at_once():
+    """Two calls in flight share nothing."""
+    a, b = Case(([500], False, 2, 4, 64, 64, "bf16", False, False, 0)), Case(([400], False, 1, 2, 96, 40, "f16", False, False, 0), 1)
+    sets = [(c.args(), c.more(), c.dev(c.dy)) for c in (a, b)]
+
+    def work(k):
+        args, more, dy = sets[k]
+        y, saved = tg.gated_delta_rule_train(*args, **more)
+        return [y] + [t for t in tg.gated_delta_rule_backward(dy, *args, saved, **more) if t is not None]
+    want = [work(0), work(1)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], [[], []]
+    for _ in range(3):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k] = work(k)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for k in range(2) for p, q in zip(got[k], want[k]))
