@@ -3,7 +3,8 @@
 The compute path is a C-ABI shared library (``libtgconv.so``, built from
 ``csrc/``) of hand-written HIP kernels; ``binding`` wraps it with ctypes and
 uses PyTorch only for device memory and streams; ``sequence`` does the same
-for the sequence operators (layer norm, causal convolution, selective scan).
+for the sequence operators (layer norm, group norm, causal convolution, selective
+scan, gated delta rule).
 ``inputs`` holds the seeded
 synthetic data recipes shared by tests and the benchmark.
 

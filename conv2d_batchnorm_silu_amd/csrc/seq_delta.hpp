@@ -10,9 +10,9 @@
 // fp32's range, which fp16 parts would not have.
 //
 // Prompts of 16-bit tensors that keep nothing for training take two parts (kMid: 17
-// bits, 2^-18 of the value): the states, off by 2 to 6e-6 of their norm, go on to
-// tokens that are rounded to 8 or 11 bits, and 4 x 4096 tokens of 16 heads take 164 us
-// in place of 208. In training it left dA and ddt_bias, sums over all tokens that
+// bits, 2^-18 of the value): the states, off by 2 to 5e-6 of their norm, go on to
+// tokens that are rounded to 8 or 11 bits, and 4 x 4096 tokens of 16 heads take 185 us
+// in place of 220. In training it left dA and ddt_bias, sums over all tokens that
 // cancel, off by up to 6e-5. Products that only reach y take two parts of 16-bit tensors
 // (a single one left bf16 outputs off by 1.6 times their rounding), those that only
 // reach the gradients of q and k as many as an input has.
@@ -308,8 +308,8 @@ constexpr int prep_bytes(int C, int parts) { return kScales * C * 4 + frag_count
 // What the passes keep for a chunk (`saved`: the state before it and its corrections;
 // `back`: the gradient of the state after it and of v): for each 16 columns of V the
 // accumulators of KP/16 and C/16 tiles as they are, four floats of a lane after the
-// other, so that a wave writes a kilobyte at a time (rows of V took 54 of 178 us of the
-// backward walk). In floats:
+// other, so that a wave writes a kilobyte at a time (2 x 2048 tokens of 16 heads: the
+// backward walk takes 107 us, with rows of V 178). In floats:
 inline __host__ __device__ int64_t kept_floats(int V, int KP, int C) {
     return (int64_t)((V + 15) / 16) * (KP / 16 + C / 16) * 256;
 }
@@ -428,12 +428,14 @@ __device__ __forceinline__ float decay_between(double hi, double lo) {
 // split into parts once for all columns), a chunk ahead and the loads another
 // chunk ahead, and form what the recurrence does not wait for. A wave loads the
 // prepared fragments of its own tokens to registers as soon as it has used the last
-// chunk's. 4 x 4096 tokens of 16 heads, bf16: a wave for 16 whole columns and four that
-// load 215 us, four waves that share S and everything else 206, with helpers FWD_US.
+// chunk's. 4 x 4096 tokens of 16 heads of 128 x 128, bf16: a wave for 16 whole columns and
+// four that load 215 us, four waves that share S and everything else 230, with helpers
+// 164 (185 since y is made of two parts): 2.9 us a chunk, of which a carrying wave
+// computes for about 40% and waits for LDS, matrix results and barriers for the rest.
 constexpr int slice_of(int in, int KP) { return in * KP > 512 ? 16 : 32; }
 
 // A barrier for what lies in LDS: __syncthreads would also wait for the loads and
-// stores of global memory that are on their way (258 us in place of what it takes now).
+// stores of global memory that are on their way.
 __device__ __forceinline__ void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();

@@ -9,6 +9,10 @@ namespace {
 
 // ---- the chunks' own gradients
 //
+// 2 x 2048 tokens of 16 heads of 128 x 128, bf16: 137 us, a wave on each SIMD (120 KB of
+// LDS), half of its time waiting: the next block of V in registers while one is worked
+// on took 133 there but 34 for 22 on 64 columns, eight waves 238 (spilled).
+//
 // One workgroup for a chunk and key head; its value heads one after another, dq
 // and dk added up in registers. Wave w has the 16 rows (tokens) of tile w % (C/16)
 // and, of each KB columns of q and k, KW. V goes by in blocks of 32.

@@ -1,5 +1,6 @@
-"""Sequence operators of libtgconv.so (include/tg_sequence.h): layer norm, the
-short causal convolution with SiLU and the selective state space scan.
+"""Sequence operators of libtgconv.so (include/tg_sequence.h): layer norm, group
+norm, the short causal convolution with SiLU, the selective state space scan and
+the gated delta rule.
 
 Like ``binding``, this is argument checking and ctypes marshalling: the HIP
 kernels behind the C ABI compute every step, and PyTorch supplies device
@@ -110,7 +111,7 @@ def _lib():
         return _loaded
     lib = library()
     f, psz = ctypes.c_float, ctypes.POINTER(sz)
-    conv = scan = vp  # structures, or bytes of their layout
+    conv = scan = delta = group = vp  # structures, or bytes of their layout
     grads = ctypes.POINTER(_ScanGrads)
     lib.tg_layer_norm.argtypes = [vp, i64, vp, i64, vp, vp, f, i64, i32, i32, vp, vp, vp, vp, vp]
     lib.tg_layer_norm_backward_workspace.argtypes = [i64, i32, i32, psz]
@@ -125,13 +126,13 @@ def _lib():
     lib.tg_selective_scan.argtypes = [scan, vp, sz, vp, sz, vp]
     lib.tg_selective_scan_backward.argtypes = [scan, grads, vp, sz, vp, sz, vp]
     lib.tg_selective_scan_step.argtypes = [scan, vp, i64, vp, vp]
-    delta = group = vp
     lib.tg_group_norm_sizes.argtypes = [group, psz, psz]
     lib.tg_group_norm.argtypes = [group, vp, sz, vp]
     lib.tg_group_norm_backward.argtypes = [group, ctypes.POINTER(_GroupNormGrads), vp, sz, vp]
     lib.tg_gated_delta_rule_sizes.argtypes = [delta, psz, psz, psz]
     lib.tg_gated_delta_rule.argtypes = [delta, vp, sz, vp, sz, vp]
-    lib.tg_gated_delta_rule_backward.argtypes = [delta, ctypes.POINTER(_DeltaGrads), vp, sz, vp, sz, vp]
+    lib.tg_gated_delta_rule_backward.argtypes = [delta, ctypes.POINTER(_DeltaGrads), vp, sz, vp,
+                                                 sz, vp]
     lib.tg_gated_delta_rule_step.argtypes = [delta, vp, i64, vp, vp]
     _loaded = lib
     return lib

@@ -1,12 +1,13 @@
 /*
  * tg_sequence.h -- C ABI of the sequence operators of libtgconv.so for AMD
- * Instinct MI355X (gfx950): layer norm, the short causal convolution with
- * SiLU, and the selective state space scan, each for prompts, for training
- * (forward and backward) and, where there is a state, for single tokens.
+ * Instinct MI355X (gfx950): layer norm, group norm, the short causal convolution
+ * with SiLU, the selective state space scan and the gated delta rule, each for
+ * prompts, for training (forward and backward) and, where there is a state, for
+ * single tokens.
  *
- * Tensors. Activations (x, y, z, dt, B, C and their gradients) share one
- * dtype: TG_F16, TG_BF16 or TG_F32. Parameters, statistics and scan states
- * are fp32. All arithmetic and all sums are fp32; every activation result is
+ * Tensors. Activations (x, y, z, dt, B, C, q, k, v, beta and their gradients) share
+ * one dtype: TG_F16, TG_BF16 or TG_F32. Parameters, statistics and states of the scan
+ * and the delta rule are fp32. All arithmetic and all sums are fp32; every activation result is
  * rounded once, to nearest even. Channels are contiguous; a row is one token.
  *
  * Sequences. A batch is dense or packed (tg_seqs):
