@@ -864,15 +864,23 @@ def _delta_args(q, k, v, dt, A, beta, dt_bias, softplus, sigmoid, normalize, sca
                 seqs, packed, dev):
     """A function of (y's rows, address of the final states) that gives the
     call's arguments; value heads, V; the states' shape."""
-    d, dtype, lead = _dtype(v, "v"), v.dtype, v.shape[:-2]
-    HV, V = _heads(v, "v", lead)
-    HK, K = _heads(_some(k, "k"), "k", lead)
+    d, dtype, shape = _dtype(v, "v"), v.dtype, v.shape
+    lead, dims = shape[:-2], len(shape)
+    HV, V = shape[-2], shape[-1]
+    # Each tensor of heads in full only if something is wrong with it.
+    if HV < 1 or V < 1 or (HV > 1 and v.stride(-2) != V):
+        _heads(v, "v", lead)
+    if k is None or k.dim() != dims or k.shape[:-2] != lead or k.shape[-1] < 1 or k.shape[-2] < 1:
+        _heads(_some(k, "k"), "k", lead)
+    HK, K = k.shape[-2], k.shape[-1]
+    if HK > 1 and k.stride(-2) != K:
+        _heads(k, "k", lead)
     if HV % HK:
         raise ValueError("the %d heads of k must divide the %d of v" % (HK, HV))
-    held = (seqs[0], HV, K, V)
-    if q is not None and q.dim() == len(lead) + 2:
+    if HK > 1 and q is not None and q.dim() == dims and q.stride(-2) != K:
         _heads(q, "q", lead)
-    gates = lead + (HV,)
+    held = (seqs[0], HV, K, V)
+    gates = shape[:-1]
     if scale is None:
         scale = K ** -0.5
     head = (*seqs, HK, HV, K, V, d, 1 if softplus else 0, 1 if sigmoid else 0,
