@@ -290,6 +290,42 @@ def test_decays_at_both_ends():
     D.near("y", first, y[:1], rel, F32)
 
 
+@pytest.mark.parametrize("train", [False, True])
+@pytest.mark.parametrize("lengths", [[1100], [4096], [65, 300]], ids=str)
+def test_growing_decays(lengths, train):
+    """Decays above 1, over chunks and over segments. An error of a share u of the
+    largest state grows by no more than all decays together, e^G, up to the end: the
+    state may be off by e^G times what it may be off without growth, of the largest
+    state; y, q of length 1 and scale 1, by as much in every row."""
+    c = Case((lengths, True, 2, 2, 16, 24, "f32", True, False, 0))
+    rate = 3.0 / max(max(lengths), 1000)
+    c.dt_bias, c.A = None, torch.tensor([1.0, 0.5])
+    c.dt = torch.full((c.T, 2), rate)
+    more = dict(initial_state=up(c.initial), offsets=c.offsets, softplus=False, scale=1.0)
+    if train:
+        got, s, _ = tg.gated_delta_rule_train(*c.args(), return_state=True, **more)
+    else:
+        got, s = tg.gated_delta_rule(*c.args(), return_state=True, **more)
+    q, k, v, dt, A, beta, initial = (t.double() for t in (c.q, c.k, c.v, c.dt, c.A, c.beta, c.initial))
+    args = (q, k, v, dt, A, beta, None, False, True, True, 1.0, initial)
+    y, state, _, kap, chunks = D.delta(c.bounds, *args)
+    # The largest state of each sequence, from the chunks' ends: between them it grows
+    # by less than e^(32 rate) < 1.4 and what the values add.
+    for i, (lo, hi) in enumerate(zip(c.bounds[:-1], c.bounds[1:])):
+        _, g, b = D.gates(dt[lo:hi], A, beta[lo:hi], None, False, True)
+        S, most = initial[i], initial[i].norm()
+        for at in range(lo, hi, 32):
+            to = min(at + 32, hi)
+            S = D.walk(D.unit(q[at:to], True), D.unit(k[at:to], True), v[at:to], g[at - lo:to - lo],
+                       b[at - lo:to - lo], 1.0, S)[1]
+            most = torch.maximum(most, S.norm() + v[at:to].norm())
+        bound = float(1.4 * most * torch.exp(g.sum(0)).max()) * D.allowed(F32, kap, chunks)
+        off = (s[i].double().cpu() - state[i]).norm()
+        assert off <= bound + D.E * state[i].norm(), (float(off), bound)
+        rows = (got[lo:hi].double().cpu() - y[lo:hi]).flatten(1).norm(dim=1)
+        assert bool((rows <= bound + D.E * y[lo:hi].flatten(1).norm(dim=1)).all()), (float(rows.max()), bound)
+
+
 def test_a_bad_value_stays_in_its_sequence_and_head():
     c = Case(([70, 70, 70], True, 2, 2, 32, 16, "bf16", False, False, 0))
     off = torch.tensor(c.bounds, dtype=torch.int32, device="cuda")
