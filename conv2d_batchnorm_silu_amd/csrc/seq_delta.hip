@@ -109,8 +109,8 @@ struct PrepShape {
     static constexpr int lds = kScales * C * 4 + C * 8 + (square > rows ? square : rows);
 };
 
-// One workgroup for a chunk and value head. NM: parts of X; BACK: the transposed matrices.
-template <typename T, int KP, int NM, bool BACK, bool WIDE>
+// One workgroup for a chunk and value head. BACK: the transposed matrices.
+template <typename T, int KP, bool BACK, bool WIDE>
 __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
     using Sh = PrepShape<T, KP>;
     constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, ML = Sh::ML, NT = C / 16;
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
                 if (qk_here) scal[kUnitQ * C + i] = a.normalize ? rsqrtf(qq[r] + kUnitEps) : 1.0f;
             }
     lds_barrier();
-    char* out = a.prep + (int64_t)blockIdx.x * prep_bytes(C, NM + PP);
+    char* out = a.prep + (int64_t)blockIdx.x * prep_bytes(C, kParts + PP);
     if (tid < C) {
         const float e = __builtin_amdgcn_exp2f((float)G[tid]), t = decay_between(G[C - 1], G[tid]);
         const float rk = scal[kUnitK * C + tid], rq = scal[kUnitQ * C + tid];
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
 
     // As fragments, in the order in which the serial kernel reads them.
     bf16* fx = (bf16*)(out + kScales * C * 4);
-    bf16* fp = fx + frag_count(C) * 512 * NM;
+    bf16* fp = fx + frag_count(C) * 512 * kParts;
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt)
 #pragma unroll
@@ -226,10 +226,10 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
                 x[j] = BACK ? mat[i * ML + o] : mat[o * ML + i];
                 p[j] = BACK ? pm[i * ML + o] : pm[o * ML + i];
             }
-            const Frag<NM> xf = frag_of<NM>(x);
+            const Frag<kParts> xf = frag_of<kParts>(x);
             const Frag<PP> pf = frag_of<PP>(p);
 #pragma unroll
-            for (int q = 0; q < NM; ++q) *(bf16x8_t*)(fx + (f * NM + q) * 512 + l * 8) = xf.p[q];
+            for (int q = 0; q < kParts; ++q) *(bf16x8_t*)(fx + (f * kParts + q) * 512 + l * 8) = xf.p[q];
 #pragma unroll
             for (int q = 0; q < PP; ++q) *(bf16x8_t*)(fp + (f * PP + q) * 512 + l * 8) = pf.p[q];
         }
@@ -368,19 +368,19 @@ hipError_t in_segments(const DeltaArgs& a, const float* first, bool reverse, flo
     return walk(b);
 }
 
-template <typename T, int NM>
+template <typename T>
 hipError_t forward_typed(const DeltaArgs& a, int64_t slots, float* states, hipStream_t st) {
     const int KP = delta_padded(a.K);
-    const hipError_t e = launch_delta_prep<T, NM, false>(a, KP, slots, st);
-    if (e != hipSuccess || !a.segment) return e == hipSuccess ? launch_delta_forward<T, NM>(a, KP, st) : e;
+    const hipError_t e = launch_delta_prep<T, false>(a, KP, slots, st);
+    if (e != hipSuccess || !a.segment) return e == hipSuccess ? launch_delta_forward<T>(a, KP, st) : e;
     return in_segments(a, a.initial, false, states, KP, slice_of(kIn<T>, KP), st, [&](const DeltaArgs& b) {
-        return launch_delta_forward<T, NM>(b, KP, st);
+        return launch_delta_forward<T>(b, KP, st);
     });
 }
 template <typename T>
 hipError_t backward_typed(const DeltaArgs& a, int64_t slots, float* states, hipStream_t st) {
     const int KP = delta_padded(a.K);
-    hipError_t e = launch_delta_prep<T, kParts, true>(a, KP, slots, st);
+    hipError_t e = launch_delta_prep<T, true>(a, KP, slots, st);
     if (e != hipSuccess) return e;
     if (a.segment)
         e = in_segments(a, a.dfinal, true, states, KP, slice_of(kIn<T>, KP), st,
@@ -391,15 +391,15 @@ hipError_t backward_typed(const DeltaArgs& a, int64_t slots, float* states, hipS
 
 }  // namespace
 
-template <typename T, int NM, bool BACK>
+template <typename T, bool BACK>
 hipError_t launch_delta_prep(const DeltaArgs& a, int KP, int64_t slots, hipStream_t st) {
     const unsigned grid = (unsigned)(slots * a.HV);
     if (grid == 0) return hipSuccess;
 #define TG_X(KP_)                                                                               \
     do {                                                                                        \
         constexpr int bytes = PrepShape<T, KP_>::lds;                                           \
-        const auto kernel = a.wide_qk ? delta_prep<T, KP_, NM, BACK, true>                      \
-                                      : delta_prep<T, KP_, NM, BACK, false>;                    \
+        const auto kernel = a.wide_qk ? delta_prep<T, KP_, BACK, true>                          \
+                                      : delta_prep<T, KP_, BACK, false>;                        \
         const hipError_t e = ensure_dynamic_lds((const void*)kernel, bytes);                    \
         if (e != hipSuccess) return e;                                                          \
         kernel<<<grid, 256, bytes, st>>>(a);                                                    \
@@ -489,12 +489,9 @@ hipError_t launch_delta(const tg_delta_args& a, void* ws, void* saved, hipStream
     b.maps = (float*)(b.prep + prep_room(a, kParts + delta_out(a.dtype)));
     float* states = (float*)((char*)b.maps + room.maps);
     const int64_t slots = delta_slots(a.seqs, delta_chunk_of(a));
-    if (a.dtype == TG_F32) return forward_typed<float, kParts>(b, slots, states, st);
-    if (a.dtype == TG_BF16)
-        return saved ? forward_typed<bf16, kParts>(b, slots, states, st)
-                     : forward_typed<bf16, kMid<bf16>>(b, slots, states, st);
-    return saved ? forward_typed<f16, kParts>(b, slots, states, st)
-                 : forward_typed<f16, kMid<f16>>(b, slots, states, st);
+    if (a.dtype == TG_F32) return forward_typed<float>(b, slots, states, st);
+    if (a.dtype == TG_BF16) return forward_typed<bf16>(b, slots, states, st);
+    return forward_typed<f16>(b, slots, states, st);
 }
 
 hipError_t launch_delta_backward(const tg_delta_args& a, const tg_delta_grads& gr,

@@ -9,13 +9,11 @@
 // instructions a product, fewer than the fp32 matrix instructions' sixteen, and with
 // fp32's range, which fp16 parts would not have.
 //
-// Prompts of 16-bit tensors that keep nothing for training take two parts (kMid: 17
-// bits, 2^-18 of the value): the states, off by 2 to 5e-6 of their norm, go on to
-// tokens that are rounded to 8 or 11 bits, and 4 x 4096 tokens of 16 heads take 185 us
-// in place of 220. In training it left dA and ddt_bias, sums over all tokens that
-// cancel, off by up to 6e-5. Products that only reach y take two parts of 16-bit tensors
-// (a single one left bf16 outputs off by 1.6 times their rounding), those that only
-// reach the gradients of q and k as many as an input has.
+// That holds for prompts too, where two parts (17 bits) left the fp32 states off by 2 to
+// 5e-6 of their norm, ten times as much, for 185 us in place of 220 (4 x 4096 tokens of 16
+// heads). Products that only reach y take two parts of 16-bit tensors (a single one left
+// bf16 outputs off by 1.6 times their rounding), those that only reach the gradients of q
+// and k as many as an input has.
 //
 // Fragments. Lane l of a wave holds row (of the left operand) or column (of the
 // right) l % 16 and, with g = l / 16, the eight inner indices 4g .. 4g+3 and
@@ -42,8 +40,6 @@ inline constexpr int kIn<bf16> = 1;
 template <typename T>
 inline constexpr int kOut = kIn<T> > 2 ? 3 : 2;  // of what only reaches y
 constexpr int kParts = 3;                        // of what lies between
-template <typename T>
-inline constexpr int kMid = kIn<T> > 2 ? 3 : 2;  // and of it in prompts
 
 // Tokens of a chunk: 64, or 32 where two chunks' parts of q and k (padded to KP) and
 // the matrices made from them would not fit LDS together.
@@ -487,10 +483,10 @@ __device__ __forceinline__ float4_t scales(const float* scal, int C, DeltaScale 
     return *(const float4_t*)(scal + which * C + mt * 16 + 4 * ((threadIdx.x & 63) >> 4));
 }
 
-// The kernels' launches; NM: parts of what lies between; BACK: the transposed matrices.
-template <typename T, int NM, bool BACK>
+// The kernels' launches; BACK: the transposed matrices.
+template <typename T, bool BACK>
 hipError_t launch_delta_prep(const DeltaArgs& a, int KP, int64_t slots, hipStream_t st);
-template <typename T, int NM>
+template <typename T>
 hipError_t launch_delta_forward(const DeltaArgs& a, int KP, hipStream_t st);
 template <typename T>
 hipError_t launch_delta_states(const DeltaArgs& a, int KP, hipStream_t st);

@@ -27,26 +27,24 @@ __device__ __forceinline__ float4_t values4(const T* p, int ld, int row0, int co
     return o;
 }
 
-template <typename T, int KP, int NM>
+template <typename T, int KP>
 struct FwdShape {
     static constexpr int NI = kIn<T>, NO = kOut<T>, C = delta_chunk(NI, KP), LD = KP + 8, NT = C / 16;
     static constexpr int slice = slice_of(NI, KP), cols = slice / 16, VL = slice + 8;
     static constexpr int rows = NI * C * LD * 2;
     static constexpr int stage = kScales * C * 4 + 2 * rows + C * VL * (int)sizeof(T);
     // For 16 columns: sums of halves; right sides, corrections for S and for y; S for y.
-    static constexpr int sums = NT * 1024, share = sums + NT * 512 * (2 * NM + NO) + KP / 32 * NO * 1024;
+    static constexpr int sums = NT * 1024, share = sums + NT * 512 * (2 * kParts + NO) + KP / 32 * NO * 1024;
     static constexpr int stages = 2 * stage + cols * share <= 160 * 1024 ? 2 : 1;
     static constexpr int lds = stages * stage + cols * share, carriers = cols * 2, threads = carriers * 128;
     static_assert(lds <= 160 * 1024, "more LDS than a compute unit has");
 };
 
-template <typename T, int KP, int NM, bool WIDE, bool WIDE_V>
+template <typename T, int KP, bool WIDE, bool WIDE_V>
 __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(const DeltaArgs a) {
-    using Sh = FwdShape<T, KP, NM>;
+    using Sh = FwdShape<T, KP>;
     constexpr int NI = Sh::NI, NO = Sh::NO, C = Sh::C, LD = Sh::LD, VL = Sh::VL, NT = Sh::NT, HT = NT / 2;
     constexpr int KH = KP / 2, KT = KH / 16, NK = KH / 32, CT = C / 32;
-    // Products with k: for fp16 in two parts with that of both second parts (k's is exact).
-    constexpr int NS = NI == 2 && NM == 2 ? 3 : NM;
     extern __shared__ float4 lds[];
     const int w = (threadIdx.x >> 6) % Sh::carriers, l = threadIdx.x & 63, g = l >> 4, col = l & 15;
     const int ct = w % Sh::cols, hf = w / Sh::cols;
@@ -65,8 +63,8 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
     const int v0 = unity ? 0 : at.slice * Sh::slice;
     char* share = (char*)lds + Sh::stages * Sh::stage + ct * Sh::share;
     float* xsum = (float*)share;
-    const HalfFrags<NM> rx{(bf16*)(share + Sh::sums)}, wx{rx.p + NT * NM * 256};
-    const HalfFrags<NO> ux{wx.p + NT * NM * 256};
+    const HalfFrags<kParts> rx{(bf16*)(share + Sh::sums)}, wx{rx.p + NT * kParts * 256};
+    const HalfFrags<NO> ux{wx.p + NT * kParts * 256};
     bf16* sx = ux.p + NT * NO * 256;  // S's fragments, NO parts
 
     // A stage: scales, k, q, the slice of v.
@@ -75,7 +73,7 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
         return Planes<NI>{(bf16*)(stage(c) + kScales * C * 4 + which * Sh::rows), LD, C * LD};
     };
     const auto record = [&](int c) {
-        return a.prep + ((int64_t)(slot0 + c) * a.HV + h) * prep_bytes(C, NM + NO);
+        return a.prep + ((int64_t)(slot0 + c) * a.HV + h) * prep_bytes(C, kParts + NO);
     };
     // Tiles hf * HT + i of X and P, blocks of 32 columns up to theirs.
     const auto used = [&](int t) { return t == 0 || hf != 0; };
@@ -113,7 +111,7 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
         };
         const auto fetch_p = [&](int c) {
             const bf16* f =
-                (const bf16*)(record(imin(c, chunks - 1)) + kScales * C * 4) + frag_count(C) * 512 * NM;
+                (const bf16*)(record(imin(c, chunks - 1)) + kScales * C * 4) + frag_count(C) * 512 * kParts;
 #pragma unroll
             for (int i = 0; i < HT; ++i)
 #pragma unroll
@@ -202,7 +200,7 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
     const int64_t KV = (int64_t)a.K * a.V;
     const float* before = a.initial ? a.initial + ((int64_t)(a.segment ? unit : s) * a.HV + h) * KV : nullptr;
     const auto tile_at = [&](int i) { return i < HT ? (1 - hf) * HT + i : hf * HT + i - HT; };
-    Frag<NM> xf[HT][CT];
+    Frag<kParts> xf[HT][CT];
     const auto fetch_x = [&](int c) {
         const bf16* f = (const bf16*)(record(imin(c, chunks - 1)) + kScales * C * 4);
 #pragma unroll
@@ -230,14 +228,14 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
         float4_t x[NT] = {};
 #pragma unroll
         for (int t = 0; t < NK; ++t) {
-            const Frag<NM> sf = frag_of<NM>(S[2 * t], S[2 * t + 1]);
+            const Frag<kParts> sf = frag_of<kParts>(S[2 * t], S[2 * t + 1]);
 #pragma unroll
             for (int q = 0; q < NO; ++q)
                 *(bf16x8_t*)(sx + ((hf * NK + t) * NO + q) * 512 + l * 8) = sf.p[q];
             Frag<NI> f[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i) f[i] = kp.rows(tile_at(i) * 16, k0 + t * 32);
-            mma_rows<NS>(x, f, sf, All());
+            mma_rows<kParts>(x, f, sf, All());
         }
 #pragma unroll
         for (int i = 0; i < HT; ++i) *sum_at(xsum, tile_at(i)) = x[i];
@@ -255,11 +253,11 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
 #pragma unroll
         for (int t = 0; t < CT; ++t)
             if (used(t)) {
-                const Frag<NM> rf = rx.frag(t);
-                Frag<NM> f[HT];
+                const Frag<kParts> rf = rx.frag(t);
+                Frag<kParts> f[HT];
 #pragma unroll
                 for (int i = 0; i < HT; ++i) f[i] = xf[i][t];
-                mma_rows<NM>(e, f, rf, All());
+                mma_rows<kParts>(e, f, rf, All());
             }
         fetch_x(c + 1);
 #pragma unroll
@@ -284,11 +282,11 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
         for (int t = 0; t < KT; ++t) S[t] *= total;
 #pragma unroll
         for (int u = 0; u < CT; ++u) {
-            const Frag<NM> wf = wx.frag(u);
+            const Frag<kParts> wf = wx.frag(u);
             Frag<NI> f[KT];
 #pragma unroll
             for (int t = 0; t < KT; ++t) f[t] = kp.cols(u * 32, k0 + t * 16);
-            mma_rows<NS>(S, f, wf, All());
+            mma_rows<kParts>(S, f, wf, All());
         }
         if (Sh::stages == 1) lds_barrier();
     }
@@ -311,12 +309,12 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
     }
 }
 
-template <typename T, int KP, int NM>
+template <typename T, int KP>
 hipError_t forward_at(const DeltaArgs& a, hipStream_t st) {
-    using Sh = FwdShape<T, KP, NM>;
-    const auto kernel = !a.wide_qk  ? delta_forward<T, KP, NM, false, false>
-                        : a.wide_v ? delta_forward<T, KP, NM, true, true>
-                                   : delta_forward<T, KP, NM, true, false>;
+    using Sh = FwdShape<T, KP>;
+    const auto kernel = !a.wide_qk  ? delta_forward<T, KP, false, false>
+                        : a.wide_v ? delta_forward<T, KP, true, true>
+                                   : delta_forward<T, KP, true, false>;
     const hipError_t e = ensure_dynamic_lds((const void*)kernel, Sh::lds);
     if (e != hipSuccess) return e;
     const int slices = (int)ceil_div(a.V, Sh::slice) + (a.through ? KP / Sh::slice : 0);
@@ -327,16 +325,14 @@ hipError_t forward_at(const DeltaArgs& a, hipStream_t st) {
 
 }  // namespace
 
-template <typename T, int NM>
+template <typename T>
 hipError_t launch_delta_forward(const DeltaArgs& a, int KP, hipStream_t st) {
-    if (KP == 64) return forward_at<T, 64, NM>(a, st);
-    if (KP == 128) return forward_at<T, 128, NM>(a, st);
-    return forward_at<T, 256, NM>(a, st);
+    if (KP == 64) return forward_at<T, 64>(a, st);
+    if (KP == 128) return forward_at<T, 128>(a, st);
+    return forward_at<T, 256>(a, st);
 }
-template hipError_t launch_delta_forward<float, kParts>(const DeltaArgs&, int, hipStream_t);
-template hipError_t launch_delta_forward<bf16, kParts>(const DeltaArgs&, int, hipStream_t);
-template hipError_t launch_delta_forward<bf16, kMid<bf16>>(const DeltaArgs&, int, hipStream_t);
-template hipError_t launch_delta_forward<f16, kParts>(const DeltaArgs&, int, hipStream_t);
-template hipError_t launch_delta_forward<f16, kMid<f16>>(const DeltaArgs&, int, hipStream_t);
+template hipError_t launch_delta_forward<float>(const DeltaArgs&, int, hipStream_t);
+template hipError_t launch_delta_forward<bf16>(const DeltaArgs&, int, hipStream_t);
+template hipError_t launch_delta_forward<f16>(const DeltaArgs&, int, hipStream_t);
 
 }  // namespace tg

@@ -946,8 +946,7 @@ def gated_delta_rule(q, k, v, dt, A, beta, dt_bias=None, softplus=True, sigmoid=
     (default zeros). Returns y, or with ``return_state`` (y, state). ``out`` may
     be v.
 
-    With 16-bit tensors the states are computed to 17 bits (in training to fp32's 24).
-    Decays above 1 (A > 0) are taken as they are while the product over any tokens in
+    The states are computed to fp32's 24 bits, in training and without. Decays above 1 (A > 0) are taken as they are while the product over any tokens in
     a row stays within fp32."""
     dev = _device(v, "v")
     there = _elsewhere(dev, stream)

@@ -1,0 +1,50 @@
+"""What the gated delta rule's outputs may be off beside the rounding of their type,
+held more tightly than the worst cases of delta_ref.py: by root sums of squares.
+
+A 2-norm over thousands of elements adds independent roundings up by their squares.
+With delta_ref's counts (fewer than STEPS roundings of u = 2^-24 each on the way from
+one chunk's state to the next, amplified by KAPPA) the states after n chunks are off
+by less than sqrt(n STEPS) KAPPA u of their norm; twice that is allowed."""
+from __future__ import annotations
+
+import pytest
+
+import conv2d_batchnorm_silu_amd as tg
+import delta_ref as D
+from gpu_cases import note
+from test_delta_gpu import Case
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+# A chunk or three, all types and widths of both chunk lengths, states and gates.
+SHORT = [
+    ([64], False, 2, 2, 64, 64, "bf16", True, False, 0), ([64, 64], False, 1, 2, 128, 96, "bf16", True, False, 0),
+    ([96], False, 1, 2, 96, 81, "f16", True, False, 0), ([70, 0, 33], True, 1, 2, 64, 48, "f16", True, False, 3),
+    ([90], False, 1, 1, 200, 64, "bf16", True, False, 0), ([64], False, 1, 1, 256, 40, "f16", True, False, 0),
+    ([60], False, 2, 2, 64, 64, "f32", True, False, 0), ([80], False, 1, 2, 256, 33, "f32", True, False, 0),
+]
+
+
+def off(got, want):
+    d = got.detach().double().cpu() - want
+    return float(d.norm() / want.norm())
+
+
+@pytest.mark.parametrize("case", SHORT, ids=str)
+def test_states_are_held_to_fp32(case):
+    note("delta states %s" % (case,))
+    c = Case(case)
+    _, _, _, _, state, _, kap, chunks = c.want()
+    _, s = tg.gated_delta_rule(*c.args(), return_state=True, **c.more())
+    allowed = 2 * (chunks * D.STEPS) ** 0.5 * kap * D.E
+    assert off(s, state) <= allowed, "%.3g, allowed %.3g" % (off(s, state), allowed)
+
+
+@pytest.mark.parametrize("case", SHORT + [([3300], True, 1, 2, 64, 40, "bf16", True, False, 0)], ids=str)
+def test_prompts_and_training_are_the_same(case):
+    """What is kept for the gradients does not change what comes out."""
+    c = Case(case)
+    y, s = tg.gated_delta_rule(*c.args(), return_state=True, **c.more())
+    y2, s2, _ = tg.gated_delta_rule_train(*c.args(), return_state=True, **c.more())
+    assert torch.equal(y, y2) and torch.equal(s, s2)
