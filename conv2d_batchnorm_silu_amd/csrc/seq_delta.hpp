@@ -11,9 +11,9 @@
 //
 // That holds for prompts too, where two parts (17 bits) left the fp32 states off by 2 to
 // 5e-6 of their norm, ten times as much, for 185 us in place of 220 (4 x 4096 tokens of 16
-// heads). Products that only reach y take two parts of 16-bit tensors (a single one left
-// bf16 outputs off by 1.6 times their rounding), those that only reach the gradients of q
-// and k as many as an input has.
+// heads). Products that only reach y, or only the gradients of q and k, take two parts of
+// 16-bit tensors: a single one left bf16 outputs off by 1.6 times their rounding, dq and
+// dk by 1.3, and by any share where most of them is taken off again along q and k.
 //
 // Fragments. Lane l of a wave holds row (of the left operand) or column (of the
 // right) l % 16 and, with g = l / 16, the eight inner indices 4g .. 4g+3 and
@@ -38,7 +38,7 @@ inline constexpr int kIn = sizeof(T) == 4 ? 3 : 2;  // parts of an input
 template <>
 inline constexpr int kIn<bf16> = 1;
 template <typename T>
-inline constexpr int kOut = kIn<T> > 2 ? 3 : 2;  // of what only reaches y
+inline constexpr int kOut = kIn<T> > 2 ? 3 : 2;  // of what only reaches y, dq or dk
 constexpr int kParts = 3;                        // of what lies between
 
 // Tokens of a chunk: 64, or 32 where two chunks' parts of q and k (padded to KP) and

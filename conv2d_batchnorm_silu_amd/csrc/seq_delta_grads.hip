@@ -24,7 +24,7 @@ struct GradShape {
     static constexpr int VB = 32, VL = VB + 8, ML = C + 8, CL = C + 8, KL = KB + 8;
     // A block of V: dy as rows of tokens; E, R, S0 and dS as rows of V.
     static constexpr int wide = NI * C * VL * 2 + 2 * kParts * VB * (CL + KL) * 2;
-    static constexpr int square = 2 * NI * C * ML * 2;                                  // C x C
+    static constexpr int NP = kOut<T>, square = 2 * NP * C * ML * 2;                    // C x C
     static constexpr int scratch = wide > square ? wide : square;
     static constexpr int floats = 9 * C + NT * C + 2 * parts * C + 2 * waves * 16 + 16;
     static constexpr int lds = C * 8 + floats * 4 + 2 * NI * C * LD * 2 + scratch;
@@ -34,7 +34,7 @@ template <typename T, int KP, bool WIDE>
 __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const DeltaArgs a) {
     using Sh = GradShape<T, KP>;
     constexpr int kThreads = 64 * Sh::waves;
-    constexpr int NI = Sh::NI, C = Sh::C, LD = Sh::LD, NT = Sh::NT, NB = Sh::NB, KB = Sh::KB;
+    constexpr int NI = Sh::NI, NP = Sh::NP, C = Sh::C, LD = Sh::LD, NT = Sh::NT, NB = Sh::NB, KB = Sh::KB;
     constexpr int KW = Sh::KW, WT = KW / 16, VB = Sh::VB, VL = Sh::VL, ML = Sh::ML, CL = Sh::CL, KL = Sh::KL;
     extern __shared__ float4 lds[];
     double* G = (double*)lds;
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
     const Planes<NI> wp{scratch, VL, C * VL};
     const Planes<kParts> ep{wp.p + NI * C * VL, CL, VB * CL}, rp{ep.p + kParts * VB * CL, CL, VB * CL};
     const Planes<kParts> sp{rp.p + kParts * VB * CL, KL, VB * KL}, dp{sp.p + kParts * VB * KL, KL, VB * KL};
-    const Planes<NI> bm{scratch, ML, C * ML}, mm{bm.p + NI * C * ML, ML, C * ML};
+    const Planes<NP> bm{scratch, ML, C * ML}, mm{bm.p + NP * C * ML, ML, C * ML};
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g = l >> 4, col = l & 15;
     const int tile = w % NT, part = w / NT, row0 = tile * 16;
     const int slot = blockIdx.x / a.HK, hk = blockIdx.x % a.HK, rep = a.HV / a.HK;
@@ -315,8 +315,8 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
 #pragma unroll 1
         for (int t = 0; t < C / 32; ++t) {
             const bool low = t * 32 <= row0 + 15, high = t * 32 + 31 >= row0;
-            const Frag<NI> br = bm.rows(row0, t * 32), mr = mm.rows(row0, t * 32);
-            const Frag<NI> bc = bm.cols(t * 32, row0), mc = mm.cols(t * 32, row0);
+            const Frag<NP> br = bm.rows(row0, t * 32), mr = mm.rows(row0, t * 32);
+            const Frag<NP> bc = bm.cols(t * 32, row0), mc = mm.cols(t * 32, row0);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -324,12 +324,12 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
                     const int k = nb * KB + part * KW + u * 16;
                     const Frag<NI> kc = kp.cols(t * 32, k);
                     if (low) {
-                        mma<NI>(dq[nb][u], br, kc);
-                        mma<NI>(dk[nb][u], mr, kc);
+                        mma<NP>(dq[nb][u], br, kc);
+                        mma<NP>(dk[nb][u], mr, kc);
                     }
                     if (high) {
-                        mma<NI>(dk[nb][u], bc, qp.cols(t * 32, k));
-                        mma<NI>(dk[nb][u], mc, kc);
+                        mma<NP>(dk[nb][u], bc, qp.cols(t * 32, k));
+                        mma<NP>(dk[nb][u], mc, kc);
                     }
                 }
         }

@@ -210,8 +210,8 @@ tg_status tg_selective_scan_step(const tg_scan_args *a, float *state, int64_t nu
  * A step d of 0 keeps the state for any A, -inf included; decays below 2^-126 are
  * taken as 0. Decays above 1 are taken as they are while the product over any tokens
  * in a row is within fp32; past it results are infinite or NaN. States and what lies
- * between enter the products with 24 bits, what only reaches y of 16-bit tensors with
- * 17. A NaN or infinite value of a
+ * between enter the products with 24 bits, what only reaches y, and the pairs of tokens
+ * in dq and dk, of 16-bit tensors with 17. A NaN or infinite value of a
  * token may reach the up to 63 tokens before it that share its 64 (counted from its
  * sequence's first; 32 for fp16, fp32 and K > 128), and all after it, of its head.
  * TG_ERR_UNSUPPORTED for K > 256, row strides of 2^25 elements or more, 2^23 or more

@@ -12,7 +12,7 @@ import pytest
 import conv2d_batchnorm_silu_amd as tg
 import delta_ref as D
 from gpu_cases import note
-from test_delta_gpu import Case
+from test_delta_gpu import Case, up
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -48,3 +48,28 @@ def test_prompts_and_training_are_the_same(case):
     y, s = tg.gated_delta_rule(*c.args(), return_state=True, **c.more())
     y2, s2, _ = tg.gated_delta_rule_train(*c.args(), return_state=True, **c.more())
     assert torch.equal(y, y2) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("case", [c for c in SHORT if c[6] != "f32"], ids=str)
+def test_gradients_of_q_and_k_round_once(case):
+    """An error of e, relative to the value, moves it past the middle between two
+    numbers of its type in a share 2 e / step of all elements, with step at least eps/2
+    of the value. What leads to dq and dk is off by three operands of 2^-17 (two parts and
+    the product of two second ones) and by fp32's roundings, of what an element is a
+    difference of; four standard deviations of the count are added."""
+    note("delta dq, dk %s" % (case,))
+    c = Case(case)
+    x, bias, initial, y, state, g, kap, chunks = c.want(True)
+    total = (y * c.dy.double()).sum() + (state * c.dstate.double()).sum()
+    dq, dk, uq, uk = torch.autograd.grad(total, [x[0], x[1], g[1], g[2]])
+    _, saved = tg.gated_delta_rule_train(*c.args(), **c.more())
+    got = tg.gated_delta_rule_backward(c.dev(c.dy), *c.args(), saved, dstate=up(c.dstate), **c.more())
+    e = 3 * 2.0 ** -17 + 2 * (chunks * D.STEPS) ** 0.5 * kap * kap * D.E
+    for name, want, at, unit in (("dq", dq, 0, uq), ("dk", dk, 1, uk)):
+        size = torch.maximum(want.abs(), D.unit_size(x[at].detach(), unit))
+        rms = size.norm() / size.numel() ** 0.5
+        half = torch.finfo(c.dtype).eps / 2
+        share = (2 * e * torch.maximum(size, rms) / (want.abs() * half)).clamp(max=1)
+        n = int((getattr(got, name).cpu().reshape(want.shape) != want.to(c.dtype)).sum())
+        most = float(share.sum()) + 4 * float((share * (1 - share)).sum()) ** 0.5 + 1
+        assert n <= most, "%s: %d of %d not the rounded value, allowed %.0f" % (name, n, want.numel(), most)
