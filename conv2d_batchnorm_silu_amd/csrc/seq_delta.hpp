@@ -398,6 +398,20 @@ __device__ __forceinline__ DeltaGate delta_gate(const DeltaArgs& a, float dt, fl
     o.b = a.sigmoid ? sigmoid_f32(beta) : beta;
     return o;
 }
+// Within each 16 lanes: the value N lanes below (0 where there is none), and the sum of
+// the lanes up to one's own.
+template <int N>
+__device__ __forceinline__ float row_shift16(float v) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x110 + N, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float row_prefix16(float v) {
+    v += row_shift16<1>(v);
+    v += row_shift16<2>(v);
+    v += row_shift16<4>(v);
+    v += row_shift16<8>(v);
+    return v;
+}
 __device__ __forceinline__ double wave_prefix(double v) {
     const int l = threadIdx.x & 63;
 #pragma unroll

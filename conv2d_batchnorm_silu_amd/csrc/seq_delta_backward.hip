@@ -10,12 +10,12 @@
 //     dk = (scale b D F)^T q + e^(G[C-1]-G) b E dS^T - e^G R S0^T + (M + M^T) k,
 //          M = b D H, strictly lower
 //     db[j] = Z[j] + sum_i T[i,j],        T = (D scale q k^T) F + (D k k^T) H
-//     dG[i] = sum_j T[i,j] b[j] - b[i] db[i] + e^G[i] (scale q[i].(w S0^T)[i] - k[i].(R S0^T)[i])
-//             (without T[i,i] in either sum)
-//     dG[C-1] += e^(G[C-1]) <dS, S0> + sum_j b[j] Z[j]
-// and a token's decay logarithm gets the sum of dG from it to the chunk's end:
-// the pairs of tokens on either side of it, nothing that cancels but T's own
-// row and column sums.
+// and the logarithm of token t's decay gets what passes it:
+//     dg[t] = sum_{j < t <= i} T[i,j] b[j] + sum_{j < t} b[j] Z[j] + e^(G[C-1]) <dS, S0>
+//             + sum_{i >= t} e^G[i] (scale q[i].(w S0^T)[i] - k[i].(R S0^T)[i])
+// Each term holds t's decay as a factor, so dg is small where the decay is strong. (As
+// sums of dG[i] from t to the chunk's end, which are fewer, terms that do not pass
+// t cancel but for their rounding, which a large rate would multiply.)
 #include "seq_delta.hpp"
 #include "tg_internal.hpp"
 

@@ -26,7 +26,7 @@ struct GradShape {
     static constexpr int wide = NI * C * VL * 2 + 2 * kParts * VB * (CL + KL) * 2;
     static constexpr int NP = kOut<T>, square = 2 * NP * C * ML * 2;                    // C x C
     static constexpr int scratch = wide > square ? wide : square;
-    static constexpr int floats = 9 * C + NT * C + 2 * parts * C + 2 * waves * 16 + 16;
+    static constexpr int floats = 8 * C + 2 * NT * C + 2 * parts * C + 2 * waves * 16 + 16;
     static constexpr int lds = C * 8 + floats * 4 + 2 * NI * C * LD * 2 + scratch;
 };
 
@@ -47,7 +47,8 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
     float* rq = rk + C;
     float* own = rq + C;             // T's diagonal
     float* colsum = own + C;         // [NT][C]: column sums of T by row tile
-    float* dots = colsum + NT * C;   // [2][parts][C]: rows' sums by part: the S0 terms and T, Z
+    float* across = colsum + NT * C;  // [NT][C]: by row tile, T b of the pairs on either side of a token
+    float* dots = across + NT * C;    // [2][parts][C]: rows' sums by part: the S0 terms, Z
     float* inner = dots + 2 * Sh::parts * C;   // [2][waves][16]: dq.q and dk.k of a tile's rows
     float* red = inner + 2 * Sh::waves * 16;   // <dS, S0> by wave
     const Planes<NI> kp{(bf16*)((float*)(G + C) + Sh::floats), LD, C * LD};
@@ -227,29 +228,34 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
                 }
         }
         lds_barrier();  // the last block of V has been read
-        float rowt[4] = {};
+        float before[4] = {};  // T b of each row, columns before the tile
 #pragma unroll
         for (int jt = 0; jt < NT; ++jt) {
             const int j = jt * 16 + col;
             const float b = gb[j];
-            float sum = 0.0f;
+            float sum = 0.0f, over = 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = row0 + 4 * g + r;
-                float f = 0.0f, m = 0.0f;
+                float f = 0.0f, m = 0.0f, pair = 0.0f;
                 if (j <= i) {
                     const float D = decay_between(G[i], G[j]) * rk[j];
                     f = F[jt][r] * D * a.scale * rq[i];
                     m = j < i ? -H[jt][r] * D * rk[i] : 0.0f;
                     const float t = f * qk[jt][r] + m * kk[jt][r];
-                    // A token's own term has no decay: its place in the row's and the
-                    // column's sum would cancel, but for its rounding.
+                    // A token's own term has no decay.
                     if (j < i) {
                         sum += t;
-                        rowt[r] = __builtin_fmaf(t, b, rowt[r]);
+                        pair = t * b;
                     } else if (part == 0) {
                         own[i] = t;
                     }
+                }
+                // Row i's pairs with the tokens before j have j's decay if j <= i.
+                if (jt <= tile) {
+                    const float upto = row_prefix16(pair);
+                    over += j <= i ? before[r] + row_shift16<1>(upto) : 0.0f;
+                    before[r] += row_sum16(pair);
                 }
                 if (part == 0) {
                     bm.put(i, j, f * b);
@@ -258,12 +264,13 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
             }
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
-            if (part == 0 && g == 0) colsum[tile * C + j] = sum;
+            over += __shfl_xor(over, 16);
+            over += __shfl_xor(over, 32);
+            if (part == 0 && g == 0) colsum[tile * C + j] = sum, across[tile * C + j] = over;
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            // Row sums of T once, of the S0 terms by every part.
-            const float u = row_sum16(dot0[r] + (part == 0 ? rowt[r] : 0.0f)), z = row_sum16(dotz[r]);
+            const float u = row_sum16(dot0[r]), z = row_sum16(dotz[r]);
             if (col == 0) {
                 dots[part * C + row0 + 4 * g + r] = u;
                 dots[(Sh::parts + part) * C + row0 + 4 * g + r] = z;
@@ -273,39 +280,41 @@ __global__ __launch_bounds__(KP == 256 ? 512 : 256, 1) void delta_grads(const De
         if (l == 0) red[w] = whole;
         lds_barrier();
         if (w == 0) {
-            float db = 0.0f, dg = 0.0f, bz = 0.0f;
+            float db = 0.0f, dg = 0.0f, bz = 0.0f, pairs = 0.0f;
             if (l < C) {
-                float u = 0.0f, z = 0.0f;
+                float z = 0.0f;
 #pragma unroll
                 for (int p = 0; p < Sh::parts; ++p)
-                    u += dots[p * C + l], z += dots[(Sh::parts + p) * C + l];
-                float after = z;
+                    dg += dots[p * C + l], z += dots[(Sh::parts + p) * C + l];
+                db = z + own[l];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) after += colsum[t * C + l];
-                db = after + own[l];
-                dg = u - gb[l] * after;
+                for (int t = 0; t < NT; ++t) db += colsum[t * C + l], pairs += across[t * C + l];
                 bz = gb[l] * z;
             }
-            bz = wave_sum(bz);
             float both = 0.0f;
 #pragma unroll
             for (int i = 0; i < Sh::waves; ++i) both += red[i];
-            const float after = ge[C - 1] * both + bz;
-            // From each token to the chunk's end: sums over the lanes above.
+            // The S0 terms from each token on, Z of the tokens before it.
+            bz = __shfl_up(bz, 1);
+            if (l == 0) bz = 0.0f;
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) {
-                const float o = __shfl_down(dg, d);
+                const float o = __shfl_down(dg, d), z = __shfl_up(bz, d);
                 if (l + d < 64) dg += o;
+                if (l >= d) bz += z;
             }
-            dg += after;
+            dg += pairs + bz + ge[C - 1] * both;
             float pa = 0.0f, pb = 0.0f;
             if (l < n) {
-                const float dd = dg * a.A[h] * gs[l];
+                // A decay that is taken as 0 has no gradient, whatever its rate and step; an
+                // infinite rate has none beside its steps of zero either.
+                const float A = a.A[h];
+                const float dd = dg == 0.0f || __builtin_isinf(A) ? 0.0f : dg * A * gs[l];
                 const float b = gb[l];
                 row_of<T>(a.ddt, a.map, s, start, lo + l)[h] = (T)dd;
                 row_of<T>(a.dbeta, a.map, s, start, lo + l)[h] =
                     (T)(a.sigmoid ? db * b * (1.0f - b) : db);
-                pa = dg * gd[l];
+                pa = dg == 0.0f ? 0.0f : dg * gd[l];
                 pb = dd;
             }
             pa = wave_sum(pa);

@@ -208,7 +208,7 @@ tg_status tg_selective_scan_step(const tg_scan_args *a, float *state, int64_t nu
  * fp32 [seqs][HV][K][V] or NULL.
  * A sum of squares of q or k past fp32 is infinite and makes NaN.
  * A step d of 0 keeps the state for any A, -inf included; decays below 2^-126 are
- * taken as 0. Decays above 1 are taken as they are while the product over any tokens
+ * taken as 0, and have no gradient; nor has an infinite A, or dt through it. Decays above 1 are taken as they are while the product over any tokens
  * in a row is within fp32; past it results are infinite or NaN. States and what lies
  * between enter the products with 24 bits, what only reaches y, and the pairs of tokens
  * in dq and dk, of 16-bit tensors with 17. A NaN or infinite value of a
