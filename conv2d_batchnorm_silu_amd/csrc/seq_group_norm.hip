@@ -51,9 +51,13 @@ struct Moments {
     float n, mean, m2;
 };
 __device__ __forceinline__ void join(Moments& a, const Moments& b) {
-    const float n = a.n + b.n;
-    if (n == 0.0f) return;
-    const float d = b.mean - a.mean, f = b.n / n;
+    // An empty set is no set at mean 0: the distance to it may have no square in fp32.
+    if (b.n == 0.0f) return;
+    if (a.n == 0.0f) {
+        a = b;
+        return;
+    }
+    const float n = a.n + b.n, d = b.mean - a.mean, f = b.n / n;
     a.mean = __builtin_fmaf(d, f, a.mean);
     a.m2 += b.m2 + d * d * a.n * f;
     a.n = n;

@@ -1,0 +1,48 @@
+"""Group norm at the ends of its range: means far past the root of fp32's largest
+number, against the bounds of delta_ref.py."""
+from __future__ import annotations
+
+import pytest
+
+import conv2d_batchnorm_silu_amd as tg
+import delta_ref as D
+import seq_ref as R
+from gpu_cases import note
+from test_group_norm_gpu import BF16, F32, Case, up
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+# Maps of one chunk and of many, whole groups in a vector and across vectors, odd
+# channels, a long group of single rows, heads.
+SHAPES = [((2, 60, 16), 4), ((1, 5000, 8), 2), ((2, 9, 33), 3), ((3, 700), 1), ((2, 3, 4104), 2), ((5, 64), 4)]
+
+
+@pytest.mark.parametrize("shape,G", SHAPES, ids=str)
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+@pytest.mark.parametrize("value", [3e19, -3e19, 1e30, -1e35])
+def test_constant_groups_of_any_size(shape, G, dtype, value):
+    """No spread: the result is beta, the mean the value (its sum within fp32)."""
+    note("group norm of %g %s %s" % (value, shape, dtype))
+    C = shape[-1]
+    x = torch.full(shape, value, dtype=dtype, device="cuda")
+    gamma, beta = torch.ones(C, device="cuda"), torch.linspace(-1, 1, C, device="cuda")
+    y, mean, rstd = tg.group_norm_train(x, G, gamma, beta, act="none")
+    assert torch.equal(y, beta.to(dtype).expand(shape))
+    assert torch.equal(mean, x.float().reshape(shape[0], -1)[:, :1].expand_as(mean))
+    assert torch.equal(rstd, torch.full_like(rstd, float(rstd[0, 0]))) and abs(float(rstd[0, 0]) * 1e-5 ** 0.5 - 1) < 1e-6
+    d = tg.group_norm_backward(torch.ones_like(x), x, G, gamma, mean, rstd, beta, act="none")
+    assert not d.dgamma.any() and bool(torch.isfinite(d.dx).all()) and bool(torch.isfinite(d.dbeta).all())
+
+
+@pytest.mark.parametrize("shape,G", SHAPES, ids=str)
+def test_means_past_the_root_of_the_largest_number(shape, G):
+    """A mean of 1e20 with a spread of 1e16: every element within its bound."""
+    c = Case((shape, G, "f32", "none", True, False, 0))
+    c.x = c.x * 1e16 + 1e20
+    want, mean, rstd = D.group_norm(c.flat(c.x), G, c.gamma.double(), c.beta.double(), 1e-5, "none", None)
+    b = c.bounds()
+    y, m, r = tg.group_norm_train(*c.args(), **c.more())
+    R.check("y", y, want.reshape(shape), b["y"][1].reshape(shape))
+    R.check("mean", m, mean, b["mean"])
+    R.check("rstd", r, rstd, b["rstd"])
