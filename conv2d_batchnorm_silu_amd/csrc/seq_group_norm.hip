@@ -162,7 +162,9 @@ __global__ __launch_bounds__(kThreads) void map_stats(const GroupArgs a) {
                     for (int e = 0; e < V; ++e) {
                         mean[e] = __builtin_fmaf(s[e], inv, k[e]);
                         b.mean += (mean[e] - mean[0]) * (1.0f / V);
-                        b.m2 += fmaxf(q[e] - s[e] * s[e] * inv, 0.0f);
+                        // Not by fmaxf: where squares are infinite, NaN has to stay.
+                        const float m2 = q[e] - s[e] * s[e] * inv;
+                        b.m2 += m2 < 0.0f ? 0.0f : m2;
                     }
                     b.mean += mean[0];
 #pragma unroll

@@ -268,7 +268,8 @@ tg_status tg_gated_delta_rule_step(const tg_delta_args *a, float *state, int64_t
  * with act SiLU or none (TG_ACT_SILU, TG_ACT_NONE). Rows of x and z are a row
  * stride >= C apart (or 0: one row for all); y is dense and may be x or z
  * themselves (dense). beta, and mean with rstd (fp32 [N][G], for the backward
- * pass) may be NULL. N == 0 does nothing; L >= 1. TG_ERR_UNSUPPORTED for more than
+ * pass) may be NULL. N == 0 does nothing; L >= 1. A group's sum of squared distances to
+ * its mean past fp32 is infinite or NaN, as is a sum of x past it where L is 1. TG_ERR_UNSUPPORTED for more than
  * 4096 groups, or L or N*L of 2^30 or more, or N past 2^24 where a group has more than
  * 256 channels or L is not 1. */
 typedef struct {

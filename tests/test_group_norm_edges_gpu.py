@@ -46,3 +46,14 @@ def test_means_past_the_root_of_the_largest_number(shape, G):
     R.check("y", y, want.reshape(shape), b["y"][1].reshape(shape))
     R.check("mean", m, mean, b["mean"])
     R.check("rstd", r, rstd, b["rstd"])
+
+
+@pytest.mark.parametrize("shape,G", [((1, 20, 256), 256), ((2, 60, 16), 4), ((3, 700), 1)], ids=str)
+def test_a_spread_past_fp32_is_not_taken_for_none(shape, G):
+    """Squares that are infinite: y is what it should be, or no number, or nothing of h
+    is left (a variance of infinity), but never a multiple of x."""
+    c = Case((shape, G, "f32", "none", False, False, 0))
+    c.x = c.x * 1e20
+    want, _, _ = D.group_norm(c.flat(c.x), c.G, c.gamma.double(), None, 1e-5, "none", None)
+    y = tg.group_norm(*c.args(), **c.more()).double().cpu().reshape(want.shape)
+    assert bool((torch.isnan(y) | (y.abs() <= 1.01 * want.abs())).all())
