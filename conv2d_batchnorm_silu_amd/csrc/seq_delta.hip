@@ -106,7 +106,7 @@ struct PrepShape {
     static constexpr int NI = kIn<T>, C = delta_chunk(NI, KP), LD = KP + 8, ML = C + 4;
     // The matrices take the place of q and k.
     static constexpr int square = 2 * C * ML * 4, rows = 2 * NI * C * LD * 2;
-    static constexpr int lds = kScales * C * 4 + C * 8 + (square > rows ? square : rows);
+    static constexpr int lds = kScales * C * 4 + C * 8 + (square > rows ? square : rows) + 16;
 };
 
 // One workgroup for a chunk and value head. BACK: the transposed matrices.
@@ -120,6 +120,7 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
     double* G = (double*)(scal + kScales * C);
     float* mat = (float*)(G + C);
     float* pm = mat + C * ML;
+    int* odd = (int*)((char*)lds + Sh::lds - 16);  // the first token whose row of N is not finite
     const Planes<NI> kp{(bf16*)mat, LD, C * LD}, qp{kp.p + NI * C * LD, LD, C * LD};
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, g = l >> 4, col = l & 15;
     const int slot = blockIdx.x / a.HV, h = blockIdx.x % a.HV, hk = h / (a.HV / a.HK);
@@ -147,6 +148,7 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
             scal[kBeta * C + l] = t.b;
         }
     }
+    if (tid == 0) *odd = C;
     kt.put(kp);
     qt.put(qp);
     lds_barrier();
@@ -193,21 +195,41 @@ __global__ __launch_bounds__(256) void delta_prep(const DeltaArgs a) {
         o[kUnitQ * C] = rq;
         o[kDecay * C] = e;
     }
+    float bad = 0.0f;
 #pragma unroll
     for (int jt = 0; jt < NT; ++jt) {
         const int j = jt * 16 + col;
         const float rk = scal[kUnitK * C + j], b = scal[kBeta * C + j];
+        float4_t m;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = tile * 16 + 4 * g + r;
             const float D = j <= i ? decay_between(G[i], G[j]) : 0.0f;
-            if (kk_here) mat[i * ML + j] = j < i ? D * kk[jt][r] * scal[kUnitK * C + i] * rk * b : 0.0f;
+            m[r] = j < i ? D * kk[jt][r] * scal[kUnitK * C + i] * rk * b : 0.0f;
+            if (kk_here) mat[i * ML + j] = m[r];
             if (qk_here)
                 pm[i * ML + j] = j <= i ? D * qk[jt][r] * scal[kUnitQ * C + i] * rk * a.scale : 0.0f;
         }
+        bad = strange(bad, m);
     }
+    // A row of N that is infinite or NaN makes its own row of X and the later ones NaN, not
+    // the ones before it: the inverse is formed without it.
+    if (kk_here && !(bad == 0.0f))
+        for (int jt = 0; jt < NT; ++jt)
+            for (int r = 0; r < 4; ++r) {
+                const int i = tile * 16 + 4 * g + r;
+                float* at = mat + i * ML + jt * 16 + col;
+                if (*at - *at == 0.0f) continue;
+                *at = 0.0f;
+                atomicMin(odd, i);
+            }
     lds_barrier();
     invert<C, ML>(mat);
+    if (*odd < C) {
+        for (int i = tid; i < C * C; i += 256)
+            if (i / C >= *odd && i % C <= i / C) mat[i / C * ML + i % C] = __builtin_nanf("");
+        lds_barrier();
+    }
 
     // As fragments, in the order in which the serial kernel reads them.
     bf16* fx = (bf16*)(out + kScales * C * 4);

@@ -125,6 +125,32 @@ struct All {
     __device__ __forceinline__ constexpr bool operator()(int) const { return true; }
 };
 
+// Whether any of these is infinite or NaN, found by a sum: then it is not 0.
+__device__ __forceinline__ float strange(float sum, const float4_t& v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum = __builtin_fmaf(v[j], 0.0f, sum);
+    return sum;
+}
+// A right operand's block of 32 tokens t without what is infinite or NaN (a first part
+// tells): products with zeros above a diagonal would take it to tokens before its own.
+// `from` becomes the first such token of the lane's column.
+template <int N>
+__device__ __forceinline__ void put_aside(Frag<N>& f, int t, int& from) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int j = 7; j >= 0; --j) {
+        const float v = (float)f.p[0][j];
+        if (v - v == 0.0f) continue;
+        from = imin(from, t * 32 + frag_at(g, j));
+#pragma unroll
+        for (int n = 0; n < N; ++n) f.p[n][j] = (bf16)0.0f;
+    }
+}
+__device__ __forceinline__ int column_least(int v) {
+    v = imin(v, __shfl_xor(v, 16));
+    return imin(v, __shfl_xor(v, 32));
+}
+
 // A matrix in LDS, in N planes of parts: row r of a plane at r * ld elements.
 template <int N>
 struct Planes {

@@ -75,6 +75,9 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
     const auto record = [&](int c) {
         return a.prep + ((int64_t)(slot0 + c) * a.HV + h) * prep_bytes(C, kParts + NO);
     };
+    // Whether a half's corrections are not finite: in place of scales that this walk does
+    // not read.
+    const auto odd = [&](int c, int half) { return (int*)stage(c) + kTailK * C + ct * 2 + half; };
     // Tiles hf * HT + i of X and P, blocks of 32 columns up to theirs.
     const auto used = [&](int t) { return t == 0 || hf != 0; };
 
@@ -162,16 +165,29 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
                 }
                 continue;
             }
+            const bool bad = *odd(c, 0) | *odd(c, 1);
+            int from = C;
 #pragma unroll
             for (int t = 0; t < CT; ++t)
                 if (used(t)) {
-                    const Frag<NO> uf = ux.frag(t);
+                    Frag<NO> uf = ux.frag(t);
+                    if (bad) put_aside(uf, t, from);
                     Frag<NO> f[HT];
 #pragma unroll
                     for (int i = 0; i < HT; ++i) f[i] = pf[i][t];
                     mma_cols<NO>(ys, uf, f, All());
                 }
             fetch_p(c + 1);
+            if (bad) {
+                from = column_least(from);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int f = __shfl(from, 4 * g + r);
+#pragma unroll
+                    for (int i = 0; i < HT; ++i)
+                        if ((hf * HT + i) * 16 + col >= f) ys[i][r] = __builtin_nanf("");
+                }
+            }
             T* yb = row_of<T>(a.y, a.map, s, start, first + lo) + (int64_t)h * a.V + v0;
 #pragma unroll
             for (int t = 0; t < HT; ++t)
@@ -260,11 +276,44 @@ __global__ __launch_bounds__(slice_of(kIn<T>, KP) * 16, 1) void delta_forward(co
                 mma_rows<kParts>(e, f, rf, All());
             }
         fetch_x(c + 1);
+        float4_t u[HT];
+        float bad = 0.0f;
+#pragma unroll
+        for (int i = 0; i < HT; ++i) {
+            u[i] = e[i] * scales(scal, C, kBeta, hf * HT + i);
+            bad = strange(bad, u[i]);
+        }
+        const bool again = __any(!(bad == 0.0f));
+        if (l == 0) *odd(c, hf) = again;
+        if (again) {
+            // Again, without what is infinite or NaN: that reaches its own and later tokens.
+            const bf16* x = (const bf16*)(record(c) + kScales * C * 4);
+            int from = C;
+#pragma unroll
+            for (int i = 0; i < HT; ++i) e[i] = float4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+                if (used(t)) {
+                    Frag<kParts> rf = rx.frag(t), f[HT];
+                    put_aside(rf, t, from);
+#pragma unroll
+                    for (int i = 0; i < HT; ++i) prepared(f[i], x, frag_index(C, hf * HT + i, t, false));
+                    mma_rows<kParts>(e, f, rf, All());
+                }
+            from = column_least(from);
+#pragma unroll
+            for (int i = 0; i < HT; ++i) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if ((hf * HT + i) * 16 + 4 * g + r >= from) e[i][r] = __builtin_nanf("");
+                u[i] = e[i] * scales(scal, C, kBeta, hf * HT + i);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < HT; ++i) {
             const int mt = hf * HT + i;
             wx.put(mt, e[i] * scales(scal, C, kWrite, mt));
-            ux.put(mt, e[i] * scales(scal, C, kBeta, mt));
+            ux.put(mt, u[i]);
         }
         lds_barrier();
         if (a.saved && !a.through) {

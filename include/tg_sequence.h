@@ -208,12 +208,14 @@ tg_status tg_selective_scan_step(const tg_scan_args *a, float *state, int64_t nu
  * fp32 [seqs][HV][K][V] or NULL.
  * A sum of squares of q or k past fp32 is infinite and makes NaN.
  * A step d of 0 keeps the state for any A, -inf included; decays below 2^-126 are
- * taken as 0, and have no gradient; nor has an infinite A, or dt through it. Decays above 1 are taken as they are while the product over any tokens
- * in a row is within fp32; past it results are infinite or NaN. States and what lies
- * between enter the products with 24 bits, what only reaches y, and the pairs of tokens
- * in dq and dk, of 16-bit tensors with 17. A NaN or infinite value of a
- * token may reach the up to 63 tokens before it that share its 64 (counted from its
- * sequence's first; 32 for fp16, fp32 and K > 128), and all after it, of its head.
+ * taken as 0, and have no gradient; nor has an infinite A, or dt through it. Decays
+ * above 1 are taken as they are while the product over any tokens in a row is within
+ * fp32; past it results are infinite or NaN. States and what lies between enter the
+ * products with 24 bits, what only reaches y, and the pairs of tokens in dq and dk, of
+ * 16-bit tensors with 17.
+ * A NaN or infinite value of a token makes its own y and, but for q, those of the later
+ * tokens of its head infinite or NaN (of v: in its column), and no other. In the
+ * gradients it may reach any token of its sequence and key head.
  * TG_ERR_UNSUPPORTED for K > 256, row strides of 2^25 elements or more, 2^23 or more
  * pairs of a value head and 64 (32) tokens, and 2^22 or more of a sequence, a value
  * head and 16 columns. */
