@@ -32,6 +32,11 @@ namespace {
 constexpr int kBlockRows = 32;  // rows with one x0
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;  // rows on their way in a thread
+// Chunks of maps whose channels' sums are held at once, 8 bytes for each channel: those of
+// all would be four times x for a million n of one row. 16384 rows of 4096 bf16 channels
+// take 1045 us in eight launches of 2048 chunks, 968 in one; smaller ones 15 to 20% more,
+// so that 64 MB are always held.
+constexpr int64_t kMostSums = 2048, kSumBytes = (int64_t)64 << 20;
 
 struct GroupArgs {
     const void *x, *z, *dy;
@@ -43,8 +48,9 @@ struct GroupArgs {
     void *y, *dz;  // y: dx in the backward pass
     float *mean, *rstd;
     int chunks, rows;      // of an n; rows of a chunk
-    float *stats, *cols;   // [N][chunks][G][2]; [N * chunks][2][C], sums of dv h and of dv
-    int64_t units;         // heads: rows in flight; cols: [units][2][C]
+    float *stats, *cols;   // [N][chunks][G][2]; [units][2][C], sums of dv h and of dv
+    int64_t units;         // heads: rows in flight; maps: chunks of a launch of map_sums
+    int64_t first;         // the first of these chunks
 };
 
 struct Moments {
@@ -93,9 +99,9 @@ template <int V>
 struct Place {
     int64_t n, first;
     int chunk, rows, TX, TY, tx, ty;
-    __device__ __forceinline__ explicit Place(const GroupArgs& a) {
-        n = blockIdx.x / a.chunks;
-        chunk = (int)(blockIdx.x % a.chunks);
+    __device__ __forceinline__ explicit Place(const GroupArgs& a, int64_t at = blockIdx.x) {
+        n = at / a.chunks;
+        chunk = (int)(at % a.chunks);
         first = (int64_t)chunk * a.rows;
         rows = (int)(a.L - first < a.rows ? a.L - first : a.rows);
         const int cols = a.C / V;
@@ -330,7 +336,8 @@ struct Slopes {
 template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void map_sums(const GroupArgs a) {
     __shared__ float sm[2 * V][kThreads];
-    const Place<V> p(a);
+    const int64_t at = a.first + blockIdx.x;
+    const Place<V> p(a, at);
     const int Cg = a.C / a.G;
     const int64_t row0 = p.n * a.L + p.first;
     float* cols = a.cols + (int64_t)blockIdx.x * 2 * a.C;
@@ -409,7 +416,7 @@ __global__ __launch_bounds__(kThreads) void map_sums(const GroupArgs a) {
             }
         for (int d = 1; d < P; d *= 2) s += __shfl_xor(s, d), q += __shfl_xor(q, d);
         if (g < a.G && lane == 0) {
-            float* out = a.stats + ((int64_t)blockIdx.x * a.G + g) * 2;
+            float* out = a.stats + (at * a.G + g) * 2;
             out[0] = s;
             out[1] = q;
         }
@@ -663,7 +670,7 @@ __global__ __launch_bounds__(kThreads) void heads(const GroupArgs a) {
 struct GroupPlan {
     bool heads;
     int lanes, vectors;  // heads: P, NV at the width V
-    int64_t units;       // heads: rows in flight
+    int64_t units;       // heads: rows in flight; maps: chunks of a launch of map_sums
     int chunks, rows;    // maps
 };
 
@@ -683,8 +690,9 @@ GroupPlan group_plan(const tg_group_norm_args& a, bool back) {
     // By scalars: what the narrowest vectors hold, any address serves.
     if (a.L == 1 && Cg <= 256) {
         p.heads = true;
-        // 512 workgroups of whole rows in the backward pass: one row of partial sums
-        // for each.
+        // Rows in flight: 2048 workgroups of them; in the backward pass no more than 512, each
+        // a row of partial sums. That is a row of 2048 channels for a workgroup; narrower
+        // ones leave compute units idle (16384 rows of 128 channels: 49 us).
         const int64_t row_threads = ceil_div(a.C, 8);
         int64_t most = (back ? 512 : 2048) * kThreads / row_threads;
         if (most < 1) most = 1;
@@ -703,6 +711,9 @@ GroupPlan group_plan(const tg_group_norm_args& a, bool back) {
     if (rows > a.L) rows = a.L;
     p.rows = (int)rows;
     p.chunks = (int)ceil_div(a.L, rows);
+    const int64_t held = kSumBytes / (8 * (int64_t)a.C);
+    p.units = held > kMostSums ? held : kMostSums;
+    if (p.units > a.N * p.chunks) p.units = a.N * p.chunks;
     return p;
 }
 
@@ -748,9 +759,17 @@ template <typename T, int W>
 hipError_t sweeps_typed(const GroupArgs& a, bool back, hipStream_t st) {
     const unsigned grid = (unsigned)(a.N * a.chunks);
     if (back) {
-        map_sums<T, W><<<grid, kThreads, 0, st>>>(a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        // Of several launches, each one's sums become a row behind the partial ones.
+        GroupArgs b = a;
+        float* row = a.cols + a.units * 2 * a.C;
+        for (; b.first < grid; b.first += a.units, row += 2 * a.C) {
+            const int64_t left = grid - b.first, now = left < a.units ? left : a.units;
+            map_sums<T, W><<<(unsigned)now, kThreads, 0, st>>>(b);
+            hipError_t e = hipGetLastError();
+            if (e == hipSuccess && grid > a.units)
+                e = launch_column_sums(a.cols, (int)now, 2 * (int64_t)a.C, row, 2 * (int64_t)a.C, nullptr, st);
+            if (e != hipSuccess) return e;
+        }
         map_grads<T, W><<<grid, kThreads, 2 * a.G * sizeof(float), st>>>(a);
     } else {
         map_apply<T, W><<<grid, kThreads, 2 * a.G * sizeof(float), st>>>(a);
@@ -793,6 +812,15 @@ hipError_t group_run(tg_dtype dt, const GroupArgs& a, const GroupPlan& p, bool b
     return group_typed<f16>(V, W, a, p, back, st);
 }
 
+// The maps' scratch in the backward pass: the groups' sums, then the channels' of one launch
+// of map_sums, and where there are several launches a row of sums for each.
+size_t stats_bytes(const tg_group_norm_args& a, const GroupPlan& p) {
+    return up256((size_t)(a.N * p.chunks) * a.G * 2 * sizeof(float));
+}
+int64_t launch_sums(const tg_group_norm_args& a, const GroupPlan& p) {
+    return a.N * p.chunks > p.units ? ceil_div(a.N * p.chunks, p.units) : 0;
+}
+
 }  // namespace
 
 int64_t group_norm_groups(const tg_group_norm_args& a) {
@@ -805,8 +833,8 @@ void group_norm_sizes(const tg_group_norm_args& a, size_t* work, size_t* backwar
     if (work) *work = f.heads ? 0 : (size_t)(a.N * f.chunks) * a.G * 2 * sizeof(float);
     if (backward)
         *backward = b.heads ? (size_t)b.units * 2 * a.C * sizeof(float)
-                            : up256((size_t)(a.N * b.chunks) * a.G * 2 * sizeof(float)) +
-                                  (size_t)(a.N * b.chunks) * 2 * a.C * sizeof(float);
+                            : stats_bytes(a, b) +
+                                  (size_t)(b.units + launch_sums(a, b)) * 2 * a.C * sizeof(float);
 }
 
 hipError_t launch_group_norm(const tg_group_norm_args& a, void* ws, hipStream_t st) {
@@ -820,17 +848,17 @@ hipError_t launch_group_norm_backward(const tg_group_norm_args& a, const tg_grou
                                       void* ws, hipStream_t st) {
     const GroupPlan p = group_plan(a, true);
     GroupArgs b = args_of(a, p);
-    const int64_t rows = p.heads ? p.units : a.N * p.chunks;
     b.stats = (float*)ws;
-    b.cols = p.heads ? (float*)ws
-                     : (float*)((char*)ws + up256((size_t)rows * a.G * 2 * sizeof(float)));
+    b.cols = p.heads ? (float*)ws : (float*)((char*)ws + stats_bytes(a, p));
     b.dy = g.dy, b.ds = g.dy_stride, b.y = g.dx, b.dz = g.dz;
     if (a.N > 0) {
         const hipError_t e = group_run(a.dtype, b, p, true, st);
         if (e != hipSuccess) return e;
     }
-    return launch_column_sums(b.cols, a.N > 0 ? (int)rows : 0, 2 * (int64_t)a.C, g.dgamma, a.C,
-                              g.dbeta, st);
+    const int64_t sums = p.heads ? 0 : launch_sums(a, p);
+    return launch_column_sums(sums ? b.cols + p.units * 2 * a.C : b.cols,
+                              a.N > 0 ? (int)(sums ? sums : p.units) : 0, 2 * (int64_t)a.C, g.dgamma,
+                              a.C, g.dbeta, st);
 }
 
 }  // namespace tg

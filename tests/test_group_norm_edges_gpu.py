@@ -57,3 +57,45 @@ def test_a_spread_past_fp32_is_not_taken_for_none(shape, G):
     want, _, _ = D.group_norm(c.flat(c.x), c.G, c.gamma.double(), None, 1e-5, "none", None)
     y = tg.group_norm(*c.args(), **c.more()).double().cpu().reshape(want.shape)
     assert bool((torch.isnan(y) | (y.abs() <= 1.01 * want.abs())).all())
+
+
+# Maps and long groups by the thousand, the first of them more than the backward pass
+# holds channels' sums of at once.
+MANY = [((4500, 4120), 1, BF16), ((2500, 1, 600), 2, F32), ((3001, 700), 1, BF16), ((2100, 3, 40), 4, F32), ((5000, 2, 2, 33), 3, BF16)]
+
+
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("shape,G,dtype", MANY, ids=str)
+def test_many_maps(shape, G, dtype, gate):
+    """Gradients of all, against the same maps a few at a time; gamma's and beta's
+    against their sum in 64 bits."""
+    note("group norm, many maps %s %s %s" % (shape, dtype, gate))
+    c = Case((shape, G, "f32" if dtype is F32 else "bf16", "silu", True, gate, 0))
+    (x, _, gamma), more, dy = c.args(), c.more(), up(c.dy)
+    z = more.pop("z")
+    y, mean, rstd = tg.group_norm_train(x, G, gamma, z=z, **more)
+    got = tg.group_norm_backward(dy, x, G, gamma, mean, rstd, z=z, **more)
+    again = tg.group_norm_backward(dy, x, G, gamma, mean, rstd, z=z, **more)
+    assert all(a is b or torch.equal(a, b) for a, b in zip(got, again))
+    for lo in range(0, shape[0], 500):
+        cut = lambda t: None if t is None else t[lo:lo + 500]  # noqa: E731
+        some = tg.group_norm_backward(cut(dy), cut(x), G, gamma, cut(mean), cut(rstd), z=cut(z), **more)
+        assert torch.equal(some.dx, got.dx[lo:lo + 500])
+        assert z is None or torch.equal(some.dz, got.dz[lo:lo + 500])
+    C = shape[-1]
+    leaf = [c.gamma.double().requires_grad_(), c.beta.double().requires_grad_()]
+    x64, dy64, z64 = c.flat(c.x), c.flat(c.dy), c.flat(c.z)
+    out, _, _ = D.group_norm(x64, G, leaf[0], leaf[1], 1e-5, "silu", z64)
+    want = torch.autograd.grad((out * dy64).sum(), leaf)
+    h = ((x64.reshape(shape[0], -1, G, C // G) - mean.double().cpu()[:, None, :, None])
+         * rstd.double().cpu()[:, None, :, None]).reshape(x64.shape)
+    v = h * c.gamma.double() + c.beta.double()
+    s = torch.sigmoid(v)
+    dv = dy64 * (1 if z64 is None else z64 * torch.sigmoid(z64)) * s * (1 + v * (1 - s))
+    rows = dv.shape[0] * dv.shape[1]
+    # Single roundings: of h (the mean's among them), v, the slopes, products: of each term.
+    for name, w, terms in (("dgamma", want[0], dv * h), ("dbeta", want[1], dv)):
+        big = (dy64.abs() * (1 if z64 is None else z64.abs()) * (1 + h.abs()) ** 2 * (1 + c.gamma.abs().max()))
+        bound = 32 * D.E * big.sum((0, 1)) + (rows + 64) ** 0.5 * 8 * D.E * terms.abs().sum((0, 1))
+        bad = ~((getattr(got, name).double().cpu() - w).abs() <= bound)
+        assert not bad.any(), (name, int(bad.sum()))
