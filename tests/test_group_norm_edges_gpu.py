@@ -59,6 +59,27 @@ def test_a_spread_past_fp32_is_not_taken_for_none(shape, G):
     assert bool((torch.isnan(y) | (y.abs() <= 1.01 * want.abs())).all())
 
 
+def sums_of(c, mean, rstd, got):
+    """gamma's and beta's gradients against their sums in 64 bits."""
+    shape, G, C = c.shape, c.G, c.shape[-1]
+    leaf = [c.gamma.double().requires_grad_(), c.beta.double().requires_grad_()]
+    x64, dy64, z64 = c.flat(c.x), c.flat(c.dy), c.flat(c.z)
+    out, _, _ = D.group_norm(x64, G, leaf[0], leaf[1], 1e-5, "silu", z64)
+    want = torch.autograd.grad((out * dy64).sum(), leaf)
+    h = ((x64.reshape(shape[0], -1, G, C // G) - mean.double().cpu()[:, None, :, None])
+         * rstd.double().cpu()[:, None, :, None]).reshape(x64.shape)
+    v = h * c.gamma.double() + c.beta.double()
+    s = torch.sigmoid(v)
+    dv = dy64 * (1 if z64 is None else z64 * torch.sigmoid(z64)) * s * (1 + v * (1 - s))
+    rows = dv.shape[0] * dv.shape[1]
+    # Single roundings: of h (the mean's among them), v, the slopes, products: of each term.
+    for name, w, terms in (("dgamma", want[0], dv * h), ("dbeta", want[1], dv)):
+        big = (dy64.abs() * (1 if z64 is None else z64.abs()) * (1 + h.abs()) ** 2 * (1 + c.gamma.abs().max()))
+        bound = 32 * D.E * big.sum((0, 1)) + (rows + 64) ** 0.5 * 8 * D.E * terms.abs().sum((0, 1))
+        bad = ~((getattr(got, name).double().cpu() - w).abs() <= bound)
+        assert not bad.any(), (name, int(bad.sum()))
+
+
 # Maps and long groups by the thousand, the first of them more than the backward pass
 # holds channels' sums of at once.
 MANY = [((4500, 4120), 1, BF16), ((2500, 1, 600), 2, F32), ((3001, 700), 1, BF16), ((2100, 3, 40), 4, F32), ((5000, 2, 2, 33), 3, BF16)]
@@ -82,20 +103,32 @@ def test_many_maps(shape, G, dtype, gate):
         some = tg.group_norm_backward(cut(dy), cut(x), G, gamma, cut(mean), cut(rstd), z=cut(z), **more)
         assert torch.equal(some.dx, got.dx[lo:lo + 500])
         assert z is None or torch.equal(some.dz, got.dz[lo:lo + 500])
-    C = shape[-1]
-    leaf = [c.gamma.double().requires_grad_(), c.beta.double().requires_grad_()]
-    x64, dy64, z64 = c.flat(c.x), c.flat(c.dy), c.flat(c.z)
-    out, _, _ = D.group_norm(x64, G, leaf[0], leaf[1], 1e-5, "silu", z64)
-    want = torch.autograd.grad((out * dy64).sum(), leaf)
-    h = ((x64.reshape(shape[0], -1, G, C // G) - mean.double().cpu()[:, None, :, None])
-         * rstd.double().cpu()[:, None, :, None]).reshape(x64.shape)
-    v = h * c.gamma.double() + c.beta.double()
-    s = torch.sigmoid(v)
-    dv = dy64 * (1 if z64 is None else z64 * torch.sigmoid(z64)) * s * (1 + v * (1 - s))
-    rows = dv.shape[0] * dv.shape[1]
-    # Single roundings: of h (the mean's among them), v, the slopes, products: of each term.
-    for name, w, terms in (("dgamma", want[0], dv * h), ("dbeta", want[1], dv)):
-        big = (dy64.abs() * (1 if z64 is None else z64.abs()) * (1 + h.abs()) ** 2 * (1 + c.gamma.abs().max()))
-        bound = 32 * D.E * big.sum((0, 1)) + (rows + 64) ** 0.5 * 8 * D.E * terms.abs().sum((0, 1))
-        bad = ~((getattr(got, name).double().cpu() - w).abs() <= bound)
-        assert not bad.any(), (name, int(bad.sum()))
+    sums_of(c, mean, rstd, got)
+
+
+# More rows than the heads kernel has in flight (512 backward, 2048 * 2048 / C forward), the
+# last round for some of a wave's rows only; groups of one lane, of a wave, across vectors.
+ROUNDS = [((1100, 64), 4, "bf16"), ((1999, 24), 3, "f32"), ((1301, 33), 3, "f16"), ((2500, 2048), 16, "bf16"), ((2300, 2048), 8, "f32"),
+          ((1030, 512), 2, "f16"), ((530, 16), 1, "f32"), ((2700, 100), 50, "bf16")]
+
+
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("shape,G,dt", ROUNDS, ids=str)
+def test_many_rows_of_heads(shape, G, dt, gate):
+    """Forward and backward against calls of fewer rows than are in flight, which
+    test_group_norm_gpu.py holds against 64 bits; gamma's and beta's gradients here."""
+    note("group norm, many rows %s %s %s" % (shape, dt, gate))
+    c = Case((shape, G, dt, "silu", True, gate, 0))
+    (x, _, gamma), more, dy = c.args(), c.more(), up(c.dy)
+    z = more.pop("z")
+    y, mean, rstd = tg.group_norm_train(x, G, gamma, z=z, **more)
+    assert torch.equal(y, tg.group_norm(x, G, gamma, z=z, **more))
+    got = tg.group_norm_backward(dy, x, G, gamma, mean, rstd, z=z, **more)
+    for lo in range(0, shape[0], 300):
+        cut = lambda t: None if t is None else t[lo:lo + 300]  # noqa: E731
+        some = tg.group_norm_train(cut(x), G, gamma, z=cut(z), **more)
+        assert all(torch.equal(a, b[lo:lo + 300]) for a, b in zip(some, (y, mean, rstd)))
+        d = tg.group_norm_backward(cut(dy), cut(x), G, gamma, cut(mean), cut(rstd), z=cut(z), **more)
+        assert torch.equal(d.dx, got.dx[lo:lo + 300])
+        assert z is None or torch.equal(d.dz, got.dz[lo:lo + 300])
+    sums_of(c, mean, rstd, got)
