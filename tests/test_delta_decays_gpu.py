@@ -110,3 +110,24 @@ def test_infinite_steps():
     _, saved = tg.gated_delta_rule_train(*c.args(), **c.more())
     got = tg.gated_delta_rule_backward(c.dev(c.dy), *c.args(), saved, dstate=up(c.dstate), **c.more())
     assert not got.ddt[0, 20].any() and all(bool(torch.isfinite(t).all()) for t in got)
+
+
+@pytest.mark.parametrize("lengths", [[300], [65, 200, 1], [1500]], ids=str)
+def test_gradients_of_growing_decays(lengths):
+    """Decays above 1: a share u of the largest state, or of its gradient, grows by no
+    more than all decays together on its way, so that the product of both may be off by
+    e^2G times what it may be off without growth."""
+    c = Case((lengths, True, 1, 2, 16, 24, "f32", True, False, 0))
+    c.dt_bias, c.A = None, torch.tensor([1.0, 0.5])
+    c.dt = torch.full((c.T, 2), 1.5 / max(lengths))
+    leaf = [t.double().requires_grad_() for t in (c.q, c.k, c.v, c.dt, c.A, c.beta, c.initial)]
+    q, k, v, dt, A, beta, initial = leaf
+    y, state, _, kap, chunks = D.delta(c.bounds, q, k, v, dt, A, beta, None, False, True, True, None, initial)
+    want = torch.autograd.grad((y * c.dy.double()).sum() + (state * c.dstate.double()).sum(), leaf)
+    more = dict(initial_state=up(c.initial), offsets=c.offsets, softplus=False)
+    _, saved = tg.gated_delta_rule_train(*c.args(), **more)
+    got = tg.gated_delta_rule_backward(c.dev(c.dy), *c.args(), saved, dstate=up(c.dstate), **more)
+    allowed = 2 * (2 * chunks * D.STEPS) ** 0.5 * kap * kap * D.E * float(torch.exp(torch.tensor(2 * 1.5)))
+    for name, w in zip(("dq", "dk", "dv", "ddt", "dA", "dbeta", "dinitial_state"), want):
+        d = float((getattr(got, name).double().cpu().reshape(w.shape) - w).norm() / w.norm())
+        assert d <= allowed, "%s: %.3g, allowed %.3g" % (name, d, allowed)

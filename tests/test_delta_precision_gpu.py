@@ -73,3 +73,22 @@ def test_gradients_of_q_and_k_round_once(case):
         n = int((getattr(got, name).cpu().reshape(want.shape) != want.to(c.dtype)).sum())
         most = float(share.sum()) + 4 * float((share * (1 - share)).sum()) ** 0.5 + 1
         assert n <= most, "%s: %d of %d not the rounded value, allowed %.0f" % (name, n, want.numel(), most)
+
+
+@pytest.mark.parametrize("case", [c for c in SHORT if c[6] == "f32"], ids=str)
+def test_gradients_of_fp32_by_their_squares(case):
+    """Through both walks, twice the roundings of one and KAPPA for each; of what an
+    element is a difference of, for q and k."""
+    note("delta fp32 gradients %s" % (case,))
+    c = Case(case)
+    x, bias, initial, y, state, g, kap, chunks = c.want(True)
+    total = (y * c.dy.double()).sum() + (state * c.dstate.double()).sum()
+    want = torch.autograd.grad(total, x + [initial, g[1], g[2]])
+    _, saved = tg.gated_delta_rule_train(*c.args(), **c.more())
+    got = tg.gated_delta_rule_backward(c.dev(c.dy), *c.args(), saved, dstate=up(c.dstate), **c.more())
+    allowed = 2 * (2 * chunks * D.STEPS) ** 0.5 * kap * kap * D.E
+    for name, w, size in (("dq", want[0], D.unit_size(x[0].detach(), want[7])), ("dk", want[1], D.unit_size(x[1].detach(), want[8])),
+                          ("dv", want[2], want[2]), ("ddt", want[3], want[3]), ("dbeta", want[5], want[5]),
+                          ("dinitial_state", want[6], want[6])):
+        d = float((getattr(got, name).double().cpu().reshape(w.shape) - w).norm() / torch.maximum(size.abs(), w.abs()).norm())
+        assert d <= allowed, "%s: %.3g, allowed %.3g" % (name, d, allowed)
