@@ -15,7 +15,7 @@
 // q and k enter the products as they are; their inverse lengths, the decays, b
 // and the scale are factors of rows, applied to accumulators in fp32.
 //
-// The matrices take 64 us for 4 x 4096 tokens of 16 heads of 128 (3.9 TB/s of q and k read
+// The matrices take 66 us for 4 x 4096 tokens of 16 heads of 128 (4.1 TB/s of q and k read
 // and matrices written), 22 us for a quarter of them in training.
 #include "seq_delta.hpp"
 #include "tg_internal.hpp"

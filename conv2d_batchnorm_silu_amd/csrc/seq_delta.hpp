@@ -10,8 +10,8 @@
 // fp32's range, which fp16 parts would not have.
 //
 // That holds for prompts too, where two parts (17 bits) left the fp32 states off by 2 to
-// 5e-6 of their norm, ten times as much, for 185 us in place of 220 (4 x 4096 tokens of 16
-// heads). Products that only reach y, or only the gradients of q and k, take two parts of
+// 5e-6 of their norm, ten times as much, for a walk of 185 us in place of 225 (4 x 4096
+// tokens of 16 heads). Products that only reach y, or only the gradients of q and k, take two parts of
 // 16-bit tensors: a single one left bf16 outputs off by 1.6 times their rounding, dq and
 // dk by 1.3, and by any share where most of them is taken off again along q and k.
 //
@@ -466,8 +466,8 @@ __device__ __forceinline__ float decay_between(double hi, double lo) {
 // prepared fragments of its own tokens to registers as soon as it has used the last
 // chunk's. 4 x 4096 tokens of 16 heads of 128 x 128, bf16: a wave for 16 whole columns and
 // four that load 215 us, four waves that share S and everything else 230, with helpers
-// 164 (185 since y is made of two parts): 2.9 us a chunk, of which a carrying wave
-// computes for about 40% and waits for LDS, matrix results and barriers for the rest.
+// 164 (185 since y is made of two parts, 225 since the states always take three): 3.5 us a
+// chunk, half of all wave cycles waits for LDS, matrix results and barriers.
 constexpr int slice_of(int in, int KP) { return in * KP > 512 ? 16 : 32; }
 
 // A barrier for what lies in LDS: __syncthreads would also wait for the loads and

@@ -9,9 +9,11 @@ namespace {
 
 // ---- the chunks' own gradients
 //
-// 2 x 2048 tokens of 16 heads of 128 x 128, bf16: 137 us, a wave on each SIMD (120 KB of
-// LDS), half of its time waiting: the next block of V in registers while one is worked
-// on took 133 there but 34 for 22 on 64 columns, eight waves 238 (spilled).
+// 2 x 2048 tokens of 16 heads of 128 x 128, bf16: 147 us, a wave on each SIMD (120 KB of
+// LDS), half of its time waiting. (137 before the pairs' factors took two parts and the
+// decays' gradients each pair by itself; then the next block of V in registers while one is
+// worked on took 133, but 34 for 22 on 64 columns, and eight waves 238, spilled.) For K of
+// 129 to 256 all of dq and dk does not fit the registers: 80 to 250 are spilled.
 //
 // One workgroup for a chunk and key head; its value heads one after another, dq
 // and dk added up in registers. Wave w has the 16 rows (tokens) of tile w % (C/16)

@@ -946,8 +946,10 @@ def gated_delta_rule(q, k, v, dt, A, beta, dt_bias=None, softplus=True, sigmoid=
     (default zeros). Returns y, or with ``return_state`` (y, state). ``out`` may
     be v.
 
-    The states are computed to fp32's 24 bits, in training and without. Decays above 1 (A > 0) are taken as they are while the product over any tokens in
-    a row stays within fp32."""
+    The states are computed to fp32's 24 bits, in training and without. Decays above 1
+    (A > 0) are taken as they are while the product over any tokens in a row stays
+    within fp32. What is infinite or NaN in a token (a sum of squares of q or k past
+    fp32 too) reaches its own y and, but for q, later ones of its head."""
     dev = _device(v, "v")
     there = _elsewhere(dev, stream)
     if there is not None:

@@ -7,8 +7,9 @@
  *
  * Tensors. Activations (x, y, z, dt, B, C, q, k, v, beta and their gradients) share
  * one dtype: TG_F16, TG_BF16 or TG_F32. Parameters, statistics and states of the scan
- * and the delta rule are fp32. All arithmetic and all sums are fp32; every activation result is
- * rounded once, to nearest even. Channels are contiguous; a row is one token.
+ * and the delta rule are fp32. All arithmetic and all sums are fp32 or wider (but where
+ * the delta rule's text names fewer bits); every activation result is rounded once, to
+ * nearest even. Channels are contiguous; a row is one token.
  *
  * Sequences. A batch is dense or packed (tg_seqs):
  *   dense   offsets == NULL: rows = seqs * L, and row l of sequence s of a
@@ -216,9 +217,11 @@ tg_status tg_selective_scan_step(const tg_scan_args *a, float *state, int64_t nu
  * A NaN or infinite value of a token makes its own y and, but for q, those of the later
  * tokens of its head infinite or NaN (of v: in its column), and no other. In the
  * gradients it may reach any token of its sequence and key head.
- * TG_ERR_UNSUPPORTED for K > 256, row strides of 2^25 elements or more, 2^23 or more
- * pairs of a value head and 64 (32) tokens, and 2^22 or more of a sequence, a value
- * head and 16 columns. */
+ * TG_ERR_UNSUPPORTED for K > 256, row strides of 2^25 elements or more, 2^24 or more
+ * pairs of a value head and 64 tokens of a sequence (32 for fp16, fp32 and K > 128; 2^23
+ * pairs for K > 128; a packed batch counts rows/64 + seqs for each head), and 2^23 or more of a sequence and value head (a multiple of 8 of
+ * them) and 32 columns of V (16 for fp32 with K > 128); in a step 2^24 or more of a
+ * sequence, value head and 32 columns. */
 typedef struct {
     tg_seqs seqs;
     int HK, HV, K, V;
